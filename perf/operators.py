@@ -6,6 +6,7 @@
   gdn_backward  its gradients
   gdn_step      one token per request, the requests' states in a pool, updated in place
   attn_forward  causal softmax attention with grouped heads over the same rows or packed samples
+  attn_backward its gradients, from the outputs that the forward kept
 
 `run` computes the plain form in elementary torch operations where `own` is false, and calls the framework's
 operators where it is true.  `exact` is the definition token by token (the delta rule) and row by row (attention)
@@ -34,15 +35,13 @@ def listed():
     return [
         # the fp32 parity workload (text 64): the smallest call, where only latency counts
         dict(name="gdn_forward tiny fp32", op="gdn_forward", lens="64", packed=False, hk=2, hv=2, dk=32, dv=32, dtype="fp32", s0=False),
-        # a batch of text + image rows (256 + 64 x 64 tokens)
-        dict(name="gdn_forward image stream", op="gdn_forward", lens="4352,4352,4352,4352", packed=False, hk=16, hv=16, dk=128, dv=128, dtype="bf16", s0=False),
         # prompts of one to a few thousand tokens packed on one axis, continuing from kept states; two value heads to a key head
         dict(name="gdn_forward packed", op="gdn_forward", lens="1,777,64,2049,130,63,1500,3,512,901,65,333", packed=True, hk=4, hv=8, dk=128, dv=128, dtype="bf16", s0=True),
         # one text + video row (512 + 21 x 32 x 48 tokens): few heads, a long serial axis
         dict(name="gdn_forward video clip", op="gdn_forward", lens="32768", packed=False, hk=16, hv=16, dk=128, dv=128, dtype="bf16", s0=False),
         # training on packed samples with shared key heads and narrow keys
         dict(name="gdn_backward packed", op="gdn_backward", lens="700,1,1333,64,255,1024", packed=True, hk=4, hv=8, dk=64, dv=128, dtype="bf16", s0=False),
-        # training on the image-stream batch
+        # training on a batch of text + image rows (256 + 64 x 64 tokens)
         dict(name="gdn_backward image stream", op="gdn_backward", lens="4352,4352,4352,4352", packed=False, hk=16, hv=16, dk=128, dv=128, dtype="bf16", s0=False),
         # one request answered token by token
         dict(name="gdn_step one request", op="gdn_step", n=1, slots=4, hk=16, hv=16, dk=128, dv=128, dtype="bf16"),
@@ -52,10 +51,12 @@ def listed():
         dict(name="attn_forward text", op="attn_forward", lens="512", packed=True, hq=16, hkv=4, d=128, dtype="bf16"),
         # ragged prompts, one token among them, narrow heads
         dict(name="attn_forward packed", op="attn_forward", lens="1,777,64,2049,130,63,1500,3,512,901,65,333", packed=True, hq=8, hkv=2, d=64, dtype="bf16"),
-        # the image-stream batch
-        dict(name="attn_forward image stream", op="attn_forward", lens="4352,4352,4352,4352", packed=False, hq=16, hkv=4, d=128, dtype="bf16"),
         # one long row
         dict(name="attn_forward long", op="attn_forward", lens="16384", packed=False, hq=16, hkv=4, d=128, dtype="bf16"),
+        # training on packed samples, narrow heads
+        dict(name="attn_backward packed", op="attn_backward", lens="700,1,1333,64,255,1024", packed=True, hq=8, hkv=2, d=64, dtype="bf16"),
+        # training on the image-stream batch
+        dict(name="attn_backward image stream", op="attn_backward", lens="4352,4352,4352,4352", packed=False, hq=16, hkv=4, d=128, dtype="bf16"),
     ]
 
 
@@ -73,13 +74,13 @@ def _draw_lens(rng, total, most_seqs):
 
 
 def draw(rng):
-    op = rng.choice(("gdn_forward", "gdn_forward", "gdn_backward", "gdn_step", "attn_forward", "attn_forward"))
+    op = rng.choice(("gdn_forward", "gdn_forward", "gdn_backward", "gdn_step", "attn_forward", "attn_backward"))
     if op == "gdn_step":
         n = _logint(rng, 1, 256)
         hk = rng.choice((1, 2, 4, 6, 8, 16))
         return dict(op=op, n=n, slots=n + rng.randrange(0, 40), hk=hk, hv=hk * rng.choice((1, 2)), dk=rng.choice((64, 128)),
                     dv=rng.choice((64, 128)), dtype="bf16")
-    if op == "attn_forward":
+    if op in ("attn_forward", "attn_backward"):
         lens, packed = _draw_lens(rng, _logint(rng, 100, 12000), 16)
         hkv = rng.choice((1, 2, 3, 4))
         return dict(op=op, lens=",".join(map(str, lens)), packed=packed, hq=hkv * rng.choice((1, 2, 3, 4)), hkv=hkv,
@@ -96,9 +97,11 @@ def draw(rng):
 
 def work(case):
     e = 4 if case["dtype"] == "fp32" else 2
-    if case["op"] == "attn_forward":
+    if case["op"] in ("attn_forward", "attn_backward"):
         t, h, hk, d = sum(_lens(case)), case["hq"], case["hkv"], case["d"]
         pairs = sum(n * (n + 1) // 2 for n in _lens(case))
+        if case["op"] == "attn_backward":
+            return {"bytes": 4 * t * h * d * e + 4 * t * hk * d * e + 4 * t * h, "flops": 10 * pairs * h * d}
         return {"bytes": 2 * t * h * d * e + 2 * t * hk * d * e + 4 * t * h, "flops": 4 * pairs * h * d}
     hk, hv, dk, dv = case["hk"], case["hv"], case["dk"], case["dv"]
     if case["op"] == "gdn_step":
@@ -123,7 +126,7 @@ def prepare(case, seed):
         x = normal(*shape)
         return (x / x.square().sum(-1, keepdim=True).sqrt()).to(dt)
 
-    if case["op"] == "attn_forward":
+    if case["op"] in ("attn_forward", "attn_backward"):
         lens = _lens(case)
         lead = (sum(lens),) if case["packed"] else (len(lens), lens[0])
         s = {"q": normal(*lead, case["hq"], case["d"]).to(dt), "k": normal(*lead, case["hkv"], case["d"]).to(dt),
@@ -148,6 +151,9 @@ def prepare(case, seed):
     s["op"], s["packed"] = case["op"], case.get("packed", False)
     if case["op"] != "gdn_step":
         s["lens"], s["cu"] = lens, [sum(lens[:i]) for i in range(len(lens) + 1)]
+    if case["op"] == "attn_backward":
+        s["o"], s["lse"] = _plain_attention(s)  # what the forward pass of the training step kept
+        s["do"] = (0.01 * normal(*lead, case["hq"], case["d"])).to(dt)
     return s
 
 
@@ -260,6 +266,31 @@ def _plain_attention(s):
     return o.view_as(s["q"]), lse.view(s["q"].shape[:-1])
 
 
+def _plain_attention_backward(s):
+    q, k, v, do = (_flat(s[n], s["packed"]) for n in ("q", "k", "v", "do"))
+    h, d, hk = q.shape[1], q.shape[2], k.shape[1]
+    r = h // hk
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    for at, n in zip(s["cu"], s["lens"]):
+        K, V = k[at:at + n].float().transpose(0, 1), v[at:at + n].float().transpose(0, 1)
+        gK, gV = torch.zeros_like(K), torch.zeros_like(V)
+        rows = 1024
+        for i in range(0, n, rows):
+            m = min(n, i + rows)
+            Q, G = (t[at + i:at + m].float().view(m - i, hk, r, d).permute(1, 2, 0, 3).reshape(hk, -1, d) for t in (q, do))
+            x = (Q @ K[:, :m].transpose(1, 2) / math.sqrt(d)).view(hk, r, m - i, m)
+            x = torch.where(torch.arange(m, device=q.device) <= torch.arange(i, m, device=q.device)[:, None], x, -math.inf)
+            p = torch.exp(x - x.amax(-1, keepdim=True))
+            p = (p / p.sum(-1, keepdim=True)).view(hk, -1, m)
+            gp = G @ V[:, :m].transpose(1, 2)
+            gx = p * (gp - (p * gp).sum(-1, keepdim=True)) / math.sqrt(d)
+            gV[:, :m] += p.transpose(1, 2) @ G
+            gK[:, :m] += gx.transpose(1, 2) @ Q
+            dq[at + i:at + m] = (gx @ K[:, :m]).view(hk, r, m - i, d).permute(2, 0, 1, 3).reshape(m - i, h, d).to(q.dtype)
+        dk[at:at + n], dv[at:at + n] = gK.transpose(0, 1).to(k.dtype), gV.transpose(0, 1).to(v.dtype)
+    return dq.view_as(s["q"]), dk.view_as(s["k"]), dv.view_as(s["v"])
+
+
 # ---- the framework's operators --------------------------------------------------------------------------------
 def _own(s):
     from linear_attention_sequence_mshortconv_b200 import attention, gdn
@@ -270,6 +301,9 @@ def _own(s):
         if s["packed"]:
             return attention.forward_varlen(s["q"], s["k"], s["v"], s["cu"])
         return attention.forward(s["q"], s["k"], s["v"])
+    if s["op"] == "attn_backward":
+        x = [s[n] for n in ("q", "k", "v", "o", "lse", "do")]
+        return attention.backward_varlen(*x, s["cu"]) if s["packed"] else attention.backward(*x)
     x = [s[n] for n in ("q", "k", "v", "g", "beta")]
     if s["op"] == "gdn_forward":
         return gdn.forward_varlen(*x, s["cu"], s["S0"]) if s["packed"] else gdn.forward(*x, s["S0"])
@@ -284,6 +318,8 @@ def run(state):
         return _plain_step(state)
     if state["op"] == "attn_forward":
         return _plain_attention(state)
+    if state["op"] == "attn_backward":
+        return _plain_attention_backward(state)
     return _plain_gdn(state, state["op"] == "gdn_backward")
 
 
@@ -377,8 +413,28 @@ def _exact_attention(s):
     return o.view(s["q"].shape), lse.view(s["q"].shape[:-1])
 
 
+def _exact_attention_backward(s):
+    q, k, v, do = (_flat(s[n], s["packed"]) for n in ("q", "k", "v", "do"))
+    r, c = q.shape[1] // k.shape[1], q.shape[2] ** -0.5
+    dq, dk, dv = (torch.zeros(x.shape, dtype=torch.float64, device=x.device) for x in (q, k, v))
+    for at, n in zip(s["cu"], s["lens"]):
+        for h in range(q.shape[1]):
+            for i in range(0, n, 4096):
+                m = min(n, i + 4096)
+                Q, K, V, G = q[at + i:at + m, h].double(), k[at:at + m, h // r].double(), v[at:at + m, h // r].double(), do[at + i:at + m, h].double()
+                p = torch.softmax((Q @ K.T * c).masked_fill_(torch.ones(m - i, m, dtype=torch.bool, device=q.device).triu(i + 1), -math.inf), -1)
+                dv[at:at + m, h // r] += p.T @ G
+                y = G @ V.T
+                y = c * p * (y - (G * (p @ V)).sum(-1, keepdim=True))
+                dq[at + i:at + m, h] = y @ K
+                dk[at:at + m, h // r] += y.T @ Q
+    return dq.view(s["q"].shape), dk.view(s["k"].shape), dv.view(s["v"].shape)
+
+
 def exact(case, seed):
     s = prepare(case, seed)
+    if case["op"] == "attn_backward":
+        return _exact_attention_backward(s)
     if case["op"] == "gdn_step":
         return _exact_step(s)
     if case["op"] == "attn_forward":
