@@ -75,7 +75,8 @@ const char* kda_status_string(kda_status s);
 /* Reads and clears the calling thread's current device's status word, in which
  * kernels record device-side failures (KDA_OK if none; the first one recorded wins):
  * KDA_ERR_TIMEOUT (a bounded wait ran out), KDA_ERR_UNSUPPORTED (kda_backward or
- * kda_mshortconv_backward met a chunk outside its decay domain).  Synchronous: it waits
+ * kda_mshortconv_backward met a chunk outside its decay domain), KDA_ERR_INVALID_ARG
+ * (gdn_step met a slot outside its pool or named twice).  Synchronous: it waits
  * for all work on the device to finish. */
 kda_status kda_last_device_error(void);
 
@@ -405,6 +406,134 @@ kda_status kda_mshortconv_backward(const void* xq, const void* xk, const void* x
                                    float* dg, float* dbeta, float* dS0, int B, int T, int H, int D,
                                    kda_dtype dtype, void* workspace, size_t workspace_bytes,
                                    kda_stream_t stream);
+
+/* ---- the gated delta rule ------------------------------------------------------
+ *
+ * The delta rule of kda_forward with one gate per value head and token in place of one per
+ * key channel, and with value heads that share query/key heads (value head h reads
+ * query/key head h / (Hv / Hk); Hv is a multiple of Hk):
+ *     S_t = alpha_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   alpha_t = e^{g_t},
+ *     o_t = S_t^T q_t.
+ * No scaling and no normalisation happens inside.  Rows (or packed samples) are independent
+ * scans.
+ *
+ * gdn_forward -- whole sequences.
+ *   q, k    : [B, T, Hk, Dk] dtype        v : [B, T, Hv, Dv] dtype
+ *   g, beta : [B, T, Hv]     dtype        g = ln(alpha) <= 0 (-inf: alpha = 0)
+ *   S0      : [B, Hv, Dk, Dv] fp32 or NULL (zeros);  S_T : the same, written, or NULL
+ *   o       : [B, T, Hv, Dv] dtype        must not alias an input
+ *   Dk, Dv in {32, 64, 128}; dtype KDA_BF16 or KDA_F32 (every tensor but S0 and S_T).
+ *   T may be 0 (o untouched, S_T = S0).
+ *   workspace : as for kda_forward, of gdn_forward_workspace_size(...) bytes.
+ * Sums, states and gates are fp32 or wider.  A value that is not finite at one token may
+ * reach every later token of its row and the earlier tokens of its 64-token chunk, but never
+ * another row.
+ * Errors: KDA_ERR_INVALID_ARG (null tensor with work to do, bad sizes or dtype, Hv not a
+ * multiple of Hk), KDA_ERR_UNSUPPORTED (Dk or Dv outside {32, 64, 128}; B or Hv > 65535; more
+ * than 0x7fff0000 tokens), KDA_ERR_WORKSPACE, KDA_ERR_CUDA.
+ *
+ * gdn_forward_varlen -- packed samples: tensors [T_total, ...] and S0, S_T [n_seqs, ...],
+ *   cu_seqlens a HOST array of n_seqs + 1 offsets as for kda_forward_varlen (empty samples
+ *   allowed).  The offsets travel as kernel parameters, 255 samples to a launch, so a stream
+ *   capture holds its own copy of them.  Rows behind the last offset are left as they are.
+ */
+size_t gdn_forward_workspace_size(int B, int T, int Hk, int Hv, int Dk, int Dv, kda_dtype dtype);
+kda_status gdn_forward(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                       const float* S0, void* o, float* S_T, int B, int T, int Hk, int Hv, int Dk, int Dv,
+                       kda_dtype dtype, void* workspace, size_t workspace_bytes, kda_stream_t stream);
+size_t gdn_forward_varlen_workspace_size(const int32_t* cu_seqlens, int n_seqs, int Hk, int Hv, int Dk, int Dv,
+                                         kda_dtype dtype);
+kda_status gdn_forward_varlen(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                              const float* S0, void* o, float* S_T, const int32_t* cu_seqlens, int n_seqs,
+                              int Hk, int Hv, int Dk, int Dv, kda_dtype dtype, void* workspace,
+                              size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * gdn_backward -- gradients of gdn_forward for dL/do = d_o and dL/dS_T = dS_T.
+ *   q, k, v, g, beta, S0, B ... dtype : exactly as passed to gdn_forward.
+ *   d_o  : [B, T, Hv, Dv] dtype;  dS_T : [B, Hv, Dk, Dv] fp32 or NULL (zeros).
+ *   dq, dk, dv, dg, dbeta : written, with the shapes and the dtype of q, k, v, g, beta; each is
+ *          accumulated in fp32 and rounded once.  dq and dk are summed over the value heads
+ *          of a query/key head in a fixed order: results do not change from run to run.
+ *   dS0  : [B, Hv, Dk, Dv] fp32, written, or NULL.
+ * The gradient of g is that of the logarithm (alpha = e^g).  The call reruns the forward.
+ * workspace : gdn_backward_workspace_size(...) bytes.  Errors: as gdn_forward.
+ * gdn_backward_varlen -- the same over packed samples.
+ */
+size_t gdn_backward_workspace_size(int B, int T, int Hk, int Hv, int Dk, int Dv, kda_dtype dtype);
+kda_status gdn_backward(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                        const float* S0, const void* d_o, const float* dS_T, void* dq, void* dk, void* dv,
+                        void* dg, void* dbeta, float* dS0, int B, int T, int Hk, int Hv, int Dk, int Dv,
+                        kda_dtype dtype, void* workspace, size_t workspace_bytes, kda_stream_t stream);
+size_t gdn_backward_varlen_workspace_size(const int32_t* cu_seqlens, int n_seqs, int Hk, int Hv, int Dk, int Dv,
+                                          kda_dtype dtype);
+kda_status gdn_backward_varlen(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                               const float* S0, const void* d_o, const float* dS_T, void* dq, void* dk, void* dv,
+                               void* dg, void* dbeta, float* dS0, const int32_t* cu_seqlens, int n_seqs,
+                               int Hk, int Hv, int Dk, int Dv, kda_dtype dtype, void* workspace,
+                               size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * gdn_step -- one token of each of n requests, the states in a pool and updated in place.
+ *   q, k : [n, Hk, Dk] dtype;  v, o : [n, Hv, Dv] dtype;  g, beta : [n, Hv] dtype
+ *   state : [n_slots, Hv, Dk, Dv] fp32, 16-byte aligned
+ *   slots : [n] int32 (device): request i uses state[slots[i]]; NULL: request i uses state[i]
+ *           (then n <= n_slots).  A negative slot is a padding request: its o is zeros and
+ *           no state is touched.
+ * A slot of n_slots or more, and a slot that an earlier request of the call names too, is
+ * treated as padding and reported by kda_last_device_error() as KDA_ERR_INVALID_ARG (the
+ * slots are device memory: the host sees them only then); the first request that names a
+ * slot is carried out.  Needs no workspace and can be captured.
+ * Errors: as gdn_forward, and KDA_ERR_INVALID_ARG for a misaligned state;
+ * KDA_ERR_UNSUPPORTED for n > 65535.
+ */
+kda_status gdn_step(const void* q, const void* k, const void* v, const void* g, const void* beta, float* state,
+                    const int32_t* slots, void* o, int n, int n_slots, int Hk, int Hv, int Dk, int Dv,
+                    kda_dtype dtype, kda_stream_t stream);
+
+/* ---- causal attention with grouped heads ---------------------------------------
+ *
+ * The softmax layers of a hybrid stack, over the same rows or packed samples:
+ *     o_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j,  lse_i = ln sum_{j <= i} e^{scale q_i . k_j}
+ * inside each row; query head h reads key/value head h / (H / Hkv) (H a multiple of Hkv).
+ *
+ * attn_forward
+ *   q, o : [B, T, H, D] dtype;  k, v : [B, T, Hkv, D] dtype;  D in {32, 64, 128}
+ *   lse  : [B, T, H] fp32, written, or NULL
+ *   scale: finite (1 / sqrt(D) is usual; it may be negative or 0)
+ * Scores, their maximum and sum, and the output are accumulated in fp32; for bf16 the
+ * weights e^{s - max} are rounded to bf16 for the product with v.  A value that is not finite
+ * at one token may reach the earlier tokens of the same row that share its 128-token tile,
+ * and every later one, but never another row.
+ * attn_forward_varlen -- packed samples, cu_seqlens as for gdn_forward_varlen.
+ * Errors: KDA_ERR_INVALID_ARG (null tensor with work to do, bad sizes or dtype, H not a
+ * multiple of Hkv, scale not finite), KDA_ERR_UNSUPPORTED (D; B or H > 65535; more than
+ * 0x7fff0000 tokens), KDA_ERR_CUDA.
+ */
+kda_status attn_forward(const void* q, const void* k, const void* v, void* o, float* lse, int B, int T, int H,
+                        int Hkv, int D, float scale, kda_dtype dtype, kda_stream_t stream);
+kda_status attn_forward_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                               const int32_t* cu_seqlens, int n_seqs, int H, int Hkv, int D, float scale,
+                               kda_dtype dtype, kda_stream_t stream);
+
+/*
+ * attn_backward -- gradients of attn_forward for dL/do = d_o, from the o and lse it wrote.
+ *   d_o : [B, T, H, D] dtype;  dq, dk, dv : written, with the shapes and dtype of q, k, v
+ *   (accumulated in fp32, rounded once; dk and dv are summed over the query heads of a
+ *   group in a fixed order: results do not change from run to run).
+ *   workspace : attn_backward_workspace_size(tokens = B * T, ...) bytes, as for kda_forward.
+ * attn_backward_varlen -- packed samples (workspace for tokens = cu_seqlens[n_seqs]).
+ * Errors: as attn_forward, and KDA_ERR_WORKSPACE.
+ */
+size_t attn_backward_workspace_size(int64_t tokens, int H, int Hkv, int D, kda_dtype dtype);
+kda_status attn_backward(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                         const void* d_o, void* dq, void* dk, void* dv, int B, int T, int H, int Hkv, int D,
+                         float scale, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                         kda_stream_t stream);
+kda_status attn_backward_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                const void* d_o, void* dq, void* dk, void* dv, const int32_t* cu_seqlens,
+                                int n_seqs, int H, int Hkv, int D, float scale, kda_dtype dtype, void* workspace,
+                                size_t workspace_bytes, kda_stream_t stream);
 
 /* ---- diagnostics ---------------------------------------------------------------- */
 

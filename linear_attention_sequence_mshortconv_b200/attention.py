@@ -1,0 +1,95 @@
+"""Thin Python binding of libkda's causal attention with grouped heads (see include/kda.h):
+
+    o_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j,   lse_i = ln sum_{j <= i} e^{scale q_i . k_j}
+
+over rows or packed samples, H / Hkv query heads to a key/value head.  Tensors are contiguous, on
+one CUDA device, and bf16 or fp32 alike (lse is fp32); a call runs on that device, on its current
+stream unless one is given.  There is no fallback.
+"""
+from __future__ import annotations
+
+import torch
+
+from .gdn import _packed, check_tensors, launching_on, ptr, scratch
+from .kda import _check, _code, _dtype_code, load_library
+
+
+def _sizes(q, k, dims):
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != dims or k.dim() != dims:
+        raise ValueError(f"q and k must have {dims} dimensions")
+    (H, D), Hkv = q.shape[-2:], k.shape[-2]
+    if Hkv == 0 or H % Hkv:
+        raise ValueError(f"{H} query heads cannot share {Hkv} key/value heads")
+    return H, Hkv, D
+
+
+def _forward(q, k, v, seqs, scale, o, lse, want_lse, stream, fn, dims):
+    H, Hkv, D = _sizes(q, k, dims)
+    dt = _dtype_code(q)
+    kv = (*q.shape[:-2], Hkv, D)
+    check_tensors(q, [("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype),
+                      ("o", o, q.shape, q.dtype), ("lse", lse, q.shape[:-1], torch.float32)])
+    lib = load_library()
+    with launching_on(q.device, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        rc = getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(o), ptr(lse), *seqs, H, Hkv, D,
+                              float(D ** -0.5 if scale is None else scale), dt, s)
+    _check(fn, rc)
+    return o, lse
+
+
+def forward(q, k, v, *, scale=None, o=None, lse=None, want_lse: bool = True, stream=None):
+    """attn_forward: q [B,T,H,D]; k, v [B,T,Hkv,D]; scale: 1/sqrt(D) unless given.  Returns
+    (o [B,T,H,D], lse [B,T,H] fp32 or None)."""
+    return _forward(q, k, v, tuple(q.shape[:2]), scale, o, lse, want_lse, stream, "attn_forward", 4)
+
+
+def forward_varlen(q, k, v, cu_seqlens, *, scale=None, o=None, lse=None, want_lse: bool = True, stream=None):
+    """attn_forward_varlen: packed samples on one token axis ([T_total, ...] tensors); cu_seqlens: host
+    sequence of n + 1 offsets.  Tokens behind the last offset are left as they are in given outputs."""
+    arr, n = _packed(cu_seqlens, q.shape[0])
+    return _forward(q, k, v, (arr, n), scale, o, lse, want_lse, stream, "attn_forward_varlen", 3)
+
+
+def backward_workspace_size(tokens, H, Hkv, D, dtype=torch.bfloat16) -> int:
+    return int(load_library().attn_backward_workspace_size(tokens, H, Hkv, D, _code(dtype)))
+
+
+def _backward(q, k, v, o, lse, do, seqs, tokens, scale, workspace, stream, out, fn, dims):
+    H, Hkv, D = _sizes(q, k, dims)
+    dt = _dtype_code(q)
+    kv = (*q.shape[:-2], Hkv, D)
+    given = (None,) * 3 if out is None else tuple(out)
+    check_tensors(q, [("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype),
+                      ("o", o, q.shape, q.dtype), ("lse", lse, q.shape[:-1], torch.float32), ("do", do, q.shape, q.dtype),
+                      ("dq", given[0], q.shape, q.dtype), ("dk", given[1], kv, q.dtype), ("dv", given[2], kv, q.dtype)])
+    if out is not None and any(t is None for t in given):
+        raise ValueError("out must hold dq, dk and dv")
+    if o is None or lse is None or do is None:
+        raise ValueError("o, lse and do are needed")
+    lib = load_library()
+    with launching_on(q.device, stream) as s:
+        if out is None:
+            given = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+        need = int(lib.attn_backward_workspace_size(tokens, H, Hkv, D, dt))
+        keep, ws, ws_bytes = scratch(workspace, need, q.device)
+        rc = getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(o), ptr(lse), ptr(do), *map(ptr, given), *seqs, H, Hkv, D,
+                              float(D ** -0.5 if scale is None else scale), dt, ws, ws_bytes, s)
+    _check(fn, rc)
+    return given
+
+
+def backward(q, k, v, o, lse, do, *, scale=None, workspace=None, stream=None, out=None):
+    """attn_backward: (dq, dk, dv) for dL/do = do through forward(q, k, v), from the o and lse it
+    returned; the gradients have the inputs' shapes and type.  `out` may hold preallocated tensors."""
+    return _backward(q, k, v, o, lse, do, tuple(q.shape[:2]), q.shape[0] * q.shape[1], scale, workspace, stream, out,
+                     "attn_backward", 4)
+
+
+def backward_varlen(q, k, v, o, lse, do, cu_seqlens, *, scale=None, workspace=None, stream=None, out=None):
+    """attn_backward_varlen: backward() over packed samples, as in forward_varlen()."""
+    arr, n = _packed(cu_seqlens, q.shape[0])
+    return _backward(q, k, v, o, lse, do, (arr, n), int(arr[n]), scale, workspace, stream, out, "attn_backward_varlen", 3)

@@ -48,7 +48,8 @@ class ProfileScope {
 // Codes a kernel may record (first writer wins).
 // DEV_RANGE: an input outside a kernel's documented domain (the scan's backward: a
 // 32-token chunk whose decay on some key channel is 80 or more in natural-log units).
-enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_RANGE = 2 };
+// DEV_SLOT: gdn_step was given a state slot outside its pool, or the same slot twice.
+enum : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_RANGE = 2, DEV_SLOT = 3 };
 // Address of this device's status word (set up once per device; thread-safe).
 int* device_status_ptr();
 

@@ -135,6 +135,7 @@ kda_status kda_last_device_error(void)
     return v == DEV_OK ? KDA_OK
          : v == DEV_TIMEOUT ? KDA_ERR_TIMEOUT
          : v == DEV_RANGE ? KDA_ERR_UNSUPPORTED
+         : v == DEV_SLOT ? KDA_ERR_INVALID_ARG
                           : KDA_ERR_CUDA;
 }
 

@@ -30,7 +30,11 @@ EXPORTED = ("kda_status_string", "kda_last_device_error", "kda_forward_workspace
             "kda_forward_gated", "kda_forward_varlen", "kda_forward_varlen_workspace_size",
             "kda_sp_workspace_size", "kda_sp_transition", "kda_sp_prefix", "kda_sp_output",
             "kda_backward", "kda_backward_workspace_size", "mshortconv_backward",
-            "kda_mshortconv_backward", "kda_mshortconv_backward_workspace_size", "kda_forward_plan")
+            "kda_mshortconv_backward", "kda_mshortconv_backward_workspace_size", "kda_forward_plan",
+            "gdn_forward_workspace_size", "gdn_forward", "gdn_forward_varlen_workspace_size", "gdn_forward_varlen",
+            "gdn_backward_workspace_size", "gdn_backward", "gdn_backward_varlen_workspace_size",
+            "gdn_backward_varlen", "gdn_step", "attn_forward", "attn_forward_varlen",
+            "attn_backward_workspace_size", "attn_backward", "attn_backward_varlen")
 
 
 class KdaError(RuntimeError):
@@ -117,6 +121,23 @@ def load_library(path: str = LIB_PATH):
         lib.kda_profile_collect.restype = I
         lib.kda_profile_collect.argtypes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double),
                                             ctypes.POINTER(ctypes.c_int)]
+        F, L = ctypes.c_float, ctypes.c_int64
+        for name, res, args in (
+                ("gdn_forward_workspace_size", Z, [I] * 7),
+                ("gdn_forward", I, [P] * 8 + [I] * 7 + [P, Z, P]),
+                ("gdn_forward_varlen_workspace_size", Z, [P] + [I] * 6),
+                ("gdn_forward_varlen", I, [P] * 9 + [I] * 6 + [P, Z, P]),
+                ("gdn_backward_workspace_size", Z, [I] * 7),
+                ("gdn_backward", I, [P] * 14 + [I] * 7 + [P, Z, P]),
+                ("gdn_backward_varlen_workspace_size", Z, [P] + [I] * 6),
+                ("gdn_backward_varlen", I, [P] * 15 + [I] * 6 + [P, Z, P]),
+                ("gdn_step", I, [P] * 8 + [I] * 7 + [P]),
+                ("attn_forward", I, [P] * 5 + [I] * 5 + [F, I, P]),
+                ("attn_forward_varlen", I, [P] * 6 + [I] * 4 + [F, I, P]),
+                ("attn_backward_workspace_size", Z, [L] + [I] * 4),
+                ("attn_backward", I, [P] * 9 + [I] * 5 + [F, I, P, Z, P]),
+                ("attn_backward_varlen", I, [P] * 10 + [I] * 4 + [F, I, P, Z, P])):
+            getattr(lib, name).restype, getattr(lib, name).argtypes = res, args
         _lib = lib
         return lib
 
