@@ -1,0 +1,491 @@
+// Gated delta rule over whole sequences on the tensor cores (bf16; Dk = 64 or 128).
+//
+// Chunks of C = 64 tokens; with cum the inclusive sum of g in the chunk and S its entry state
+//   A = strict_lower(beta_i e^{cum_i - cum_j} k_i.k_j),  T = (I + A)^-1,
+//   P = lower(e^{cum_i - cum_j} q_i.k_j)                                (prologue kernel)
+//   R = V - e^cum o (K S),  U = T (beta o R),  O = e^cum o (Q S) + P U,
+//   S' = e^{cum_C} S + K^T (e^{cum_C - cum} o U)                        (scan kernel)
+// Every exponent is a sum of gates, so no factor exceeds 1 and any decay is safe.
+//
+// The prologue has no chain: one CTA per chunk and key head, all of them at once.  The scan is
+// a chain over the chunks of a sequence, and its value columns are independent: a CTA owns
+// 16 or 32 of them.  It keeps S transposed in the accumulators of its warps (rows: value
+// columns), so K S, T Y and K^T U are three products whose left operands are the
+// transposes of S, Y and U.
+//
+// Precision.  The state and every sum are fp32.  MMA operands that are not inputs (S, Y, U, T)
+// are split over bf16 planes: three planes carry 24 bits and keep bf16's range (fp16 would need
+// fewer, but overflows at 65504), so the state that is handed on is as exact as fp32
+// arithmetic makes it.  What only reaches o, which is rounded to bf16, takes two planes (S and U in
+// Q S and P U) or one (P).
+
+#include "gdn_tc.cuh"
+
+namespace kda {
+namespace gdn {
+
+// ---- prologue: T, P and the gates of each chunk -----------------------------------------
+// KK^T and QK^T are bf16 MMAs (exact products, fp32 sums), shared by the value heads of a key
+// head.  The unit lower triangular I + A is inverted in fp32: the two 32x32 diagonal blocks by
+// forward substitution, a column to a lane; then T21 = -T22 (A21 T11).  A 64-column
+// substitution would leave half the warps idle and is twice as long.
+template <int DK>
+constexpr int pro_smem() { return 2 * C * DK * 2 + 2 * C * 68 * 4 + 5 * C * 4; }
+
+template <int DK, int PP>
+__global__ void __launch_bounds__(128) gdn_prologue_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, char* records)
+{
+    extern __shared__ __align__(128) char sm[];
+    __nv_bfloat16* sK = (__nv_bfloat16*)sm;
+    __nv_bfloat16* sQ = sK + C * DK;
+    float (*A)[68] = (float (*)[68])(sm + 2 * C * DK * 2);
+    float (*T)[68] = A + C;
+    float* ch = (float*)(T + C);   // cum log2(e), as a sum of two floats
+    float* cl = ch + C;
+    float* bet = cl + C;
+    int seq, c;
+    if (!seqs.locate(blockIdx.x, C, seq, c)) return;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, hk = blockIdx.y, r = a.Hv / a.Hk;
+    const int valid = min(C, seqs.len(seq) - c * C);
+    const int64_t t0 = (int64_t)seqs.start(seq) + c * C;
+    const uint32_t uK = smem_addr(sK), uQ = smem_addr(sQ);
+    load_tile<DK, 128>(uK, (const __nv_bfloat16*)a.k + (t0 * a.Hk + hk) * DK, (int64_t)a.Hk * DK, valid, tid);
+    load_tile<DK, 128>(uQ, (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK, (int64_t)a.Hk * DK, valid, tid);
+    cp_async_commit();
+    cp_async_wait_all();
+    __syncthreads();
+
+    // rows 16 w .. 16 w + 15 of KK^T and QK^T, columns up to the diagonal block
+    float kk[8][4] = {}, qk[8][4] = {};
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s) {
+        uint32_t ak[4], aq[4];
+        const int arow = w * 16 + (lane & 15), apiece = 2 * s + (lane >> 4);
+        ldsm(ak, uK + tile_at<DK>(arow, apiece));
+        ldsm(aq, uQ + tile_at<DK>(arow, apiece));
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+            if (jb > w) break;
+            uint32_t b[4];
+            ldsm(b, uK + tile_at<DK>(jb * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+            mma(kk[2 * jb], ak, b[0], b[1]);
+            mma(kk[2 * jb + 1], ak, b[2], b[3]);
+            mma(qk[2 * jb], aq, b[0], b[1]);
+            mma(qk[2 * jb + 1], aq, b[2], b[3]);
+        }
+    }
+    const int g4 = lane >> 2, t2 = (lane & 3) * 2;
+    for (int h = hk * r; h < hk * r + r; ++h) {
+        char* rec = records + ((int64_t)blockIdx.x * a.Hv + h) * rec_bytes(PP);
+        float* scal = (float*)(rec + rec_scal(PP));
+        if (w == 0) {   // inclusive sum of the gates in 64 bits, two tokens a lane
+            double s[2];
+            float b[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                const int64_t off = (t0 + t) * a.Hv + h;
+                // e^g is 0 in fp32 below -104: the clamp keeps sums finite for g = -inf
+                s[i] = t < valid ? (double)fmaxf(to_f32(((const __nv_bfloat16*)a.g)[off]), -1000.f) : 0.0;
+                b[i] = t < valid ? to_f32(((const __nv_bfloat16*)a.beta)[off]) : 0.f;
+            }
+            double sum = s[0] + s[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double x = __shfl_up_sync(~0u, sum, o);
+                if (lane >= o) sum += x;
+            }
+            const double c1 = sum * 1.4426950408889634, c0 = (sum - s[1]) * 1.4426950408889634;
+            const double last = __shfl_sync(~0u, c1, 31);
+            const double cum[2] = {c0, c1};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                ch[t] = (float)cum[i];
+                cl[t] = (float)(cum[i] - (double)(float)cum[i]);
+                bet[t] = b[i];
+                scal[t] = exp2f((float)cum[i]);
+                scal[C + t] = exp2f((float)(last - cum[i]));
+                scal[2 * C + t] = b[i];
+            }
+        }
+        __syncthreads();
+        // A to shared memory, P to the record
+        const int i0 = w * 16 + g4, i1 = i0 + 8;
+        const float h0 = ch[i0], h1 = ch[i1], l0 = cl[i0], l1 = cl[i1], b0 = bet[i0], b1 = bet[i1];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            if (n > 2 * w + 1) break;
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = n * 8 + t2 + e;
+                const float hj = ch[j], lj = cl[j];
+                const float d0 = j <= i0 ? exp2f((h0 - hj) + (l0 - lj)) : 0.f;
+                const float d1 = j <= i1 ? exp2f((h1 - hj) + (l1 - lj)) : 0.f;
+                A[i0][j] = j < i0 ? b0 * d0 * kk[n][e] : 0.f;
+                A[i1][j] = j < i1 ? b1 * d1 * kk[n][2 + e] : 0.f;
+                p[e] = d0 * qk[n][e];
+                p[2 + e] = d1 * qk[n][2 + e];
+            }
+            uint32_t lo[PP], hi[PP];
+            split<PP>(p[0], p[1], lo);
+            split<PP>(p[2], p[3], hi);
+            char* dst = rec + rec_p(PP) + blk(w, n >> 1) + (n & 1) * 128 + g4 * 16 + t2 * 2;
+#pragma unroll
+            for (int q = 0; q < PP; ++q) {
+                *(uint32_t*)(dst + q * TRI) = lo[q];
+                *(uint32_t*)(dst + q * TRI + 256) = hi[q];
+            }
+        }
+        __syncthreads();
+        if (w < 2) {   // inverse of diagonal block w, column `lane`
+            const int base = 32 * w;
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                float s0 = i == lane ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+                for (int m = 0; m < i; m += 4) {   // entries at and right of the diagonal are 0
+                    const float4 v = *(const float4*)&A[base + i][base + m];
+                    s0 = fmaf(-v.x, x[m], s0);
+                    if (m + 1 < i) s1 = fmaf(-v.y, x[m + 1], s1);
+                    if (m + 2 < i) s2 = fmaf(-v.z, x[m + 2], s2);
+                    if (m + 3 < i) s3 = fmaf(-v.w, x[m + 3], s3);
+                }
+                x[i] = (s0 + s1) + (s2 + s3);
+                T[base + i][base + lane] = x[i];
+            }
+        }
+        __syncthreads();
+        const int row = tid >> 2, col = (tid & 3) * 8;   // 8 entries of a 32x32 product
+        float z[8] = {};
+#pragma unroll 4
+        for (int m = 0; m < 32; ++m) {
+            const float x = A[32 + row][m];
+            const float4 u = *(const float4*)&T[m][col], v = *(const float4*)&T[m][col + 4];
+            z[0] = fmaf(x, u.x, z[0]); z[1] = fmaf(x, u.y, z[1]); z[2] = fmaf(x, u.z, z[2]); z[3] = fmaf(x, u.w, z[3]);
+            z[4] = fmaf(x, v.x, z[4]); z[5] = fmaf(x, v.y, z[5]); z[6] = fmaf(x, v.z, z[6]); z[7] = fmaf(x, v.w, z[7]);
+        }
+        // A21 T11 goes where A's upper left block was: no one reads that any more
+        *(float4*)&A[row][col] = make_float4(z[0], z[1], z[2], z[3]);
+        *(float4*)&A[row][col + 4] = make_float4(z[4], z[5], z[6], z[7]);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = 0.f;
+#pragma unroll 4
+        for (int m = 0; m < 32; ++m) {
+            const float x = T[32 + row][32 + m];
+            const float4 u = *(const float4*)&A[m][col], v = *(const float4*)&A[m][col + 4];
+            z[0] = fmaf(-x, u.x, z[0]); z[1] = fmaf(-x, u.y, z[1]); z[2] = fmaf(-x, u.z, z[2]); z[3] = fmaf(-x, u.w, z[3]);
+            z[4] = fmaf(-x, v.x, z[4]); z[5] = fmaf(-x, v.y, z[5]); z[6] = fmaf(-x, v.z, z[6]); z[7] = fmaf(-x, v.w, z[7]);
+        }
+        *(float4*)&T[32 + row][col] = make_float4(z[0], z[1], z[2], z[3]);
+        *(float4*)&T[32 + row][col + 4] = make_float4(z[4], z[5], z[6], z[7]);
+        __syncthreads();
+        // the ten blocks, 128 pairs each, as planes
+        const int ii = ((tid >> 6) << 3) + ((tid >> 2) & 7), jj = (((tid >> 5) & 1) << 3) + (tid & 3) * 2;
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib)
+#pragma unroll
+            for (int jb = 0; jb <= ib; ++jb) {
+                const float2 v = *(const float2*)&T[ib * 16 + ii][jb * 16 + jj];
+                uint32_t p[PLANES];
+                split<PLANES>(v.x, v.y, p);
+#pragma unroll
+                for (int q = 0; q < PLANES; ++q) *(uint32_t*)(rec + q * TRI + blk(ib, jb) + tid * 4) = p[q];
+            }
+        __syncthreads();
+    }
+}
+
+cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int PP, cudaStream_t st)
+{
+    const dim3 grid(s.slots(C), a.Hk);
+    ProfileScope prof("gdn_prologue", st);
+    count_launch();
+    auto go = [&](auto kern, int smem) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<grid, 128, smem, st>>>(a, s, (char*)records);
+        return cudaGetLastError();
+    };
+    if (a.Dk == 64) return PP == 1 ? go(gdn_prologue_kernel<64, 1>, pro_smem<64>()) : go(gdn_prologue_kernel<64, 2>, pro_smem<64>());
+    return PP == 1 ? go(gdn_prologue_kernel<128, 1>, pro_smem<128>()) : go(gdn_prologue_kernel<128, 2>, pro_smem<128>());
+}
+
+// ---- scan ---------------------------------------------------------------------------------
+// MT groups of four warps; group m owns value columns 16 m .. 16 m + 15 of the CTA, and its warp
+// of quarter f owns tokens 16 f .. of every product over tokens and key channels
+// DK / 4 f .. of the state.  Per chunk: (K S, Q S) -> R, Y | Y -> U | U -> S', O, with one
+// barrier of the group at each bar, where Y, U and S pass through shared memory as planes.
+// The chunk after next comes in by cp.async meanwhile (two stages).
+template <int DK, int MT>
+struct Scan {
+    static constexpr int THREADS = 128 * MT;
+    static constexpr int VROW = 32 * MT + 16;        // bytes of a staged row of V: odd multiple of 16
+    static constexpr int SROW = 2 * DK + 16;         // of a row of the S planes
+    static constexpr int TROW = 2 * C + 16;          // of a row of the Y and U planes
+    static constexpr int K_ = 0, Q_ = K_ + C * DK * 2, REC = Q_ + C * DK * 2;
+    static constexpr int V_ = REC + rec_bytes(1), STAGE = V_ + C * VROW;
+    static constexpr int SP = 2 * STAGE;                               // [plane][16 MT][SROW]
+    static constexpr int YP = SP + PLANES * 16 * MT * SROW;            // [plane][16 MT][TROW]
+    static constexpr int UP = YP + PLANES * 16 * MT * TROW;            // decayed U
+    static constexpr int WP = UP + PLANES * 16 * MT * TROW;            // U, two planes
+    static constexpr int OS = WP + 2 * 16 * MT * TROW;                 // 512 bytes a warp
+    static constexpr int SMEM = OS + 4 * MT * 512;
+};
+
+template <int DK, int MT>
+__global__ void __launch_bounds__(128 * MT) gdn_scan_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, const char* records)
+{
+    using L = Scan<DK, MT>;
+    constexpr int NS = DK / 32;   // 8-column tiles of the state a warp holds
+    extern __shared__ __align__(128) char sm[];
+    const uint32_t base = smem_addr(sm);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int m = warp >> 2;
+    // quarter 3 has the most work in the triangular products: the groups put it on
+    // different SM partitions (warp % 4)
+    const int f = (m & 1) ? 3 - (warp & 3) : (warp & 3);
+    const int h = blockIdx.y, seq = blockIdx.z, hk = h / (a.Hv / a.Hk);
+    const int v0 = blockIdx.x * 16 * MT, row0 = m * 16;
+    const int len = seqs.len(seq), nch = (len + C - 1) / C;
+    const int64_t t0 = seqs.start(seq);
+    const __nv_bfloat16* kp = (const __nv_bfloat16*)a.k + (t0 * a.Hk + hk) * DK;
+    const __nv_bfloat16* qp = (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK;
+    const __nv_bfloat16* vp = (const __nv_bfloat16*)a.v + (t0 * a.Hv + h) * a.Dv + v0;
+    __nv_bfloat16* op = (__nv_bfloat16*)a.o + (t0 * a.Hv + h) * a.Dv + v0;
+    const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * rec_bytes(1);
+    const int g4 = lane >> 2, t2 = (lane & 3) * 2;
+
+    auto load = [&](int c) {
+        const uint32_t st = base + (c & 1) * L::STAGE;
+        const int valid = min(C, len - c * C);
+        load_tile<DK, L::THREADS>(st + L::K_, kp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, tid);
+        load_tile<DK, L::THREADS>(st + L::Q_, qp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, tid);
+        for (int e = tid; e < C * 2 * MT; e += L::THREADS) {
+            const int row = e / (2 * MT), piece = e % (2 * MT);
+            const bool in = row < valid;
+            cp16(st + L::V_ + row * L::VROW + piece * 16, vp + ((int64_t)c * C + (in ? row : 0)) * a.Hv * a.Dv + piece * 8, in);
+        }
+        const char* src = rec + (int64_t)c * a.Hv * rec_bytes(1);
+        for (int e = tid; e < rec_bytes(1) / 16; e += L::THREADS) cp16(st + L::REC + e * 16, src + e * 16, true);
+        cp_async_commit();
+    };
+
+    // S^T: row = value column, column = key channel
+    float S[NS][4];
+    const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * a.Dv + v0 + row0 + g4;
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            S[n][e] = a.S0 ? a.S0[soff + (int64_t)(f * (DK / 4) + n * 8 + t2 + (e & 1)) * a.Dv + (e >> 1) * 8] : 0.f;
+    auto put_state = [&] {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t p[PLANES];
+                split<PLANES>(S[n][2 * e], S[n][2 * e + 1], p);
+                const uint32_t dst = base + L::SP + (row0 + g4 + 8 * e) * L::SROW + (f * (DK / 4) + n * 8 + t2) * 2;
+#pragma unroll
+                for (int q = 0; q < PLANES; ++q) st_shared_b32(dst + q * 16 * MT * L::SROW, p[q]);
+            }
+    };
+    // lane's address in a plane of [16 rows][columns] for a 16x16 A operand at column block kb
+    const uint32_t a_row = (row0 + (lane & 15)), a_piece = (lane >> 4) * 16;
+
+    if (nch > 0) {
+        load(0);
+        put_state();
+    }
+    for (int c = 0; c < nch; ++c) {
+        cp_async_wait_all();
+        __syncthreads();   // chunk c has landed, S is in place, and no one reads stage (c + 1) % 2
+        if (c + 1 < nch) load(c + 1);
+        const uint32_t st = base + (c & 1) * L::STAGE;
+        const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(1));
+
+        // K S and Q S of the warp's 16 tokens (two 8-token tiles), transposed
+        float ks[2][PLANES][4] = {}, qs[2][2][4] = {};
+#pragma unroll
+        for (int s = 0; s < DK / 16; ++s) {
+            uint32_t bk[4], bq[4], x[PLANES][4];
+            const uint32_t off = tile_at<DK>(f * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1));
+            ldsm(bk, st + L::K_ + off);
+            ldsm(bq, st + L::Q_ + off);
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p)
+                ldsm(x[p], base + L::SP + p * 16 * MT * L::SROW + a_row * L::SROW + s * 32 + a_piece);
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p) {
+                mma(ks[0][p], x[p], bk[0], bk[1]);
+                mma(ks[1][p], x[p], bk[2], bk[3]);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                mma(qs[0][p], x[p], bq[0], bq[1]);
+                mma(qs[1][p], x[p], bq[2], bq[3]);
+            }
+        }
+        // Y = beta o (V - e^cum o (K S))
+        {
+            uint32_t v[4];   // tiles (token half 0, 1) x (column half 0, 1)
+            ldsm_t(v, st + L::V_ + (f * 16 + (lane & 15)) * L::VROW + (row0 + (lane >> 4) * 8) * 2);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int t = f * 16 + n * 8 + t2;
+                const float2 gr = *(const float2*)&scal[t], be = *(const float2*)&scal[2 * C + t];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t vv = v[n + 2 * e];
+                    const float y0 = be.x * (low(vv) - gr.x * (ks[n][0][2 * e] + (ks[n][1][2 * e] + ks[n][2][2 * e])));
+                    const float y1 = be.y * (high(vv) - gr.y * (ks[n][0][2 * e + 1] + (ks[n][1][2 * e + 1] + ks[n][2][2 * e + 1])));
+                    uint32_t p[PLANES];
+                    split<PLANES>(y0, y1, p);
+                    const uint32_t dst = base + L::YP + (row0 + g4 + 8 * e) * L::TROW + t * 2;
+#pragma unroll
+                    for (int q = 0; q < PLANES; ++q) st_shared_b32(dst + q * 16 * MT * L::TROW, p[q]);
+                }
+            }
+        }
+        bar_sync(1 + m, 128);
+        // U = T Y for the warp's tokens: the six products of planes above 2^-27 of the result
+        float u[2][PLANES][4] = {};
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+            if (jb > f) break;
+            uint32_t y[PLANES][4], t[PLANES][4];
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p) {
+                ldsm(y[p], base + L::YP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
+                ldsm(t[p], st + L::REC + p * TRI + blk(f, jb) + lane * 16);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+                    for (int q = 0; q < PLANES - p; ++q) mma(u[n][p], y[q], t[p][2 * n], t[p][2 * n + 1]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int t = f * 16 + n * 8 + t2;
+            const float2 en = *(const float2*)&scal[C + t];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float u0 = u[n][0][2 * e] + (u[n][1][2 * e] + u[n][2][2 * e]);
+                const float u1 = u[n][0][2 * e + 1] + (u[n][1][2 * e + 1] + u[n][2][2 * e + 1]);
+                uint32_t p[PLANES], q2[2];
+                split<PLANES>(en.x * u0, en.y * u1, p);
+                split<2>(u0, u1, q2);
+                const uint32_t off = (row0 + g4 + 8 * e) * L::TROW + t * 2;
+#pragma unroll
+                for (int q = 0; q < PLANES; ++q) st_shared_b32(base + L::UP + q * 16 * MT * L::TROW + off, p[q]);
+                st_shared_b32(base + L::WP + off, q2[0]);
+                st_shared_b32(base + L::WP + 16 * MT * L::TROW + off, q2[1]);
+            }
+        }
+        bar_sync(1 + m, 128);
+        // S' = e^{cum_C} S + K^T (decayed U), the warp's key channels
+        const float gam = scal[C - 1];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[n][e] *= gam;
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+            uint32_t x[PLANES][4];
+#pragma unroll
+            for (int p = 0; p < PLANES; ++p)
+                ldsm(x[p], base + L::UP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
+#pragma unroll
+            for (int n = 0; n < NS; n += 2) {
+                uint32_t b[4];
+                ldsm_t(b, st + L::K_ + tile_at<DK>(jb * 16 + (lane & 15), f * (DK / 32) + n + (lane >> 4)));
+#pragma unroll
+                for (int p = PLANES - 1; p >= 0; --p) {
+                    mma(S[n], x[p], b[0], b[1]);
+                    mma(S[n + 1], x[p], b[2], b[3]);
+                }
+            }
+        }
+        put_state();   // every warp of the group is past its reads of the old planes
+        // O = e^cum o (Q S) + P U, the warp's tokens
+        float o[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float2 gr = *(const float2*)&scal[f * 16 + n * 8 + t2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] = ((e & 1) ? gr.y : gr.x) * (qs[n][0][e] + qs[n][1][e]);
+        }
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+            if (jb > f) break;
+            uint32_t x[2][4], b[4];
+            ldsm(b, st + L::REC + rec_p(1) + blk(f, jb) + lane * 16);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                ldsm(x[p], base + L::WP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
+                mma(o[0], x[p], b[0], b[1]);
+                mma(o[1], x[p], b[2], b[3]);
+            }
+        }
+        // 16 tokens x 16 columns, turned over in the warp's own 512 bytes
+        const uint32_t os = base + L::OS + warp * 512;
+        const uint32_t w4[4] = {pack(o[0][0], o[0][1]), pack(o[0][2], o[0][3]), pack(o[1][0], o[1][1]), pack(o[1][2], o[1][3])};
+        stsm_t(os + ((lane >> 4) * 8 + (lane & 7)) * 32 + ((lane >> 3) & 1) * 16, w4);
+        __syncwarp();
+        const int tok = c * C + f * 16 + (lane >> 1);
+        const uint4 out = *(const uint4*)(sm + L::OS + warp * 512 + lane * 16);
+        if (tok < len) *(uint4*)(op + (int64_t)tok * a.Hv * a.Dv + row0 + (lane & 1) * 8) = out;
+        __syncwarp();
+    }
+    if (a.ST)
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                a.ST[soff + (int64_t)(f * (DK / 4) + n * 8 + t2 + (e & 1)) * a.Dv + (e >> 1) * 8] = S[n][e];
+}
+
+namespace {
+template <int DK, int MT>
+cudaError_t scan(const GdnArgs& a, const Seqs& s, const void* records, cudaStream_t st)
+{
+    auto kern = gdn_scan_kernel<DK, MT>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Scan<DK, MT>::SMEM);
+    if (e != cudaSuccess) return e;
+    ProfileScope prof("gdn_scan", st);
+    count_launch();
+    kern<<<dim3(a.Dv / (16 * MT), a.Hv, s.n), Scan<DK, MT>::THREADS, Scan<DK, MT>::SMEM, st>>>(a, s, (const char*)records);
+    return cudaGetLastError();
+}
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+}  // namespace
+}  // namespace gdn
+
+// The tensor-core path copies rows in 16-byte pieces.
+bool gdn_tc_supported(const GdnArgs& a)
+{
+    return a.t == ET_BF16 && (a.Dk == 64 || a.Dk == 128) && gdn::aligned16(a.q) && gdn::aligned16(a.k) &&
+           gdn::aligned16(a.v) && gdn::aligned16(a.o);
+}
+
+size_t gdn_tc_workspace(const Seqs& s, int Hv) { return (size_t)s.slots(gdn::C) * Hv * gdn::rec_bytes(1); }
+
+cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, cudaStream_t st)
+{
+    cudaError_t e = cudaSuccess;
+    if (s.tokens() > 0) e = gdn::launch_prologue(a, s, ws, 1, st);
+    if (e != cudaSuccess) return e;
+    // 32 columns a CTA re-read K, Q and the factors half as often; 16 put twice as many SMs to
+    // work where the heads alone do not fill them.
+    const bool wide = (int64_t)s.n * a.Hv * (a.Dv / 32) >= sms;
+    if (a.Dk == 64) return wide ? gdn::scan<64, 2>(a, s, ws, st) : gdn::scan<64, 1>(a, s, ws, st);
+    return wide ? gdn::scan<128, 2>(a, s, ws, st) : gdn::scan<128, 1>(a, s, ws, st);
+}
+
+}  // namespace kda

@@ -1,0 +1,99 @@
+// Pieces shared by the tensor-core kernels of the gated delta rule: bf16 warp MMAs, values
+// split over bf16 planes, swizzled tiles, and the record of a chunk's factors.
+#pragma once
+
+#include "mixers.h"
+#include "sm100.cuh"
+
+namespace kda {
+namespace gdn {
+
+using namespace sm100;
+
+constexpr int C = 64;          // tokens per chunk
+constexpr int PLANES = 3;      // bf16 planes that hold an fp32 value (8 + 8 + 8 bits)
+
+// D(16x8, fp32) += A(16x16, bf16, rows) * B(16x8, bf16, columns)
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi)   // bf16 pair, round to nearest even
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float low(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float high(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+// A pair of fp32 values as N bf16 planes: x = p0 + p1 + ..., each plane the rounded rest of
+// the ones before, so N planes leave 2^-(9N) of x (N = 3: less than fp32's own half step).
+template <int N>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&p)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        p[i] = pack(a, b);
+        a -= low(p[i]);
+        b -= high(p[i]);
+    }
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) { ldsm_x4(r, addr); }
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) { ldsm_x4_t(r, addr); }
+// transposing store of four 8x8 blocks: lane l gives the address of one 16-byte row
+__device__ __forceinline__ void stsm_t(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// 16 bytes global -> shared, or 16 zero bytes
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Tiles of 64 tokens x W values (bf16, W = 64 or 128): rows of 2 W bytes, the 16-byte pieces
+// of a row permuted by the row's low bits, so 8 rows of one piece lie in 8 different
+// bank groups for ldmatrix.
+template <int W>
+__device__ __forceinline__ uint32_t tile_at(int row, int piece)
+{
+    return row * (2 * W) + ((piece ^ (row & 7)) << 4);
+}
+template <int W, int THREADS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src, int64_t row_stride, int valid, int tid)
+{
+    constexpr int P = W / 8;
+#pragma unroll
+    for (int i = 0; i < C * P / THREADS; ++i) {
+        const int e = i * THREADS + tid, row = e / P, piece = e % P;
+        const bool in = row < valid;
+        cp16(dst + tile_at<W>(row, piece), src + (in ? row : 0) * row_stride + piece * 8, in);
+    }
+}
+
+// A chunk's factors for one value head, written by the prologue kernel and read by the scans:
+// T = (I + A)^-1 in PLANES planes and P = lower(e^{cum_i - cum_j} q_i.k_j) in PP planes, each
+// the ten 16x16 blocks on and below the diagonal, a block as four 8x8 core matrices of 128
+// contiguous bytes; then e^cum, e^{cum_C - cum} and beta.
+constexpr int BLK = 512;
+constexpr int TRI = 10 * BLK;
+__host__ __device__ constexpr int rec_p(int) { return PLANES * TRI; }
+__host__ __device__ constexpr int rec_scal(int PP) { return (PLANES + PP) * TRI; }
+__host__ __device__ constexpr int rec_bytes(int PP) { return rec_scal(PP) + 3 * C * 4; }
+__device__ __forceinline__ int blk(int ib, int jb) { return (ib * (ib + 1) / 2 + jb) * BLK; }
+
+// launch of the prologue kernel: one record per (slot, value head)
+cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int PP, cudaStream_t st);
+
+}  // namespace gdn
+}  // namespace kda

@@ -13,6 +13,12 @@ kda_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR
 bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 ElemType et_of(kda_dtype d) { return d == KDA_F32 ? ET_F32 : ET_BF16; }
 size_t elem(ElemType t) { return t == ET_F32 ? 4 : 2; }
+int num_sms()
+{
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
 size_t max_of(size_t a, size_t b) { return a > b ? a : b; }
 
 // The sequences of a call: B rows of T tokens (cu null), or n samples with host offsets.
@@ -93,6 +99,13 @@ kda_status check_gdn(int Hk, int Hv, int Dk, int Dv, kda_dtype dtype)
     return KDA_OK;
 }
 
+GdnArgs gdn_sizes(int Hk, int Hv, int Dk, int Dv, kda_dtype dtype)
+{
+    GdnArgs a{};
+    a.Hk = Hk; a.Hv = Hv; a.Dk = Dk; a.Dv = Dv; a.t = et_of(dtype);
+    return a;
+}
+
 GdnArgs moved(GdnArgs a, int seq, int64_t token)
 {
     a.q = at(a.q, token * a.Hk * a.Dk, a.t);
@@ -106,10 +119,33 @@ GdnArgs moved(GdnArgs a, int seq, int64_t token)
     return a;
 }
 
-kda_status run_gdn_forward(const GdnArgs& a, const Batch& b, kda_stream_t stream)
+// Workspace of the tensor-core path; asked for whenever the sizes allow that path, so the
+// answer does not depend on the tensors' alignment.
+size_t gdn_fwd_need(const GdnArgs& a, const Batch& b)
 {
+    GdnArgs x = a;
+    x.q = x.k = x.v = x.o = nullptr;
+    if (!gdn_tc_supported(x)) return 0;
+    size_t need = 0;
+    each_group(b, [&](const Seqs& s, int, int64_t) {
+        if (s.tokens() > 0) need = max_of(need, gdn_tc_workspace(s, a.Hv));
+        return KDA_OK;
+    });
+    return need;
+}
+
+kda_status run_gdn_forward(const GdnArgs& a, const Batch& b, void* workspace, size_t workspace_bytes,
+                           kda_stream_t stream)
+{
+    Scratch ws;
+    const kda_status st = ws.acquire(workspace, workspace_bytes, gdn_fwd_need(a, b), (cudaStream_t)stream);
+    if (st != KDA_OK) return st;
+    const bool tc = gdn_tc_supported(a);
+    const int sms = num_sms();
     return each_group(b, [&](const Seqs& s, int seq, int64_t token) {
-        return from_cuda(launch_gdn_recurrent(moved(a, seq, token), s, (cudaStream_t)stream));
+        const GdnArgs x = moved(a, seq, token);
+        return from_cuda(tc ? launch_gdn_tc(x, s, ws.ptr, sms, (cudaStream_t)stream)
+                            : launch_gdn_recurrent(x, s, (cudaStream_t)stream));
     });
 }
 
@@ -152,9 +188,7 @@ kda_status gdn_forward_any(GdnArgs a, const Batch& b, bool packed, kda_dtype dty
     if (st != KDA_OK) return st;
     if (b.tokens() > 0 && (!a.q || !a.k || !a.v || !a.g || !a.beta || !a.o)) return KDA_ERR_INVALID_ARG;
     a.t = et_of(dtype);
-    (void)workspace;
-    (void)workspace_bytes;
-    return run_gdn_forward(a, b, stream);
+    return run_gdn_forward(a, b, workspace, workspace_bytes, stream);
 }
 
 kda_status gdn_backward_any(GdnBwdArgs a, const Batch& b, bool packed, kda_dtype dtype, void* workspace,
@@ -233,13 +267,17 @@ extern "C" {
 
 size_t gdn_forward_workspace_size(int B, int T, int Hk, int Hv, int Dk, int Dv, kda_dtype dtype)
 {
-    return 0;
+    const Batch b{nullptr, B, T};
+    if (check_batch(b, false) != KDA_OK || check_gdn(Hk, Hv, Dk, Dv, dtype) != KDA_OK) return 0;
+    return gdn_fwd_need(gdn_sizes(Hk, Hv, Dk, Dv, dtype), b);
 }
 
 size_t gdn_forward_varlen_workspace_size(const int32_t* cu_seqlens, int n_seqs, int Hk, int Hv, int Dk, int Dv,
                                          kda_dtype dtype)
 {
-    return 0;
+    const Batch b{cu_seqlens, n_seqs, 0};
+    if (check_batch(b, true) != KDA_OK || check_gdn(Hk, Hv, Dk, Dv, dtype) != KDA_OK) return 0;
+    return gdn_fwd_need(gdn_sizes(Hk, Hv, Dk, Dv, dtype), b);
 }
 
 kda_status gdn_forward(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* S0,
@@ -263,9 +301,7 @@ size_t gdn_backward_workspace_size(int B, int T, int Hk, int Hv, int Dk, int Dv,
 {
     const Batch b{nullptr, B, T};
     if (check_batch(b, false) != KDA_OK || check_gdn(Hk, Hv, Dk, Dv, dtype) != KDA_OK) return 0;
-    GdnArgs a{};
-    a.Hk = Hk; a.Hv = Hv; a.Dk = Dk; a.Dv = Dv; a.t = et_of(dtype);
-    return gdn_bwd_need(a, b);
+    return gdn_bwd_need(gdn_sizes(Hk, Hv, Dk, Dv, dtype), b);
 }
 
 size_t gdn_backward_varlen_workspace_size(const int32_t* cu_seqlens, int n_seqs, int Hk, int Hv, int Dk, int Dv,
@@ -273,9 +309,7 @@ size_t gdn_backward_varlen_workspace_size(const int32_t* cu_seqlens, int n_seqs,
 {
     const Batch b{cu_seqlens, n_seqs, 0};
     if (check_batch(b, true) != KDA_OK || check_gdn(Hk, Hv, Dk, Dv, dtype) != KDA_OK) return 0;
-    GdnArgs a{};
-    a.Hk = Hk; a.Hv = Hv; a.Dk = Dk; a.Dv = Dv; a.t = et_of(dtype);
-    return gdn_bwd_need(a, b);
+    return gdn_bwd_need(gdn_sizes(Hk, Hv, Dk, Dv, dtype), b);
 }
 
 kda_status gdn_backward(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* S0,
