@@ -215,14 +215,17 @@ cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int 
 }
 
 // ---- scan ---------------------------------------------------------------------------------
-// MT groups of four warps; group m owns value columns 16 m .. 16 m + 15 of the CTA, and its warp
-// of quarter f owns tokens 16 f .. of every product over tokens and key channels
-// DK / 4 f .. of the state.  Per chunk: (K S, Q S) -> R, Y | Y -> U | U -> S', O, with one
-// barrier of the group at each bar, where Y, U and S pass through shared memory as planes.
-// The chunk after next comes in by cp.async meanwhile (two stages).
+// MT groups of eight warps; group m owns value columns 16 m .. 16 m + 15 of the CTA.  Four
+// warps run the chain, four the output.  The warp of quarter f owns tokens 16 f .. of every
+// product over tokens, and a chain warp key channels DK / 4 f .. of the state.  Per chunk:
+//   chain:  K S -> Y | U = T Y | S' = e^{cum_C} S + K^T U'
+//   output: next chunk's loads (cp.async, two stages), Q S | O = e^cum o (Q S) + P U
+// with a barrier at each bar, where Y, U and S pass through shared memory as planes.  The
+// chain is bound by latency (one warp a scheduler issues every fourth cycle), which the
+// output warps fill.
 template <int DK, int MT>
 struct Scan {
-    static constexpr int THREADS = 128 * MT;
+    static constexpr int THREADS = 256 * MT;
     static constexpr int VROW = 32 * MT + 16;        // bytes of a staged row of V: odd multiple of 16
     static constexpr int SROW = 2 * DK + 16;         // of a row of the S planes
     static constexpr int TROW = 2 * C + 16;          // of a row of the Y and U planes
@@ -232,223 +235,233 @@ struct Scan {
     static constexpr int YP = SP + PLANES * 16 * MT * SROW;            // [plane][16 MT][TROW]
     static constexpr int UP = YP + PLANES * 16 * MT * TROW;            // decayed U
     static constexpr int WP = UP + PLANES * 16 * MT * TROW;            // U, two planes
-    static constexpr int OS = WP + 2 * 16 * MT * TROW;                 // 512 bytes a warp
+    static constexpr int OS = WP + 2 * 16 * MT * TROW;                 // 512 bytes an output warp
     static constexpr int SMEM = OS + 4 * MT * 512;
 };
 
 template <int DK, int MT>
-__global__ void __launch_bounds__(128 * MT) gdn_scan_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, const char* records)
+__global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, const char* records)
 {
     using L = Scan<DK, MT>;
     constexpr int NS = DK / 32;   // 8-column tiles of the state a warp holds
+    constexpr int LOADERS = 128 * MT;
     extern __shared__ __align__(128) char sm[];
     const uint32_t base = smem_addr(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int m = warp >> 2;
-    // quarter 3 has the most work in the triangular products: the groups put it on
+    const bool chain = warp < 4 * MT;
+    const int m = (warp >> 2) % MT;
+    // quarter 3 has the most work in the triangular products: groups and roles put it on
     // different SM partitions (warp % 4)
-    const int f = (m & 1) ? 3 - (warp & 3) : (warp & 3);
+    const int f = ((warp >> 2) & 1) ? 3 - (warp & 3) : (warp & 3);
     const int h = blockIdx.y, seq = blockIdx.z, hk = h / (a.Hv / a.Hk);
     const int v0 = blockIdx.x * 16 * MT, row0 = m * 16;
     const int len = seqs.len(seq), nch = (len + C - 1) / C;
     const int64_t t0 = seqs.start(seq);
-    const __nv_bfloat16* kp = (const __nv_bfloat16*)a.k + (t0 * a.Hk + hk) * DK;
-    const __nv_bfloat16* qp = (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK;
-    const __nv_bfloat16* vp = (const __nv_bfloat16*)a.v + (t0 * a.Hv + h) * a.Dv + v0;
-    __nv_bfloat16* op = (__nv_bfloat16*)a.o + (t0 * a.Hv + h) * a.Dv + v0;
-    const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * rec_bytes(1);
     const int g4 = lane >> 2, t2 = (lane & 3) * 2;
+    // lane's address in a plane of [16 rows][columns] for a 16x16 A operand
+    const uint32_t a_row = row0 + (lane & 15), a_piece = (lane >> 4) * 16;
+    // lane's row and piece of 16 tokens x 16 channels as a B operand
+    const int b_row = f * 16 + (lane & 7) + ((lane >> 4) << 3), b_piece = (lane >> 3) & 1;
 
-    auto load = [&](int c) {
-        const uint32_t st = base + (c & 1) * L::STAGE;
-        const int valid = min(C, len - c * C);
-        load_tile<DK, L::THREADS>(st + L::K_, kp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, tid);
-        load_tile<DK, L::THREADS>(st + L::Q_, qp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, tid);
-        for (int e = tid; e < C * 2 * MT; e += L::THREADS) {
-            const int row = e / (2 * MT), piece = e % (2 * MT);
-            const bool in = row < valid;
-            cp16(st + L::V_ + row * L::VROW + piece * 16, vp + ((int64_t)c * C + (in ? row : 0)) * a.Hv * a.Dv + piece * 8, in);
-        }
-        const char* src = rec + (int64_t)c * a.Hv * rec_bytes(1);
-        for (int e = tid; e < rec_bytes(1) / 16; e += L::THREADS) cp16(st + L::REC + e * 16, src + e * 16, true);
-        cp_async_commit();
-    };
-
-    // S^T: row = value column, column = key channel
-    float S[NS][4];
-    const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * a.Dv + v0 + row0 + g4;
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            S[n][e] = a.S0 ? a.S0[soff + (int64_t)(f * (DK / 4) + n * 8 + t2 + (e & 1)) * a.Dv + (e >> 1) * 8] : 0.f;
-    auto put_state = [&] {
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t p[PLANES];
-                split<PLANES>(S[n][2 * e], S[n][2 * e + 1], p);
-                const uint32_t dst = base + L::SP + (row0 + g4 + 8 * e) * L::SROW + (f * (DK / 4) + n * 8 + t2) * 2;
-#pragma unroll
-                for (int q = 0; q < PLANES; ++q) st_shared_b32(dst + q * 16 * MT * L::SROW, p[q]);
-            }
-    };
-    // lane's address in a plane of [16 rows][columns] for a 16x16 A operand at column block kb
-    const uint32_t a_row = (row0 + (lane & 15)), a_piece = (lane >> 4) * 16;
-
-    if (nch > 0) {
-        load(0);
-        put_state();
-    }
-    for (int c = 0; c < nch; ++c) {
-        cp_async_wait_all();
-        __syncthreads();   // chunk c has landed, S is in place, and no one reads stage (c + 1) % 2
-        if (c + 1 < nch) load(c + 1);
-        const uint32_t st = base + (c & 1) * L::STAGE;
-        const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(1));
-
-        // K S and Q S of the warp's 16 tokens (two 8-token tiles), transposed
-        float ks[2][PLANES][4] = {}, qs[2][2][4] = {};
-#pragma unroll
-        for (int s = 0; s < DK / 16; ++s) {
-            uint32_t bk[4], bq[4], x[PLANES][4];
-            const uint32_t off = tile_at<DK>(f * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1));
-            ldsm(bk, st + L::K_ + off);
-            ldsm(bq, st + L::Q_ + off);
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p)
-                ldsm(x[p], base + L::SP + p * 16 * MT * L::SROW + a_row * L::SROW + s * 32 + a_piece);
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p) {
-                mma(ks[0][p], x[p], bk[0], bk[1]);
-                mma(ks[1][p], x[p], bk[2], bk[3]);
-            }
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                mma(qs[0][p], x[p], bq[0], bq[1]);
-                mma(qs[1][p], x[p], bq[2], bq[3]);
-            }
-        }
-        // Y = beta o (V - e^cum o (K S))
-        {
-            uint32_t v[4];   // tiles (token half 0, 1) x (column half 0, 1)
-            ldsm_t(v, st + L::V_ + (f * 16 + (lane & 15)) * L::VROW + (row0 + (lane >> 4) * 8) * 2);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int t = f * 16 + n * 8 + t2;
-                const float2 gr = *(const float2*)&scal[t], be = *(const float2*)&scal[2 * C + t];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t vv = v[n + 2 * e];
-                    const float y0 = be.x * (low(vv) - gr.x * (ks[n][0][2 * e] + (ks[n][1][2 * e] + ks[n][2][2 * e])));
-                    const float y1 = be.y * (high(vv) - gr.y * (ks[n][0][2 * e + 1] + (ks[n][1][2 * e + 1] + ks[n][2][2 * e + 1])));
-                    uint32_t p[PLANES];
-                    split<PLANES>(y0, y1, p);
-                    const uint32_t dst = base + L::YP + (row0 + g4 + 8 * e) * L::TROW + t * 2;
-#pragma unroll
-                    for (int q = 0; q < PLANES; ++q) st_shared_b32(dst + q * 16 * MT * L::TROW, p[q]);
-                }
-            }
-        }
-        bar_sync(1 + m, 128);
-        // U = T Y for the warp's tokens: the six products of planes above 2^-27 of the result
-        float u[2][PLANES][4] = {};
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-            if (jb > f) break;
-            uint32_t y[PLANES][4], t[PLANES][4];
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p) {
-                ldsm(y[p], base + L::YP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
-                ldsm(t[p], st + L::REC + p * TRI + blk(f, jb) + lane * 16);
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int p = 0; p < PLANES; ++p)
-#pragma unroll
-                    for (int q = 0; q < PLANES - p; ++q) mma(u[n][p], y[q], t[p][2 * n], t[p][2 * n + 1]);
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int t = f * 16 + n * 8 + t2;
-            const float2 en = *(const float2*)&scal[C + t];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float u0 = u[n][0][2 * e] + (u[n][1][2 * e] + u[n][2][2 * e]);
-                const float u1 = u[n][0][2 * e + 1] + (u[n][1][2 * e + 1] + u[n][2][2 * e + 1]);
-                uint32_t p[PLANES], q2[2];
-                split<PLANES>(en.x * u0, en.y * u1, p);
-                split<2>(u0, u1, q2);
-                const uint32_t off = (row0 + g4 + 8 * e) * L::TROW + t * 2;
-#pragma unroll
-                for (int q = 0; q < PLANES; ++q) st_shared_b32(base + L::UP + q * 16 * MT * L::TROW + off, p[q]);
-                st_shared_b32(base + L::WP + off, q2[0]);
-                st_shared_b32(base + L::WP + 16 * MT * L::TROW + off, q2[1]);
-            }
-        }
-        bar_sync(1 + m, 128);
-        // S' = e^{cum_C} S + K^T (decayed U), the warp's key channels
-        const float gam = scal[C - 1];
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[n][e] *= gam;
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-            uint32_t x[PLANES][4];
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p)
-                ldsm(x[p], base + L::UP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
-#pragma unroll
-            for (int n = 0; n < NS; n += 2) {
-                uint32_t b[4];
-                ldsm_t(b, st + L::K_ + tile_at<DK>(jb * 16 + (lane & 15), f * (DK / 32) + n + (lane >> 4)));
-#pragma unroll
-                for (int p = PLANES - 1; p >= 0; --p) {
-                    mma(S[n], x[p], b[0], b[1]);
-                    mma(S[n + 1], x[p], b[2], b[3]);
-                }
-            }
-        }
-        put_state();   // every warp of the group is past its reads of the old planes
-        // O = e^cum o (Q S) + P U, the warp's tokens
-        float o[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const float2 gr = *(const float2*)&scal[f * 16 + n * 8 + t2];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] = ((e & 1) ? gr.y : gr.x) * (qs[n][0][e] + qs[n][1][e]);
-        }
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-            if (jb > f) break;
-            uint32_t x[2][4], b[4];
-            ldsm(b, st + L::REC + rec_p(1) + blk(f, jb) + lane * 16);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                ldsm(x[p], base + L::WP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
-                mma(o[0], x[p], b[0], b[1]);
-                mma(o[1], x[p], b[2], b[3]);
-            }
-        }
-        // 16 tokens x 16 columns, turned over in the warp's own 512 bytes
-        const uint32_t os = base + L::OS + warp * 512;
-        const uint32_t w4[4] = {pack(o[0][0], o[0][1]), pack(o[0][2], o[0][3]), pack(o[1][0], o[1][1]), pack(o[1][2], o[1][3])};
-        stsm_t(os + ((lane >> 4) * 8 + (lane & 7)) * 32 + ((lane >> 3) & 1) * 16, w4);
-        __syncwarp();
-        const int tok = c * C + f * 16 + (lane >> 1);
-        const uint4 out = *(const uint4*)(sm + L::OS + warp * 512 + lane * 16);
-        if (tok < len) *(uint4*)(op + (int64_t)tok * a.Hv * a.Dv + row0 + (lane & 1) * 8) = out;
-        __syncwarp();
-    }
-    if (a.ST)
+    if (chain) {
+        // S^T: row = value column, column = key channel
+        float S[NS][4];
+        const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * a.Dv + v0 + row0 + g4;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                a.ST[soff + (int64_t)(f * (DK / 4) + n * 8 + t2 + (e & 1)) * a.Dv + (e >> 1) * 8] = S[n][e];
+                S[n][e] = a.S0 ? a.S0[soff + (int64_t)(f * (DK / 4) + n * 8 + t2 + (e & 1)) * a.Dv + (e >> 1) * 8] : 0.f;
+        auto put_state = [&] {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t p[PLANES];
+                    split<PLANES>(S[n][2 * e], S[n][2 * e + 1], p);
+                    const uint32_t dst = base + L::SP + (row0 + g4 + 8 * e) * L::SROW + (f * (DK / 4) + n * 8 + t2) * 2;
+#pragma unroll
+                    for (int q = 0; q < PLANES; ++q) st_shared_b32(dst + q * 16 * MT * L::SROW, p[q]);
+                }
+        };
+        put_state();
+        for (int c = 0; c < nch; ++c) {
+            __syncthreads();   // chunk c has landed and S is in place
+            const uint32_t st = base + (c & 1) * L::STAGE;
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(1));
+            // K S of the warp's 16 tokens (two 8-token tiles), transposed
+            float ks[2][PLANES][4] = {};
+#pragma unroll
+            for (int s = 0; s < DK / 16; ++s) {
+                uint32_t bk[4], x[PLANES][4];
+                ldsm(bk, st + L::K_ + tile_at<DK>(b_row, 2 * s + b_piece));
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p)
+                    ldsm(x[p], base + L::SP + p * 16 * MT * L::SROW + a_row * L::SROW + s * 32 + a_piece);
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p) {
+                    mma(ks[0][p], x[p], bk[0], bk[1]);
+                    mma(ks[1][p], x[p], bk[2], bk[3]);
+                }
+            }
+            // Y = beta o (V - e^cum o (K S))
+            {
+                uint32_t v[4];   // tiles (token half 0, 1) x (column half 0, 1)
+                ldsm_t(v, st + L::V_ + (f * 16 + (lane & 15)) * L::VROW + (row0 + (lane >> 4) * 8) * 2);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int t = f * 16 + n * 8 + t2;
+                    const float2 gr = *(const float2*)&scal[t], be = *(const float2*)&scal[2 * C + t];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t vv = v[n + 2 * e];
+                        const float y0 = be.x * (low(vv) - gr.x * (ks[n][0][2 * e] + (ks[n][1][2 * e] + ks[n][2][2 * e])));
+                        const float y1 = be.y * (high(vv) - gr.y * (ks[n][0][2 * e + 1] + (ks[n][1][2 * e + 1] + ks[n][2][2 * e + 1])));
+                        uint32_t p[PLANES];
+                        split<PLANES>(y0, y1, p);
+                        const uint32_t dst = base + L::YP + (row0 + g4 + 8 * e) * L::TROW + t * 2;
+#pragma unroll
+                        for (int q = 0; q < PLANES; ++q) st_shared_b32(dst + q * 16 * MT * L::TROW, p[q]);
+                    }
+                }
+            }
+            bar_sync(1 + m, 128);
+            // U = T Y for the warp's tokens: the six products of planes above 2^-27 of the result
+            float u[2][PLANES][4] = {};
+#pragma unroll
+            for (int jb = 0; jb < 4; ++jb) {
+                if (jb > f) break;
+                uint32_t y[PLANES][4], t[PLANES][4];
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p) {
+                    ldsm(y[p], base + L::YP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
+                    ldsm(t[p], st + L::REC + p * TRI + blk(f, jb) + lane * 16);
+                }
+#pragma unroll
+                for (int q = 0; q < PLANES; ++q)
+#pragma unroll
+                    for (int p = 0; p < PLANES - q; ++p)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma(u[n][p], y[q], t[p][2 * n], t[p][2 * n + 1]);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int t = f * 16 + n * 8 + t2;
+                const float2 en = *(const float2*)&scal[C + t];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float u0 = u[n][0][2 * e] + (u[n][1][2 * e] + u[n][2][2 * e]);
+                    const float u1 = u[n][0][2 * e + 1] + (u[n][1][2 * e + 1] + u[n][2][2 * e + 1]);
+                    uint32_t p[PLANES], q2[2];
+                    split<PLANES>(en.x * u0, en.y * u1, p);
+                    split<2>(u0, u1, q2);
+                    const uint32_t off = (row0 + g4 + 8 * e) * L::TROW + t * 2;
+#pragma unroll
+                    for (int q = 0; q < PLANES; ++q) st_shared_b32(base + L::UP + q * 16 * MT * L::TROW + off, p[q]);
+                    st_shared_b32(base + L::WP + off, q2[0]);
+                    st_shared_b32(base + L::WP + 16 * MT * L::TROW + off, q2[1]);
+                }
+            }
+            bar_sync(1 + MT + m, 256);   // U is in place; no warp of the group reads the planes of S any more
+            // S' = e^{cum_C} S + K^T (decayed U), the warp's key channels
+            const float gam = scal[C - 1];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[n][e] *= gam;
+#pragma unroll
+            for (int jb = 0; jb < 4; ++jb) {
+                uint32_t x[PLANES][4], b[NS / 2][4];
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p)
+                    ldsm(x[p], base + L::UP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
+#pragma unroll
+                for (int n = 0; n < NS; n += 2)
+                    ldsm_t(b[n / 2], st + L::K_ + tile_at<DK>(jb * 16 + (lane & 15), f * (DK / 32) + n + (lane >> 4)));
+#pragma unroll
+                for (int p = PLANES - 1; p >= 0; --p)
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) mma(S[n], x[p], b[n / 2][(n & 1) * 2], b[n / 2][(n & 1) * 2 + 1]);
+            }
+            put_state();
+        }
+        if (a.ST)
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    a.ST[soff + (int64_t)(f * (DK / 4) + n * 8 + t2 + (e & 1)) * a.Dv + (e >> 1) * 8] = S[n][e];
+    } else {
+        const int lt = tid - LOADERS;
+        const __nv_bfloat16* kp = (const __nv_bfloat16*)a.k + (t0 * a.Hk + hk) * DK;
+        const __nv_bfloat16* qp = (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK;
+        const __nv_bfloat16* vp = (const __nv_bfloat16*)a.v + (t0 * a.Hv + h) * a.Dv + v0;
+        __nv_bfloat16* op = (__nv_bfloat16*)a.o + (t0 * a.Hv + h) * a.Dv + v0;
+        const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * rec_bytes(1);
+        auto load = [&](int c) {
+            const uint32_t st = base + (c & 1) * L::STAGE;
+            const int valid = min(C, len - c * C);
+            load_tile<DK, LOADERS>(st + L::K_, kp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, lt);
+            load_tile<DK, LOADERS>(st + L::Q_, qp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, lt);
+            for (int e = lt; e < C * 2 * MT; e += LOADERS) {
+                const int row = e / (2 * MT), piece = e % (2 * MT);
+                const bool in = row < valid;
+                cp16(st + L::V_ + row * L::VROW + piece * 16, vp + ((int64_t)c * C + (in ? row : 0)) * a.Hv * a.Dv + piece * 8, in);
+            }
+            const char* src = rec + (int64_t)c * a.Hv * rec_bytes(1);
+            for (int e = lt; e < rec_bytes(1) / 16; e += LOADERS) cp16(st + L::REC + e * 16, src + e * 16, true);
+            cp_async_commit();
+        };
+        if (nch > 0) load(0);
+        for (int c = 0; c < nch; ++c) {
+            cp_async_wait_all();
+            __syncthreads();   // chunk c has landed; no one reads stage (c + 1) % 2
+            if (c + 1 < nch) load(c + 1);
+            const uint32_t st = base + (c & 1) * L::STAGE;
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(1));
+            float qs[2][2][4] = {};
+#pragma unroll
+            for (int s = 0; s < DK / 16; ++s) {
+                uint32_t bq[4], x[2][4];
+                ldsm(bq, st + L::Q_ + tile_at<DK>(b_row, 2 * s + b_piece));
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    ldsm(x[p], base + L::SP + p * 16 * MT * L::SROW + a_row * L::SROW + s * 32 + a_piece);
+                    mma(qs[0][p], x[p], bq[0], bq[1]);
+                    mma(qs[1][p], x[p], bq[2], bq[3]);
+                }
+            }
+            float o[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float2 gr = *(const float2*)&scal[f * 16 + n * 8 + t2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][e] = ((e & 1) ? gr.y : gr.x) * (qs[n][0][e] + qs[n][1][e]);
+            }
+            bar_sync(1 + MT + m, 256);
+#pragma unroll
+            for (int jb = 0; jb < 4; ++jb) {
+                if (jb > f) break;
+                uint32_t x[2][4], b[4];
+                ldsm(b, st + L::REC + rec_p(1) + blk(f, jb) + lane * 16);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    ldsm(x[p], base + L::WP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
+                    mma(o[0], x[p], b[0], b[1]);
+                    mma(o[1], x[p], b[2], b[3]);
+                }
+            }
+            // 16 tokens x 16 columns, turned over in the warp's own 512 bytes
+            const int mine = L::OS + (warp - 4 * MT) * 512;
+            const uint32_t w4[4] = {pack(o[0][0], o[0][1]), pack(o[0][2], o[0][3]), pack(o[1][0], o[1][1]), pack(o[1][2], o[1][3])};
+            stsm_t(base + mine + ((lane >> 4) * 8 + (lane & 7)) * 32 + ((lane >> 3) & 1) * 16, w4);
+            __syncwarp();
+            const int tok = c * C + f * 16 + (lane >> 1);
+            const uint4 out = *(const uint4*)(sm + mine + lane * 16);
+            if (tok < len) *(uint4*)(op + (int64_t)tok * a.Hv * a.Dv + row0 + (lane & 1) * 8) = out;
+            __syncwarp();
+        }
+    }
 }
 
 namespace {
