@@ -190,10 +190,10 @@ __global__ void __launch_bounds__(128) gdn_prologue_kernel(GdnArgs a, const __gr
 #pragma unroll
             for (int jb = 0; jb <= ib; ++jb) {
                 const float2 v = *(const float2*)&T[ib * 16 + ii][jb * 16 + jj];
-                uint32_t p[PLANES];
-                split<PLANES>(v.x, v.y, p);
+                uint32_t p[TPL];
+                split<TPL>(v.x, v.y, p);
 #pragma unroll
-                for (int q = 0; q < PLANES; ++q) *(uint32_t*)(rec + q * TRI + blk(ib, jb) + tid * 4) = p[q];
+                for (int q = 0; q < TPL; ++q) *(uint32_t*)(rec + q * TRI + blk(ib, jb) + tid * 4) = p[q];
             }
         __syncthreads();
     }
@@ -232,7 +232,7 @@ struct Scan {
     static constexpr int K_ = 0, Q_ = K_ + C * DK * 2, REC = Q_ + C * DK * 2;
     static constexpr int V_ = REC + rec_bytes(1), STAGE = V_ + C * VROW;
     static constexpr int SP = 2 * STAGE;                               // [plane][16 MT][SROW]
-    static constexpr int YP = SP + PLANES * 16 * MT * SROW;            // [plane][16 MT][TROW]
+    static constexpr int YP = SP + SPL * 16 * MT * SROW;            // [plane][16 MT][TROW]
     static constexpr int UP = YP + PLANES * 16 * MT * TROW;            // decayed U
     static constexpr int WP = UP + PLANES * 16 * MT * TROW;            // U, two planes
     static constexpr int OS = WP + 2 * 16 * MT * TROW;                 // 512 bytes an output warp
@@ -277,11 +277,11 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    uint32_t p[PLANES];
-                    split<PLANES>(S[n][2 * e], S[n][2 * e + 1], p);
+                    uint32_t p[SPL];
+                    split<SPL>(S[n][2 * e], S[n][2 * e + 1], p);
                     const uint32_t dst = base + L::SP + (row0 + g4 + 8 * e) * L::SROW + (f * (DK / 4) + n * 8 + t2) * 2;
 #pragma unroll
-                    for (int q = 0; q < PLANES; ++q) st_shared_b32(dst + q * 16 * MT * L::SROW, p[q]);
+                    for (int q = 0; q < SPL; ++q) st_shared_b32(dst + q * 16 * MT * L::SROW, p[q]);
                 }
         };
         put_state();
@@ -290,16 +290,16 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
             const uint32_t st = base + (c & 1) * L::STAGE;
             const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(1));
             // K S of the warp's 16 tokens (two 8-token tiles), transposed
-            float ks[2][PLANES][4] = {};
+            float ks[2][SPL][4] = {};
 #pragma unroll
             for (int s = 0; s < DK / 16; ++s) {
-                uint32_t bk[4], x[PLANES][4];
+                uint32_t bk[4], x[SPL][4];
                 ldsm(bk, st + L::K_ + tile_at<DK>(b_row, 2 * s + b_piece));
 #pragma unroll
-                for (int p = 0; p < PLANES; ++p)
+                for (int p = 0; p < SPL; ++p)
                     ldsm(x[p], base + L::SP + p * 16 * MT * L::SROW + a_row * L::SROW + s * 32 + a_piece);
 #pragma unroll
-                for (int p = 0; p < PLANES; ++p) {
+                for (int p = 0; p < SPL; ++p) {
                     mma(ks[0][p], x[p], bk[0], bk[1]);
                     mma(ks[1][p], x[p], bk[2], bk[3]);
                 }
@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t vv = v[n + 2 * e];
-                        const float y0 = be.x * (low(vv) - gr.x * (ks[n][0][2 * e] + (ks[n][1][2 * e] + ks[n][2][2 * e])));
-                        const float y1 = be.y * (high(vv) - gr.y * (ks[n][0][2 * e + 1] + (ks[n][1][2 * e + 1] + ks[n][2][2 * e + 1])));
+                        const float y0 = be.x * (low(vv) - gr.x * (ks[n][0][2 * e] + ks[n][1][2 * e]));
+                        const float y1 = be.y * (high(vv) - gr.y * (ks[n][0][2 * e + 1] + ks[n][1][2 * e + 1]));
                         uint32_t p[PLANES];
                         split<PLANES>(y0, y1, p);
                         const uint32_t dst = base + L::YP + (row0 + g4 + 8 * e) * L::TROW + t * 2;
@@ -326,23 +326,27 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
                 }
             }
             bar_sync(1 + m, 128);
-            // U = T Y for the warp's tokens: the six products of planes above 2^-27 of the result
+            // U = T Y for the warp's tokens: every product of planes but T1 Y2 (2^-27 of the result)
             float u[2][PLANES][4] = {};
 #pragma unroll
             for (int jb = 0; jb < 4; ++jb) {
                 if (jb > f) break;
-                uint32_t y[PLANES][4], t[PLANES][4];
+                uint32_t y[PLANES][4], t[TPL][4];
 #pragma unroll
-                for (int p = 0; p < PLANES; ++p) {
-                    ldsm(y[p], base + L::YP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
-                    ldsm(t[p], st + L::REC + p * TRI + blk(f, jb) + lane * 16);
+                for (int p = 0; p < PLANES; ++p) ldsm(y[p], base + L::YP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
+#pragma unroll
+                for (int p = 0; p < TPL; ++p) ldsm(t[p], st + L::REC + p * TRI + blk(f, jb) + lane * 16);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    mma(u[n][0], y[0], t[0][2 * n], t[0][2 * n + 1]);
+                    mma(u[n][1], y[1], t[0][2 * n], t[0][2 * n + 1]);
+                    mma(u[n][2], y[2], t[0][2 * n], t[0][2 * n + 1]);
                 }
 #pragma unroll
-                for (int q = 0; q < PLANES; ++q)
-#pragma unroll
-                    for (int p = 0; p < PLANES - q; ++p)
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) mma(u[n][p], y[q], t[p][2 * n], t[p][2 * n + 1]);
+                for (int n = 0; n < 2; ++n) {
+                    mma(u[n][1], y[0], t[1][2 * n], t[1][2 * n + 1]);
+                    mma(u[n][2], y[1], t[1][2 * n], t[1][2 * n + 1]);
+                }
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {

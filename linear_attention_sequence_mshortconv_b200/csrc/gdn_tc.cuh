@@ -11,7 +11,11 @@ namespace gdn {
 using namespace sm100;
 
 constexpr int C = 64;          // tokens per chunk
-constexpr int PLANES = 3;      // bf16 planes that hold an fp32 value (8 + 8 + 8 bits)
+// bf16 planes of the MMA operands that are not inputs.  Three carry fp32's 24 bits, two 16 to 17.
+// What enters the state directly (Y = beta o R and U) has three.  Two are enough for S in K S and
+// for T: their rounding (2^-18) reaches U only through K S, a fraction of V, and through T's
+// off-diagonal entries, beta k_i.k_j.
+constexpr int PLANES = 3, SPL = 2, TPL = 2;
 
 // D(16x8, fp32) += A(16x16, bf16, rows) * B(16x8, bf16, columns)
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -82,13 +86,13 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src
 }
 
 // A chunk's factors for one value head, written by the prologue kernel and read by the scans:
-// T = (I + A)^-1 in PLANES planes and P = lower(e^{cum_i - cum_j} q_i.k_j) in PP planes, each
+// T = (I + A)^-1 in TPL planes and P = lower(e^{cum_i - cum_j} q_i.k_j) in PP planes, each
 // the ten 16x16 blocks on and below the diagonal, a block as four 8x8 core matrices of 128
 // contiguous bytes; then e^cum, e^{cum_C - cum} and beta.
 constexpr int BLK = 512;
 constexpr int TRI = 10 * BLK;
-__host__ __device__ constexpr int rec_p(int) { return PLANES * TRI; }
-__host__ __device__ constexpr int rec_scal(int PP) { return (PLANES + PP) * TRI; }
+__host__ __device__ constexpr int rec_p(int) { return TPL * TRI; }
+__host__ __device__ constexpr int rec_scal(int PP) { return (TPL + PP) * TRI; }
 __host__ __device__ constexpr int rec_bytes(int PP) { return rec_scal(PP) + 3 * C * 4; }
 __device__ __forceinline__ int blk(int ib, int jb) { return (ib * (ib + 1) / 2 + jb) * BLK; }
 
