@@ -107,6 +107,10 @@ __global__ void __launch_bounds__(128) gdn_prologue_kernel(GdnArgs a, const __gr
                 scal[t] = exp2f((float)cum[i]);
                 scal[C + t] = exp2f((float)(last - cum[i]));
                 scal[2 * C + t] = b[i];
+                if (PP == 2) {
+                    scal[3 * C + t] = ch[t];
+                    scal[4 * C + t] = cl[t];
+                }
             }
         }
         __syncthreads();
@@ -223,26 +227,31 @@ cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int 
 // with a barrier at each bar, where Y, U and S pass through shared memory as planes.  The
 // chain is bound by latency (one warp a scheduler issues every fourth cycle), which the
 // output warps fill.
-template <int DK, int MT>
+//
+// KEEP: the scan of the backward.  The output warps then write what the gradients need of each
+// chunk (the planes of S and U and R) in place of the output.
+template <int DK, int MT, bool KEEP>
 struct Scan {
+    static constexpr int PP = KEEP ? 2 : 1;
     static constexpr int THREADS = 256 * MT;
     static constexpr int VROW = 32 * MT + 16;        // bytes of a staged row of V: odd multiple of 16
     static constexpr int SROW = 2 * DK + 16;         // of a row of the S planes
     static constexpr int TROW = 2 * C + 16;          // of a row of the Y and U planes
-    static constexpr int K_ = 0, Q_ = K_ + C * DK * 2, REC = Q_ + C * DK * 2;
-    static constexpr int V_ = REC + rec_bytes(1), STAGE = V_ + C * VROW;
+    static constexpr int K_ = 0, Q_ = K_ + C * DK * 2, REC = Q_ + (KEEP ? 0 : C * DK * 2);
+    static constexpr int V_ = REC + rec_bytes(PP), STAGE = V_ + C * VROW;
     static constexpr int SP = 2 * STAGE;                               // [plane][16 MT][SROW]
     static constexpr int YP = SP + SPL * 16 * MT * SROW;            // [plane][16 MT][TROW]
     static constexpr int UP = YP + PLANES * 16 * MT * TROW;            // decayed U
     static constexpr int WP = UP + PLANES * 16 * MT * TROW;            // U, two planes
-    static constexpr int OS = WP + 2 * 16 * MT * TROW;                 // 512 bytes an output warp
-    static constexpr int SMEM = OS + 4 * MT * 512;
+    static constexpr int OS = WP + 2 * 16 * MT * TROW;                 // 512 bytes an output warp, or R
+    static constexpr int SMEM = OS + (KEEP ? 16 * MT * TROW : 4 * MT * 512);
 };
 
-template <int DK, int MT>
-__global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, const char* records)
+template <int DK, int MT, bool KEEP>
+__global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, const char* records,
+                                                            char* kept)
 {
-    using L = Scan<DK, MT>;
+    using L = Scan<DK, MT, KEEP>;
     constexpr int NS = DK / 32;   // 8-column tiles of the state a warp holds
     constexpr int LOADERS = 128 * MT;
     extern __shared__ __align__(128) char sm[];
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
         for (int c = 0; c < nch; ++c) {
             __syncthreads();   // chunk c has landed and S is in place
             const uint32_t st = base + (c & 1) * L::STAGE;
-            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(1));
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(L::PP));
             // K S of the warp's 16 tokens (two 8-token tiles), transposed
             float ks[2][SPL][4] = {};
 #pragma unroll
@@ -315,11 +324,12 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t vv = v[n + 2 * e];
-                        const float y0 = be.x * (low(vv) - gr.x * (ks[n][0][2 * e] + ks[n][1][2 * e]));
-                        const float y1 = be.y * (high(vv) - gr.y * (ks[n][0][2 * e + 1] + ks[n][1][2 * e + 1]));
+                        const float r0 = low(vv) - gr.x * (ks[n][0][2 * e] + ks[n][1][2 * e]);
+                        const float r1 = high(vv) - gr.y * (ks[n][0][2 * e + 1] + ks[n][1][2 * e + 1]);
                         uint32_t p[PLANES];
-                        split<PLANES>(y0, y1, p);
+                        split<PLANES>(be.x * r0, be.y * r1, p);
                         const uint32_t dst = base + L::YP + (row0 + g4 + 8 * e) * L::TROW + t * 2;
+                        if (KEEP) st_shared_b32(base + L::OS + (row0 + g4 + 8 * e) * L::TROW + t * 2, pack(r0, r1));
 #pragma unroll
                         for (int q = 0; q < PLANES; ++q) st_shared_b32(dst + q * 16 * MT * L::TROW, p[q]);
                     }
@@ -366,7 +376,8 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
                     st_shared_b32(base + L::WP + 16 * MT * L::TROW + off, q2[1]);
                 }
             }
-            bar_sync(1 + MT + m, 256);   // U is in place; no warp of the group reads the planes of S any more
+            // U is in place; no warp of the group reads the planes of S any more
+            bar_sync(1 + MT + m, KEEP ? 128 + LOADERS : 256);
             // S' = e^{cum_C} S + K^T (decayed U), the warp's key channels
             const float gam = scal[C - 1];
 #pragma unroll
@@ -401,19 +412,20 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
         const __nv_bfloat16* qp = (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK;
         const __nv_bfloat16* vp = (const __nv_bfloat16*)a.v + (t0 * a.Hv + h) * a.Dv + v0;
         __nv_bfloat16* op = (__nv_bfloat16*)a.o + (t0 * a.Hv + h) * a.Dv + v0;
-        const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * rec_bytes(1);
+        const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * rec_bytes(L::PP);
+        const Kept keep{DK, a.Dv};
         auto load = [&](int c) {
             const uint32_t st = base + (c & 1) * L::STAGE;
             const int valid = min(C, len - c * C);
             load_tile<DK, LOADERS>(st + L::K_, kp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, lt);
-            load_tile<DK, LOADERS>(st + L::Q_, qp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, lt);
+            if (!KEEP) load_tile<DK, LOADERS>(st + L::Q_, qp + (int64_t)c * C * a.Hk * DK, (int64_t)a.Hk * DK, valid, lt);
             for (int e = lt; e < C * 2 * MT; e += LOADERS) {
                 const int row = e / (2 * MT), piece = e % (2 * MT);
                 const bool in = row < valid;
                 cp16(st + L::V_ + row * L::VROW + piece * 16, vp + ((int64_t)c * C + (in ? row : 0)) * a.Hv * a.Dv + piece * 8, in);
             }
-            const char* src = rec + (int64_t)c * a.Hv * rec_bytes(1);
-            for (int e = lt; e < rec_bytes(1) / 16; e += LOADERS) cp16(st + L::REC + e * 16, src + e * 16, true);
+            const char* src = rec + (int64_t)c * a.Hv * rec_bytes(L::PP);
+            for (int e = lt; e < rec_bytes(L::PP) / 16; e += LOADERS) cp16(st + L::REC + e * 16, src + e * 16, true);
             cp_async_commit();
         };
         if (nch > 0) load(0);
@@ -422,7 +434,23 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
             __syncthreads();   // chunk c has landed; no one reads stage (c + 1) % 2
             if (c + 1 < nch) load(c + 1);
             const uint32_t st = base + (c & 1) * L::STAGE;
-            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(1));
+            if (KEEP) {
+                char* dst = kept + ((int64_t)(seqs.slot0(seq, C) + c) * a.Hv + h) * keep.bytes();
+                for (int e = lt; e < SPL * 16 * MT * DK / 8; e += LOADERS) {
+                    const int piece = e % (DK / 8), row = e / (DK / 8) % (16 * MT), p = e / (DK / 8) / (16 * MT);
+                    *(uint4*)(dst + keep.s() + p * keep.state() + ((v0 + row) * DK + piece * 8) * 2) =
+                        *(const uint4*)(sm + L::SP + (p * 16 * MT + row) * L::SROW + piece * 16);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) bar_sync(1 + MT + i, 128 + LOADERS);
+                for (int e = lt; e < 3 * 16 * MT * 8; e += LOADERS) {
+                    const int piece = e & 7, row = e / 8 % (16 * MT), p = e / 8 / (16 * MT);
+                    const uint4 x = *(const uint4*)(sm + (p < 2 ? L::WP + (p * 16 * MT + row) * L::TROW : L::OS + row * L::TROW) + piece * 16);
+                    *(uint4*)(dst + (p < 2 ? keep.u() + p * keep.rows() : keep.r()) + ((v0 + row) * C + piece * 8) * 2) = x;
+                }
+                continue;
+            }
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(L::PP));
             float qs[2][2][4] = {};
 #pragma unroll
             for (int s = 0; s < DK / 16; ++s) {
@@ -447,7 +475,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
             for (int jb = 0; jb < 4; ++jb) {
                 if (jb > f) break;
                 uint32_t x[2][4], b[4];
-                ldsm(b, st + L::REC + rec_p(1) + blk(f, jb) + lane * 16);
+                ldsm(b, st + L::REC + rec_p(L::PP) + blk(f, jb) + lane * 16);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     ldsm(x[p], base + L::WP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
@@ -469,19 +497,33 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
 }
 
 namespace {
-template <int DK, int MT>
-cudaError_t scan(const GdnArgs& a, const Seqs& s, const void* records, cudaStream_t st)
+template <int DK, int MT, bool KEEP>
+cudaError_t scan(const GdnArgs& a, const Seqs& s, const void* records, void* kept, cudaStream_t st)
 {
-    auto kern = gdn_scan_kernel<DK, MT>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Scan<DK, MT>::SMEM);
+    using L = Scan<DK, MT, KEEP>;
+    auto kern = gdn_scan_kernel<DK, MT, KEEP>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
-    ProfileScope prof("gdn_scan", st);
+    ProfileScope prof(KEEP ? "gdn_scan_keep" : "gdn_scan", st);
     count_launch();
-    kern<<<dim3(a.Dv / (16 * MT), a.Hv, s.n), Scan<DK, MT>::THREADS, Scan<DK, MT>::SMEM, st>>>(a, s, (const char*)records);
+    kern<<<dim3(a.Dv / (16 * MT), a.Hv, s.n), L::THREADS, L::SMEM, st>>>(a, s, (const char*)records, (char*)kept);
     return cudaGetLastError();
 }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 }  // namespace
+
+cudaError_t launch_scan(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int sms, cudaStream_t st)
+{
+    // 32 columns a CTA re-read K, Q and the factors half as often; 16 put twice as many SMs to
+    // work where the heads alone do not fill them.
+    const bool wide = (int64_t)s.n * a.Hv * (a.Dv / 32) >= sms;
+    if (kept) {
+        if (a.Dk == 64) return wide ? scan<64, 2, true>(a, s, records, kept, st) : scan<64, 1, true>(a, s, records, kept, st);
+        return wide ? scan<128, 2, true>(a, s, records, kept, st) : scan<128, 1, true>(a, s, records, kept, st);
+    }
+    if (a.Dk == 64) return wide ? scan<64, 2, false>(a, s, records, kept, st) : scan<64, 1, false>(a, s, records, kept, st);
+    return wide ? scan<128, 2, false>(a, s, records, kept, st) : scan<128, 1, false>(a, s, records, kept, st);
+}
 }  // namespace gdn
 
 // The tensor-core path copies rows in 16-byte pieces.
@@ -498,11 +540,7 @@ cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, cu
     cudaError_t e = cudaSuccess;
     if (s.tokens() > 0) e = gdn::launch_prologue(a, s, ws, 1, st);
     if (e != cudaSuccess) return e;
-    // 32 columns a CTA re-read K, Q and the factors half as often; 16 put twice as many SMs to
-    // work where the heads alone do not fill them.
-    const bool wide = (int64_t)s.n * a.Hv * (a.Dv / 32) >= sms;
-    if (a.Dk == 64) return wide ? gdn::scan<64, 2>(a, s, ws, st) : gdn::scan<64, 1>(a, s, ws, st);
-    return wide ? gdn::scan<128, 2>(a, s, ws, st) : gdn::scan<128, 1>(a, s, ws, st);
+    return gdn::launch_scan(a, s, ws, nullptr, sms, st);
 }
 
 }  // namespace kda

@@ -65,20 +65,20 @@ __device__ __forceinline__ void bar_sync(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Tiles of 64 tokens x W values (bf16, W = 64 or 128): rows of 2 W bytes, the 16-byte pieces
-// of a row permuted by the row's low bits, so 8 rows of one piece lie in 8 different
-// bank groups for ldmatrix.
+// Tiles of rows of W values (bf16, W = 32, 64 or 128): the 16-byte pieces of a row are
+// permuted by the row's low bits, so 8 rows of one piece lie in 8 different bank groups
+// for ldmatrix.
 template <int W>
 __device__ __forceinline__ uint32_t tile_at(int row, int piece)
 {
-    return row * (2 * W) + ((piece ^ (row & 7)) << 4);
+    return row * (2 * W) + ((piece ^ (W == 32 ? (row >> 1) & 3 : row & 7)) << 4);
 }
-template <int W, int THREADS>
+template <int W, int THREADS, int ROWS = C>
 __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src, int64_t row_stride, int valid, int tid)
 {
     constexpr int P = W / 8;
 #pragma unroll
-    for (int i = 0; i < C * P / THREADS; ++i) {
+    for (int i = 0; i < ROWS * P / THREADS; ++i) {
         const int e = i * THREADS + tid, row = e / P, piece = e % P;
         const bool in = row < valid;
         cp16(dst + tile_at<W>(row, piece), src + (in ? row : 0) * row_stride + piece * 8, in);
@@ -88,14 +88,34 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src
 // A chunk's factors for one value head, written by the prologue kernel and read by the scans:
 // T = (I + A)^-1 in TPL planes and P = lower(e^{cum_i - cum_j} q_i.k_j) in PP planes, each
 // the ten 16x16 blocks on and below the diagonal, a block as four 8x8 core matrices of 128
-// contiguous bytes; then e^cum, e^{cum_C - cum} and beta.
+// contiguous bytes; then e^cum, e^{cum_C - cum}, beta and, with PP = 2 (the backward), cum
+// log2(e) as a sum of two floats.
 constexpr int BLK = 512;
 constexpr int TRI = 10 * BLK;
 __host__ __device__ constexpr int rec_p(int) { return TPL * TRI; }
 __host__ __device__ constexpr int rec_scal(int PP) { return (TPL + PP) * TRI; }
-__host__ __device__ constexpr int rec_bytes(int PP) { return rec_scal(PP) + 3 * C * 4; }
+__host__ __device__ constexpr int rec_bytes(int PP) { return rec_scal(PP) + (PP == 2 ? 5 : 3) * C * 4; }
 __device__ __forceinline__ int blk(int ib, int jb) { return (ib * (ib + 1) / 2 + jb) * BLK; }
 
+// What the backward keeps of each chunk and value head, bf16: the entry state S^T and the
+// gradient D^T of the exit state, [Dv][Dk] in two planes each; U^T and dY^T, [Dv][64] in two
+// planes each; R^T, [Dv][64].  Then per-warp parts of <exit state, D>, fp32, Dv / 4.
+struct Kept {
+    int Dk, Dv;
+    __host__ __device__ size_t state() const { return (size_t)Dv * Dk * 2; }     // bytes of a plane
+    __host__ __device__ size_t rows() const { return (size_t)Dv * C * 2; }
+    __host__ __device__ size_t s() const { return 0; }
+    __host__ __device__ size_t d() const { return 2 * state(); }
+    __host__ __device__ size_t u() const { return 4 * state(); }
+    __host__ __device__ size_t y() const { return u() + 2 * rows(); }
+    __host__ __device__ size_t r() const { return y() + 2 * rows(); }
+    __host__ __device__ size_t exit() const { return r() + rows(); }
+    __host__ __device__ size_t bytes() const { return (exit() + Dv + 255) / 256 * 256; }
+};
+
+// launch of the forward scan: o and S_T (kept null), or what the backward needs (kept and, if
+// not null, S_T; o unused)
+cudaError_t launch_scan(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int sms, cudaStream_t st);
 // launch of the prologue kernel: one record per (slot, value head)
 cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int PP, cudaStream_t st);
 

@@ -67,6 +67,9 @@ cudaError_t launch_gdn_recurrent(const GdnArgs& a, const Seqs& s, cudaStream_t s
 bool gdn_tc_supported(const GdnArgs& a);
 size_t gdn_tc_workspace(const Seqs& s, int Hv);
 cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, cudaStream_t st);
+bool gdn_tc_bwd_supported(const GdnBwdArgs& a);
+size_t gdn_tc_bwd_workspace(const Seqs& s, int Hv, int Dk, int Dv);
+cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& a, const Seqs& s, void* ws, int sms, cudaStream_t st);
 size_t gdn_generic_bwd_workspace(int slots16, int tokens, int Hv, int Dk, int Dv);
 cudaError_t launch_gdn_generic_bwd(const GdnBwdArgs& a, const Seqs& s, void* ws, cudaStream_t st);
 

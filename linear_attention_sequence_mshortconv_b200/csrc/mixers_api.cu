@@ -151,9 +151,13 @@ kda_status run_gdn_forward(const GdnArgs& a, const Batch& b, void* workspace, si
 
 size_t gdn_bwd_need(const GdnArgs& a, const Batch& b)
 {
+    GdnArgs x = a;
+    x.q = x.k = x.v = x.o = nullptr;
+    const bool tc = gdn_tc_supported(x);
     size_t need = 0;
     each_group(b, [&](const Seqs& s, int, int64_t) {
         need = max_of(need, gdn_generic_bwd_workspace(s.slots(16), s.tokens(), a.Hv, a.Dk, a.Dv));
+        if (tc) need = max_of(need, gdn_tc_bwd_workspace(s, a.Hv, a.Dk, a.Dv));
         return KDA_OK;
     });
     return need;
@@ -165,6 +169,8 @@ kda_status run_gdn_backward(const GdnBwdArgs& a, const Batch& b, void* workspace
     Scratch ws;
     kda_status st = ws.acquire(workspace, workspace_bytes, gdn_bwd_need(a.f, b), (cudaStream_t)stream);
     if (st != KDA_OK) return st;
+    const bool tc = gdn_tc_bwd_supported(a);
+    const int sms = num_sms();
     return each_group(b, [&](const Seqs& s, int seq, int64_t token) {
         GdnBwdArgs x = a;
         x.f = moved(a.f, seq, token);
@@ -176,7 +182,8 @@ kda_status run_gdn_backward(const GdnBwdArgs& a, const Batch& b, void* workspace
         x.dv = at(a.dv, token * a.f.Hv * a.f.Dv, a.f.t);
         x.dg = at(a.dg, token * a.f.Hv, a.f.t);
         x.dbeta = at(a.dbeta, token * a.f.Hv, a.f.t);
-        return from_cuda(launch_gdn_generic_bwd(x, s, ws.ptr, (cudaStream_t)stream));
+        return from_cuda(tc ? launch_gdn_tc_bwd(x, s, ws.ptr, sms, (cudaStream_t)stream)
+                            : launch_gdn_generic_bwd(x, s, ws.ptr, (cudaStream_t)stream));
     });
 }
 
