@@ -1,0 +1,353 @@
+// Causal attention with grouped heads on tcgen05 tensor cores (bf16, head width 64 or 128).
+//
+//   s_ij = scale q_i.k_j,  m_i = max_j s_ij,  p_ij = e^{s_ij - m_i},  o_i = sum_j p_ij v_j / sum_j p_ij,
+// over the keys in blocks of 128 from the first, with a running m and sum.
+//
+// A CTA owns 256 rows of one key/value head's query group (row = token x query head of the
+// group, so the group shares every K and V tile, and a tile's keys end soon after its first
+// token) as two tiles of 128 rows:
+//   warps 0-3 and 4-7: the softmax of tile 0 and 1, one row to a thread, so maxima and sums need
+//                      no exchange;
+//   warp 8: issues the MMAs, S = Q K^T and O += P V (P from tensor memory, where it takes the
+//           place of S), of the two tiles in turn: the tensor cores work on one tile while the
+//           other's softmax runs;
+//   warp 9: TMA loads of K and V into rings.
+// Tensor memory (512 columns): S0, S1 (128 each), O0, O1 (D each).
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 since the reference of
+// its exponents was set (sums and weights then stay below 2^8 times their size, far from
+// overflow), which after the first blocks is rare; the result does not depend on the reference.
+
+#include "attn_tc.cuh"
+
+namespace kda {
+namespace attn {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int rows)
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
+    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)rows}, es[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr int QR = 128;   // rows of a tile
+constexpr int KB = 128;   // keys of a block
+
+template <int D>
+struct Fwd {
+    static constexpr int PANEL = 128 * 128;                 // bytes of 128 rows x 64 values
+    static constexpr int TILE = D / 64 * PANEL;
+    static constexpr int STAGES = D == 64 ? 4 : 2;          // K and V tiles in flight, each
+    static constexpr int Q_ = 0, K_ = Q_ + 2 * TILE, V_ = K_ + STAGES * TILE, BAR = V_ + STAGES * TILE;
+    static constexpr int SMEM = BAR + 512 + 1024;           // the base is aligned up to 1024 bytes
+    static constexpr int THREADS = 320;
+    // tensor memory columns
+    static constexpr int S_ = 0, O_ = 2 * KB;
+};
+
+template <int D>
+__global__ void __launch_bounds__(320, 1)
+attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnArgs a,
+                const __grid_constant__ Seqs seqs, int* status)
+{
+    using L = Fwd<D>;
+    extern __shared__ char raw[];
+    char* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t base = smem_addr(sm);
+    uint64_t* bars = (uint64_t*)(sm + L::BAR);
+    uint64_t *kfull = bars, *kempty = kfull + L::STAGES, *vfull = kempty + L::STAGES, *vempty = vfull + L::STAGES;
+    uint64_t *sfull = vempty + L::STAGES, *pready = sfull + 2, *pvdone = pready + 4, *vfix = pvdone + 2, *drain = vfix + 1;
+    uint32_t* tm_ptr = (uint32_t*)(drain + 1);
+    const Guard guard{(volatile int*)(tm_ptr + 1), status};
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hk = blockIdx.y;
+    const Rows rows{a.H / a.Hkv};
+    int seq, tile;
+    // the last tiles of a sequence have the most keys: they start first
+    if (!rows.locate(seqs, (int64_t)gridDim.x - 1 - blockIdx.x, 2 * QR, seq, tile)) return;
+    const int64_t t0 = seqs.start(seq);
+    const int len = seqs.len(seq);
+    const int64_t all = (int64_t)len * rows.r, first = (int64_t)tile * 2 * QR;
+    auto blocks = [&](int t) {   // key blocks tile t sees
+        const int64_t r0 = first + t * QR;
+        return r0 >= all ? 0 : (int)(min(r0 + QR, all) - 1) / rows.r / KB + 1;
+    };
+    const int n0 = blocks(0), n1 = blocks(1), n = max(n0, n1);
+
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int i = 0; i < L::STAGES; ++i) {
+                mbar_init(kfull + i, 1);
+                mbar_init(kempty + i, 1);
+                mbar_init(vfull + i, 1);
+                mbar_init(vempty + i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(sfull + i, 1);
+                mbar_init(pready + 2 * i, QR);
+                mbar_init(pready + 2 * i + 1, QR);
+                mbar_init(pvdone + i, 1);
+            }
+            mbar_init(vfix, 32);
+            mbar_init(drain, 1);
+            *guard.flag = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(tm_ptr, 512);
+        tmem_relinquish();
+    }
+    // Q: rows past the sequence's end are zeros
+    for (int e = tid; e < 2 * QR * (D / 8); e += L::THREADS) {
+        const int piece = e % (D / 8), row = e / (D / 8);
+        const int64_t i = first + row;
+        const bool in = i < all;
+        const int64_t off = in ? ((t0 + i / rows.r) * a.H + (int64_t)hk * rows.r + i % rows.r) * D + piece * 8 : 0;
+        cp16(base + L::Q_ + (row / QR) * L::TILE + (piece >> 3) * L::PANEL + piece_at(row % QR, piece & 7),
+             (const __nv_bfloat16*)a.q + off, in);
+    }
+    cp_async_commit();
+    cp_async_wait_all();
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm_ptr;
+
+    if (warp == 9) {
+        if (lane == 0) {
+            for (int j = 0; j < n && !guard.up(); ++j) {
+                const int s = j % L::STAGES, u = j / L::STAGES;
+                const int y = (int)t0 + j * KB;
+                wait(kempty + s, (u & 1) ^ 1, guard);
+                if (guard.up()) break;
+                mbar_arrive_expect_tx(kfull + s, L::TILE);
+                for (int p = 0; p < D / 64; ++p)
+                    tma_load_3d(sm + L::K_ + s * L::TILE + p * L::PANEL, &tm_k, kfull + s, p * 64, hk, y);
+                wait(vempty + s, (u & 1) ^ 1, guard);
+                if (guard.up()) {   // this block's K has no V: let it land before leaving
+                    mbar_wait_bounded(kfull + s, u & 1, kWaitNs);
+                    break;
+                }
+                mbar_arrive_expect_tx(vfull + s, L::TILE);
+                for (int p = 0; p < D / 64; ++p)
+                    tma_load_3d(sm + L::V_ + s * L::TILE + p * L::PANEL, &tm_v, vfull + s, p * 64, hk, y);
+            }
+        }
+        __syncwarp();
+        // The last block's rows past the end hold the next sequence, or nothing: their weights are
+        // 0, but 0 times a value that is not finite is not.  The whole warp clears them.
+        const int tail = len - (n - 1) * KB;
+        if (tail < KB && !guard.up()) {
+            const int s = (n - 1) % L::STAGES;
+            wait(vfull + s, ((n - 1) / L::STAGES) & 1, guard);
+            for (int e = lane; e < (KB - tail) * (D / 8); e += 32) {
+                const int row = tail + e / (D / 8), piece = e % (D / 8);
+                *(uint4*)(sm + L::V_ + s * L::TILE + (piece >> 3) * L::PANEL + piece_at(row, piece & 7)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            mbar_arrive(vfix);
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            const uint32_t id_s = idesc_f16(QR, KB, false, false, a.scale < 0.f, true);
+            const uint32_t id_o = idesc_f16(QR, D, false, true, false, true);
+            auto scores = [&](int t, int j) {
+                const int s = j % L::STAGES;
+                wait(kfull + s, (j / L::STAGES) & 1, guard);
+                if (guard.up()) return;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = (x >> 2) * L::PANEL + (x & 3) * 32;
+                    umma_f16(tmem + L::S_ + t * KB, desc_rows(base + L::Q_ + t * L::TILE + off),
+                             desc_rows(base + L::K_ + s * L::TILE + off), id_s, x > 0);
+                }
+                umma_commit(sfull + t);
+                if (t == 1 || n1 <= j) umma_commit(kempty + s);
+            };
+            // tile 1 sees every block tile 0 does, unless it has no rows
+            if (n0 > 0) scores(0, 0);
+            if (n1 > 0) scores(1, 0);
+            for (int j = 0; j < n && !guard.up(); ++j)
+                for (int t = 0; t < 2; ++t) {
+                    if (j >= (t ? n1 : n0)) continue;
+                    const int s = j % L::STAGES;
+                    wait(vfull + s, (j / L::STAGES) & 1, guard);
+                    if (j == n - 1 && len - j * KB < KB) wait(vfix, 0, guard);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        wait(pready + 2 * t + half, j & 1, guard);
+                        if (guard.up()) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = half * 4; x < half * 4 + 4; ++x)
+                            umma_f16_ts(tmem + L::O_ + t * D, tmem + L::S_ + t * KB + x * 8,
+                                        desc_cols(base + L::V_ + s * L::TILE + x * 2048, L::PANEL), id_o, j > 0 || x > 0);
+                    }
+                    if (guard.up()) break;
+                    if (t == 1 || n1 <= j) umma_commit(vempty + s);
+                    umma_commit(pvdone + t);
+                    if (j + 1 < (t ? n1 : n0)) {
+                        wait(pvdone + t, j & 1, guard);   // P is in S's place: it must have been read
+                        if (guard.up()) break;
+                        scores(t, j + 1);
+                    }
+                }
+            if (guard.up()) {   // leave nothing in flight
+                umma_commit(drain);
+                mbar_wait_bounded(drain, 0, kWaitNs);
+            }
+        }
+    } else {
+        const int t = warp >> 2, nt = t ? n1 : n0;
+        const int64_t i = first + t * QR + (tid & 127);
+        const bool real = i < all;
+        const int token = (int)(min(i, all - 1) / rows.r);
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t ts = tmem + L::S_ + t * KB + lanes, to = tmem + L::O_ + t * D + lanes;
+        // scores come with the sign of scale applied by the MMA; never 0, so that a masked -inf stays one
+        const float sl = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+        // the warp's first row sees the fewest keys
+        const int least = (int)(min(first + t * QR + (warp & 3) * 32, all - 1) / rows.r);
+        float ref = 0.f, sum = 0.f;
+        for (int j = 0; j < nt && !guard.up(); ++j) {
+            wait(sfull + t, j & 1, guard);
+            tc_fence_after();
+            float s[128];
+            {
+                float (&lo)[64] = *(float (*)[64])s, (&hi)[64] = *(float (*)[64])(s + 64);
+                tmem_ld64(ts, lo);
+                tmem_ld64(ts + 64, hi);
+            }
+            if (j * KB + KB - 1 > least) {
+                const int seen = token - j * KB;   // keys 0 .. seen of the block
+#pragma unroll
+                for (int x = 0; x < 128; ++x)
+                    if (x > seen) s[x] = -INFINITY;
+            }
+            float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+            for (int x = 4; x < 128; x += 4) {
+                m0 = fmaxf(m0, s[x]);
+                m1 = fmaxf(m1, s[x + 1]);
+                m2 = fmaxf(m2, s[x + 2]);
+                m3 = fmaxf(m3, s[x + 3]);
+            }
+            const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+            if (j == 0) {
+                ref = top;
+            } else if (__any_sync(~0u, (top - ref) * sl > 8.f)) {
+                const bool grown = (top - ref) * sl > 8.f;
+                const float f = grown ? ex2_approx((ref - top) * sl) : 1.f;
+                if (grown) ref = top;
+                sum *= f;
+                wait(pvdone + t, (j - 1) & 1, guard);
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < D; x += 32) {
+                    float o[32];
+                    tmem_ld32(to + x, o);
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] *= f;
+                    tmem_st32(to + x, o);
+                }
+            }
+            const float off = -ref * sl;
+            float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t p[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const float e0 = ex2_approx(fmaf(s[half * 64 + 2 * x], sl, off));
+                    const float e1 = ex2_approx(fmaf(s[half * 64 + 2 * x + 1], sl, off));
+                    z0 += e0;
+                    z1 += e1;
+                    p[x] = pack_bf16(e0, e1);
+                }
+                tmem_st32u_nowait(ts + half * 32, p);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(pready + 2 * t + half);
+            }
+            sum += z0 + z1;
+        }
+        if (nt > 0) {
+            wait(pvdone + t, (nt - 1) & 1, guard);
+            tc_fence_after();
+            if (!guard.up()) {
+                const int64_t row = real ? (t0 + token) * a.H + (int64_t)hk * rows.r + i % rows.r : 0;
+                const float inv = 1.f / sum;
+                __nv_bfloat16* o = (__nv_bfloat16*)a.o + row * D;
+#pragma unroll
+                for (int x = 0; x < D; x += 32) {
+                    float v[32];
+                    tmem_ld32(to + x, v);
+                    if (real)
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8)
+                            *(uint4*)(o + x + y) = make_uint4(pack_bf16(v[y] * inv, v[y + 1] * inv), pack_bf16(v[y + 2] * inv, v[y + 3] * inv),
+                                                              pack_bf16(v[y + 4] * inv, v[y + 5] * inv), pack_bf16(v[y + 6] * inv, v[y + 7] * inv));
+                }
+                if (real && a.lse) a.lse[row] = (ref * sl + log2f(sum)) * kLn2;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t forward(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t st)
+{
+    using L = Fwd<D>;
+    CUtensorMap k, v;
+    if (!make_map(&k, a.k, s.tokens(), a.Hkv, D, KB) || !make_map(&v, a.v, s.tokens(), a.Hkv, D, KB))
+        return cudaErrorInvalidValue;
+    auto kern = attn_fwd_kernel<D>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    if (e != cudaSuccess) return e;
+    ProfileScope prof("attn_fwd", st);
+    count_launch();
+    kern<<<dim3((unsigned)Rows{a.H / a.Hkv}.slots(s, 2 * QR), a.Hkv), L::THREADS, L::SMEM, st>>>(k, v, a, s, status);
+    return cudaGetLastError();
+}
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+}  // namespace
+}  // namespace attn
+
+bool attn_tc_supported(const AttnArgs& a)
+{
+    return a.t == ET_BF16 && (a.D == 64 || a.D == 128) && attn::aligned16(a.q) && attn::aligned16(a.k) &&
+           attn::aligned16(a.v) && attn::aligned16(a.o);
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t st)
+{
+    return a.D == 64 ? attn::forward<64>(a, s, status, st) : attn::forward<128>(a, s, status, st);
+}
+
+}  // namespace kda

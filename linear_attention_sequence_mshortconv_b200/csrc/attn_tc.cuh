@@ -1,0 +1,96 @@
+// Pieces shared by the tensor-core kernels of causal attention: tensor maps of 128-byte
+// swizzled tiles, their MMA descriptors, bounded waits.
+#pragma once
+
+#include <mutex>
+
+#include "mixers.h"
+#include "sm100.cuh"
+
+namespace kda {
+namespace attn {
+
+using namespace sm100;
+
+constexpr uint64_t kWaitNs = 2000000000ull;   // a wait that lasts longer is reported and given up
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// ---- waits ------------------------------------------------------------------------------
+// The first wait that runs out raises the CTA's flag and records DEV_TIMEOUT; from then on no
+// wait waits, no MMA or copy is issued, and every role runs to its end.
+struct Guard {
+    volatile int* flag;
+    int* status;
+    __device__ __forceinline__ bool up() const { return *flag != 0; }
+};
+__device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, Guard g)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!g.up()) {
+        if (mbar_try_wait_sleep(bar, parity, 20000u)) return;
+        if (globaltimer_ns() - t0 > kWaitNs) {
+            *g.flag = 1;
+            atomicCAS(g.status, DEV_OK, DEV_TIMEOUT);
+        }
+    }
+}
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, const Guard& g)
+{
+    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, g);
+}
+
+// ---- tiles ------------------------------------------------------------------------------
+// A tile of R rows x D values (bf16): D / 64 panels of R x 64, a row of a panel 128 bytes, its
+// eight 16-byte pieces permuted by the row's low three bits (the 128-byte swizzle of the
+// copy engine and of the MMA's descriptors).  Panels start on 1024-byte boundaries.
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+
+// rows as M or N, values as K ("K-major"): 8 rows x 128 bytes is one unit, 1024 bytes apart
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr)
+{
+    return sdesc(addr, 16, 1024) | (2ull << 61);
+}
+// values as M or N, rows as K ("MN-major"): 64 values x 8 rows is one unit; units 1024 bytes apart
+// along the rows, a panel apart along the values
+__device__ __forceinline__ uint64_t desc_cols(uint32_t addr, uint32_t panel)
+{
+    return sdesc(addr, panel, 1024) | (2ull << 61);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+
+// [tokens, heads, D] bf16, box = `rows` tokens x 1 head x 64 values, landing as a panel
+bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int rows);
+
+// ---- rows of a key/value head's query group -----------------------------------------------
+// The query heads that share a key/value head are rows of one matrix: row i is token i / r, head
+// i % r of the group (r = H / Hkv).  Tiles of rows of a sequence are numbered like Seqs's tiles
+// of tokens.
+struct Rows {
+    int r;
+    __host__ __device__ int64_t slot0(const Seqs& s, int i, int R) const { return (int64_t)s.start(i) * r / R + i; }
+    __host__ int64_t slots(const Seqs& s, int R) const { return (int64_t)s.tokens() * r / R + s.n; }
+    __device__ bool locate(const Seqs& s, int64_t slot, int R, int& seq, int& tile) const
+    {
+        int lo = 0, hi = s.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (slot0(s, mid, R) <= slot) lo = mid; else hi = mid - 1;
+        }
+        seq = lo;
+        tile = (int)(slot - slot0(s, lo, R));
+        return (int64_t)tile * R < (int64_t)s.len(lo) * r;
+    }
+};
+
+}  // namespace attn
+}  // namespace kda

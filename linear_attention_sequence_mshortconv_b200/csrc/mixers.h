@@ -98,6 +98,9 @@ struct AttnBwdArgs {
     const void* dout;
     void *dq, *dk, *dv;
 };
+// tcgen05 (bf16, D = 64 or 128, 16-byte aligned tensors)
+bool attn_tc_supported(const AttnArgs& a);
+cudaError_t launch_attn_tc(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t st);
 cudaError_t launch_attn_generic(const AttnArgs& a, const Seqs& s, cudaStream_t st);
 cudaError_t launch_attn_generic_bwd(const AttnBwdArgs& a, const Seqs& s, cudaStream_t st);
 

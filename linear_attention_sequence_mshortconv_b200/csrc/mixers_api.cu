@@ -238,9 +238,13 @@ kda_status attn_forward_any(AttnArgs a, const Batch& b, bool packed, kda_dtype d
     if (b.tokens() == 0) return KDA_OK;
     if (!a.q || !a.k || !a.v || !a.o) return KDA_ERR_INVALID_ARG;
     a.t = et_of(dtype);
+    const bool tc = attn_tc_supported(a);
+    int* status = tc ? device_status_ptr() : nullptr;
+    if (tc && !status) return KDA_ERR_CUDA;
     return each_group(b, [&](const Seqs& s, int, int64_t token) {
         if (s.tokens() == 0) return KDA_OK;
-        return from_cuda(launch_attn_generic(moved(a, token), s, (cudaStream_t)stream));
+        const AttnArgs x = moved(a, token);
+        return from_cuda(tc ? launch_attn_tc(x, s, status, (cudaStream_t)stream) : launch_attn_generic(x, s, (cudaStream_t)stream));
     });
 }
 
