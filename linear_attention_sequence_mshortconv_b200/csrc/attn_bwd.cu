@@ -1,0 +1,579 @@
+// Gradients of causal attention with grouped heads on tcgen05 tensor cores (bf16, head width 64
+// or 128):
+//   p_ij = e^{s_ij - lse_i},  dv_j = sum_i p_ij do_i,
+//   ds_ij = p_ij (do_i.v_j - delta_i),  delta_i = do_i.o_i,
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i.
+//
+// Two kernels, so that every sum has one owner and no atomics are needed: one owns 128 keys and
+// goes over the rows (token x query head of the group) that see them, so dk and dv are summed
+// over the group where they are accumulated; the other owns 256 rows and goes over the keys.
+// That computes s and do.v twice (7 products instead of 5), but results do not depend on an
+// order of arrival and no fp32 gradient passes through memory.  A first kernel computes delta and
+// lays it and lse log2(e) out row by row.
+//
+// Both kernels have the forward's roles: warps 0-3 and 4-7 turn scores into the operands of the
+// next product, warp 8 issues the MMAs, warp 9 the loads.
+
+#include "attn_tc.cuh"
+
+namespace kda {
+namespace attn {
+namespace {
+
+// ---- delta ----------------------------------------------------------------------------------
+// [key/value head][token][head of the group]: {lse log2(e), delta}
+template <int D>
+__global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs a, const __nv_bfloat16* dout, float2* rows, int64_t tokens)
+{
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= tokens * a.H) return;
+    constexpr int N = D / 32;
+    const __nv_bfloat16* o = (const __nv_bfloat16*)a.o + row * D + lane * N;
+    const __nv_bfloat16* g = dout + row * D + lane * N;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 x = __bfloat1622float2(*(const __nv_bfloat162*)(o + i)), y = __bfloat1622float2(*(const __nv_bfloat162*)(g + i));
+        s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+    if (lane == 0) {
+        const int h = (int)(row % a.H), r = a.H / a.Hkv;
+        rows[((int64_t)(h / r) * tokens + row / a.H) * r + h % r] = make_float2(a.lse[row] * kLog2e, s);
+    }
+}
+
+// what the MMA-issuing thread does on the way out after a timeout: leave nothing in flight
+__device__ __forceinline__ void drain_mma(uint64_t* bar)
+{
+    umma_commit(bar);
+    mbar_wait_bounded(bar, 0, kWaitNs);
+}
+
+// 32 fp32 columns of tensor memory, scaled, as 64 bytes of a bf16 row
+__device__ __forceinline__ void store32(uint32_t taddr, float f, __nv_bfloat16* dst, bool real)
+{
+    float v[32];
+    tmem_ld32(taddr, v);
+    if (!real) return;
+#pragma unroll
+    for (int y = 0; y < 32; y += 8)
+        *(uint4*)(dst + y) = make_uint4(pack_bf16(v[y] * f, v[y + 1] * f), pack_bf16(v[y + 2] * f, v[y + 3] * f),
+                                        pack_bf16(v[y + 4] * f, v[y + 5] * f), pack_bf16(v[y + 6] * f, v[y + 7] * f));
+}
+
+// ---- dk and dv ------------------------------------------------------------------------------
+// Keys are rows of every product: S^T = K Q^T and dP^T = V dO^T for 64 rows at a time, then
+// dV += P^T dO and dK += dS^T Q with P^T and dS^T read from tensor memory.  Two buffers of
+// (S^T, dP^T), one to each softmax warpgroup: while one is turned into P and dS, the tensor cores
+// fill or read the other.  Tensor memory: dV, dK (D columns each), 2 x (64 + 64).
+// A tile holds 64 / r tokens, all heads of the group, as one TMA box; rows left over where r does
+// not divide 64 stay zero.
+template <int D>
+struct Keys {
+    static constexpr int KEYS = 128, RB = 64;
+    static constexpr int KPANEL = KEYS * 128, KTILE = D / 64 * KPANEL;
+    static constexpr int RPANEL = RB * 128, RTILE = D / 64 * RPANEL;
+    static constexpr int STAGES = D == 64 ? 6 : 4;          // (Q, dO) tiles in flight
+    static constexpr int K_ = 0, V_ = K_ + KTILE, Q_ = V_ + KTILE, G_ = Q_ + STAGES * RTILE;
+    static constexpr int LD = G_ + STAGES * RTILE;          // float2 [2 warpgroups][2][64]
+    static constexpr int BAR = LD + 4 * RB * 8;
+    static constexpr int SMEM = BAR + 512 + 1024;
+    static constexpr int DV_ = 0, DK_ = D, S_ = 2 * D, P_ = 2 * D + RB, BUF = 2 * RB;
+};
+
+template <int D>
+__global__ void __launch_bounds__(320, 1)
+attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g, AttnBwdArgs b,
+                     const __grid_constant__ Seqs seqs, const float2* rows, int* status)
+{
+    using L = Keys<D>;
+    const AttnArgs& a = b.f;
+    extern __shared__ char raw[];
+    char* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t base = smem_addr(sm);
+    uint64_t* bars = (uint64_t*)(sm + L::BAR);
+    uint64_t *kvfull = bars, *full = kvfull + 1, *empty = full + L::STAGES, *sfull = empty + L::STAGES, *gfull = sfull + 2;
+    uint64_t *pready = gfull + 2, *dready = pready + 2, *done = dready + 2, *fix = done + 2, *all_done = fix + 1, *drain = all_done + 1;
+    uint32_t* tm_ptr = (uint32_t*)(drain + 1);
+    const Guard guard{(volatile int*)(tm_ptr + 1), status};
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hk = blockIdx.y, r = a.H / a.Hkv;
+    int seq, tile;
+    if (!seqs.locate(blockIdx.x, L::KEYS, seq, tile)) return;   // the first tiles have the most rows
+    const int64_t t0 = seqs.start(seq);
+    const int len = seqs.len(seq), key0 = tile * L::KEYS;
+    const int tq = L::RB / r;                                // tokens of a tile of rows
+    const int n = (len - key0 + tq - 1) / tq;
+    const int tail = (len - key0 - (n - 1) * tq) * r;        // rows of the last tile
+
+    if (warp == 8) {
+        if (lane == 0) {
+            mbar_init(kvfull, 1);
+            for (int i = 0; i < L::STAGES; ++i) {
+                mbar_init(full + i, 1);
+                mbar_init(empty + i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(sfull + i, 1);
+                mbar_init(gfull + i, 1);
+                mbar_init(pready + i, 128);
+                mbar_init(dready + i, 128);
+                mbar_init(done + i, 1);
+            }
+            mbar_init(fix, 32);
+            mbar_init(all_done, 1);
+            mbar_init(drain, 1);
+            *guard.flag = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(tm_ptr, 512);
+        tmem_relinquish();
+    }
+    if (tq * r < L::RB)
+        for (int e = tid; e < 2 * L::STAGES * (L::RB - tq * r) * (D / 8); e += 320) {
+            const int piece = e % (D / 8), row = tq * r + e / (D / 8) % (L::RB - tq * r), st = e / (D / 8) / (L::RB - tq * r);
+            *(uint4*)(sm + L::Q_ + st * L::RTILE + (piece >> 3) * L::RPANEL + piece_at(row, piece & 7)) = make_uint4(0, 0, 0, 0);
+        }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm_ptr;
+
+    if (warp == 9) {
+        const uint32_t bytes = (uint32_t)(tq * r * D * 2);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(kvfull, 2 * L::KTILE);
+            for (int p = 0; p < D / 64; ++p) {
+                tma_load_3d(sm + L::K_ + p * L::KPANEL, &tm_k, kvfull, p * 64, hk, (int)t0 + key0);
+                tma_load_3d(sm + L::V_ + p * L::KPANEL, &tm_v, kvfull, p * 64, hk, (int)t0 + key0);
+            }
+            int issued = 0;
+            for (int j = 0; j < n; ++j, ++issued) {
+                const int s = j % L::STAGES;
+                wait(empty + s, ((j / L::STAGES) & 1) ^ 1, guard);
+                if (guard.up()) break;
+                mbar_arrive_expect_tx(full + s, 2 * bytes);
+                for (int p = 0; p < D / 64; ++p) {
+                    tma_load_3d(sm + L::Q_ + s * L::RTILE + p * L::RPANEL, &tm_q, full + s, p * 64, hk * r, (int)t0 + key0 + j * tq);
+                    tma_load_3d(sm + L::G_ + s * L::RTILE + p * L::RPANEL, &tm_g, full + s, p * 64, hk * r, (int)t0 + key0 + j * tq);
+                }
+            }
+            if (guard.up()) {
+                mbar_wait_bounded(kvfull, 0, kWaitNs);
+                drain_ring(full, L::STAGES, issued);
+            }
+        }
+        __syncwarp();
+        // rows of the last tile past the end: their weights are 0, but 0 times a value that is not
+        // finite (the next sequence's) is not
+        if (tail < tq * r && !guard.up()) {
+            const int s = (n - 1) % L::STAGES;
+            wait(full + s, ((n - 1) / L::STAGES) & 1, guard);
+            for (int e = lane; e < 2 * (tq * r - tail) * (D / 8); e += 32) {
+                const int piece = e % (D / 8), row = tail + e / (D / 8) % (tq * r - tail), g = e / (D / 8) / (tq * r - tail);
+                *(uint4*)(sm + (g ? L::G_ : L::Q_) + s * L::RTILE + (piece >> 3) * L::RPANEL + piece_at(row, piece & 7)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            mbar_arrive(fix);
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            const uint32_t id_s = idesc_f16(L::KEYS, L::RB, false, false, a.scale < 0.f, true);
+            const uint32_t id_g = idesc_f16(L::KEYS, L::RB, false, false, false, true);
+            const uint32_t id_o = idesc_f16(L::KEYS, D, false, true, false, true);
+            auto scores = [&](int j) {
+                const int s = j % L::STAGES, w = j & 1;
+                wait(full + s, (j / L::STAGES) & 1, guard);
+                if (j == n - 1 && tail < tq * r) wait(fix, 0, guard);
+                if (guard.up()) return;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    umma_f16(tmem + L::S_ + w * L::BUF, desc_rows(base + L::K_ + (x >> 2) * L::KPANEL + (x & 3) * 32),
+                             desc_rows(base + L::Q_ + s * L::RTILE + (x >> 2) * L::RPANEL + (x & 3) * 32), id_s, x > 0);
+                umma_commit(sfull + w);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    umma_f16(tmem + L::P_ + w * L::BUF, desc_rows(base + L::V_ + (x >> 2) * L::KPANEL + (x & 3) * 32),
+                             desc_rows(base + L::G_ + s * L::RTILE + (x >> 2) * L::RPANEL + (x & 3) * 32), id_g, x > 0);
+                umma_commit(gfull + w);
+            };
+            wait(kvfull, 0, guard);
+            if (!guard.up()) scores(0);
+            if (n > 1 && !guard.up()) scores(1);
+            for (int j = 0; j < n && !guard.up(); ++j) {
+                const int s = j % L::STAGES, w = j & 1, u = (j >> 1) & 1;
+                wait(pready + w, u, guard);
+                if (guard.up()) break;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < L::RB / 16; ++x)
+                    umma_f16_ts(tmem + L::DV_, tmem + L::S_ + w * L::BUF + x * 8, desc_cols(base + L::G_ + s * L::RTILE + x * 2048, L::RPANEL),
+                                id_o, j > 0 || x > 0);
+                wait(dready + w, u, guard);
+                if (guard.up()) break;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < L::RB / 16; ++x)
+                    umma_f16_ts(tmem + L::DK_, tmem + L::P_ + w * L::BUF + x * 8, desc_cols(base + L::Q_ + s * L::RTILE + x * 2048, L::RPANEL),
+                                id_o, j > 0 || x > 0);
+                umma_commit(empty + s);
+                umma_commit(done + w);
+                if (j + 2 < n) {
+                    wait(done + w, u, guard);   // P and dS are in the places of S and dP
+                    if (guard.up()) break;
+                    scores(j + 2);
+                }
+            }
+            if (guard.up())
+                drain_mma(drain);
+            else
+                umma_commit(all_done);
+        }
+    } else {
+        const int w = warp >> 2, key = key0 + (tid & 127);
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t ts = tmem + L::S_ + w * L::BUF + lanes, tp = tmem + L::P_ + w * L::BUF + lanes;
+        const float sl = fabsf(a.scale) * kLog2e;
+        const float2* src = rows + ((int64_t)hk * seqs.tokens() + t0 + key0) * r;
+        float2* ld = (float2*)(sm + L::LD) + w * 2 * L::RB;
+        for (int j = w; j < n; j += 2) {
+            const int u = (j >> 1) & 1;
+            const int live = j == n - 1 ? tail : tq * r;   // rows of this tile
+            if ((tid & 127) < L::RB)
+                ld[u * L::RB + (tid & 127)] = (tid & 127) < live ? src[(int64_t)j * tq * r + (tid & 127)] : make_float2(0.f, 0.f);
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+            const float4* col = (const float4*)(ld + u * L::RB);   // two rows
+            // the first row (column) that sees this key
+            const int lo = (key - key0 - j * tq) * r;
+            wait(sfull + w, u, guard);
+            tc_fence_after();
+            float p[64];
+            tmem_ld64(ts, p);
+#pragma unroll
+            for (int x = 0; x < 64; x += 2) {
+                const float4 c = col[x / 2];
+                p[x] = ex2_approx(fmaf(p[x], sl, -c.x));
+                p[x + 1] = ex2_approx(fmaf(p[x + 1], sl, -c.z));
+            }
+            const bool edge = j * tq < L::KEYS || live < L::RB;   // warp-uniform
+            if (edge)
+#pragma unroll
+                for (int x = 0; x < 64; ++x)
+                    if (x < lo || x >= live) p[x] = 0.f;
+            uint32_t q[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) q[x] = pack_bf16(p[2 * x], p[2 * x + 1]);
+            tmem_st32u_nowait(ts, q);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(pready + w);
+            wait(gfull + w, u, guard);
+            tc_fence_after();
+#pragma unroll
+            for (int hlf = 0; hlf < 2; ++hlf) {
+                float g[32];
+                tmem_ld32(tp + hlf * 32, g);
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                    const float4 c = col[hlf * 16 + x / 2];
+                    g[x] = p[hlf * 32 + x] * (g[x] - c.y);
+                    g[x + 1] = p[hlf * 32 + x + 1] * (g[x + 1] - c.w);
+                }
+                if (edge)   // what a masked dP held may not be finite
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (hlf * 32 + x < lo || hlf * 32 + x >= live) g[x] = 0.f;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) q[hlf * 16 + x] = pack_bf16(g[2 * x], g[2 * x + 1]);
+            }
+            tmem_st32u_nowait(tp, q);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(dready + w);
+        }
+        wait(all_done, 0, guard);
+        tc_fence_after();
+        if (!warp_up(guard)) {
+            const bool real = key < len;
+            const int64_t off = real ? ((t0 + key) * a.Hkv + hk) * D : 0;
+            for (int x = 0; x < D; x += 32)
+                if (w == 0)
+                    store32(tmem + L::DV_ + lanes + x, 1.f, (__nv_bfloat16*)b.dv + off + x, real);
+                else
+                    store32(tmem + L::DK_ + lanes + x, a.scale, (__nv_bfloat16*)b.dk + off + x, real);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// ---- dq -------------------------------------------------------------------------------------
+// The forward's layout: two tiles of 128 rows in turn over blocks of 64 keys, S = Q K^T and
+// dP = dO V^T, then dQ += dS K.  Tensor memory: dQ0, dQ1 (D each), 2 x (S 64, dP 64).
+template <int D>
+struct Dq {
+    static constexpr int QR = 128, KB = 64;
+    static constexpr int QPANEL = QR * 128, QTILE = D / 64 * QPANEL;
+    static constexpr int KPANEL = KB * 128, KTILE = D / 64 * KPANEL;
+    static constexpr int STAGES = D == 64 ? 6 : 2;
+    static constexpr int Q_ = 0, G_ = Q_ + 2 * QTILE, K_ = G_ + 2 * QTILE, V_ = K_ + STAGES * KTILE;
+    static constexpr int BAR = V_ + STAGES * KTILE, SMEM = BAR + 512 + 1024;
+    static constexpr int DQ_ = 0, S_ = 2 * D, P_ = 2 * D + KB, BUF = 2 * KB;
+};
+
+template <int D>
+__global__ void __launch_bounds__(320, 1)
+attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnBwdArgs b,
+                     const __grid_constant__ Seqs seqs, const float2* rowdata, int* status)
+{
+    using L = Dq<D>;
+    const AttnArgs& a = b.f;
+    extern __shared__ char raw[];
+    char* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t base = smem_addr(sm);
+    uint64_t* bars = (uint64_t*)(sm + L::BAR);
+    uint64_t *full = bars, *empty = full + L::STAGES, *sfull = empty + L::STAGES, *gfull = sfull + 2, *dready = gfull + 2;
+    uint64_t *done = dready + 2, *fix = done + 2, *drain = fix + 1;
+    uint32_t* tm_ptr = (uint32_t*)(drain + 1);
+    const Guard guard{(volatile int*)(tm_ptr + 1), status};
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hk = blockIdx.y;
+    const Rows rows{a.H / a.Hkv};
+    int seq, tile;
+    if (!rows.locate(seqs, (int64_t)gridDim.x - 1 - blockIdx.x, 2 * L::QR, seq, tile)) return;
+    const int64_t t0 = seqs.start(seq);
+    const int len = seqs.len(seq);
+    const int64_t all = (int64_t)len * rows.r, first = (int64_t)tile * 2 * L::QR;
+    auto blocks = [&](int t) {
+        const int64_t r0 = first + t * L::QR;
+        return r0 >= all ? 0 : (int)(min(r0 + L::QR, all) - 1) / rows.r / L::KB + 1;
+    };
+    const int n0 = blocks(0), n1 = blocks(1), n = max(n0, n1);
+    const int tail = len - (n - 1) * L::KB;   // keys of the last block
+
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int i = 0; i < L::STAGES; ++i) {
+                mbar_init(full + i, 1);
+                mbar_init(empty + i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(sfull + i, 1);
+                mbar_init(gfull + i, 1);
+                mbar_init(dready + i, 128);
+                mbar_init(done + i, 1);
+            }
+            mbar_init(fix, 32);
+            mbar_init(drain, 1);
+            *guard.flag = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(tm_ptr, 512);
+        tmem_relinquish();
+    }
+    for (int e = tid; e < 2 * L::QR * (D / 8); e += 320) {
+        const int piece = e % (D / 8), row = e / (D / 8);
+        const int64_t i = first + row;
+        const bool in = i < all;
+        const int64_t off = in ? ((t0 + i / rows.r) * a.H + (int64_t)hk * rows.r + i % rows.r) * D + piece * 8 : 0;
+        const uint32_t at = (row / L::QR) * L::QTILE + (piece >> 3) * L::QPANEL + piece_at(row % L::QR, piece & 7);
+        cp16(base + L::Q_ + at, (const __nv_bfloat16*)a.q + off, in);
+        cp16(base + L::G_ + at, (const __nv_bfloat16*)b.dout + off, in);
+    }
+    cp_async_commit();
+    cp_async_wait_all();
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm_ptr;
+
+    if (warp == 9) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int j = 0; j < n; ++j, ++issued) {
+                const int s = j % L::STAGES;
+                wait(empty + s, ((j / L::STAGES) & 1) ^ 1, guard);
+                if (guard.up()) break;
+                mbar_arrive_expect_tx(full + s, 2 * L::KTILE);
+                for (int p = 0; p < D / 64; ++p) {
+                    tma_load_3d(sm + L::K_ + s * L::KTILE + p * L::KPANEL, &tm_k, full + s, p * 64, hk, (int)t0 + j * L::KB);
+                    tma_load_3d(sm + L::V_ + s * L::KTILE + p * L::KPANEL, &tm_v, full + s, p * 64, hk, (int)t0 + j * L::KB);
+                }
+            }
+            if (guard.up()) drain_ring(full, L::STAGES, issued);
+        }
+        __syncwarp();
+        if (tail < L::KB && !guard.up()) {   // keys past the end (dS is 0 there): K must be finite
+            const int s = (n - 1) % L::STAGES;
+            wait(full + s, ((n - 1) / L::STAGES) & 1, guard);
+            for (int e = lane; e < (L::KB - tail) * (D / 8); e += 32) {
+                const int row = tail + e / (D / 8), piece = e % (D / 8);
+                *(uint4*)(sm + L::K_ + s * L::KTILE + (piece >> 3) * L::KPANEL + piece_at(row, piece & 7)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            mbar_arrive(fix);
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            const uint32_t id_s = idesc_f16(L::QR, L::KB, false, false, a.scale < 0.f, true);
+            const uint32_t id_g = idesc_f16(L::QR, L::KB, false, false, false, true);
+            const uint32_t id_o = idesc_f16(L::QR, D, false, true, false, true);
+            auto scores = [&](int t, int j) {
+                const int s = j % L::STAGES;
+                wait(full + s, (j / L::STAGES) & 1, guard);
+                if (guard.up()) return;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    umma_f16(tmem + L::S_ + t * L::BUF, desc_rows(base + L::Q_ + t * L::QTILE + (x >> 2) * L::QPANEL + (x & 3) * 32),
+                             desc_rows(base + L::K_ + s * L::KTILE + (x >> 2) * L::KPANEL + (x & 3) * 32), id_s, x > 0);
+                umma_commit(sfull + t);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    umma_f16(tmem + L::P_ + t * L::BUF, desc_rows(base + L::G_ + t * L::QTILE + (x >> 2) * L::QPANEL + (x & 3) * 32),
+                             desc_rows(base + L::V_ + s * L::KTILE + (x >> 2) * L::KPANEL + (x & 3) * 32), id_g, x > 0);
+                umma_commit(gfull + t);
+            };
+            if (n0 > 0) scores(0, 0);
+            if (n1 > 0 && !guard.up()) scores(1, 0);
+            for (int j = 0; j < n && !guard.up(); ++j)
+                for (int t = 0; t < 2; ++t) {
+                    if (j >= (t ? n1 : n0)) continue;
+                    const int s = j % L::STAGES;
+                    wait(dready + t, j & 1, guard);
+                    if (j == n - 1 && tail < L::KB) wait(fix, 0, guard);
+                    if (guard.up()) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int x = 0; x < L::KB / 16; ++x)
+                        umma_f16_ts(tmem + L::DQ_ + t * D, tmem + L::P_ + t * L::BUF + x * 8,
+                                    desc_cols(base + L::K_ + s * L::KTILE + x * 2048, L::KPANEL), id_o, j > 0 || x > 0);
+                    if (t == 1 || n1 <= j) umma_commit(empty + s);
+                    umma_commit(done + t);
+                    if (j + 1 < (t ? n1 : n0)) {
+                        wait(done + t, j & 1, guard);   // dS is in dP's place
+                        if (guard.up()) break;
+                        scores(t, j + 1);
+                    }
+                }
+            if (guard.up()) drain_mma(drain);
+        }
+    } else {
+        const int t = warp >> 2, nt = t ? n1 : n0;
+        const int64_t i = first + t * L::QR + (tid & 127);
+        const bool real = i < all;
+        const int token = (int)(min(i, all - 1) / rows.r);
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
+        const uint32_t ts = tmem + L::S_ + t * L::BUF + lanes, tp = tmem + L::P_ + t * L::BUF + lanes;
+        const float sl = fabsf(a.scale) * kLog2e;
+        const int least = (int)(min(first + t * L::QR + (warp & 3) * 32, all - 1) / rows.r);
+        const float2 rd = real ? rowdata[((int64_t)hk * seqs.tokens() + t0) * rows.r + i] : make_float2(0.f, 0.f);
+        for (int j = 0; j < nt; ++j) {
+            wait(sfull + t, j & 1, guard);
+            tc_fence_after();
+            float p[64];
+            tmem_ld64(ts, p);
+#pragma unroll
+            for (int x = 0; x < 64; ++x) p[x] = ex2_approx(fmaf(p[x], sl, -rd.x));
+            wait(gfull + t, j & 1, guard);
+            tc_fence_after();
+            const bool edge = j * L::KB + L::KB - 1 > least;
+            const int seen = token - j * L::KB;
+            uint32_t q[32];
+#pragma unroll
+            for (int hlf = 0; hlf < 2; ++hlf) {
+                float g[32];
+                tmem_ld32(tp + hlf * 32, g);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) g[x] = p[hlf * 32 + x] * (g[x] - rd.y);
+                if (edge)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (hlf * 32 + x > seen) g[x] = 0.f;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) q[hlf * 16 + x] = pack_bf16(g[2 * x], g[2 * x + 1]);
+            }
+            tmem_st32u_nowait(tp, q);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(dready + t);
+        }
+        if (nt > 0) {
+            wait(done + t, (nt - 1) & 1, guard);
+            tc_fence_after();
+            if (!warp_up(guard)) {
+                const int64_t off = real ? ((t0 + token) * a.H + (int64_t)hk * rows.r + i % rows.r) * D : 0;
+                for (int x = 0; x < D; x += 32) store32(tmem + L::DQ_ + t * D + lanes + x, a.scale, (__nv_bfloat16*)b.dq + off + x, real);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float2* rows, int* status, cudaStream_t st)
+{
+    const AttnArgs& a = b.f;
+    const int64_t T = s.tokens();
+    const int r = a.H / a.Hkv;
+    CUtensorMap k128, v128, k64, v64, q, g;
+    if (!make_map(&k128, a.k, T, a.Hkv, D, 1, 128) || !make_map(&v128, a.v, T, a.Hkv, D, 1, 128) ||
+        !make_map(&k64, a.k, T, a.Hkv, D, 1, 64) || !make_map(&v64, a.v, T, a.Hkv, D, 1, 64) ||
+        !make_map(&q, a.q, T, a.H, D, r, 64 / r) || !make_map(&g, b.dout, T, a.H, D, r, 64 / r))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attn_bwd_keys_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Keys<D>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attn_bwd_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dq<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    {
+        ProfileScope prof("attn_delta", st);
+        count_launch();
+        attn_delta_kernel<D><<<(unsigned)((T * a.H + 7) / 8), 256, 0, st>>>(a, (const __nv_bfloat16*)b.dout, rows, T);
+    }
+    {
+        ProfileScope prof("attn_bwd_keys", st);
+        count_launch();
+        attn_bwd_keys_kernel<D><<<dim3(s.slots(128), a.Hkv), 320, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, rows, status);
+    }
+    {
+        ProfileScope prof("attn_bwd_rows", st);
+        count_launch();
+        attn_bwd_rows_kernel<D><<<dim3((unsigned)Rows{r}.slots(s, 256), a.Hkv), 320, Dq<D>::SMEM, st>>>(k64, v64, b, s, rows, status);
+    }
+    return cudaGetLastError();
+}
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+}  // namespace
+}  // namespace attn
+
+// A group of more than 64 query heads does not fit the tile of rows of the dk/dv kernel.
+bool attn_tc_bwd_supported(const AttnBwdArgs& b)
+{
+    return attn_tc_supported(b.f) && b.f.H / b.f.Hkv <= 64 && attn::aligned16(b.dout) && attn::aligned16(b.dq) &&
+           attn::aligned16(b.dk) && attn::aligned16(b.dv);
+}
+
+size_t attn_tc_bwd_workspace(int64_t tokens, int H) { return (size_t)tokens * H * sizeof(float2); }
+
+cudaError_t launch_attn_tc_bwd(const AttnBwdArgs& b, const Seqs& s, void* ws, int* status, cudaStream_t st)
+{
+    return b.f.D == 64 ? attn::backward<64>(b, s, (float2*)ws, status, st) : attn::backward<128>(b, s, (float2*)ws, status, st);
+}
+
+}  // namespace kda

@@ -27,7 +27,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int rows)
+bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int r, int rows)
 {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
@@ -41,7 +41,7 @@ bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
-    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)rows}, es[3] = {1u, 1u, 1u};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)r, (cuuint32_t)rows}, es[3] = {1u, 1u, 1u};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -136,7 +136,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
     if (warp == 9) {
         if (lane == 0) {
-            for (int j = 0; j < n && !guard.up(); ++j) {
+            int k_issued = 0, v_issued = 0;
+            for (int j = 0; j < n; ++j) {
                 const int s = j % L::STAGES, u = j / L::STAGES;
                 const int y = (int)t0 + j * KB;
                 wait(kempty + s, (u & 1) ^ 1, guard);
@@ -144,14 +145,17 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 mbar_arrive_expect_tx(kfull + s, L::TILE);
                 for (int p = 0; p < D / 64; ++p)
                     tma_load_3d(sm + L::K_ + s * L::TILE + p * L::PANEL, &tm_k, kfull + s, p * 64, hk, y);
+                ++k_issued;
                 wait(vempty + s, (u & 1) ^ 1, guard);
-                if (guard.up()) {   // this block's K has no V: let it land before leaving
-                    mbar_wait_bounded(kfull + s, u & 1, kWaitNs);
-                    break;
-                }
+                if (guard.up()) break;
                 mbar_arrive_expect_tx(vfull + s, L::TILE);
                 for (int p = 0; p < D / 64; ++p)
                     tma_load_3d(sm + L::V_ + s * L::TILE + p * L::PANEL, &tm_v, vfull + s, p * 64, hk, y);
+                ++v_issued;
+            }
+            if (guard.up()) {
+                drain_ring(kfull, L::STAGES, k_issued);
+                drain_ring(vfull, L::STAGES, v_issued);
             }
         }
         __syncwarp();
@@ -231,7 +235,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // the warp's first row sees the fewest keys
         const int least = (int)(min(first + t * QR + (warp & 3) * 32, all - 1) / rows.r);
         float ref = 0.f, sum = 0.f;
-        for (int j = 0; j < nt && !guard.up(); ++j) {
+        for (int j = 0; j < nt; ++j) {
             wait(sfull + t, j & 1, guard);
             tc_fence_after();
             float s[128];
@@ -296,7 +300,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (nt > 0) {
             wait(pvdone + t, (nt - 1) & 1, guard);
             tc_fence_after();
-            if (!guard.up()) {
+            if (!warp_up(guard)) {
                 const int64_t row = real ? (t0 + token) * a.H + (int64_t)hk * rows.r + i % rows.r : 0;
                 const float inv = 1.f / sum;
                 __nv_bfloat16* o = (__nv_bfloat16*)a.o + row * D;
@@ -325,7 +329,7 @@ cudaError_t forward(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t 
 {
     using L = Fwd<D>;
     CUtensorMap k, v;
-    if (!make_map(&k, a.k, s.tokens(), a.Hkv, D, KB) || !make_map(&v, a.v, s.tokens(), a.Hkv, D, KB))
+    if (!make_map(&k, a.k, s.tokens(), a.Hkv, D, 1, KB) || !make_map(&v, a.v, s.tokens(), a.Hkv, D, 1, KB))
         return cudaErrorInvalidValue;
     auto kern = attn_fwd_kernel<D>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);

@@ -17,13 +17,14 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---- waits ------------------------------------------------------------------------------
 // The first wait that runs out raises the CTA's flag and records DEV_TIMEOUT; from then on no
-// wait waits, no MMA or copy is issued, and every role runs to its end.
+// wait waits, no MMA or copy is issued, and every role runs to its end.  Warps that use warp-wide
+// instructions or barriers keep their loops whole: the flag is seen by lanes at different times.
 struct Guard {
     volatile int* flag;
     int* status;
     __device__ __forceinline__ bool up() const { return *flag != 0; }
 };
-__device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, Guard g)
+static __device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, Guard g)
 {
     const uint64_t t0 = globaltimer_ns();
     while (!g.up()) {
@@ -37,6 +38,16 @@ __device__ __noinline__ void wait_slow(uint64_t* bar, uint32_t parity, Guard g)
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, const Guard& g)
 {
     if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity, g);
+}
+
+// Whole-warp form for code with warp-wide instructions: the same answer in every lane.
+__device__ __forceinline__ bool warp_up(const Guard& g) { return __any_sync(~0u, g.up()); }
+// After a timeout: the copies issued into a ring (the last STAGES of `issued`) land before the
+// CTA leaves.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int issued)
+{
+    for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
+        mbar_wait_bounded(full + j % stages, (j / stages) & 1, kWaitNs);
 }
 
 // ---- tiles ------------------------------------------------------------------------------
@@ -68,8 +79,8 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
-// [tokens, heads, D] bf16, box = `rows` tokens x 1 head x 64 values, landing as a panel
-bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int rows);
+// [tokens, heads, D] bf16, box = `rows` tokens x r heads x 64 values, landing as a panel
+bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int r, int rows);
 
 // ---- rows of a key/value head's query group -----------------------------------------------
 // The query heads that share a key/value head are rows of one matrix: row i is token i / r, head

@@ -102,6 +102,9 @@ struct AttnBwdArgs {
 bool attn_tc_supported(const AttnArgs& a);
 cudaError_t launch_attn_tc(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t st);
 cudaError_t launch_attn_generic(const AttnArgs& a, const Seqs& s, cudaStream_t st);
+bool attn_tc_bwd_supported(const AttnBwdArgs& b);
+size_t attn_tc_bwd_workspace(int64_t tokens, int H);
+cudaError_t launch_attn_tc_bwd(const AttnBwdArgs& b, const Seqs& s, void* ws, int* status, cudaStream_t st);
 cudaError_t launch_attn_generic_bwd(const AttnBwdArgs& a, const Seqs& s, cudaStream_t st);
 
 }  // namespace kda

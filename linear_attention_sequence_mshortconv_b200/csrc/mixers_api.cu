@@ -248,6 +248,11 @@ kda_status attn_forward_any(AttnArgs a, const Batch& b, bool packed, kda_dtype d
     });
 }
 
+size_t attn_bwd_need(int64_t tokens, int H, int D, kda_dtype dtype)
+{
+    return dtype == KDA_BF16 && D != 32 ? attn_tc_bwd_workspace(tokens, H) : 0;
+}
+
 kda_status attn_backward_any(AttnBwdArgs a, const Batch& b, bool packed, kda_dtype dtype, void* workspace,
                              size_t workspace_bytes, kda_stream_t stream)
 {
@@ -258,8 +263,12 @@ kda_status attn_backward_any(AttnBwdArgs a, const Batch& b, bool packed, kda_dty
     if (!a.f.q || !a.f.k || !a.f.v || !a.f.o || !a.f.lse || !a.dout || !a.dq || !a.dk || !a.dv)
         return KDA_ERR_INVALID_ARG;
     a.f.t = et_of(dtype);
-    (void)workspace;
-    (void)workspace_bytes;
+    Scratch ws;
+    st = ws.acquire(workspace, workspace_bytes, attn_bwd_need(b.tokens(), a.f.H, a.f.D, dtype), (cudaStream_t)stream);
+    if (st != KDA_OK) return st;
+    const bool tc = attn_tc_bwd_supported(a);
+    int* status = tc ? device_status_ptr() : nullptr;
+    if (tc && !status) return KDA_ERR_CUDA;
     return each_group(b, [&](const Seqs& s, int, int64_t token) {
         if (s.tokens() == 0) return KDA_OK;
         AttnBwdArgs x = a;
@@ -268,7 +277,8 @@ kda_status attn_backward_any(AttnBwdArgs a, const Batch& b, bool packed, kda_dty
         x.dq = at(a.dq, token * a.f.H * a.f.D, a.f.t);
         x.dk = at(a.dk, token * a.f.Hkv * a.f.D, a.f.t);
         x.dv = at(a.dv, token * a.f.Hkv * a.f.D, a.f.t);
-        return from_cuda(launch_attn_generic_bwd(x, s, (cudaStream_t)stream));
+        return from_cuda(tc ? launch_attn_tc_bwd(x, s, ws.ptr, status, (cudaStream_t)stream)
+                            : launch_attn_generic_bwd(x, s, (cudaStream_t)stream));
     });
 }
 
@@ -379,7 +389,8 @@ kda_status attn_forward_varlen(const void* q, const void* k, const void* v, void
 
 size_t attn_backward_workspace_size(int64_t tokens, int H, int Hkv, int D, kda_dtype dtype)
 {
-    return 0;
+    if (tokens < 0 || check_attn(H, Hkv, D, 1.f, dtype) != KDA_OK) return 0;
+    return attn_bwd_need(tokens, H, D, dtype);
 }
 
 kda_status attn_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
