@@ -8,10 +8,10 @@
 // token) as two tiles of 128 rows:
 //   warps 0-3 and 4-7: the softmax of tile 0 and 1, one row to a thread, so maxima and sums need
 //                      no exchange;
-//   warp 8: issues the MMAs, S = Q K^T and O += P V (P from tensor memory, where it takes the
-//           place of S), of the two tiles in turn: the tensor cores work on one tile while the
-//           other's softmax runs;
-//   warp 9: TMA loads of K and V into rings.
+//   warps 8 and 9:     issue the MMAs of tile 0 and 1, S = Q K^T and O += P V (P from tensor
+//                      memory, where it takes the place of S): the tensor cores work on one tile
+//                      while the other's softmax runs, in whichever order they get ready;
+//   warp 10:           TMA loads of K and V into rings.
 // Tensor memory (512 columns): S0, S1 (128 each), O0, O1 (D each).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the reference of
@@ -59,13 +59,26 @@ struct Fwd {
     static constexpr int STAGES = D == 64 ? 4 : 2;          // K and V tiles in flight, each
     static constexpr int Q_ = 0, K_ = Q_ + 2 * TILE, V_ = K_ + STAGES * TILE, BAR = V_ + STAGES * TILE;
     static constexpr int SMEM = BAR + 512 + 1024;           // the base is aligned up to 1024 bytes
-    static constexpr int THREADS = 320;
+    static constexpr int THREADS = 384;
     // tensor memory columns
     static constexpr int S_ = 0, O_ = 2 * KB;
 };
 
+__device__ __forceinline__ float max_of(const float (&s)[64])
+{
+    float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+    for (int x = 4; x < 60; x += 8) {
+        m0 = max3(m0, s[x], s[x + 1]);
+        m1 = max3(m1, s[x + 2], s[x + 3]);
+        m2 = max3(m2, s[x + 4], s[x + 5]);
+        m3 = max3(m3, s[x + 6], s[x + 7]);
+    }
+    return max3(max3(m0, s[60], s[61]), max3(m1, s[62], s[63]), fmaxf(m2, m3));
+}
+
 template <int D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(384, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnArgs a,
                 const __grid_constant__ Seqs seqs, int* status)
 {
@@ -76,7 +89,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
     uint64_t *kfull = bars, *kempty = kfull + L::STAGES, *vfull = kempty + L::STAGES, *vempty = vfull + L::STAGES;
     uint64_t *sfull = vempty + L::STAGES, *pready = sfull + 2, *pvdone = pready + 4, *vfix = pvdone + 2, *drain = vfix + 1;
-    uint32_t* tm_ptr = (uint32_t*)(drain + 1);
+    uint32_t* tm_ptr = (uint32_t*)(drain + 2);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -98,9 +111,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (lane == 0) {
             for (int i = 0; i < L::STAGES; ++i) {
                 mbar_init(kfull + i, 1);
-                mbar_init(kempty + i, 1);
+                mbar_init(kempty + i, 2);
                 mbar_init(vfull + i, 1);
-                mbar_init(vempty + i, 1);
+                mbar_init(vempty + i, 2);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(sfull + i, 1);
@@ -110,6 +123,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             mbar_init(vfix, 32);
             mbar_init(drain, 1);
+            mbar_init(drain + 1, 1);
             *guard.flag = 0;
             fence_mbar_init();
         }
@@ -134,8 +148,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tm_ptr;
 
-    if (warp == 9) {
-        if (lane == 0) {
+    if (warp >= 10) {
+        if (warp == 10 && lane == 0) {
             int k_issued = 0, v_issued = 0;
             for (int j = 0; j < n; ++j) {
                 const int s = j % L::STAGES, u = j / L::STAGES;
@@ -162,7 +176,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // The last block's rows past the end hold the next sequence, or nothing: their weights are
         // 0, but 0 times a value that is not finite is not.  The whole warp clears them.
         const int tail = len - (n - 1) * KB;
-        if (tail < KB && !guard.up()) {
+        if (warp == 10 && tail < KB && !guard.up()) {
             const int s = (n - 1) % L::STAGES;
             wait(vfull + s, ((n - 1) / L::STAGES) & 1, guard);
             for (int e = lane; e < (KB - tail) * (D / 8); e += 32) {
@@ -172,11 +186,12 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             fence_async_smem();
             mbar_arrive(vfix);
         }
-    } else if (warp == 8) {
+    } else if (warp >= 8) {
         if (lane == 0) {
+            const int t = warp - 8, nt = t ? n1 : n0;
             const uint32_t id_s = idesc_f16(QR, KB, false, false, a.scale < 0.f, true);
             const uint32_t id_o = idesc_f16(QR, D, false, true, false, true);
-            auto scores = [&](int t, int j) {
+            auto scores = [&](int j) {
                 const int s = j % L::STAGES;
                 wait(kfull + s, (j / L::STAGES) & 1, guard);
                 if (guard.up()) return;
@@ -188,39 +203,44 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                              desc_rows(base + L::K_ + s * L::TILE + off), id_s, x > 0);
                 }
                 umma_commit(sfull + t);
-                if (t == 1 || n1 <= j) umma_commit(kempty + s);
+                umma_commit(kempty + s);
             };
-            // tile 1 sees every block tile 0 does, unless it has no rows
-            if (n0 > 0) scores(0, 0);
-            if (n1 > 0) scores(1, 0);
-            for (int j = 0; j < n && !guard.up(); ++j)
-                for (int t = 0; t < 2; ++t) {
-                    if (j >= (t ? n1 : n0)) continue;
-                    const int s = j % L::STAGES;
-                    wait(vfull + s, (j / L::STAGES) & 1, guard);
-                    if (j == n - 1 && len - j * KB < KB) wait(vfix, 0, guard);
+            if (nt > 0) scores(0);
+            for (int j = 0; j < nt && !guard.up(); ++j) {
+                const int s = j % L::STAGES;
+                wait(vfull + s, (j / L::STAGES) & 1, guard);
+                if (j == n - 1 && len - j * KB < KB) wait(vfix, 0, guard);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        wait(pready + 2 * t + half, j & 1, guard);
-                        if (guard.up()) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int x = half * 4; x < half * 4 + 4; ++x)
-                            umma_f16_ts(tmem + L::O_ + t * D, tmem + L::S_ + t * KB + x * 8,
-                                        desc_cols(base + L::V_ + s * L::TILE + x * 2048, L::PANEL), id_o, j > 0 || x > 0);
-                    }
+                for (int half = 0; half < 2; ++half) {
+                    wait(pready + 2 * t + half, j & 1, guard);
                     if (guard.up()) break;
-                    if (t == 1 || n1 <= j) umma_commit(vempty + s);
-                    umma_commit(pvdone + t);
-                    if (j + 1 < (t ? n1 : n0)) {
-                        wait(pvdone + t, j & 1, guard);   // P is in S's place: it must have been read
-                        if (guard.up()) break;
-                        scores(t, j + 1);
-                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int x = half * 4; x < half * 4 + 4; ++x)
+                        umma_f16_ts(tmem + L::O_ + t * D, tmem + L::S_ + t * KB + x * 8,
+                                    desc_cols(base + L::V_ + s * L::TILE + x * 2048, L::PANEL), id_o, j > 0 || x > 0);
                 }
+                if (guard.up()) break;
+                umma_commit(vempty + s);
+                umma_commit(pvdone + t);
+                if (j + 1 < nt) {
+                    wait(pvdone + t, j & 1, guard);   // P is in S's place: it must have been read
+                    if (guard.up()) break;
+                    scores(j + 1);
+                }
+            }
+            // blocks that only the other tile sees: this one is done with them, once the stage's
+            // use before has ended (an arrival counts for the phase that is open)
+            for (int j = nt; j < n && !guard.up(); ++j) {
+                const int s = j % L::STAGES, u = j / L::STAGES;
+                wait(kempty + s, (u & 1) ^ 1, guard);
+                mbar_arrive(kempty + s);
+                wait(vempty + s, (u & 1) ^ 1, guard);
+                mbar_arrive(vempty + s);
+            }
             if (guard.up()) {   // leave nothing in flight
-                umma_commit(drain);
-                mbar_wait_bounded(drain, 0, kWaitNs);
+                umma_commit(drain + t);
+                mbar_wait_bounded(drain + t, 0, kWaitNs);
             }
         }
     } else {
@@ -238,27 +258,22 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int j = 0; j < nt; ++j) {
             wait(sfull + t, j & 1, guard);
             tc_fence_after();
-            float s[128];
-            {
-                float (&lo)[64] = *(float (*)[64])s, (&hi)[64] = *(float (*)[64])(s + 64);
-                tmem_ld64(ts, lo);
-                tmem_ld64(ts + 64, hi);
-            }
-            if (j * KB + KB - 1 > least) {
-                const int seen = token - j * KB;   // keys 0 .. seen of the block
+            const bool edge = j * KB + KB - 1 > least;
+            const int seen = token - j * KB;   // keys 0 .. seen of the block
+            // half the block at a time: the second half is read again after the maximum is known,
+            // which costs less than holding 128 scores
+            auto load = [&](int half, float (&s)[64]) {
+                tmem_ld64(ts + half * 64, s);
+                if (edge)
 #pragma unroll
-                for (int x = 0; x < 128; ++x)
-                    if (x > seen) s[x] = -INFINITY;
-            }
-            float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
-#pragma unroll
-            for (int x = 4; x < 128; x += 4) {
-                m0 = fmaxf(m0, s[x]);
-                m1 = fmaxf(m1, s[x + 1]);
-                m2 = fmaxf(m2, s[x + 2]);
-                m3 = fmaxf(m3, s[x + 3]);
-            }
-            const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                    for (int x = 0; x < 64; ++x)
+                        if (half * 64 + x > seen) s[x] = -INFINITY;
+            };
+            float s[64], top;
+            load(1, s);
+            top = max_of(s);
+            load(0, s);
+            top = fmaxf(top, max_of(s));
             if (j == 0) {
                 ref = top;
             } else if (__any_sync(~0u, (top - ref) * sl > 8.f)) {
@@ -277,17 +292,19 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     tmem_st32(to + x, o);
                 }
             }
-            const float off = -ref * sl;
-            float z0 = 0.f, z1 = 0.f;
+            const uint64_t sl2 = pair(sl, sl), off2 = pair(-ref * sl, -ref * sl);
+            uint64_t z = 0, y = 0;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+                if (half) load(1, s);
                 uint32_t p[32];
 #pragma unroll
                 for (int x = 0; x < 32; ++x) {
-                    const float e0 = ex2_approx(fmaf(s[half * 64 + 2 * x], sl, off));
-                    const float e1 = ex2_approx(fmaf(s[half * 64 + 2 * x + 1], sl, off));
-                    z0 += e0;
-                    z1 += e1;
+                    float e0, e1;
+                    unpair(fma2(pair(s[2 * x], s[2 * x + 1]), sl2, off2), e0, e1);
+                    e0 = ex2_approx(e0);
+                    e1 = ex2_approx(e1);
+                    if (x & 1) y = add2(y, pair(e0, e1)); else z = add2(z, pair(e0, e1));
                     p[x] = pack_bf16(e0, e1);
                 }
                 tmem_st32u_nowait(ts + half * 32, p);
@@ -295,6 +312,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 tc_fence_before();
                 mbar_arrive(pready + 2 * t + half);
             }
+            float z0, z1;
+            unpair(add2(z, y), z0, z1);
             sum += z0 + z1;
         }
         if (nt > 0) {
