@@ -88,8 +88,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const uint32_t base = smem_addr(sm);
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
     uint64_t *kfull = bars, *kempty = kfull + L::STAGES, *vfull = kempty + L::STAGES, *vempty = vfull + L::STAGES;
-    uint64_t *sfull = vempty + L::STAGES, *pready = sfull + 2, *pvdone = pready + 4, *vfix = pvdone + 2, *drain = vfix + 1;
-    uint32_t* tm_ptr = (uint32_t*)(drain + 2);
+    uint64_t *sfull = vempty + L::STAGES, *pready = sfull + 2, *pvdone = pready + 4, *vfix = pvdone + 2, *drain = vfix + 1, *turn = drain + 2;
+    uint32_t* tm_ptr = (uint32_t*)(turn + 2);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -120,6 +120,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 mbar_init(pready + 2 * i, QR);
                 mbar_init(pready + 2 * i + 1, QR);
                 mbar_init(pvdone + i, 1);
+                mbar_init(turn + i, QR);
             }
             mbar_init(vfix, 32);
             mbar_init(drain, 1);
@@ -292,6 +293,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     tmem_st32(to + x, o);
                 }
             }
+            // The exponentials of the two tiles take turns: side by side they would share one unit,
+            // and then both tiles would wait for the tensor cores at the same time.
+            if (t ? j < n0 : j > 0 && n1 > 0) wait(turn + t, (t ? j : j - 1) & 1, guard);
             const uint64_t sl2 = pair(sl, sl), off2 = pair(-ref * sl, -ref * sl);
             uint64_t z = 0, y = 0;
 #pragma unroll
@@ -312,6 +316,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 tc_fence_before();
                 mbar_arrive(pready + 2 * t + half);
             }
+            mbar_arrive(turn + 1 - t);
             float z0, z1;
             unpair(add2(z, y), z0, z1);
             sum += z0 + z1;
