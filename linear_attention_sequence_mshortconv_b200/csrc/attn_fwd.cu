@@ -92,7 +92,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     uint32_t* tm_ptr = (uint32_t*)(turn + 2);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
     const int hk = blockIdx.y;
     const Rows rows{a.H / a.Hkv};
     int seq, tile;
@@ -188,48 +188,51 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             mbar_arrive(vfix);
         }
     } else if (warp >= 8) {
-        if (lane == 0) {
-            const int t = warp - 8, nt = t ? n1 : n0;
-            const uint32_t id_s = idesc_f16(QR, KB, false, false, a.scale < 0.f, true);
-            const uint32_t id_o = idesc_f16(QR, D, false, true, false, true);
-            auto scores = [&](int j) {
-                const int s = j % L::STAGES;
-                wait(kfull + s, (j / L::STAGES) & 1, guard);
-                if (guard.up()) return;
-                tc_fence_after();
+        const int t = warp - 8, nt = t ? n1 : n0;
+        const uint32_t id_s = idesc_f16(QR, KB, false, false, a.scale < 0.f, true);
+        const uint32_t id_o = idesc_f16(QR, D, false, true, false, true);
+        const uint32_t ts = tmem + L::S_ + t * KB, to = tmem + L::O_ + t * D;
+        const uint64_t dq = desc_rows(base + L::Q_ + t * L::TILE), dk = desc_rows(base + L::K_), dv = desc_cols(base + L::V_, L::PANEL);
+        auto scores = [&](int j) {
+            const int s = j % L::STAGES;
+            wait(kfull + s, (j / L::STAGES) & 1, guard);
+            tc_fence_after();
+            if (elect()) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t off = (x >> 2) * L::PANEL + (x & 3) * 32;
-                    umma_f16(tmem + L::S_ + t * KB, desc_rows(base + L::Q_ + t * L::TILE + off),
-                             desc_rows(base + L::K_ + s * L::TILE + off), id_s, x > 0);
-                }
+                for (int x = 0; x < D / 16; ++x)
+                    umma_f16(ts, step_rows(dq, x, L::PANEL), step_rows(dk + (s * L::TILE >> 4), x, L::PANEL), id_s, x > 0);
                 umma_commit(sfull + t);
                 umma_commit(kempty + s);
-            };
-            if (nt > 0) scores(0);
-            for (int j = 0; j < nt && !guard.up(); ++j) {
-                const int s = j % L::STAGES;
-                wait(vfull + s, (j / L::STAGES) & 1, guard);
-                if (j == n - 1 && len - j * KB < KB) wait(vfix, 0, guard);
+            }
+        };
+        if (nt > 0) scores(0);
+        for (int j = 0; j < nt; ++j) {
+            const int s = j % L::STAGES;
+            wait(vfull + s, (j / L::STAGES) & 1, guard);
+            if (j == n - 1 && len - j * KB < KB) wait(vfix, 0, guard);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    wait(pready + 2 * t + half, j & 1, guard);
-                    if (guard.up()) break;
-                    tc_fence_after();
+            for (int half = 0; half < 2; ++half) {
+                wait(pready + 2 * t + half, j & 1, guard);
+                tc_fence_after();
+                if (warp_up(guard)) break;
+                if (elect()) {
 #pragma unroll
                     for (int x = half * 4; x < half * 4 + 4; ++x)
-                        umma_f16_ts(tmem + L::O_ + t * D, tmem + L::S_ + t * KB + x * 8,
-                                    desc_cols(base + L::V_ + s * L::TILE + x * 2048, L::PANEL), id_o, j > 0 || x > 0);
-                }
-                if (guard.up()) break;
-                umma_commit(vempty + s);
-                umma_commit(pvdone + t);
-                if (j + 1 < nt) {
-                    wait(pvdone + t, j & 1, guard);   // P is in S's place: it must have been read
-                    if (guard.up()) break;
-                    scores(j + 1);
+                        umma_f16_ts(to, ts + x * 8, step_cols(dv + (s * L::TILE >> 4), x), id_o, j > 0 || x > 0);
+                    if (half) {
+                        umma_commit(vempty + s);
+                        umma_commit(pvdone + t);
+                    }
                 }
             }
+            if (warp_up(guard)) break;
+            if (j + 1 < nt) {
+                wait(pvdone + t, j & 1, guard);   // P is in S's place: it must have been read
+                if (warp_up(guard)) break;
+                scores(j + 1);
+            }
+        }
+        if (lane == 0) {
             // blocks that only the other tile sees: this one is done with them, once the stage's
             // use before has ended (an arrival counts for the phase that is open)
             for (int j = nt; j < n && !guard.up(); ++j) {
@@ -239,10 +242,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 wait(vempty + s, (u & 1) ^ 1, guard);
                 mbar_arrive(vempty + s);
             }
-            if (guard.up()) {   // leave nothing in flight
-                umma_commit(drain + t);
-                mbar_wait_bounded(drain + t, 0, kWaitNs);
-            }
+        }
+        if (warp_up(guard)) {   // leave nothing in flight
+            if (elect()) umma_commit(drain + t);
+            mbar_wait_bounded(drain + t, 0, kWaitNs);
         }
     } else {
         const int t = warp >> 2, nt = t ? n1 : n0;

@@ -68,6 +68,23 @@ __device__ __forceinline__ uint64_t desc_cols(uint32_t addr, uint32_t panel)
     return sdesc(addr, panel, 1024) | (2ull << 61);
 }
 
+// One lane of a converged warp, the same each time.  The issuing warps run their loops whole and
+// let one lane issue: the descriptors then stay in uniform registers, where an MMA takes them
+// from (inside a one-lane branch each would be moved there first, about 100 cycles an MMA).
+__device__ __forceinline__ bool elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0); }
+// K-step x (16 values) of an operand whose values are K, and of one whose rows are K
+__device__ __forceinline__ uint64_t step_rows(uint64_t desc, int x, uint32_t panel)
+{
+    return desc + (((x >> 2) * panel + (x & 3) * 32) >> 4);
+}
+__device__ __forceinline__ uint64_t step_cols(uint64_t desc, int x) { return desc + ((x * 2048) >> 4); }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
