@@ -1,7 +1,7 @@
 // Causal attention with grouped heads on tcgen05 tensor cores (bf16, head width 64 or 128).
 //
 //   s_ij = scale q_i.k_j,  m_i = max_j s_ij,  p_ij = e^{s_ij - m_i},  o_i = sum_j p_ij v_j / sum_j p_ij,
-// over the keys in blocks of 128 from the first, with a running m and sum.
+// over the keys in blocks of 64 from the first, with a running m and sum.
 //
 // A CTA owns 256 rows of one key/value head's query group (row = token x query head of the
 // group, so the group shares every K and V tile, and a tile's keys end soon after its first
@@ -9,10 +9,13 @@
 //   warps 0-3 and 4-7: the softmax of tile 0 and 1, one row to a thread, so maxima and sums need
 //                      no exchange;
 //   warps 8 and 9:     issue the MMAs of tile 0 and 1, S = Q K^T and O += P V (P from tensor
-//                      memory, where it takes the place of S): the tensor cores work on one tile
-//                      while the other's softmax runs, in whichever order they get ready;
+//                      memory, where it takes the place of S);
 //   warp 10:           TMA loads of K and V into rings.
-// Tensor memory (512 columns): S0, S1 (128 each), O0, O1 (D each).
+// Each tile has two buffers of scores: while one block's softmax runs, P V of the block before
+// and the scores of the block after are computed, so neither waits for the other.  With blocks
+// of 128 keys there is room for one buffer a tile only; the chain S -> softmax -> P V -> S then
+// left the tensor cores idle half of the time (16384 tokens, 16 heads, width 128: 0.93 ms).
+// Tensor memory (512 columns): 2 x 2 x S (64 each), O0, O1 (D each).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the reference of
 // its exponents was set (sums and weights then stay below 2^8 times their size, far from
@@ -50,18 +53,18 @@ bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D
 namespace {
 
 constexpr int QR = 128;   // rows of a tile
-constexpr int KB = 128;   // keys of a block
+constexpr int KB = 64;    // keys of a block
 
 template <int D>
 struct Fwd {
-    static constexpr int PANEL = 128 * 128;                 // bytes of 128 rows x 64 values
-    static constexpr int TILE = D / 64 * PANEL;
-    static constexpr int STAGES = D == 64 ? 4 : 2;          // K and V tiles in flight, each
-    static constexpr int Q_ = 0, K_ = Q_ + 2 * TILE, V_ = K_ + STAGES * TILE, BAR = V_ + STAGES * TILE;
+    static constexpr int QPANEL = QR * 128, QTILE = D / 64 * QPANEL;   // bytes of 128 rows x 64 values, of a tile
+    static constexpr int PANEL = KB * 128, TILE = D / 64 * PANEL;
+    static constexpr int STAGES = D == 64 ? 6 : 4;          // K and V tiles in flight, each
+    static constexpr int Q_ = 0, K_ = Q_ + 2 * QTILE, V_ = K_ + STAGES * TILE, BAR = V_ + STAGES * TILE;
     static constexpr int SMEM = BAR + 512 + 1024;           // the base is aligned up to 1024 bytes
     static constexpr int THREADS = 384;
     // tensor memory columns
-    static constexpr int S_ = 0, O_ = 2 * KB;
+    static constexpr int S_ = 0, O_ = 4 * KB;
 };
 
 __device__ __forceinline__ float max_of(const float (&s)[64])
@@ -88,8 +91,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const uint32_t base = smem_addr(sm);
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
     uint64_t *kfull = bars, *kempty = kfull + L::STAGES, *vfull = kempty + L::STAGES, *vempty = vfull + L::STAGES;
-    uint64_t *sfull = vempty + L::STAGES, *pready = sfull + 2, *pvdone = pready + 4, *vfix = pvdone + 2, *drain = vfix + 1, *turn = drain + 2;
-    uint32_t* tm_ptr = (uint32_t*)(turn + 2);
+    uint64_t *sfull = vempty + L::STAGES, *pready = sfull + 4, *pvdone = pready + 4, *vfix = pvdone + 4, *drain = vfix + 1;
+    uint32_t* tm_ptr = (uint32_t*)(drain + 2);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
@@ -115,12 +118,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 mbar_init(vfull + i, 1);
                 mbar_init(vempty + i, 2);
             }
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {   // 2 x tile + buffer
                 mbar_init(sfull + i, 1);
-                mbar_init(pready + 2 * i, QR);
-                mbar_init(pready + 2 * i + 1, QR);
+                mbar_init(pready + i, QR);
                 mbar_init(pvdone + i, 1);
-                mbar_init(turn + i, QR);
             }
             mbar_init(vfix, 32);
             mbar_init(drain, 1);
@@ -138,7 +139,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int64_t i = first + row;
         const bool in = i < all;
         const int64_t off = in ? ((t0 + i / rows.r) * a.H + (int64_t)hk * rows.r + i % rows.r) * D + piece * 8 : 0;
-        cp16(base + L::Q_ + (row / QR) * L::TILE + (piece >> 3) * L::PANEL + piece_at(row % QR, piece & 7),
+        cp16(base + L::Q_ + (row / QR) * L::QTILE + (piece >> 3) * L::QPANEL + piece_at(row % QR, piece & 7),
              (const __nv_bfloat16*)a.q + off, in);
     }
     cp_async_commit();
@@ -191,8 +192,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int t = warp - 8, nt = t ? n1 : n0;
         const uint32_t id_s = idesc_f16(QR, KB, false, false, a.scale < 0.f, true);
         const uint32_t id_o = idesc_f16(QR, D, false, true, false, true);
-        const uint32_t ts = tmem + L::S_ + t * KB, to = tmem + L::O_ + t * D;
-        const uint64_t dq = desc_rows(base + L::Q_ + t * L::TILE), dk = desc_rows(base + L::K_), dv = desc_cols(base + L::V_, L::PANEL);
+        const uint32_t ts = tmem + L::S_ + t * 2 * KB, to = tmem + L::O_ + t * D;
+        const uint64_t dq = desc_rows(base + L::Q_ + t * L::QTILE), dk = desc_rows(base + L::K_), dv = desc_cols(base + L::V_, L::PANEL);
         auto scores = [&](int j) {
             const int s = j % L::STAGES;
             wait(kfull + s, (j / L::STAGES) & 1, guard);
@@ -200,36 +201,31 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             if (elect()) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    umma_f16(ts, step_rows(dq, x, L::PANEL), step_rows(dk + (s * L::TILE >> 4), x, L::PANEL), id_s, x > 0);
-                umma_commit(sfull + t);
+                    umma_f16(ts + (j & 1) * KB, step_rows(dq, x, L::QPANEL), step_rows(dk + (s * L::TILE >> 4), x, L::PANEL), id_s, x > 0);
+                umma_commit(sfull + 2 * t + (j & 1));
                 umma_commit(kempty + s);
             }
         };
         if (nt > 0) scores(0);
+        if (nt > 1) scores(1);
         for (int j = 0; j < nt; ++j) {
-            const int s = j % L::STAGES;
+            const int s = j % L::STAGES, w = 2 * t + (j & 1), u = (j >> 1) & 1;
             wait(vfull + s, (j / L::STAGES) & 1, guard);
             if (j == n - 1 && len - j * KB < KB) wait(vfix, 0, guard);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                wait(pready + 2 * t + half, j & 1, guard);
-                tc_fence_after();
-                if (warp_up(guard)) break;
-                if (elect()) {
-#pragma unroll
-                    for (int x = half * 4; x < half * 4 + 4; ++x)
-                        umma_f16_ts(to, ts + x * 8, step_cols(dv + (s * L::TILE >> 4), x), id_o, j > 0 || x > 0);
-                    if (half) {
-                        umma_commit(vempty + s);
-                        umma_commit(pvdone + t);
-                    }
-                }
-            }
+            wait(pready + w, u, guard);
+            tc_fence_after();
             if (warp_up(guard)) break;
-            if (j + 1 < nt) {
-                wait(pvdone + t, j & 1, guard);   // P is in S's place: it must have been read
+            if (elect()) {
+#pragma unroll
+                for (int x = 0; x < KB / 16; ++x)
+                    umma_f16_ts(to, ts + (j & 1) * KB + x * 8, step_cols(dv + (s * L::TILE >> 4), x), id_o, j > 0 || x > 0);
+                umma_commit(vempty + s);
+                umma_commit(pvdone + w);
+            }
+            if (j + 2 < nt) {
+                wait(pvdone + w, u, guard);   // P is in S's place: it must have been read
                 if (warp_up(guard)) break;
-                scores(j + 1);
+                scores(j + 2);
             }
         }
         if (lane == 0) {
@@ -253,31 +249,25 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const bool real = i < all;
         const int token = (int)(min(i, all - 1) / rows.r);
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-        const uint32_t ts = tmem + L::S_ + t * KB + lanes, to = tmem + L::O_ + t * D + lanes;
+        const uint32_t ts = tmem + L::S_ + t * 2 * KB + lanes, to = tmem + L::O_ + t * D + lanes;
         // scores come with the sign of scale applied by the MMA; never 0, so that a masked -inf stays one
         const float sl = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
         // the warp's first row sees the fewest keys
         const int least = (int)(min(first + t * QR + (warp & 3) * 32, all - 1) / rows.r);
         float ref = 0.f, sum = 0.f;
         for (int j = 0; j < nt; ++j) {
-            wait(sfull + t, j & 1, guard);
+            const int w = 2 * t + (j & 1), u = (j >> 1) & 1;
+            wait(sfull + w, u, guard);
             tc_fence_after();
-            const bool edge = j * KB + KB - 1 > least;
-            const int seen = token - j * KB;   // keys 0 .. seen of the block
-            // half the block at a time: the second half is read again after the maximum is known,
-            // which costs less than holding 128 scores
-            auto load = [&](int half, float (&s)[64]) {
-                tmem_ld64(ts + half * 64, s);
-                if (edge)
+            float s[64];
+            tmem_ld64(ts + (j & 1) * KB, s);
+            if (j * KB + KB - 1 > least) {
+                const int seen = token - j * KB;   // keys 0 .. seen of the block
 #pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (half * 64 + x > seen) s[x] = -INFINITY;
-            };
-            float s[64], top;
-            load(1, s);
-            top = max_of(s);
-            load(0, s);
-            top = fmaxf(top, max_of(s));
+                for (int x = 0; x < 64; ++x)
+                    if (x > seen) s[x] = -INFINITY;
+            }
+            const float top = max_of(s);
             if (j == 0) {
                 ref = top;
             } else if (__any_sync(~0u, (top - ref) * sl > 8.f)) {
@@ -285,7 +275,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const float f = grown ? ex2_approx((ref - top) * sl) : 1.f;
                 if (grown) ref = top;
                 sum *= f;
-                wait(pvdone + t, (j - 1) & 1, guard);
+                wait(pvdone + (w ^ 1), ((j - 1) >> 1) & 1, guard);
                 tc_fence_after();
 #pragma unroll
                 for (int x = 0; x < D; x += 32) {
@@ -296,36 +286,28 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     tmem_st32(to + x, o);
                 }
             }
-            // The exponentials of the two tiles take turns: side by side they would share one unit,
-            // and then both tiles would wait for the tensor cores at the same time.
-            if (t ? j < n0 : j > 0 && n1 > 0) wait(turn + t, (t ? j : j - 1) & 1, guard);
             const uint64_t sl2 = pair(sl, sl), off2 = pair(-ref * sl, -ref * sl);
             uint64_t z = 0, y = 0;
+            uint32_t p[32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (half) load(1, s);
-                uint32_t p[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    float e0, e1;
-                    unpair(fma2(pair(s[2 * x], s[2 * x + 1]), sl2, off2), e0, e1);
-                    e0 = ex2_approx(e0);
-                    e1 = ex2_approx(e1);
-                    if (x & 1) y = add2(y, pair(e0, e1)); else z = add2(z, pair(e0, e1));
-                    p[x] = pack_bf16(e0, e1);
-                }
-                tmem_st32u_nowait(ts + half * 32, p);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(pready + 2 * t + half);
+            for (int x = 0; x < 32; ++x) {
+                float e0, e1;
+                unpair(fma2(pair(s[2 * x], s[2 * x + 1]), sl2, off2), e0, e1);
+                e0 = ex2_approx(e0);
+                e1 = ex2_approx(e1);
+                if (x & 1) y = add2(y, pair(e0, e1)); else z = add2(z, pair(e0, e1));
+                p[x] = pack_bf16(e0, e1);
             }
-            mbar_arrive(turn + 1 - t);
+            tmem_st32u_nowait(ts + (j & 1) * KB, p);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(pready + w);
             float z0, z1;
             unpair(add2(z, y), z0, z1);
             sum += z0 + z1;
         }
         if (nt > 0) {
-            wait(pvdone + t, (nt - 1) & 1, guard);
+            wait(pvdone + 2 * t + ((nt - 1) & 1), ((nt - 1) >> 1) & 1, guard);
             tc_fence_after();
             if (!warp_up(guard)) {
                 const int64_t row = real ? (t0 + token) * a.H + (int64_t)hk * rows.r + i % rows.r : 0;
