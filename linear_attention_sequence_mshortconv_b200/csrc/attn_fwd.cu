@@ -196,7 +196,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const uint64_t dq = desc_rows(base + L::Q_ + t * L::QTILE), dk = desc_rows(base + L::K_), dv = desc_cols(base + L::V_, L::PANEL);
         auto scores = [&](int j) {
             const int s = j % L::STAGES;
-            wait(kfull + s, (j / L::STAGES) & 1, guard);
             tc_fence_after();
             if (elect()) {
 #pragma unroll
@@ -206,15 +205,18 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 umma_commit(kempty + s);
             }
         };
-        if (nt > 0) scores(0);
-        if (nt > 1) scores(1);
+        // Each wait costs some 85 cycles even when there is nothing to wait for: those for the copies
+        // are made while MMAs already issued run.
+        for (int j = 0; j < 2 && j < nt; ++j) {
+            wait(kfull + j, 0, guard);
+            scores(j);
+        }
         for (int j = 0; j < nt; ++j) {
             const int s = j % L::STAGES, w = 2 * t + (j & 1), u = (j >> 1) & 1;
             wait(vfull + s, (j / L::STAGES) & 1, guard);
             if (j == n - 1 && len - j * KB < KB) wait(vfix, 0, guard);
             wait(pready + w, u, guard);
             tc_fence_after();
-            if (warp_up(guard)) break;
             if (elect()) {
 #pragma unroll
                 for (int x = 0; x < KB / 16; ++x)
@@ -223,8 +225,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 umma_commit(pvdone + w);
             }
             if (j + 2 < nt) {
+                wait(kfull + (j + 2) % L::STAGES, ((j + 2) / L::STAGES) & 1, guard);
                 wait(pvdone + w, u, guard);   // P is in S's place: it must have been read
-                if (warp_up(guard)) break;
                 scores(j + 2);
             }
         }

@@ -17,8 +17,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---- waits ------------------------------------------------------------------------------
 // The first wait that runs out raises the CTA's flag and records DEV_TIMEOUT; from then on no
-// wait waits, no MMA or copy is issued, and every role runs to its end.  Warps that use warp-wide
-// instructions or barriers keep their loops whole: the flag is seen by lanes at different times.
+// wait waits, no copy is issued, and every role runs to its end (MMAs still issued work on whatever
+// is there).  Warps that use warp-wide instructions or barriers keep their loops whole: the flag
+// is seen by lanes at different times.
 struct Guard {
     volatile int* flag;
     int* status;
