@@ -103,14 +103,28 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     if (!rows.locate(seqs, (int64_t)gridDim.x - 1 - blockIdx.x, 2 * QR, seq, tile)) return;
     const int64_t t0 = seqs.start(seq);
     const int len = seqs.len(seq);
-    const int64_t all = (int64_t)len * rows.r, first = (int64_t)tile * 2 * QR;
+    const uint32_t r = rows.r, all = (uint32_t)len * r, first = (uint32_t)tile * 2 * QR;
     auto blocks = [&](int t) {   // key blocks tile t sees
-        const int64_t r0 = first + t * QR;
-        return r0 >= all ? 0 : (int)(min(r0 + QR, all) - 1) / rows.r / KB + 1;
+        const uint32_t r0 = first + t * QR;
+        return r0 >= all ? 0 : (int)((min(r0 + QR, all) - 1) / r / KB + 1);
     };
     const int n0 = blocks(0), n1 = blocks(1), n = max(n0, n1);
 
-    if (warp == 8) {
+    const RowAt row_at{t0, a.H, hk * rows.r, rows.r, D};
+
+    auto load_k = [&](int j) {
+        const int s = j % L::STAGES;
+        mbar_arrive_expect_tx(kfull + s, L::TILE);
+        for (int p = 0; p < D / 64; ++p)
+            tma_load_3d(sm + L::K_ + s * L::TILE + p * L::PANEL, &tm_k, kfull + s, p * 64, hk, (int)t0 + j * KB);
+    };
+    auto load_v = [&](int j) {
+        const int s = j % L::STAGES;
+        mbar_arrive_expect_tx(vfull + s, L::TILE);
+        for (int p = 0; p < D / 64; ++p)
+            tma_load_3d(sm + L::V_ + s * L::TILE + p * L::PANEL, &tm_v, vfull + s, p * 64, hk, (int)t0 + j * KB);
+    };
+    if (warp == 10) {
         if (lane == 0) {
             for (int i = 0; i < L::STAGES; ++i) {
                 mbar_init(kfull + i, 1);
@@ -128,23 +142,27 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             mbar_init(drain + 1, 1);
             *guard.flag = 0;
             fence_mbar_init();
+            fence_async_smem();
+            for (int j = 0; j < n && j < L::STAGES; ++j) {
+                load_k(j);
+                load_v(j);
+            }
         }
-        __syncwarp();
+    } else if (warp == 8) {
         tmem_alloc(tm_ptr, 512);
         tmem_relinquish();
+    } else if (warp < 8) {
+        // Q: rows past the sequence's end are zeros
+        for (int e = tid; e < 2 * QR * (D / 8); e += 256) {
+            const int piece = e % (D / 8), row = e / (D / 8);
+            const bool in = first + row < all;
+            cp16(base + L::Q_ + (row / QR) * L::QTILE + (piece >> 3) * L::QPANEL + piece_at(row % QR, piece & 7),
+                 (const __nv_bfloat16*)a.q + (in ? row_at(first + row) + piece * 8 : 0), in);
+        }
+        cp_async_commit();
+        cp_async_wait_all();
+        fence_async_smem();
     }
-    // Q: rows past the sequence's end are zeros
-    for (int e = tid; e < 2 * QR * (D / 8); e += L::THREADS) {
-        const int piece = e % (D / 8), row = e / (D / 8);
-        const int64_t i = first + row;
-        const bool in = i < all;
-        const int64_t off = in ? ((t0 + i / rows.r) * a.H + (int64_t)hk * rows.r + i % rows.r) * D + piece * 8 : 0;
-        cp16(base + L::Q_ + (row / QR) * L::QTILE + (piece >> 3) * L::QPANEL + piece_at(row % QR, piece & 7),
-             (const __nv_bfloat16*)a.q + off, in);
-    }
-    cp_async_commit();
-    cp_async_wait_all();
-    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -152,21 +170,16 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
     if (warp >= 10) {
         if (warp == 10 && lane == 0) {
-            int k_issued = 0, v_issued = 0;
-            for (int j = 0; j < n; ++j) {
+            int k_issued = min(n, L::STAGES), v_issued = k_issued;
+            for (int j = k_issued; j < n; ++j) {
                 const int s = j % L::STAGES, u = j / L::STAGES;
-                const int y = (int)t0 + j * KB;
                 wait(kempty + s, (u & 1) ^ 1, guard);
                 if (guard.up()) break;
-                mbar_arrive_expect_tx(kfull + s, L::TILE);
-                for (int p = 0; p < D / 64; ++p)
-                    tma_load_3d(sm + L::K_ + s * L::TILE + p * L::PANEL, &tm_k, kfull + s, p * 64, hk, y);
+                load_k(j);
                 ++k_issued;
                 wait(vempty + s, (u & 1) ^ 1, guard);
                 if (guard.up()) break;
-                mbar_arrive_expect_tx(vfull + s, L::TILE);
-                for (int p = 0; p < D / 64; ++p)
-                    tma_load_3d(sm + L::V_ + s * L::TILE + p * L::PANEL, &tm_v, vfull + s, p * 64, hk, y);
+                load_v(j);
                 ++v_issued;
             }
             if (guard.up()) {
@@ -247,15 +260,15 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
     } else {
         const int t = warp >> 2, nt = t ? n1 : n0;
-        const int64_t i = first + t * QR + (tid & 127);
+        const uint32_t i = first + t * QR + (tid & 127);
         const bool real = i < all;
-        const int token = (int)(min(i, all - 1) / rows.r);
+        const int token = (int)(min(i, all - 1) / r);
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
         const uint32_t ts = tmem + L::S_ + t * 2 * KB + lanes, to = tmem + L::O_ + t * D + lanes;
         // scores come with the sign of scale applied by the MMA; never 0, so that a masked -inf stays one
         const float sl = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
         // the warp's first row sees the fewest keys
-        const int least = (int)(min(first + t * QR + (warp & 3) * 32, all - 1) / rows.r);
+        const int least = (int)(min(first + t * QR + (warp & 3) * 32, all - 1) / r);
         float ref = 0.f, sum = 0.f;
         for (int j = 0; j < nt; ++j) {
             const int w = 2 * t + (j & 1), u = (j >> 1) & 1;
@@ -312,20 +325,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             wait(pvdone + 2 * t + ((nt - 1) & 1), ((nt - 1) >> 1) & 1, guard);
             tc_fence_after();
             if (!warp_up(guard)) {
-                const int64_t row = real ? (t0 + token) * a.H + (int64_t)hk * rows.r + i % rows.r : 0;
-                const float inv = 1.f / sum;
-                __nv_bfloat16* o = (__nv_bfloat16*)a.o + row * D;
-#pragma unroll
-                for (int x = 0; x < D; x += 32) {
-                    float v[32];
-                    tmem_ld32(to + x, v);
-                    if (real)
-#pragma unroll
-                        for (int y = 0; y < 32; y += 8)
-                            *(uint4*)(o + x + y) = make_uint4(pack_bf16(v[y] * inv, v[y + 1] * inv), pack_bf16(v[y + 2] * inv, v[y + 3] * inv),
-                                                              pack_bf16(v[y + 4] * inv, v[y + 5] * inv), pack_bf16(v[y + 6] * inv, v[y + 7] * inv));
-                }
-                if (real && a.lse) a.lse[row] = (ref * sl + log2f(sum)) * kLn2;
+                // every product that read Q has ended: its tile takes the output
+                const int64_t off = real ? row_at(i) : -1;
+                store_rows<D>(to, 1.f / sum, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)a.o, off, tid & 127);
+                if (real && a.lse) a.lse[off / D] = (ref * sl + log2f(sum)) * kLn2;
             }
         }
     }

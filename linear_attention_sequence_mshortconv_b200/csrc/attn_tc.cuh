@@ -146,6 +146,39 @@ struct Rows {
         return (int64_t)tile * R < (int64_t)s.len(lo) * r;
     }
 };
+// Rows of one sequence and group: the offset of row i in a [tokens, H, D] tensor.  A tensor that
+// fits the device has fewer than 2^32 rows of 64 values, so rows count in 32 bits.
+struct RowAt {
+    int64_t t0;       // first token
+    int H, h0, r, D;  // heads, the group's first, the group's
+    __device__ __forceinline__ int64_t operator()(uint32_t i) const { return ((t0 + i / r) * H + h0 + i % r) * D; }
+};
+// A thread's row (of 128, to a warp 32) of a finished D-column accumulator, scaled, to memory: 16-byte
+// pieces through a tile of shared memory, so that a warp writes whole rows.  off: the row's offset,
+// negative for a row that is not written.
+template <int D>
+__device__ __forceinline__ void store_rows(uint32_t taddr, float f, char* tile, __nv_bfloat16* dst, int64_t off, int row)
+{
+    constexpr int P = D / 8;
+    const int lane = threadIdx.x & 31;
+    auto at = [&](int r, int piece) { return tile + r * (2 * D) + (((piece & ~7) | ((piece ^ r) & 7)) << 4); };
+#pragma unroll
+    for (int x = 0; x < D; x += 32) {
+        float v[32];
+        tmem_ld32(taddr + x, v);
+#pragma unroll
+        for (int y = 0; y < 32; y += 8)
+            *(uint4*)at(row, (x + y) / 8) = make_uint4(pack_bf16(v[y] * f, v[y + 1] * f), pack_bf16(v[y + 2] * f, v[y + 3] * f),
+                                                       pack_bf16(v[y + 4] * f, v[y + 5] * f), pack_bf16(v[y + 6] * f, v[y + 7] * f));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        const int r = k * (32 / P) + lane / P;   // of the warp's 32
+        const int64_t o = __shfl_sync(~0u, off, r);
+        if (o >= 0) *(uint4*)(dst + o + (lane % P) * 8) = *(const uint4*)at((row & ~31) + r, lane % P);
+    }
+}
 
 }  // namespace attn
 }  // namespace kda
