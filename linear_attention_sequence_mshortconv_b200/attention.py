@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from .gdn import _packed, check_tensors, launching_on, ptr, scratch
+from .gdn import _packed, check_tensors, launch, ptr, scratch
 from .kda import _check, _code, _dtype_code, load_library
 
 
@@ -27,18 +27,18 @@ def _forward(q, k, v, seqs, scale, o, lse, want_lse, stream, fn, dims):
     H, Hkv, D = _sizes(q, k, dims)
     dt = _dtype_code(q)
     kv = (*q.shape[:-2], Hkv, D)
-    check_tensors(q, [("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype),
-                      ("o", o, q.shape, q.dtype), ("lse", lse, q.shape[:-1], torch.float32)])
+    index = check_tensors(q, [("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype),
+                              ("o", o, q.shape, q.dtype), ("lse", lse, q.shape[:-1], torch.float32)])
     lib = load_library()
-    with launching_on(q.device, stream) as s:
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-        rc = getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(o), ptr(lse), *seqs, H, Hkv, D,
-                              float(D ** -0.5 if scale is None else scale), dt, s)
-    _check(fn, rc)
-    return o, lse
+
+    def body(s):
+        out = torch.empty_like(q) if o is None else o
+        sums = q.new_empty(q.shape[:-1], dtype=torch.float32) if lse is None and want_lse else lse
+        _check(fn, getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(out), ptr(sums), *seqs, H, Hkv, D,
+                                    D ** -0.5 if scale is None else float(scale), dt, s))
+        return out, sums
+
+    return launch(index, stream, body)
 
 
 def forward(q, k, v, *, scale=None, o=None, lse=None, want_lse: bool = True, stream=None):
@@ -63,23 +63,23 @@ def _backward(q, k, v, o, lse, do, seqs, tokens, scale, workspace, stream, out, 
     dt = _dtype_code(q)
     kv = (*q.shape[:-2], Hkv, D)
     given = (None,) * 3 if out is None else tuple(out)
-    check_tensors(q, [("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype),
-                      ("o", o, q.shape, q.dtype), ("lse", lse, q.shape[:-1], torch.float32), ("do", do, q.shape, q.dtype),
-                      ("dq", given[0], q.shape, q.dtype), ("dk", given[1], kv, q.dtype), ("dv", given[2], kv, q.dtype)])
+    index = check_tensors(q, [("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype),
+                              ("o", o, q.shape, q.dtype), ("lse", lse, q.shape[:-1], torch.float32), ("do", do, q.shape, q.dtype),
+                              ("dq", given[0], q.shape, q.dtype), ("dk", given[1], kv, q.dtype), ("dv", given[2], kv, q.dtype)])
     if out is not None and any(t is None for t in given):
         raise ValueError("out must hold dq, dk and dv")
     if o is None or lse is None or do is None:
         raise ValueError("o, lse and do are needed")
     lib = load_library()
-    with launching_on(q.device, stream) as s:
-        if out is None:
-            given = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
-        need = int(lib.attn_backward_workspace_size(tokens, H, Hkv, D, dt))
-        keep, ws, ws_bytes = scratch(workspace, need, q.device)
-        rc = getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(o), ptr(lse), ptr(do), *map(ptr, given), *seqs, H, Hkv, D,
-                              float(D ** -0.5 if scale is None else scale), dt, ws, ws_bytes, s)
-    _check(fn, rc)
-    return given
+
+    def body(s):
+        d = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)) if out is None else given
+        keep, ws, ws_bytes = scratch(workspace, int(lib.attn_backward_workspace_size(tokens, H, Hkv, D, dt)), q)
+        _check(fn, getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(o), ptr(lse), ptr(do), *map(ptr, d), *seqs, H, Hkv, D,
+                                    D ** -0.5 if scale is None else float(scale), dt, ws, ws_bytes, s))
+        return d
+
+    return launch(index, stream, body)
 
 
 def backward(q, k, v, o, lse, do, *, scale=None, workspace=None, stream=None, out=None):

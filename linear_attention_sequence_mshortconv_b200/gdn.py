@@ -13,56 +13,65 @@ device is current.  There is no fallback: without ``libkda.so`` or a CUDA tensor
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from .kda import _check, _code, _cu_array, _dtype_code, load_library
 
+# The current stream's handle without building a Stream object (some 3 us of a call whose
+# kernel may take 5); torch's public way where a version lacks it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def check_tensors(first, named):
-    """The tensors of a call are CUDA tensors of the first one's device, contiguous, and of the
-    shape and type given; None passes for an optional one."""
+    """The tensors of a call, (name, tensor or None, shape, dtype), are contiguous CUDA tensors of the
+    first one's device and of the shape and type given; None passes.  Returns the device's index."""
     if not isinstance(first, torch.Tensor) or not first.is_cuda:
         raise TypeError("q must be a CUDA tensor")
+    index = first.get_device()
     for name, t, shape, dtype in named:
-        if t is None:
+        if t is None or (isinstance(t, torch.Tensor) and t.get_device() == index and t.shape == shape
+                         and t.dtype is dtype and t.is_contiguous()):
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        if t.device != first.device:
+        if t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, q on {first.device}")
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} must be contiguous")
+    return index
 
 
 def ptr(t):
     return None if t is None else t.data_ptr()
 
 
-@contextlib.contextmanager
-def launching_on(device, stream):
-    """The tensors' device and the launching stream are current inside, so that what a call
-    allocates belongs to the stream it runs on; yields that stream's handle."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield torch.cuda.current_stream(device).cuda_stream
+def launch(index, stream, body):
+    """body(stream handle) with the tensors' device and the launching stream current, so that what a
+    call allocates belongs to the stream it runs on."""
+    if stream is None:
+        if torch.cuda.current_device() == index:
+            return body(_raw_stream(index))
+        with torch.cuda.device(index):
+            return body(_raw_stream(index))
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
-def scratch(workspace, need, device):
+def scratch(workspace, need, like):
     """(tensor, address, bytes): the caller's workspace, or one from torch's allocator."""
     if workspace is not None:
-        if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if not isinstance(workspace, torch.Tensor) or workspace.device != like.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
         return None, None, 0
-    t = torch.empty(need, dtype=torch.uint8, device=device)
+    t = like.new_empty(need, dtype=torch.uint8)
     return t, t.data_ptr(), need
 
 
@@ -110,19 +119,19 @@ def _forward(q, k, v, g, beta, S0, lead, rows, seqs, need, o, S_T, want_state, w
     Hk, Hv, Dk, Dv = _sizes(q, v, len(lead))
     dt = _dtype_code(q)
     state = (rows, Hv, Dk, Dv)
-    check_tensors(q, _inputs(q, k, v, g, beta, lead, Hv) + [
-        ("S0", S0, state, torch.float32), ("o", o, (*lead, Hv, Dv), q.dtype), ("S_T", S_T, state, torch.float32)])
+    index = check_tensors(q, _inputs(q, k, v, g, beta, lead, Hv) + [
+        ("S0", S0, state, torch.float32), ("o", o, v.shape, q.dtype), ("S_T", S_T, state, torch.float32)])
     lib = load_library()
-    with launching_on(q.device, stream) as s:
-        if o is None:
-            o = torch.empty((*lead, Hv, Dv), dtype=q.dtype, device=q.device)
-        if S_T is None and want_state:
-            S_T = torch.empty(state, dtype=torch.float32, device=q.device)
-        keep, ws, ws_bytes = scratch(workspace, need(lib, Hk, Hv, Dk, Dv, dt), q.device)
-        rc = getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), ptr(S0), ptr(o), ptr(S_T), *seqs,
-                              Hk, Hv, Dk, Dv, dt, ws, ws_bytes, s)
-    _check(fn, rc)
-    return o, S_T
+
+    def body(s):
+        out = torch.empty_like(v) if o is None else o
+        final = q.new_empty(state, dtype=torch.float32) if S_T is None and want_state else S_T
+        keep, ws, ws_bytes = scratch(workspace, need(lib, Hk, Hv, Dk, Dv, dt), q)
+        _check(fn, getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), ptr(S0), ptr(out), ptr(final), *seqs,
+                                    Hk, Hv, Dk, Dv, dt, ws, ws_bytes, s))
+        return out, final
+
+    return launch(index, stream, body)
 
 
 def forward(q, k, v, g, beta, S0=None, *, o=None, S_T=None, want_state: bool = True, workspace=None, stream=None):
@@ -156,21 +165,24 @@ def _backward(q, k, v, g, beta, do, S0, dS_T, lead, rows, seqs, need, want_dS0, 
     state = (rows, Hv, Dk, Dv)
     grads = [("dq", q.shape), ("dk", q.shape), ("dv", v.shape), ("dg", (*lead, Hv)), ("dbeta", (*lead, Hv))]
     given = (None,) * 6 if out is None else tuple(out)
-    check_tensors(q, _inputs(q, k, v, g, beta, lead, Hv) + [
+    index = check_tensors(q, _inputs(q, k, v, g, beta, lead, Hv) + [
         ("do", do, v.shape, q.dtype), ("S0", S0, state, torch.float32), ("dS_T", dS_T, state, torch.float32)] + [
         (name, t, shape, q.dtype) for (name, shape), t in zip(grads, given)] + [("dS0", given[5], state, torch.float32)])
     if out is not None and any(t is None for t in given[:5]):
         raise ValueError("out must hold dq, dk, dv, dg, dbeta and dS0 or None")
     lib = load_library()
-    with launching_on(q.device, stream) as s:
+
+    def body(s):
+        d = given
         if out is None:
-            given = (*(torch.empty(shape, dtype=q.dtype, device=q.device) for _, shape in grads),
-                     torch.empty(state, dtype=torch.float32, device=q.device) if want_dS0 else None)
-        keep, ws, ws_bytes = scratch(workspace, need(lib, Hk, Hv, Dk, Dv, dt), q.device)
-        rc = getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), ptr(S0), ptr(do), ptr(dS_T),
-                              *map(ptr, given), *seqs, Hk, Hv, Dk, Dv, dt, ws, ws_bytes, s)
-    _check(fn, rc)
-    return given
+            d = (*(torch.empty_like(t) for t in (q, k, v, g, beta)),
+                 q.new_empty(state, dtype=torch.float32) if want_dS0 else None)
+        keep, ws, ws_bytes = scratch(workspace, need(lib, Hk, Hv, Dk, Dv, dt), q)
+        _check(fn, getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), ptr(S0), ptr(do), ptr(dS_T),
+                                    *map(ptr, d), *seqs, Hk, Hv, Dk, Dv, dt, ws, ws_bytes, s))
+        return d
+
+    return launch(index, stream, body)
 
 
 def backward(q, k, v, g, beta, do, S0=None, dS_T=None, *, want_dS0: bool = True, workspace=None, stream=None,
@@ -207,14 +219,16 @@ def step(q, k, v, g, beta, state, slots=None, *, o=None, stream=None):
     n = q.shape[0]
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be [n_slots,Hv,Dk,Dv]")
-    check_tensors(q, _inputs(q, k, v, g, beta, (n,), Hv) + [
+    index = check_tensors(q, _inputs(q, k, v, g, beta, (n,), Hv) + [
         ("state", state, (state.shape[0], Hv, Dk, Dv), torch.float32), ("slots", slots, (n,), torch.int32),
         ("o", o, v.shape, q.dtype)])
     lib = load_library()
-    with launching_on(q.device, stream) as s:
-        if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
-        rc = lib.gdn_step(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), ptr(state), ptr(slots), ptr(o), n, state.shape[0],
-                          Hk, Hv, Dk, Dv, dt, s)
-    _check("gdn_step", rc)
-    return o
+
+    def body(s):
+        out = torch.empty_like(v) if o is None else o
+        _check("gdn_step", lib.gdn_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                        state.data_ptr(), ptr(slots), out.data_ptr(), n, state.shape[0], Hk, Hv, Dk, Dv,
+                                        dt, s))
+        return out
+
+    return launch(index, stream, body)
