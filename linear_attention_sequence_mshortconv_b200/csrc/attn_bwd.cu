@@ -12,7 +12,7 @@
 // lays it and lse log2(e) out row by row.
 //
 // Both kernels have the forward's roles: warps 0-3 and 4-7 turn scores into the operands of the
-// next product, warp 8 issues the MMAs, warp 9 the loads.
+// next product, warps 8 and 9 issue the MMAs, warp 10 the loads.
 
 #include "attn_tc.cuh"
 
@@ -45,23 +45,12 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs a, const __nv_
     }
 }
 
-// what the MMA-issuing thread does on the way out after a timeout: leave nothing in flight
-__device__ __forceinline__ void drain_mma(uint64_t* bar)
+// What an issuing warp does on the way out after a timeout: leave nothing in flight.
+__device__ __forceinline__ void drain_mma(uint64_t* bar, const Guard& guard)
 {
-    umma_commit(bar);
+    if (!warp_up(guard)) return;
+    if (elect()) umma_commit(bar);
     mbar_wait_bounded(bar, 0, kWaitNs);
-}
-
-// 32 fp32 columns of tensor memory, scaled, as 64 bytes of a bf16 row
-__device__ __forceinline__ void store32(uint32_t taddr, float f, __nv_bfloat16* dst, bool real)
-{
-    float v[32];
-    tmem_ld32(taddr, v);
-    if (!real) return;
-#pragma unroll
-    for (int y = 0; y < 32; y += 8)
-        *(uint4*)(dst + y) = make_uint4(pack_bf16(v[y] * f, v[y + 1] * f), pack_bf16(v[y + 2] * f, v[y + 3] * f),
-                                        pack_bf16(v[y + 4] * f, v[y + 5] * f), pack_bf16(v[y + 6] * f, v[y + 7] * f));
 }
 
 // ---- dk and dv ------------------------------------------------------------------------------
@@ -85,7 +74,7 @@ struct Keys {
 };
 
 template <int D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(384, 1)
 attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g, AttnBwdArgs b,
                      const __grid_constant__ Seqs seqs, const float2* rows, int* status)
@@ -98,10 +87,10 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
     uint64_t *kvfull = bars, *full = kvfull + 1, *empty = full + L::STAGES, *sfull = empty + L::STAGES, *gfull = sfull + 2;
     uint64_t *pready = gfull + 2, *dready = pready + 2, *done = dready + 2, *fix = done + 2, *all_done = fix + 1, *drain = all_done + 1;
-    uint32_t* tm_ptr = (uint32_t*)(drain + 1);
+    uint32_t* tm_ptr = (uint32_t*)(drain + 2);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
     const int hk = blockIdx.y, r = a.H / a.Hkv;
     int seq, tile;
     if (!seqs.locate(blockIdx.x, L::KEYS, seq, tile)) return;   // the first tiles have the most rows
@@ -111,7 +100,15 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int n = (len - key0 + tq - 1) / tq;
     const int tail = (len - key0 - (n - 1) * tq) * r;        // rows of the last tile
 
-    if (warp == 8) {
+    auto load = [&](int j) {
+        const int s = j % L::STAGES;
+        mbar_arrive_expect_tx(full + s, (uint32_t)(2 * tq * r * D * 2));
+        for (int p = 0; p < D / 64; ++p) {
+            tma_load_3d(sm + L::Q_ + s * L::RTILE + p * L::RPANEL, &tm_q, full + s, p * 64, hk * r, (int)t0 + key0 + j * tq);
+            tma_load_3d(sm + L::G_ + s * L::RTILE + p * L::RPANEL, &tm_g, full + s, p * 64, hk * r, (int)t0 + key0 + j * tq);
+        }
+    };
+    if (warp == 10) {
         if (lane == 0) {
             mbar_init(kvfull, 1);
             for (int i = 0; i < L::STAGES; ++i) {
@@ -124,46 +121,42 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 mbar_init(pready + i, 128);
                 mbar_init(dready + i, 128);
                 mbar_init(done + i, 1);
+                mbar_init(drain + i, 1);
             }
             mbar_init(fix, 32);
             mbar_init(all_done, 1);
-            mbar_init(drain, 1);
             *guard.flag = 0;
             fence_mbar_init();
+            fence_async_smem();
+            mbar_arrive_expect_tx(kvfull, 2 * L::KTILE);
+            for (int p = 0; p < D / 64; ++p) {
+                tma_load_3d(sm + L::K_ + p * L::KPANEL, &tm_k, kvfull, p * 64, hk, (int)t0 + key0);
+                tma_load_3d(sm + L::V_ + p * L::KPANEL, &tm_v, kvfull, p * 64, hk, (int)t0 + key0);
+            }
+            for (int j = 0; j < n && j < L::STAGES; ++j) load(j);
         }
-        __syncwarp();
+    } else if (warp == 8) {
         tmem_alloc(tm_ptr, 512);
         tmem_relinquish();
-    }
-    if (tq * r < L::RB)
-        for (int e = tid; e < 2 * L::STAGES * (L::RB - tq * r) * (D / 8); e += 320) {
+    } else if (tq * r < L::RB && warp < 8) {   // rows that no copy writes
+        for (int e = tid; e < 2 * L::STAGES * (L::RB - tq * r) * (D / 8); e += 256) {
             const int piece = e % (D / 8), row = tq * r + e / (D / 8) % (L::RB - tq * r), st = e / (D / 8) / (L::RB - tq * r);
             *(uint4*)(sm + L::Q_ + st * L::RTILE + (piece >> 3) * L::RPANEL + piece_at(row, piece & 7)) = make_uint4(0, 0, 0, 0);
         }
+    }
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tm_ptr;
 
-    if (warp == 9) {
-        const uint32_t bytes = (uint32_t)(tq * r * D * 2);
-        if (lane == 0) {
-            mbar_arrive_expect_tx(kvfull, 2 * L::KTILE);
-            for (int p = 0; p < D / 64; ++p) {
-                tma_load_3d(sm + L::K_ + p * L::KPANEL, &tm_k, kvfull, p * 64, hk, (int)t0 + key0);
-                tma_load_3d(sm + L::V_ + p * L::KPANEL, &tm_v, kvfull, p * 64, hk, (int)t0 + key0);
-            }
-            int issued = 0;
-            for (int j = 0; j < n; ++j, ++issued) {
-                const int s = j % L::STAGES;
-                wait(empty + s, ((j / L::STAGES) & 1) ^ 1, guard);
+    if (warp >= 10) {
+        if (warp == 10 && lane == 0) {
+            int issued = min(n, L::STAGES);
+            for (; issued < n; ++issued) {
+                wait(empty + issued % L::STAGES, ((issued / L::STAGES) & 1) ^ 1, guard);
                 if (guard.up()) break;
-                mbar_arrive_expect_tx(full + s, 2 * bytes);
-                for (int p = 0; p < D / 64; ++p) {
-                    tma_load_3d(sm + L::Q_ + s * L::RTILE + p * L::RPANEL, &tm_q, full + s, p * 64, hk * r, (int)t0 + key0 + j * tq);
-                    tma_load_3d(sm + L::G_ + s * L::RTILE + p * L::RPANEL, &tm_g, full + s, p * 64, hk * r, (int)t0 + key0 + j * tq);
-                }
+                load(issued);
             }
             if (guard.up()) {
                 mbar_wait_bounded(kvfull, 0, kWaitNs);
@@ -173,7 +166,7 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         __syncwarp();
         // rows of the last tile past the end: their weights are 0, but 0 times a value that is not
         // finite (the next sequence's) is not
-        if (tail < tq * r && !guard.up()) {
+        if (warp == 10 && tail < tq * r && !guard.up()) {
             const int s = (n - 1) % L::STAGES;
             wait(full + s, ((n - 1) / L::STAGES) & 1, guard);
             for (int e = lane; e < 2 * (tq * r - tail) * (D / 8); e += 32) {
@@ -183,60 +176,53 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             fence_async_smem();
             mbar_arrive(fix);
         }
-    } else if (warp == 8) {
-        if (lane == 0) {
-            const uint32_t id_s = idesc_f16(L::KEYS, L::RB, false, false, a.scale < 0.f, true);
-            const uint32_t id_g = idesc_f16(L::KEYS, L::RB, false, false, false, true);
-            const uint32_t id_o = idesc_f16(L::KEYS, D, false, true, false, true);
-            auto scores = [&](int j) {
-                const int s = j % L::STAGES, w = j & 1;
-                wait(full + s, (j / L::STAGES) & 1, guard);
-                if (j == n - 1 && tail < tq * r) wait(fix, 0, guard);
-                if (guard.up()) return;
-                tc_fence_after();
+    } else if (warp == 9) {   // scores and dP
+        const uint32_t id_s = idesc_f16(L::KEYS, L::RB, false, false, a.scale < 0.f, true);
+        const uint32_t id_g = idesc_f16(L::KEYS, L::RB, false, false, false, true);
+        const uint64_t dk = desc_rows(base + L::K_), dv = desc_rows(base + L::V_), dq = desc_rows(base + L::Q_), dg = desc_rows(base + L::G_);
+        wait(kvfull, 0, guard);
+        for (int j = 0; j < n; ++j) {
+            const int s = j % L::STAGES, w = j & 1;
+            wait(full + s, (j / L::STAGES) & 1, guard);
+            if (j == n - 1 && tail < tq * r) wait(fix, 0, guard);
+            if (j >= 2) wait(done + w, ((j - 2) >> 1) & 1, guard);   // P and dS are in the places of S and dP
+            tc_fence_after();
+            if (elect()) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    umma_f16(tmem + L::S_ + w * L::BUF, desc_rows(base + L::K_ + (x >> 2) * L::KPANEL + (x & 3) * 32),
-                             desc_rows(base + L::Q_ + s * L::RTILE + (x >> 2) * L::RPANEL + (x & 3) * 32), id_s, x > 0);
+                    umma_f16(tmem + L::S_ + w * L::BUF, step_rows(dk, x, L::KPANEL), step_rows(dq + (s * L::RTILE >> 4), x, L::RPANEL), id_s, x > 0);
                 umma_commit(sfull + w);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    umma_f16(tmem + L::P_ + w * L::BUF, desc_rows(base + L::V_ + (x >> 2) * L::KPANEL + (x & 3) * 32),
-                             desc_rows(base + L::G_ + s * L::RTILE + (x >> 2) * L::RPANEL + (x & 3) * 32), id_g, x > 0);
+                    umma_f16(tmem + L::P_ + w * L::BUF, step_rows(dv, x, L::KPANEL), step_rows(dg + (s * L::RTILE >> 4), x, L::RPANEL), id_g, x > 0);
                 umma_commit(gfull + w);
-            };
-            wait(kvfull, 0, guard);
-            if (!guard.up()) scores(0);
-            if (n > 1 && !guard.up()) scores(1);
-            for (int j = 0; j < n && !guard.up(); ++j) {
-                const int s = j % L::STAGES, w = j & 1, u = (j >> 1) & 1;
-                wait(pready + w, u, guard);
-                if (guard.up()) break;
-                tc_fence_after();
+            }
+        }
+        drain_mma(drain + 1, guard);
+    } else if (warp == 8) {   // dV and dK
+        const uint32_t id_o = idesc_f16(L::KEYS, D, false, true, false, true);
+        const uint64_t dq = desc_cols(base + L::Q_, L::RPANEL), dg = desc_cols(base + L::G_, L::RPANEL);
+        for (int j = 0; j < n; ++j) {
+            const int s = j % L::STAGES, w = j & 1, u = (j >> 1) & 1;
+            wait(pready + w, u, guard);
+            tc_fence_after();
+            if (elect()) {
 #pragma unroll
                 for (int x = 0; x < L::RB / 16; ++x)
-                    umma_f16_ts(tmem + L::DV_, tmem + L::S_ + w * L::BUF + x * 8, desc_cols(base + L::G_ + s * L::RTILE + x * 2048, L::RPANEL),
-                                id_o, j > 0 || x > 0);
-                wait(dready + w, u, guard);
-                if (guard.up()) break;
-                tc_fence_after();
+                    umma_f16_ts(tmem + L::DV_, tmem + L::S_ + w * L::BUF + x * 8, step_cols(dg + (s * L::RTILE >> 4), x), id_o, j > 0 || x > 0);
+            }
+            wait(dready + w, u, guard);
+            tc_fence_after();
+            if (elect()) {
 #pragma unroll
                 for (int x = 0; x < L::RB / 16; ++x)
-                    umma_f16_ts(tmem + L::DK_, tmem + L::P_ + w * L::BUF + x * 8, desc_cols(base + L::Q_ + s * L::RTILE + x * 2048, L::RPANEL),
-                                id_o, j > 0 || x > 0);
+                    umma_f16_ts(tmem + L::DK_, tmem + L::P_ + w * L::BUF + x * 8, step_cols(dq + (s * L::RTILE >> 4), x), id_o, j > 0 || x > 0);
                 umma_commit(empty + s);
                 umma_commit(done + w);
-                if (j + 2 < n) {
-                    wait(done + w, u, guard);   // P and dS are in the places of S and dP
-                    if (guard.up()) break;
-                    scores(j + 2);
-                }
+                if (j == n - 1) umma_commit(all_done);
             }
-            if (guard.up())
-                drain_mma(drain);
-            else
-                umma_commit(all_done);
         }
+        drain_mma(drain, guard);
     } else {
         const int w = warp >> 2, key = key0 + (tid & 127);
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
@@ -302,13 +288,12 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         wait(all_done, 0, guard);
         tc_fence_after();
         if (!warp_up(guard)) {
-            const bool real = key < len;
-            const int64_t off = real ? ((t0 + key) * a.Hkv + hk) * D : 0;
-            for (int x = 0; x < D; x += 32)
-                if (w == 0)
-                    store32(tmem + L::DV_ + lanes + x, 1.f, (__nv_bfloat16*)b.dv + off + x, real);
-                else
-                    store32(tmem + L::DK_ + lanes + x, a.scale, (__nv_bfloat16*)b.dk + off + x, real);
+            const int64_t off = key < len ? ((t0 + key) * a.Hkv + hk) * D : -1;
+            // K and V have been read: dV and dK go out through their places
+            if (w == 0)
+                store_rows<D>(tmem + L::DV_ + lanes, 1.f, sm + L::V_, (__nv_bfloat16*)b.dv, off, tid & 127);
+            else
+                store_rows<D>(tmem + L::DK_ + lanes, a.scale, sm + L::K_, (__nv_bfloat16*)b.dk, off, tid & 127);
         }
     }
     tc_fence_before();
@@ -332,7 +317,7 @@ struct Dq {
 };
 
 template <int D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(384, 1)
 attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnBwdArgs b,
                      const __grid_constant__ Seqs seqs, const float2* rowdata, int* status)
 {
@@ -344,79 +329,85 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
     uint64_t *full = bars, *empty = full + L::STAGES, *sfull = empty + L::STAGES, *gfull = sfull + 2, *dready = gfull + 2;
     uint64_t *done = dready + 2, *fix = done + 2, *drain = fix + 1;
-    uint32_t* tm_ptr = (uint32_t*)(drain + 1);
+    uint32_t* tm_ptr = (uint32_t*)(drain + 2);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
     const int hk = blockIdx.y;
     const Rows rows{a.H / a.Hkv};
     int seq, tile;
     if (!rows.locate(seqs, (int64_t)gridDim.x - 1 - blockIdx.x, 2 * L::QR, seq, tile)) return;
     const int64_t t0 = seqs.start(seq);
     const int len = seqs.len(seq);
-    const int64_t all = (int64_t)len * rows.r, first = (int64_t)tile * 2 * L::QR;
+    const uint32_t r = rows.r, all = (uint32_t)len * r, first = (uint32_t)tile * 2 * L::QR;
     auto blocks = [&](int t) {
-        const int64_t r0 = first + t * L::QR;
-        return r0 >= all ? 0 : (int)(min(r0 + L::QR, all) - 1) / rows.r / L::KB + 1;
+        const uint32_t r0 = first + t * L::QR;
+        return r0 >= all ? 0 : (int)((min(r0 + L::QR, all) - 1) / r / L::KB + 1);
     };
     const int n0 = blocks(0), n1 = blocks(1), n = max(n0, n1);
     const int tail = len - (n - 1) * L::KB;   // keys of the last block
 
-    if (warp == 8) {
+    const RowAt row_at{t0, a.H, hk * rows.r, rows.r, D};
+    auto load = [&](int j) {
+        const int s = j % L::STAGES;
+        mbar_arrive_expect_tx(full + s, 2 * L::KTILE);
+        for (int p = 0; p < D / 64; ++p) {
+            tma_load_3d(sm + L::K_ + s * L::KTILE + p * L::KPANEL, &tm_k, full + s, p * 64, hk, (int)t0 + j * L::KB);
+            tma_load_3d(sm + L::V_ + s * L::KTILE + p * L::KPANEL, &tm_v, full + s, p * 64, hk, (int)t0 + j * L::KB);
+        }
+    };
+    if (warp == 10) {
         if (lane == 0) {
             for (int i = 0; i < L::STAGES; ++i) {
                 mbar_init(full + i, 1);
-                mbar_init(empty + i, 1);
+                mbar_init(empty + i, 2);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(sfull + i, 1);
                 mbar_init(gfull + i, 1);
                 mbar_init(dready + i, 128);
                 mbar_init(done + i, 1);
+                mbar_init(drain + i, 1);
             }
             mbar_init(fix, 32);
-            mbar_init(drain, 1);
             *guard.flag = 0;
             fence_mbar_init();
+            fence_async_smem();
+            for (int j = 0; j < n && j < L::STAGES; ++j) load(j);
         }
-        __syncwarp();
+    } else if (warp == 8) {
         tmem_alloc(tm_ptr, 512);
         tmem_relinquish();
+    } else if (warp < 8) {
+        for (int e = tid; e < 2 * L::QR * (D / 8); e += 256) {
+            const int piece = e % (D / 8), row = e / (D / 8);
+            const bool in = first + row < all;
+            const int64_t off = in ? row_at(first + row) + piece * 8 : 0;
+            const uint32_t at = (row / L::QR) * L::QTILE + (piece >> 3) * L::QPANEL + piece_at(row % L::QR, piece & 7);
+            cp16(base + L::Q_ + at, (const __nv_bfloat16*)a.q + off, in);
+            cp16(base + L::G_ + at, (const __nv_bfloat16*)b.dout + off, in);
+        }
+        cp_async_commit();
+        cp_async_wait_all();
+        fence_async_smem();
     }
-    for (int e = tid; e < 2 * L::QR * (D / 8); e += 320) {
-        const int piece = e % (D / 8), row = e / (D / 8);
-        const int64_t i = first + row;
-        const bool in = i < all;
-        const int64_t off = in ? ((t0 + i / rows.r) * a.H + (int64_t)hk * rows.r + i % rows.r) * D + piece * 8 : 0;
-        const uint32_t at = (row / L::QR) * L::QTILE + (piece >> 3) * L::QPANEL + piece_at(row % L::QR, piece & 7);
-        cp16(base + L::Q_ + at, (const __nv_bfloat16*)a.q + off, in);
-        cp16(base + L::G_ + at, (const __nv_bfloat16*)b.dout + off, in);
-    }
-    cp_async_commit();
-    cp_async_wait_all();
-    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tm_ptr;
 
-    if (warp == 9) {
-        if (lane == 0) {
-            int issued = 0;
-            for (int j = 0; j < n; ++j, ++issued) {
-                const int s = j % L::STAGES;
-                wait(empty + s, ((j / L::STAGES) & 1) ^ 1, guard);
+    if (warp >= 10) {
+        if (warp == 10 && lane == 0) {
+            int issued = min(n, L::STAGES);
+            for (; issued < n; ++issued) {
+                wait(empty + issued % L::STAGES, ((issued / L::STAGES) & 1) ^ 1, guard);
                 if (guard.up()) break;
-                mbar_arrive_expect_tx(full + s, 2 * L::KTILE);
-                for (int p = 0; p < D / 64; ++p) {
-                    tma_load_3d(sm + L::K_ + s * L::KTILE + p * L::KPANEL, &tm_k, full + s, p * 64, hk, (int)t0 + j * L::KB);
-                    tma_load_3d(sm + L::V_ + s * L::KTILE + p * L::KPANEL, &tm_v, full + s, p * 64, hk, (int)t0 + j * L::KB);
-                }
+                load(issued);
             }
             if (guard.up()) drain_ring(full, L::STAGES, issued);
         }
         __syncwarp();
-        if (tail < L::KB && !guard.up()) {   // keys past the end (dS is 0 there): K must be finite
+        if (warp == 10 && tail < L::KB && !guard.up()) {   // keys past the end (dS is 0 there): K must be finite
             const int s = (n - 1) % L::STAGES;
             wait(full + s, ((n - 1) / L::STAGES) & 1, guard);
             for (int e = lane; e < (L::KB - tail) * (D / 8); e += 32) {
@@ -426,60 +417,56 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             fence_async_smem();
             mbar_arrive(fix);
         }
-    } else if (warp == 8) {
-        if (lane == 0) {
-            const uint32_t id_s = idesc_f16(L::QR, L::KB, false, false, a.scale < 0.f, true);
-            const uint32_t id_g = idesc_f16(L::QR, L::KB, false, false, false, true);
-            const uint32_t id_o = idesc_f16(L::QR, D, false, true, false, true);
-            auto scores = [&](int t, int j) {
-                const int s = j % L::STAGES;
-                wait(full + s, (j / L::STAGES) & 1, guard);
-                if (guard.up()) return;
-                tc_fence_after();
+    } else if (warp >= 8) {
+        const int t = warp - 8, nt = t ? n1 : n0;
+        const uint32_t id_s = idesc_f16(L::QR, L::KB, false, false, a.scale < 0.f, true);
+        const uint32_t id_g = idesc_f16(L::QR, L::KB, false, false, false, true);
+        const uint32_t id_o = idesc_f16(L::QR, D, false, true, false, true);
+        const uint32_t ts = tmem + L::S_ + t * L::BUF, tp = tmem + L::P_ + t * L::BUF, to = tmem + L::DQ_ + t * D;
+        const uint64_t dq = desc_rows(base + L::Q_ + t * L::QTILE), dg = desc_rows(base + L::G_ + t * L::QTILE);
+        const uint64_t dk = desc_rows(base + L::K_), dv = desc_rows(base + L::V_), dkc = desc_cols(base + L::K_, L::KPANEL);
+        for (int j = 0; j < nt; ++j) {
+            const int s = j % L::STAGES;
+            wait(full + s, (j / L::STAGES) & 1, guard);
+            if (j > 0) wait(done + t, (j - 1) & 1, guard);   // dS is in dP's place
+            tc_fence_after();
+            if (elect()) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    umma_f16(tmem + L::S_ + t * L::BUF, desc_rows(base + L::Q_ + t * L::QTILE + (x >> 2) * L::QPANEL + (x & 3) * 32),
-                             desc_rows(base + L::K_ + s * L::KTILE + (x >> 2) * L::KPANEL + (x & 3) * 32), id_s, x > 0);
+                    umma_f16(ts, step_rows(dq, x, L::QPANEL), step_rows(dk + (s * L::KTILE >> 4), x, L::KPANEL), id_s, x > 0);
                 umma_commit(sfull + t);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
-                    umma_f16(tmem + L::P_ + t * L::BUF, desc_rows(base + L::G_ + t * L::QTILE + (x >> 2) * L::QPANEL + (x & 3) * 32),
-                             desc_rows(base + L::V_ + s * L::KTILE + (x >> 2) * L::KPANEL + (x & 3) * 32), id_g, x > 0);
+                    umma_f16(tp, step_rows(dg, x, L::QPANEL), step_rows(dv + (s * L::KTILE >> 4), x, L::KPANEL), id_g, x > 0);
                 umma_commit(gfull + t);
-            };
-            if (n0 > 0) scores(0, 0);
-            if (n1 > 0 && !guard.up()) scores(1, 0);
-            for (int j = 0; j < n && !guard.up(); ++j)
-                for (int t = 0; t < 2; ++t) {
-                    if (j >= (t ? n1 : n0)) continue;
-                    const int s = j % L::STAGES;
-                    wait(dready + t, j & 1, guard);
-                    if (j == n - 1 && tail < L::KB) wait(fix, 0, guard);
-                    if (guard.up()) break;
-                    tc_fence_after();
+            }
+            if (j == n - 1 && tail < L::KB) wait(fix, 0, guard);
+            wait(dready + t, j & 1, guard);
+            tc_fence_after();
+            if (elect()) {
 #pragma unroll
-                    for (int x = 0; x < L::KB / 16; ++x)
-                        umma_f16_ts(tmem + L::DQ_ + t * D, tmem + L::P_ + t * L::BUF + x * 8,
-                                    desc_cols(base + L::K_ + s * L::KTILE + x * 2048, L::KPANEL), id_o, j > 0 || x > 0);
-                    if (t == 1 || n1 <= j) umma_commit(empty + s);
-                    umma_commit(done + t);
-                    if (j + 1 < (t ? n1 : n0)) {
-                        wait(done + t, j & 1, guard);   // dS is in dP's place
-                        if (guard.up()) break;
-                        scores(t, j + 1);
-                    }
-                }
-            if (guard.up()) drain_mma(drain);
+                for (int x = 0; x < L::KB / 16; ++x)
+                    umma_f16_ts(to, tp + x * 8, step_cols(dkc + (s * L::KTILE >> 4), x), id_o, j > 0 || x > 0);
+                umma_commit(empty + s);
+                umma_commit(done + t);
+            }
         }
+        if (lane == 0)   // blocks that only the other tile sees (as in the forward)
+            for (int j = nt; j < n && !guard.up(); ++j) {
+                wait(empty + j % L::STAGES, ((j / L::STAGES) & 1) ^ 1, guard);
+                mbar_arrive(empty + j % L::STAGES);
+            }
+        __syncwarp();
+        drain_mma(drain + t, guard);
     } else {
         const int t = warp >> 2, nt = t ? n1 : n0;
-        const int64_t i = first + t * L::QR + (tid & 127);
+        const uint32_t i = first + t * L::QR + (tid & 127);
         const bool real = i < all;
-        const int token = (int)(min(i, all - 1) / rows.r);
+        const int token = (int)(min(i, all - 1) / r);
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
         const uint32_t ts = tmem + L::S_ + t * L::BUF + lanes, tp = tmem + L::P_ + t * L::BUF + lanes;
         const float sl = fabsf(a.scale) * kLog2e;
-        const int least = (int)(min(first + t * L::QR + (warp & 3) * 32, all - 1) / rows.r);
+        const int least = (int)(min(first + t * L::QR + (warp & 3) * 32, all - 1) / r);
         const float2 rd = real ? rowdata[((int64_t)hk * seqs.tokens() + t0) * rows.r + i] : make_float2(0.f, 0.f);
         for (int j = 0; j < nt; ++j) {
             wait(sfull + t, j & 1, guard);
@@ -515,8 +502,8 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             wait(done + t, (nt - 1) & 1, guard);
             tc_fence_after();
             if (!warp_up(guard)) {
-                const int64_t off = real ? ((t0 + token) * a.H + (int64_t)hk * rows.r + i % rows.r) * D : 0;
-                for (int x = 0; x < D; x += 32) store32(tmem + L::DQ_ + t * D + lanes + x, a.scale, (__nv_bfloat16*)b.dq + off + x, real);
+                store_rows<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)b.dq,
+                              real ? row_at(i) : -1, tid & 127);
             }
         }
     }
@@ -549,12 +536,12 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float2* rows, int* sta
     {
         ProfileScope prof("attn_bwd_keys", st);
         count_launch();
-        attn_bwd_keys_kernel<D><<<dim3(s.slots(128), a.Hkv), 320, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, rows, status);
+        attn_bwd_keys_kernel<D><<<dim3(s.slots(128), a.Hkv), 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, rows, status);
     }
     {
         ProfileScope prof("attn_bwd_rows", st);
         count_launch();
-        attn_bwd_rows_kernel<D><<<dim3((unsigned)Rows{r}.slots(s, 256), a.Hkv), 320, Dq<D>::SMEM, st>>>(k64, v64, b, s, rows, status);
+        attn_bwd_rows_kernel<D><<<dim3((unsigned)Rows{r}.slots(s, 256), a.Hkv), 384, Dq<D>::SMEM, st>>>(k64, v64, b, s, rows, status);
     }
     return cudaGetLastError();
 }

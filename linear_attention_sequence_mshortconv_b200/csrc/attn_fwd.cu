@@ -254,6 +254,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 mbar_arrive(vempty + s);
             }
         }
+        __syncwarp();
         if (warp_up(guard)) {   // leave nothing in flight
             if (elect()) umma_commit(drain + t);
             mbar_wait_bounded(drain + t, 0, kWaitNs);
