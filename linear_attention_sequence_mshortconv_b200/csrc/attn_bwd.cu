@@ -9,7 +9,7 @@
 // over the group where they are accumulated; the other owns 256 rows and goes over the keys.
 // That computes s and do.v twice (7 products instead of 5), but results do not depend on an
 // order of arrival and no fp32 gradient passes through memory.  A first kernel computes delta and
-// lays it and lse log2(e) out row by row.
+// lays it and lse out row by row.
 //
 // Both kernels have the forward's roles: warps 0-3 and 4-7 turn scores into the operands of the
 // next product, warps 8 and 9 issue the MMAs, warp 10 the loads.
@@ -21,27 +21,39 @@ namespace attn {
 namespace {
 
 // ---- delta ----------------------------------------------------------------------------------
-// [key/value head][token][head of the group]: {lse log2(e), delta}
+// -lse log2(e) and -delta of every row, [key/value head][token][head of the group] each.  Bound by
+// the bytes of o and do: D / 8 lanes to a row, 16 bytes of each a lane, four rows in flight.
 template <int D>
-__global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs a, const __nv_bfloat16* dout, float2* rows, int64_t tokens)
+__global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs a, const __nv_bfloat16* dout, float* nlse, float* ndelta, int64_t tokens)
 {
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= tokens * a.H) return;
-    constexpr int N = D / 32;
-    const __nv_bfloat16* o = (const __nv_bfloat16*)a.o + row * D + lane * N;
-    const __nv_bfloat16* g = dout + row * D + lane * N;
-    float s = 0.f;
+    constexpr int P = D / 8, PER = 256 / P, U = 4;   // lanes to a row, rows of a block at once
+    const int piece = threadIdx.x % P;
+    const int64_t row0 = (int64_t)blockIdx.x * PER * U + threadIdx.x / P, n = tokens * a.H;
+    uint4 x[U], y[U];
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float2 x = __bfloat1622float2(*(const __nv_bfloat162*)(o + i)), y = __bfloat1622float2(*(const __nv_bfloat162*)(g + i));
-        s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = row0 + u * PER;
+        const bool in = row < n;
+        x[u] = in ? *(const uint4*)((const __nv_bfloat16*)a.o + row * D + piece * 8) : make_uint4(0, 0, 0, 0);
+        y[u] = in ? *(const uint4*)(dout + row * D + piece * 8) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    if (lane == 0) {
-        const int h = (int)(row % a.H), r = a.H / a.Hkv;
-        rows[((int64_t)(h / r) * tokens + row / a.H) * r + h % r] = make_float2(a.lse[row] * kLog2e, s);
+    for (int u = 0; u < U; ++u) {
+        const uint32_t p[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, q[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s = fmaf(__uint_as_float(p[i] << 16), __uint_as_float(q[i] << 16),
+                     fmaf(__uint_as_float(p[i] & 0xffff0000u), __uint_as_float(q[i] & 0xffff0000u), s));
+#pragma unroll
+        for (int o = 1; o < P; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
+        const int64_t row = row0 + u * PER;
+        if (piece == 0 && row < n) {
+            const int h = (int)(row % a.H), r = a.H / a.Hkv;
+            const int64_t at = ((int64_t)(h / r) * tokens + row / a.H) * r + h % r;
+            nlse[at] = -a.lse[row] * kLog2e;
+            ndelta[at] = -s;
+        }
     }
 }
 
@@ -67,8 +79,8 @@ struct Keys {
     static constexpr int RPANEL = RB * 128, RTILE = D / 64 * RPANEL;
     static constexpr int STAGES = D == 64 ? 6 : 4;          // (Q, dO) tiles in flight
     static constexpr int K_ = 0, V_ = K_ + KTILE, Q_ = V_ + KTILE, G_ = Q_ + STAGES * RTILE;
-    static constexpr int LD = G_ + STAGES * RTILE;          // float2 [2 warpgroups][2][64]
-    static constexpr int BAR = LD + 4 * RB * 8;
+    static constexpr int LD = G_ + STAGES * RTILE;          // [2 warpgroups][2][-lse, -delta][64]
+    static constexpr int BAR = LD + 8 * RB * 4;
     static constexpr int SMEM = BAR + 512 + 1024;
     static constexpr int DV_ = 0, DK_ = D, S_ = 2 * D, P_ = 2 * D + RB, BUF = 2 * RB;
 };
@@ -77,7 +89,7 @@ template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g, AttnBwdArgs b,
-                     const __grid_constant__ Seqs seqs, const float2* rows, int* status)
+                     const __grid_constant__ Seqs seqs, const float* nlse, const float* ndelta, int* status)
 {
     using L = Keys<D>;
     const AttnArgs& a = b.f;
@@ -228,15 +240,19 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
         const uint32_t ts = tmem + L::S_ + w * L::BUF + lanes, tp = tmem + L::P_ + w * L::BUF + lanes;
         const float sl = fabsf(a.scale) * kLog2e;
-        const float2* src = rows + ((int64_t)hk * seqs.tokens() + t0 + key0) * r;
-        float2* ld = (float2*)(sm + L::LD) + w * 2 * L::RB;
+        const uint64_t sl2 = pair(sl, sl);
+        // threads 0-63 fetch -lse of the tile's rows, 64-127 -delta: one tile ahead, in registers
+        const float* src = ((tid & 64) ? ndelta : nlse) + ((int64_t)hk * seqs.tokens() + t0 + key0) * r + (tid & 63);
+        auto fetch = [&](int j) { return j < n && (tid & 63) < (j == n - 1 ? tail : tq * r) ? src[(int64_t)j * tq * r] : 0.f; };
+        float* ld = (float*)(sm + L::LD) + w * 4 * L::RB;
+        float ahead = fetch(w);
         for (int j = w; j < n; j += 2) {
             const int u = (j >> 1) & 1;
             const int live = j == n - 1 ? tail : tq * r;   // rows of this tile
-            if ((tid & 127) < L::RB)
-                ld[u * L::RB + (tid & 127)] = (tid & 127) < live ? src[(int64_t)j * tq * r + (tid & 127)] : make_float2(0.f, 0.f);
+            ld[u * 2 * L::RB + (tid & 127)] = ahead;
             asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
-            const float4* col = (const float4*)(ld + u * L::RB);   // two rows
+            ahead = fetch(j + 2);
+            const ulonglong2* col = (const ulonglong2*)(ld + u * 2 * L::RB);   // -lse of four rows; -delta 16 further
             // the first row (column) that sees this key
             const int lo = (key - key0 - j * tq) * r;
             wait(sfull + w, u, guard);
@@ -244,11 +260,13 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             float p[64];
             tmem_ld64(ts, p);
 #pragma unroll
-            for (int x = 0; x < 64; x += 2) {
-                const float4 c = col[x / 2];
-                p[x] = ex2_approx(fmaf(p[x], sl, -c.x));
-                p[x + 1] = ex2_approx(fmaf(p[x + 1], sl, -c.z));
+            for (int x = 0; x < 64; x += 4) {
+                const ulonglong2 c = col[x / 4];
+                unpair(fma2(pair(p[x], p[x + 1]), sl2, c.x), p[x], p[x + 1]);
+                unpair(fma2(pair(p[x + 2], p[x + 3]), sl2, c.y), p[x + 2], p[x + 3]);
             }
+#pragma unroll
+            for (int x = 0; x < 64; ++x) p[x] = ex2_approx(p[x]);
             const bool edge = j * tq < L::KEYS || live < L::RB;   // warp-uniform
             if (edge)
 #pragma unroll
@@ -268,10 +286,10 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 float g[32];
                 tmem_ld32(tp + hlf * 32, g);
 #pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                    const float4 c = col[hlf * 16 + x / 2];
-                    g[x] = p[hlf * 32 + x] * (g[x] - c.y);
-                    g[x + 1] = p[hlf * 32 + x + 1] * (g[x + 1] - c.w);
+                for (int x = 0; x < 32; x += 4) {
+                    const ulonglong2 c = col[16 + hlf * 8 + x / 4];
+                    unpair(mul2(pair(p[hlf * 32 + x], p[hlf * 32 + x + 1]), add2(pair(g[x], g[x + 1]), c.x)), g[x], g[x + 1]);
+                    unpair(mul2(pair(p[hlf * 32 + x + 2], p[hlf * 32 + x + 3]), add2(pair(g[x + 2], g[x + 3]), c.y)), g[x + 2], g[x + 3]);
                 }
                 if (edge)   // what a masked dP held may not be finite
 #pragma unroll
@@ -319,7 +337,7 @@ struct Dq {
 template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnBwdArgs b,
-                     const __grid_constant__ Seqs seqs, const float2* rowdata, int* status)
+                     const __grid_constant__ Seqs seqs, const float* nlse, const float* ndelta, int* status)
 {
     using L = Dq<D>;
     const AttnArgs& a = b.f;
@@ -467,14 +485,20 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const uint32_t ts = tmem + L::S_ + t * L::BUF + lanes, tp = tmem + L::P_ + t * L::BUF + lanes;
         const float sl = fabsf(a.scale) * kLog2e;
         const int least = (int)(min(first + t * L::QR + (warp & 3) * 32, all - 1) / r);
-        const float2 rd = real ? rowdata[((int64_t)hk * seqs.tokens() + t0) * rows.r + i] : make_float2(0.f, 0.f);
+        const int64_t rd = ((int64_t)hk * seqs.tokens() + t0) * r + i;
+        const float nl = real ? nlse[rd] : 0.f, nd = real ? ndelta[rd] : 0.f;
+        const uint64_t sl2 = pair(sl, sl), nl2 = pair(nl, nl), nd2 = pair(nd, nd);
         for (int j = 0; j < nt; ++j) {
             wait(sfull + t, j & 1, guard);
             tc_fence_after();
             float p[64];
             tmem_ld64(ts, p);
 #pragma unroll
-            for (int x = 0; x < 64; ++x) p[x] = ex2_approx(fmaf(p[x], sl, -rd.x));
+            for (int x = 0; x < 64; x += 2) {
+                unpair(fma2(pair(p[x], p[x + 1]), sl2, nl2), p[x], p[x + 1]);
+                p[x] = ex2_approx(p[x]);
+                p[x + 1] = ex2_approx(p[x + 1]);
+            }
             wait(gfull + t, j & 1, guard);
             tc_fence_after();
             const bool edge = j * L::KB + L::KB - 1 > least;
@@ -485,7 +509,8 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 float g[32];
                 tmem_ld32(tp + hlf * 32, g);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) g[x] = p[hlf * 32 + x] * (g[x] - rd.y);
+                for (int x = 0; x < 32; x += 2)
+                    unpair(mul2(pair(p[hlf * 32 + x], p[hlf * 32 + x + 1]), add2(pair(g[x], g[x + 1]), nd2)), g[x], g[x + 1]);
                 if (edge)
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
@@ -514,11 +539,12 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 }
 
 template <int D>
-cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float2* rows, int* status, cudaStream_t st)
+cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float* nlse, int* status, cudaStream_t st)
 {
     const AttnArgs& a = b.f;
     const int64_t T = s.tokens();
     const int r = a.H / a.Hkv;
+    float* ndelta = nlse + T * a.H;
     CUtensorMap k128, v128, k64, v64, q, g;
     if (!make_map(&k128, a.k, T, a.Hkv, D, 1, 128) || !make_map(&v128, a.v, T, a.Hkv, D, 1, 128) ||
         !make_map(&k64, a.k, T, a.Hkv, D, 1, 64) || !make_map(&v64, a.v, T, a.Hkv, D, 1, 64) ||
@@ -531,17 +557,18 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float2* rows, int* sta
     {
         ProfileScope prof("attn_delta", st);
         count_launch();
-        attn_delta_kernel<D><<<(unsigned)((T * a.H + 7) / 8), 256, 0, st>>>(a, (const __nv_bfloat16*)b.dout, rows, T);
+        constexpr int PER = 256 / (D / 8) * 4;
+        attn_delta_kernel<D><<<(unsigned)((T * a.H + PER - 1) / PER), 256, 0, st>>>(a, (const __nv_bfloat16*)b.dout, nlse, ndelta, T);
     }
     {
         ProfileScope prof("attn_bwd_keys", st);
         count_launch();
-        attn_bwd_keys_kernel<D><<<dim3(s.slots(128), a.Hkv), 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, rows, status);
+        attn_bwd_keys_kernel<D><<<dim3(s.slots(128), a.Hkv), 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, nlse, ndelta, status);
     }
     {
         ProfileScope prof("attn_bwd_rows", st);
         count_launch();
-        attn_bwd_rows_kernel<D><<<dim3((unsigned)Rows{r}.slots(s, 256), a.Hkv), 384, Dq<D>::SMEM, st>>>(k64, v64, b, s, rows, status);
+        attn_bwd_rows_kernel<D><<<dim3((unsigned)Rows{r}.slots(s, 256), a.Hkv), 384, Dq<D>::SMEM, st>>>(k64, v64, b, s, nlse, ndelta, status);
     }
     return cudaGetLastError();
 }
@@ -556,11 +583,11 @@ bool attn_tc_bwd_supported(const AttnBwdArgs& b)
            attn::aligned16(b.dk) && attn::aligned16(b.dv);
 }
 
-size_t attn_tc_bwd_workspace(int64_t tokens, int H) { return (size_t)tokens * H * sizeof(float2); }
+size_t attn_tc_bwd_workspace(int64_t tokens, int H) { return (size_t)tokens * H * 2 * sizeof(float); }
 
 cudaError_t launch_attn_tc_bwd(const AttnBwdArgs& b, const Seqs& s, void* ws, int* status, cudaStream_t st)
 {
-    return b.f.D == 64 ? attn::backward<64>(b, s, (float2*)ws, status, st) : attn::backward<128>(b, s, (float2*)ws, status, st);
+    return b.f.D == 64 ? attn::backward<64>(b, s, (float*)ws, status, st) : attn::backward<128>(b, s, (float*)ws, status, st);
 }
 
 }  // namespace kda
