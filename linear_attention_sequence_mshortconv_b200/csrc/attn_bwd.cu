@@ -89,7 +89,7 @@ template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g, AttnBwdArgs b,
-                     const __grid_constant__ Seqs seqs, const float* nlse, const float* ndelta, int* status)
+                     const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, const float* ndelta, int* status)
 {
     using L = Keys<D>;
     const AttnArgs& a = b.f;
@@ -103,11 +103,11 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
-    const int hk = blockIdx.y, r = a.H / a.Hkv;
-    int seq, tile;
-    if (!seqs.locate(blockIdx.x, L::KEYS, seq, tile)) return;   // the first tiles have the most rows
+    const int r = a.H / a.Hkv;
+    int hk, seq, rank;
+    tiles.locate(blockIdx.x, hk, seq, rank);
     const int64_t t0 = seqs.start(seq);
-    const int len = seqs.len(seq), key0 = tile * L::KEYS;
+    const int len = seqs.len(seq), key0 = rank * L::KEYS;   // a sequence's first tile has the most rows
     const int tq = L::RB / r;                                // tokens of a tile of rows
     const int n = (len - key0 + tq - 1) / tq;
     const int tail = (len - key0 - (n - 1) * tq) * r;        // rows of the last tile
@@ -337,7 +337,7 @@ struct Dq {
 template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnBwdArgs b,
-                     const __grid_constant__ Seqs seqs, const float* nlse, const float* ndelta, int* status)
+                     const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, const float* ndelta, int* status)
 {
     using L = Dq<D>;
     const AttnArgs& a = b.f;
@@ -351,13 +351,11 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
-    const int hk = blockIdx.y;
-    const Rows rows{a.H / a.Hkv};
-    int seq, tile;
-    if (!rows.locate(seqs, (int64_t)gridDim.x - 1 - blockIdx.x, 2 * L::QR, seq, tile)) return;
+    int hk, seq, rank;
+    tiles.locate(blockIdx.x, hk, seq, rank);
     const int64_t t0 = seqs.start(seq);
     const int len = seqs.len(seq);
-    const uint32_t r = rows.r, all = (uint32_t)len * r, first = (uint32_t)tile * 2 * L::QR;
+    const uint32_t r = a.H / a.Hkv, all = (uint32_t)len * r, first = ((all + 2 * L::QR - 1) / (2 * L::QR) - 1 - rank) * 2 * L::QR;
     auto blocks = [&](int t) {
         const uint32_t r0 = first + t * L::QR;
         return r0 >= all ? 0 : (int)((min(r0 + L::QR, all) - 1) / r / L::KB + 1);
@@ -365,7 +363,7 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int n0 = blocks(0), n1 = blocks(1), n = max(n0, n1);
     const int tail = len - (n - 1) * L::KB;   // keys of the last block
 
-    const RowAt row_at{t0, a.H, hk * rows.r, rows.r, D};
+    const RowAt row_at{t0, a.H, hk * (int)r, (int)r, D};
     auto load = [&](int j) {
         const int s = j % L::STAGES;
         mbar_arrive_expect_tx(full + s, 2 * L::KTILE);
@@ -554,6 +552,7 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float* nlse, int* stat
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attn_bwd_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dq<D>::SMEM);
     if (e != cudaSuccess) return e;
+    Tiles tiles;
     {
         ProfileScope prof("attn_delta", st);
         count_launch();
@@ -563,12 +562,14 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float* nlse, int* stat
     {
         ProfileScope prof("attn_bwd_keys", st);
         count_launch();
-        attn_bwd_keys_kernel<D><<<dim3(s.slots(128), a.Hkv), 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, nlse, ndelta, status);
+        const int64_t ctas = make_tiles(tiles, s, a.Hkv, 1, 128);
+        attn_bwd_keys_kernel<D><<<(unsigned)ctas, 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, tiles, nlse, ndelta, status);
     }
     {
         ProfileScope prof("attn_bwd_rows", st);
         count_launch();
-        attn_bwd_rows_kernel<D><<<dim3((unsigned)Rows{r}.slots(s, 256), a.Hkv), 384, Dq<D>::SMEM, st>>>(k64, v64, b, s, nlse, ndelta, status);
+        const int64_t ctas = make_tiles(tiles, s, a.Hkv, r, 256);
+        attn_bwd_rows_kernel<D><<<(unsigned)ctas, 384, Dq<D>::SMEM, st>>>(k64, v64, b, s, tiles, nlse, ndelta, status);
     }
     return cudaGetLastError();
 }

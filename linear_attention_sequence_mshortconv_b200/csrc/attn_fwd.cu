@@ -83,7 +83,7 @@ __device__ __forceinline__ float max_of(const float (&s)[64])
 template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnArgs a,
-                const __grid_constant__ Seqs seqs, int* status)
+                const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, int* status)
 {
     using L = Fwd<D>;
     extern __shared__ char raw[];
@@ -96,21 +96,19 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
-    const int hk = blockIdx.y;
-    const Rows rows{a.H / a.Hkv};
-    int seq, tile;
-    // the last tiles of a sequence have the most keys: they start first
-    if (!rows.locate(seqs, (int64_t)gridDim.x - 1 - blockIdx.x, 2 * QR, seq, tile)) return;
+    int hk, seq, rank;
+    tiles.locate(blockIdx.x, hk, seq, rank);
     const int64_t t0 = seqs.start(seq);
     const int len = seqs.len(seq);
-    const uint32_t r = rows.r, all = (uint32_t)len * r, first = (uint32_t)tile * 2 * QR;
+    // a sequence's last tile has the most keys
+    const uint32_t r = a.H / a.Hkv, all = (uint32_t)len * r, first = ((all + 2 * QR - 1) / (2 * QR) - 1 - rank) * 2 * QR;
     auto blocks = [&](int t) {   // key blocks tile t sees
         const uint32_t r0 = first + t * QR;
         return r0 >= all ? 0 : (int)((min(r0 + QR, all) - 1) / r / KB + 1);
     };
     const int n0 = blocks(0), n1 = blocks(1), n = max(n0, n1);
 
-    const RowAt row_at{t0, a.H, hk * rows.r, rows.r, D};
+    const RowAt row_at{t0, a.H, hk * (int)r, (int)r, D};
 
     auto load_k = [&](int j) {
         const int s = j % L::STAGES;
@@ -349,9 +347,11 @@ cudaError_t forward(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t 
     auto kern = attn_fwd_kernel<D>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
+    Tiles tiles;
+    const int64_t ctas = make_tiles(tiles, s, a.Hkv, a.H / a.Hkv, 2 * QR);
     ProfileScope prof("attn_fwd", st);
     count_launch();
-    kern<<<dim3((unsigned)Rows{a.H / a.Hkv}.slots(s, 2 * QR), a.Hkv), L::THREADS, L::SMEM, st>>>(k, v, a, s, status);
+    kern<<<(unsigned)ctas, L::THREADS, L::SMEM, st>>>(k, v, a, s, tiles, status);
     return cudaGetLastError();
 }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }

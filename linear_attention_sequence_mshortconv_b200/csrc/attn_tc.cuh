@@ -2,6 +2,7 @@
 // swizzled tiles, their MMA descriptors, bounded waits.
 #pragma once
 
+#include <algorithm>
 #include <mutex>
 
 #include "mixers.h"
@@ -132,26 +133,53 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real)
 // [tokens, heads, D] bf16, box = `rows` tokens x r heads x 64 values, landing as a panel
 bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int r, int rows);
 
-// ---- rows of a key/value head's query group -----------------------------------------------
+// ---- tiles of a launch --------------------------------------------------------------------
 // The query heads that share a key/value head are rows of one matrix: row i is token i / r, head
-// i % r of the group (r = H / Hkv).  Tiles of rows of a sequence are numbered like Seqs's tiles
-// of tokens.
-struct Rows {
-    int r;
-    __host__ __device__ int64_t slot0(const Seqs& s, int i, int R) const { return (int64_t)s.start(i) * r / R + i; }
-    __host__ int64_t slots(const Seqs& s, int R) const { return (int64_t)s.tokens() * r / R + s.n; }
-    __device__ bool locate(const Seqs& s, int64_t slot, int R, int& seq, int& tile) const
+// i % r of the group (r = H / Hkv).  A launch has one CTA per tile of R rows (or keys, r = 1) and
+// key/value head.  Tiles of one sequence differ in work from none to the whole sequence, so they
+// start in order of it, or a heavy one that comes last runs alone: equal rows tile by tile, packed
+// samples from the longest on, all heads of a tile together.
+struct Tiles {
+    int n, heads;
+    int per;                       // >= 0: equal rows of `per` tiles; < 0: packed
+    uint8_t seq[kMaxSeqs];         // samples by length
+    int32_t first[kMaxSeqs + 1];   // their first tiles
+    // CTA -> head, sequence and how many tiles of the sequence start before this one
+    __device__ __forceinline__ void locate(int block, int& head, int& s, int& rank) const
     {
-        int lo = 0, hi = s.n - 1;
+        head = block % heads;
+        const int b = block / heads;
+        if (per >= 0) {
+            s = b % n;
+            rank = b / n;
+            return;
+        }
+        int lo = 0, hi = n - 1;   // the last sample whose first tile is <= b
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (slot0(s, mid, R) <= slot) lo = mid; else hi = mid - 1;
+            if (first[mid] <= b) lo = mid; else hi = mid - 1;
         }
-        seq = lo;
-        tile = (int)(slot - slot0(s, lo, R));
-        return (int64_t)tile * R < (int64_t)s.len(lo) * r;
+        s = seq[lo];
+        rank = b - first[lo];
     }
 };
+inline int tiles_of(int len, int r, int R) { return (int)(((int64_t)len * r + R - 1) / R); }
+// returns the number of CTAs
+inline int64_t make_tiles(Tiles& t, const Seqs& s, int heads, int r, int R)
+{
+    t.n = s.n;
+    t.heads = heads;
+    if (s.T >= 0) {
+        t.per = tiles_of(s.T, r, R);
+        return (int64_t)t.per * s.n * heads;
+    }
+    t.per = -1;
+    for (int i = 0; i < s.n; ++i) t.seq[i] = (uint8_t)i;
+    std::sort(t.seq, t.seq + s.n, [&](uint8_t x, uint8_t y) { return s.len(x) != s.len(y) ? s.len(x) > s.len(y) : x < y; });
+    t.first[0] = 0;
+    for (int i = 0; i < s.n; ++i) t.first[i + 1] = t.first[i] + tiles_of(s.len(t.seq[i]), r, R);
+    return (int64_t)t.first[s.n] * heads;
+}
 // Rows of one sequence and group: the offset of row i in a [tokens, H, D] tensor.  A tensor that
 // fits the device has fewer than 2^32 rows of 64 values, so rows count in 32 bits.
 struct RowAt {
