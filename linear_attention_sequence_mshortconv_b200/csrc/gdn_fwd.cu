@@ -26,32 +26,109 @@ namespace gdn {
 
 // ---- prologue: T, P and the gates of each chunk -----------------------------------------
 // KK^T and QK^T are bf16 MMAs (exact products, fp32 sums), shared by the value heads of a key
-// head.  The unit lower triangular I + A is inverted in fp32: the two 32x32 diagonal blocks by
-// forward substitution, a column to a lane; then T21 = -T22 (A21 T11).  A 64-column
-// substitution would leave half the warps idle and is twice as long.
+// head.  The unit lower triangular I + A is inverted in fp32: the four 16x16 diagonal blocks by
+// forward substitution, a warp each, a column to a lane; then twice T21 = -T22 (A21 T11), on
+// the two 32x32 and on the one 64x64 block.  Nothing here waits for another chunk, so what bounds
+// it is the latency of these steps against the warps an SM holds: A and T take the place of K and
+// Q, and 102 registers a thread let five CTAs share an SM.
+constexpr int ALD = 68;   // row of A and T in floats: rows of a warp's reads fall in different banks
 template <int DK>
-constexpr int pro_smem() { return 2 * C * DK * 2 + 2 * C * 68 * 4 + 5 * C * 4; }
+constexpr int pro_smem()
+{
+    constexpr int tiles = 2 * C * DK * 2, at = 2 * C * ALD * 4;
+    return (tiles > at ? tiles : at) + 4 * 3 * C * 4;
+}
+
+// One thread's share of X = A B (fp32, row-major with ALD): rows i and, if TWO, i + 16, columns
+// c .. c + 3, K terms.
+template <int K, bool TWO>
+__device__ __forceinline__ void small_mm(const float (*A)[ALD], const float (*B)[ALD], int i, int c, float (&x)[2][4])
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[0][e] = x[1][e] = 0.f;
+#pragma unroll
+    for (int m = 0; m < K; m += 4) {
+        float a[2][4];
+#pragma unroll
+        for (int q = 0; q < (TWO ? 2 : 1); ++q) {
+            const float4 v = *(const float4*)&A[i + 16 * q][m];
+            a[q][0] = v.x; a[q][1] = v.y; a[q][2] = v.z; a[q][3] = v.w;
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const float4 v = *(const float4*)&B[m + z][c];
+#pragma unroll
+            for (int q = 0; q < (TWO ? 2 : 1); ++q) {
+                x[q][0] = fmaf(a[q][z], v.x, x[q][0]); x[q][1] = fmaf(a[q][z], v.y, x[q][1]);
+                x[q][2] = fmaf(a[q][z], v.z, x[q][2]); x[q][3] = fmaf(a[q][z], v.w, x[q][3]);
+            }
+        }
+    }
+}
 
 template <int DK, int PP>
-__global__ void __launch_bounds__(128) gdn_prologue_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, char* records)
+__global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, char* records)
 {
     extern __shared__ __align__(128) char sm[];
-    __nv_bfloat16* sK = (__nv_bfloat16*)sm;
-    __nv_bfloat16* sQ = sK + C * DK;
-    float (*A)[68] = (float (*)[68])(sm + 2 * C * DK * 2);
-    float (*T)[68] = A + C;
-    float* ch = (float*)(T + C);   // cum log2(e), as a sum of two floats
-    float* cl = ch + C;
-    float* bet = cl + C;
+    float (*A)[ALD] = (float (*)[ALD])sm;
+    float (*T)[ALD] = A + C;
+    // of up to four heads: cum log2(e), as a sum of two floats, and beta
+    float* gates = (float*)(sm + pro_smem<DK>() - 4 * 3 * C * 4);
     int seq, c;
     if (!seqs.locate(blockIdx.x, C, seq, c)) return;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, hk = blockIdx.y, r = a.Hv / a.Hk;
     const int valid = min(C, seqs.len(seq) - c * C);
     const int64_t t0 = (int64_t)seqs.start(seq) + c * C;
-    const uint32_t uK = smem_addr(sK), uQ = smem_addr(sQ);
+    const uint32_t uK = smem_addr(sm), uQ = uK + C * DK * 2;
     load_tile<DK, 128>(uK, (const __nv_bfloat16*)a.k + (t0 * a.Hk + hk) * DK, (int64_t)a.Hk * DK, valid, tid);
     load_tile<DK, 128>(uQ, (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK, (int64_t)a.Hk * DK, valid, tid);
     cp_async_commit();
+
+    // a warp per head: inclusive sum of the gates in 64 bits, two tokens a lane
+    auto sum_gates = [&](int h) {
+        float* scal = (float*)(records + ((int64_t)blockIdx.x * a.Hv + h) * rec_bytes(PP) + rec_scal(PP));
+        double s[2];
+        float b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const int64_t off = (t0 + t) * a.Hv + h;
+            // e^g is 0 in fp32 below -104: the clamp keeps sums finite for g = -inf
+            s[i] = t < valid ? (double)fmaxf(to_f32(((const __nv_bfloat16*)a.g)[off]), -1000.f) : 0.0;
+            b[i] = t < valid ? to_f32(((const __nv_bfloat16*)a.beta)[off]) : 0.f;
+        }
+        double sum = s[0] + s[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double x = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += x;
+        }
+        const double c1 = sum * 1.4426950408889634, c0 = (sum - s[1]) * 1.4426950408889634;
+        const double last = __shfl_sync(~0u, c1, 31);
+        const double cum[2] = {c0, c1};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const float hi = (float)cum[i], lo = (float)(cum[i] - (double)hi);
+            float* g = gates + (h & 3) * 3 * C;
+            g[t] = hi;
+            g[C + t] = lo;
+            g[2 * C + t] = b[i];
+            scal[t] = exp2f(hi);
+            scal[C + t] = exp2f((float)(last - cum[i]));
+            scal[2 * C + t] = b[i];
+            if (PP == 2) {
+                scal[3 * C + t] = hi;
+                scal[4 * C + t] = lo;
+            }
+        }
+    };
+    // heads hk r .. hk r + r - 1 in groups that share h / 4: slot h & 3 of `gates`, warp h & 3
+    auto gates_from = [&](int h) {
+        const int mine = (h & ~3) + w;
+        if (mine >= h && mine < hk * r + r) sum_gates(mine);
+    };
+    gates_from(hk * r);
     cp_async_wait_all();
     __syncthreads();
 
@@ -74,67 +151,39 @@ __global__ void __launch_bounds__(128) gdn_prologue_kernel(GdnArgs a, const __gr
             mma(qk[2 * jb + 1], aq, b[2], b[3]);
         }
     }
+    __syncthreads();   // K and Q have been read: A and T take their place
     const int g4 = lane >> 2, t2 = (lane & 3) * 2;
     for (int h = hk * r; h < hk * r + r; ++h) {
         char* rec = records + ((int64_t)blockIdx.x * a.Hv + h) * rec_bytes(PP);
-        float* scal = (float*)(rec + rec_scal(PP));
-        if (w == 0) {   // inclusive sum of the gates in 64 bits, two tokens a lane
-            double s[2];
-            float b[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                const int64_t off = (t0 + t) * a.Hv + h;
-                // e^g is 0 in fp32 below -104: the clamp keeps sums finite for g = -inf
-                s[i] = t < valid ? (double)fmaxf(to_f32(((const __nv_bfloat16*)a.g)[off]), -1000.f) : 0.0;
-                b[i] = t < valid ? to_f32(((const __nv_bfloat16*)a.beta)[off]) : 0.f;
-            }
-            double sum = s[0] + s[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_up_sync(~0u, sum, o);
-                if (lane >= o) sum += x;
-            }
-            const double c1 = sum * 1.4426950408889634, c0 = (sum - s[1]) * 1.4426950408889634;
-            const double last = __shfl_sync(~0u, c1, 31);
-            const double cum[2] = {c0, c1};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                ch[t] = (float)cum[i];
-                cl[t] = (float)(cum[i] - (double)(float)cum[i]);
-                bet[t] = b[i];
-                scal[t] = exp2f((float)cum[i]);
-                scal[C + t] = exp2f((float)(last - cum[i]));
-                scal[2 * C + t] = b[i];
-                if (PP == 2) {
-                    scal[3 * C + t] = ch[t];
-                    scal[4 * C + t] = cl[t];
-                }
-            }
+        if (h > hk * r && (h & 3) == 0) {
+            gates_from(h);
+            __syncthreads();
         }
-        __syncthreads();
+        const float* ch = gates + (h & 3) * 3 * C;
+        const float *cl = ch + C, *bet = cl + C;
         // A to shared memory, P to the record
         const int i0 = w * 16 + g4, i1 = i0 + 8;
         const float h0 = ch[i0], h1 = ch[i1], l0 = cl[i0], l1 = cl[i1], b0 = bet[i0], b1 = bet[i1];
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             if (n > 2 * w + 1) break;
-            float p[4];
+            const int j = n * 8 + t2;
+            const float2 hj = *(const float2*)&ch[j], lj = *(const float2*)&cl[j];
+            float d[4] = {ex2_approx((h0 - hj.x) + (l0 - lj.x)), ex2_approx((h0 - hj.y) + (l0 - lj.y)),
+                          ex2_approx((h1 - hj.x) + (l1 - lj.x)), ex2_approx((h1 - hj.y) + (l1 - lj.y))};
+            if (n >= 2 * w) {   // the diagonal block
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int j = n * 8 + t2 + e;
-                const float hj = ch[j], lj = cl[j];
-                const float d0 = j <= i0 ? exp2f((h0 - hj) + (l0 - lj)) : 0.f;
-                const float d1 = j <= i1 ? exp2f((h1 - hj) + (l1 - lj)) : 0.f;
-                A[i0][j] = j < i0 ? b0 * d0 * kk[n][e] : 0.f;
-                A[i1][j] = j < i1 ? b1 * d1 * kk[n][2 + e] : 0.f;
-                p[e] = d0 * qk[n][e];
-                p[2 + e] = d1 * qk[n][2 + e];
+                for (int e = 0; e < 4; ++e)
+                    if (j + (e & 1) > (e < 2 ? i0 : i1)) d[e] = 0.f;
+                *(float2*)&A[i0][j] = make_float2(j < i0 ? b0 * d[0] * kk[n][0] : 0.f, j + 1 < i0 ? b0 * d[1] * kk[n][1] : 0.f);
+                *(float2*)&A[i1][j] = make_float2(j < i1 ? b1 * d[2] * kk[n][2] : 0.f, j + 1 < i1 ? b1 * d[3] * kk[n][3] : 0.f);
+            } else {
+                *(float2*)&A[i0][j] = make_float2(b0 * d[0] * kk[n][0], b0 * d[1] * kk[n][1]);
+                *(float2*)&A[i1][j] = make_float2(b1 * d[2] * kk[n][2], b1 * d[3] * kk[n][3]);
             }
             uint32_t lo[PP], hi[PP];
-            split<PP>(p[0], p[1], lo);
-            split<PP>(p[2], p[3], hi);
+            split<PP>(d[0] * qk[n][0], d[1] * qk[n][1], lo);
+            split<PP>(d[2] * qk[n][2], d[3] * qk[n][3], hi);
             char* dst = rec + rec_p(PP) + blk(w, n >> 1) + (n & 1) * 128 + g4 * 16 + t2 * 2;
 #pragma unroll
             for (int q = 0; q < PP; ++q) {
@@ -142,50 +191,50 @@ __global__ void __launch_bounds__(128) gdn_prologue_kernel(GdnArgs a, const __gr
                 *(uint32_t*)(dst + q * TRI + 256) = hi[q];
             }
         }
-        __syncthreads();
-        if (w < 2) {   // inverse of diagonal block w, column `lane`
-            const int base = 32 * w;
-            float x[32];
+        __syncwarp();   // a warp's diagonal block is its own
+        if (lane < 16) {
+            const int base = 16 * w;
+            float x[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                float s0 = i == lane ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            for (int i = 0; i < 16; ++i) {
+                float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
                 for (int m = 0; m < i; m += 4) {   // entries at and right of the diagonal are 0
                     const float4 v = *(const float4*)&A[base + i][base + m];
                     s0 = fmaf(-v.x, x[m], s0);
                     if (m + 1 < i) s1 = fmaf(-v.y, x[m + 1], s1);
-                    if (m + 2 < i) s2 = fmaf(-v.z, x[m + 2], s2);
-                    if (m + 3 < i) s3 = fmaf(-v.w, x[m + 3], s3);
+                    if (m + 2 < i) s0 = fmaf(-v.z, x[m + 2], s0);
+                    if (m + 3 < i) s1 = fmaf(-v.w, x[m + 3], s1);
                 }
-                x[i] = (s0 + s1) + (s2 + s3);
+                x[i] = s0 + s1;
                 T[base + i][base + lane] = x[i];
             }
         }
         __syncthreads();
-        const int row = tid >> 2, col = (tid & 3) * 8;   // 8 entries of a 32x32 product
-        float z[8] = {};
-#pragma unroll 4
-        for (int m = 0; m < 32; ++m) {
-            const float x = A[32 + row][m];
-            const float4 u = *(const float4*)&T[m][col], v = *(const float4*)&T[m][col + 4];
-            z[0] = fmaf(x, u.x, z[0]); z[1] = fmaf(x, u.y, z[1]); z[2] = fmaf(x, u.z, z[2]); z[3] = fmaf(x, u.w, z[3]);
-            z[4] = fmaf(x, v.x, z[4]); z[5] = fmaf(x, v.y, z[5]); z[6] = fmaf(x, v.z, z[6]); z[7] = fmaf(x, v.w, z[7]);
+        // the products A21 T11 go to blocks above A's diagonal, which nothing else uses
+        float x[2][4];
+        {
+            const int p = (tid >> 6) * 32, i = (tid >> 2) & 15, cc = (tid & 3) * 4;   // two 32x32 blocks
+            auto at = [&](float (*M)[ALD], int ro, int co) { return (float (*)[ALD])&M[ro][co]; };
+            small_mm<16, false>(at(A, p + 16, p), at(T, p, p), i, cc, x);
+            *(float4*)&A[p + i][p + 16 + cc] = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+            __syncthreads();
+            small_mm<16, false>(at(T, p + 16, p + 16), at(A, p, p + 16), i, cc, x);
+            *(float4*)&T[p + 16 + i][p + cc] = make_float4(-x[0][0], -x[0][1], -x[0][2], -x[0][3]);
+            __syncthreads();
+            const int i2 = (tid >> 3) & 15, c2 = (tid & 7) * 4;   // the 64x64 block: rows i2, i2 + 16
+            // T's 32x32 diagonal blocks are 0 above their own 16x16 ones
+            if (tid < 64) *(float4*)&T[(tid >> 5) * 32 + (tid & 15)][(tid >> 5) * 32 + 16 + ((tid >> 4) & 1) * 8] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (tid < 64) *(float4*)&T[(tid >> 5) * 32 + (tid & 15)][(tid >> 5) * 32 + 20 + ((tid >> 4) & 1) * 8] = make_float4(0.f, 0.f, 0.f, 0.f);
+            __syncthreads();
+            small_mm<32, true>(at(A, 32, 0), at(T, 0, 0), i2, c2, x);
+            *(float4*)&A[i2][32 + c2] = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+            *(float4*)&A[i2 + 16][32 + c2] = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
+            __syncthreads();
+            small_mm<32, true>(at(T, 32, 32), at(A, 0, 32), i2, c2, x);
+            *(float4*)&T[32 + i2][c2] = make_float4(-x[0][0], -x[0][1], -x[0][2], -x[0][3]);
+            *(float4*)&T[48 + i2][c2] = make_float4(-x[1][0], -x[1][1], -x[1][2], -x[1][3]);
         }
-        // A21 T11 goes where A's upper left block was: no one reads that any more
-        *(float4*)&A[row][col] = make_float4(z[0], z[1], z[2], z[3]);
-        *(float4*)&A[row][col + 4] = make_float4(z[4], z[5], z[6], z[7]);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = 0.f;
-#pragma unroll 4
-        for (int m = 0; m < 32; ++m) {
-            const float x = T[32 + row][32 + m];
-            const float4 u = *(const float4*)&A[m][col], v = *(const float4*)&A[m][col + 4];
-            z[0] = fmaf(-x, u.x, z[0]); z[1] = fmaf(-x, u.y, z[1]); z[2] = fmaf(-x, u.z, z[2]); z[3] = fmaf(-x, u.w, z[3]);
-            z[4] = fmaf(-x, v.x, z[4]); z[5] = fmaf(-x, v.y, z[5]); z[6] = fmaf(-x, v.z, z[6]); z[7] = fmaf(-x, v.w, z[7]);
-        }
-        *(float4*)&T[32 + row][col] = make_float4(z[0], z[1], z[2], z[3]);
-        *(float4*)&T[32 + row][col + 4] = make_float4(z[4], z[5], z[6], z[7]);
         __syncthreads();
         // the ten blocks, 128 pairs each, as planes
         const int ii = ((tid >> 6) << 3) + ((tid >> 2) & 7), jj = (((tid >> 5) & 1) << 3) + (tid & 3) * 2;
