@@ -544,13 +544,12 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float* nlse, int* stat
     const int r = a.H / a.Hkv;
     float* ndelta = nlse + T * a.H;
     CUtensorMap k128, v128, k64, v64, q, g;
-    if (!make_map(&k128, a.k, T, a.Hkv, D, 1, 128) || !make_map(&v128, a.v, T, a.Hkv, D, 1, 128) ||
-        !make_map(&k64, a.k, T, a.Hkv, D, 1, 64) || !make_map(&v64, a.v, T, a.Hkv, D, 1, 64) ||
-        !make_map(&q, a.q, T, a.H, D, r, 64 / r) || !make_map(&g, b.dout, T, a.H, D, r, 64 / r))
+    if (!make_map(&k128, a.k, T, a.Hkv, D, 64, 1, 128) || !make_map(&v128, a.v, T, a.Hkv, D, 64, 1, 128) ||
+        !make_map(&k64, a.k, T, a.Hkv, D, 64, 1, 64) || !make_map(&v64, a.v, T, a.Hkv, D, 64, 1, 64) ||
+        !make_map(&q, a.q, T, a.H, D, 64, r, 64 / r) || !make_map(&g, b.dout, T, a.H, D, 64, r, 64 / r))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attn_bwd_keys_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Keys<D>::SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attn_bwd_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dq<D>::SMEM);
+    cudaError_t e = allow_smem<attn_bwd_keys_kernel<D>>(Keys<D>::SMEM);
+    if (e == cudaSuccess) e = allow_smem<attn_bwd_rows_kernel<D>>(Dq<D>::SMEM);
     if (e != cudaSuccess) return e;
     Tiles tiles;
     {

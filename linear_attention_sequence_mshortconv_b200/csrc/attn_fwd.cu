@@ -26,30 +26,6 @@
 namespace kda {
 namespace attn {
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int r, int rows)
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)r, (cuuint32_t)rows}, es[3] = {1u, 1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 namespace {
 
 constexpr int QR = 128;   // rows of a tile
@@ -342,16 +318,15 @@ cudaError_t forward(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t 
 {
     using L = Fwd<D>;
     CUtensorMap k, v;
-    if (!make_map(&k, a.k, s.tokens(), a.Hkv, D, 1, KB) || !make_map(&v, a.v, s.tokens(), a.Hkv, D, 1, KB))
+    if (!make_map(&k, a.k, s.tokens(), a.Hkv, D, 64, 1, KB) || !make_map(&v, a.v, s.tokens(), a.Hkv, D, 64, 1, KB))
         return cudaErrorInvalidValue;
-    auto kern = attn_fwd_kernel<D>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    const cudaError_t e = allow_smem<attn_fwd_kernel<D>>(L::SMEM);
     if (e != cudaSuccess) return e;
     Tiles tiles;
     const int64_t ctas = make_tiles(tiles, s, a.Hkv, a.H / a.Hkv, 2 * QR);
     ProfileScope prof("attn_fwd", st);
     count_launch();
-    kern<<<(unsigned)ctas, L::THREADS, L::SMEM, st>>>(k, v, a, s, tiles, status);
+    attn_fwd_kernel<D><<<(unsigned)ctas, L::THREADS, L::SMEM, st>>>(k, v, a, s, tiles, status);
     return cudaGetLastError();
 }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }

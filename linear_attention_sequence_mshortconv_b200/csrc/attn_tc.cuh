@@ -3,7 +3,6 @@
 #pragma once
 
 #include <algorithm>
-#include <mutex>
 
 #include "mixers.h"
 #include "sm100.cuh"
@@ -129,9 +128,6 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
-
-// [tokens, heads, D] bf16, box = `rows` tokens x r heads x 64 values, landing as a panel
-bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int r, int rows);
 
 // ---- tiles of a launch --------------------------------------------------------------------
 // The query heads that share a key/value head are rows of one matrix: row i is token i / r, head

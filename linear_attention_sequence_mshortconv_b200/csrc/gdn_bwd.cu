@@ -712,7 +712,7 @@ cudaError_t rscan(const GdnBwdArgs& a, const Seqs& s, const void* records, void*
 {
     using L = RScan<DK, MT>;
     auto kern = gdn_rscan_kernel<DK, MT>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    const cudaError_t e = allow_smem<gdn_rscan_kernel<DK, MT>>(L::SMEM);
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_rscan", st);
     count_launch();
@@ -725,7 +725,7 @@ cudaError_t grads(const GdnBwdArgs& a, const Seqs& s, const void* records, const
 {
     using L = Grads<DK, DV>;
     auto kern = gdn_grads_kernel<DK, DV>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    const cudaError_t e = allow_smem<gdn_grads_kernel<DK, DV>>(L::SMEM);
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_grads", st);
     count_launch();
@@ -751,7 +751,7 @@ size_t gdn_tc_bwd_workspace(const Seqs& s, int Hv, int Dk, int Dv)
     return gdn::rec_part(s, Hv) + gdn::kept_part(s, Hv, Dk, Dv) + (size_t)s.n * Hv * Dk * Dv * sizeof(float);
 }
 
-cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& b, const Seqs& s, void* ws, int sms, cudaStream_t st)
+cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& b, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st)
 {
     using namespace gdn;
     char* records = (char*)ws;

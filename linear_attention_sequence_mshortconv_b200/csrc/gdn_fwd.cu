@@ -257,14 +257,15 @@ cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int 
     const dim3 grid(s.slots(C), a.Hk);
     ProfileScope prof("gdn_prologue", st);
     count_launch();
-    auto go = [&](auto kern, int smem) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
+    auto go = [&](auto kern, cudaError_t allowed, int smem) {
+        if (allowed != cudaSuccess) return allowed;
         kern<<<grid, 128, smem, st>>>(a, s, (char*)records);
         return cudaGetLastError();
     };
-    if (a.Dk == 64) return PP == 1 ? go(gdn_prologue_kernel<64, 1>, pro_smem<64>()) : go(gdn_prologue_kernel<64, 2>, pro_smem<64>());
-    return PP == 1 ? go(gdn_prologue_kernel<128, 1>, pro_smem<128>()) : go(gdn_prologue_kernel<128, 2>, pro_smem<128>());
+#define KDA_PROLOGUE(DK, PP) go(gdn_prologue_kernel<DK, PP>, allow_smem<gdn_prologue_kernel<DK, PP>>(pro_smem<DK>()), pro_smem<DK>())
+    if (a.Dk == 64) return PP == 1 ? KDA_PROLOGUE(64, 1) : KDA_PROLOGUE(64, 2);
+    return PP == 1 ? KDA_PROLOGUE(128, 1) : KDA_PROLOGUE(128, 2);
+#undef KDA_PROLOGUE
 }
 
 // ---- scan ---------------------------------------------------------------------------------
@@ -551,7 +552,7 @@ cudaError_t scan(const GdnArgs& a, const Seqs& s, const void* records, void* kep
 {
     using L = Scan<DK, MT, KEEP>;
     auto kern = gdn_scan_kernel<DK, MT, KEEP>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    const cudaError_t e = allow_smem<gdn_scan_kernel<DK, MT, KEEP>>(L::SMEM);
     if (e != cudaSuccess) return e;
     ProfileScope prof(KEEP ? "gdn_scan_keep" : "gdn_scan", st);
     count_launch();
@@ -584,7 +585,7 @@ bool gdn_tc_supported(const GdnArgs& a)
 
 size_t gdn_tc_workspace(const Seqs& s, int Hv) { return (size_t)s.slots(gdn::C) * Hv * gdn::rec_bytes(1); }
 
-cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, cudaStream_t st)
+cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st)
 {
     cudaError_t e = cudaSuccess;
     if (s.tokens() > 0) e = gdn::launch_prologue(a, s, ws, 1, st);

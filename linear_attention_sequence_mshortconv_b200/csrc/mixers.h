@@ -1,7 +1,10 @@
 // Internal declarations of the gated delta rule and of causal attention (not installed).
 #pragma once
 
+#include <cuda.h>
 #include <stddef.h>
+
+#include <atomic>
 
 #include "internal.h"
 
@@ -45,6 +48,25 @@ struct Seqs {
     }
 };
 
+// Tensor map of a [tokens, heads, D] bf16 tensor (16-byte aligned), box = rows tokens x box_heads heads
+// x cols values.  cols = 64 lands as rows of 128 bytes whose eight 16-byte pieces are permuted by
+// the row's low three bits (the 128-byte swizzle); other widths land as they are.
+bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int D, int cols, int box_heads, int rows);
+
+// Lets a kernel use `bytes` of dynamic shared memory; asked of the driver once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+    return e;
+}
+
 // ---- gated delta rule ---------------------------------------------------------------
 struct GdnArgs {
     const void *q, *k, *v, *g, *beta;   // [tokens, Hk, Dk] x 2, [tokens, Hv, Dv], [tokens, Hv] x 2
@@ -66,10 +88,10 @@ cudaError_t launch_gdn_recurrent(const GdnArgs& a, const Seqs& s, cudaStream_t s
 // tensor cores (bf16, Dk = 64 or 128, 16-byte aligned tensors)
 bool gdn_tc_supported(const GdnArgs& a);
 size_t gdn_tc_workspace(const Seqs& s, int Hv);
-cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, cudaStream_t st);
+cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st);
 bool gdn_tc_bwd_supported(const GdnBwdArgs& a);
 size_t gdn_tc_bwd_workspace(const Seqs& s, int Hv, int Dk, int Dv);
-cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& a, const Seqs& s, void* ws, int sms, cudaStream_t st);
+cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& a, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st);
 size_t gdn_generic_bwd_workspace(int slots16, int tokens, int Hv, int Dk, int Dv);
 cudaError_t launch_gdn_generic_bwd(const GdnBwdArgs& a, const Seqs& s, void* ws, cudaStream_t st);
 

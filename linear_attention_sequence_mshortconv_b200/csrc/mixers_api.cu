@@ -142,9 +142,11 @@ kda_status run_gdn_forward(const GdnArgs& a, const Batch& b, void* workspace, si
     if (st != KDA_OK) return st;
     const bool tc = gdn_tc_supported(a);
     const int sms = num_sms();
+    int* status = tc ? device_status_ptr() : nullptr;
+    if (tc && !status) return KDA_ERR_CUDA;
     return each_group(b, [&](const Seqs& s, int seq, int64_t token) {
         const GdnArgs x = moved(a, seq, token);
-        return from_cuda(tc ? launch_gdn_tc(x, s, ws.ptr, sms, (cudaStream_t)stream)
+        return from_cuda(tc ? launch_gdn_tc(x, s, ws.ptr, sms, status, (cudaStream_t)stream)
                             : launch_gdn_recurrent(x, s, (cudaStream_t)stream));
     });
 }
@@ -171,6 +173,8 @@ kda_status run_gdn_backward(const GdnBwdArgs& a, const Batch& b, void* workspace
     if (st != KDA_OK) return st;
     const bool tc = gdn_tc_bwd_supported(a);
     const int sms = num_sms();
+    int* status = tc ? device_status_ptr() : nullptr;
+    if (tc && !status) return KDA_ERR_CUDA;
     return each_group(b, [&](const Seqs& s, int seq, int64_t token) {
         GdnBwdArgs x = a;
         x.f = moved(a.f, seq, token);
@@ -182,7 +186,7 @@ kda_status run_gdn_backward(const GdnBwdArgs& a, const Batch& b, void* workspace
         x.dv = at(a.dv, token * a.f.Hv * a.f.Dv, a.f.t);
         x.dg = at(a.dg, token * a.f.Hv, a.f.t);
         x.dbeta = at(a.dbeta, token * a.f.Hv, a.f.t);
-        return from_cuda(tc ? launch_gdn_tc_bwd(x, s, ws.ptr, sms, (cudaStream_t)stream)
+        return from_cuda(tc ? launch_gdn_tc_bwd(x, s, ws.ptr, sms, status, (cudaStream_t)stream)
                             : launch_gdn_generic_bwd(x, s, ws.ptr, (cudaStream_t)stream));
     });
 }
