@@ -36,7 +36,7 @@ struct RScan {
     static constexpr int VROW = 32 * MT + 16, SROW = 2 * DK + 16, TROW = 2 * C + 16;
     static constexpr int WROW = DK + 4, PROW = C + 4;                  // floats
     static constexpr int K_ = 0, Q_ = K_ + C * DK * 2, REC = Q_ + C * DK * 2;
-    static constexpr int G_ = REC + rec_bytes(2), STAGE = G_ + C * VROW;
+    static constexpr int G_ = REC + REC_BYTES, STAGE = G_ + C * VROW;
     static constexpr int DP = 2 * STAGE;                               // planes of D [2][16 MT][SROW]
     static constexpr int UP = DP + 2 * 16 * MT * SROW;                 // of dU [2][16 MT][TROW]
     static constexpr int YP = UP + 2 * 16 * MT * TROW;                 // of dY
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
         for (int c = nch - 1; c >= 0; --c) {
             __syncthreads();   // chunk c has landed and D is in place
             const uint32_t st = base + (c & 1) * L::STAGE;
-            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(2));
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL);
             float kd[2][2][4] = {};
 #pragma unroll
             for (int s = 0; s < DK / 16; ++s) {
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
         const __nv_bfloat16* qp = (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK;
         const __nv_bfloat16* gp = (const __nv_bfloat16*)b.dout + (t0 * a.Hv + h) * a.Dv + v0;
         __nv_bfloat16* vp = (__nv_bfloat16*)b.dv + (t0 * a.Hv + h) * a.Dv + v0;
-        const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * rec_bytes(2);
+        const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * REC_BYTES;
         auto load = [&](int c) {
             const uint32_t st = base + (c & 1) * L::STAGE;
             const int valid = min(C, len - c * C);
@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
                 const bool in = row < valid;
                 cp16(st + L::G_ + row * L::VROW + piece * 16, gp + ((int64_t)c * C + (in ? row : 0)) * a.Hv * a.Dv + piece * 8, in);
             }
-            const char* src = rec + (int64_t)c * a.Hv * rec_bytes(2);
-            for (int e = lt; e < rec_bytes(2) / 16; e += LOADERS) cp16(st + L::REC + e * 16, src + e * 16, true);
+            const char* src = rec + (int64_t)c * a.Hv * REC_BYTES;
+            for (int e = lt; e < REC_BYTES / 16; e += LOADERS) cp16(st + L::REC + e * 16, src + e * 16, true);
             cp_async_commit();
         };
         if (nch > 0) load(nch - 1);
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
             cp_async_wait_all();
             __syncthreads();
             const uint32_t st = base + (c & 1) * L::STAGE;
-            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(2));
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL);
             char* dst = mine + c * next;
             // dO^T, 16 columns x 64 tokens, as A operands
             uint32_t g[4][4];
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
                     uint32_t p[2][4];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        ldsm_t(p[q], st + L::REC + rec_p(2) + q * TRI + blk(ib, f) + t_off);
+                        ldsm_t(p[q], st + L::REC + REC_P + q * TRI + blk(ib, f) + t_off);
                         mma(o[0][q], g[ib], p[q][0], p[q][1]);
                         mma(o[1][q], g[ib], p[q][2], p[q][3]);
                     }
@@ -382,14 +382,14 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
     float sq[NK][4] = {}, sk[NK][4] = {};
     for (int h = hk * r; h < hk * r + r; ++h) {
         const char* mine = kept + ((int64_t)blockIdx.x * a.Hv + h) * keep.bytes();
-        const char* rec = records + ((int64_t)blockIdx.x * a.Hv + h) * rec_bytes(2);
+        const char* rec = records + ((int64_t)blockIdx.x * a.Hv + h) * REC_BYTES;
         auto plane = [&](uint32_t dst, size_t off) { load_tile<DK, 256, DV>(dst, (const __nv_bfloat16*)(mine + off), DK, DV, tid); };
         load_tile<DV, 256>(base + L::G_, (const __nv_bfloat16*)b.dout + (t0 * a.Hv + h) * DV, (int64_t)a.Hv * DV, valid, tid);
         for (int p = 0; p < 2; ++p) {
             load_tile<C, 256, DV>(base + L::U_ + p * DV * C * 2, (const __nv_bfloat16*)(mine + keep.u() + p * keep.rows()), C, DV, tid);
             load_tile<C, 256, DV>(base + L::Y_ + p * DV * C * 2, (const __nv_bfloat16*)(mine + keep.y() + p * keep.rows()), C, DV, tid);
         }
-        for (int e = tid; e < 5 * C / 4; e += 256) cp16(base + L::SC + e * 16, rec + rec_scal(2) + e * 16, true);
+        for (int e = tid; e < 5 * C / 4; e += 256) cp16(base + L::SC + e * 16, rec + REC_SCAL + e * 16, true);
         cp_async_commit();
         for (int p = 0; p < 2; ++p) plane(base + L::SB + p * DV * DK * 2, keep.s() + p * keep.state());
         cp_async_commit();
@@ -734,7 +734,7 @@ cudaError_t grads(const GdnBwdArgs& a, const Seqs& s, const void* records, const
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-size_t rec_part(const Seqs& s, int Hv) { return up256((size_t)s.slots(C) * Hv * rec_bytes(2)); }
+size_t rec_part(const Seqs& s, int Hv) { return up256((size_t)s.slots(C) * Hv * REC_BYTES); }
 size_t kept_part(const Seqs& s, int Hv, int Dk, int Dv) { return (size_t)s.slots(C) * Hv * Kept{Dk, Dv}.bytes(); }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 }  // namespace
@@ -761,8 +761,8 @@ cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& b, const Seqs& s, void* ws, int 
     if (s.tokens() > 0) {
         GdnArgs f = b.f;
         f.ST = ST;
-        e = launch_prologue(f, s, records, 2, st);
-        if (e == cudaSuccess) e = launch_scan(f, s, records, kept, sms, st);
+        e = launch_prologue(f, s, records, st);
+        if (e == cudaSuccess) e = whole_heads(f, s, sms) ? launch_chain(f, s, records, kept, status, st) : launch_scan(f, s, records, kept, sms, st);
     }
     const bool wide = (int64_t)s.n * b.f.Hv * (b.f.Dv / 32) >= sms;   // as in the forward scan
     if (e == cudaSuccess)

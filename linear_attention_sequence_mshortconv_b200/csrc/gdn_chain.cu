@@ -1,0 +1,441 @@
+// The forward scan of the gated delta rule on tcgen05 tensor cores (bf16; Dk and Dv 64 or 128), one
+// CTA per sequence and value head.
+//
+// The mathematics, the prologue and the planes are those of gdn_fwd.cu.  There a CTA owns 16 or 32
+// value columns, so a head's K, Q and factors are read once per 16 or 32 columns, and shared
+// memory bounds it as soon as the heads fill the SMs.  Here all Dv columns are the 128 rows of every
+// product: S, Y and U are left operands in tensor memory (lane = value column), and K, Q, T and P
+// are read from shared memory once per chunk and plane.  A chunk takes about as long as there
+// (both are a chain of three products), for 4 to 8 times the columns.
+//
+//   warps 0-7  (two warpgroups, each with half of the columns of every operand): K S -> Y,
+//              U -> decayed U, S -> planes: what lies between the products, in fp32
+//   warps 8-11 the output: O = e^cum o (Q S), to which P U is added, and its store
+//   warp 12    issues the MMAs: K S, Q S | T Y | K^T U, P U
+//   warp 13    the loads of the next chunk
+//
+// Tensor memory (512 columns): S (fp32, Dk), its two planes (Dk), R (128: K S, then the planes of Y,
+// then of decayed U), U (64: the product, then its planes), O (64).  A warpgroup writes planes only
+// where its own half of a product was or where nothing is, so the two need no barrier between them.
+//
+// Every wait is bounded; after one runs out the chain runs to its end on whatever is there.
+
+#include "gdn_tc.cuh"
+#include "tc.cuh"
+
+namespace kda {
+namespace gdn {
+namespace {
+
+using namespace tc;
+
+template <int DK, int DV, bool KEEP>
+struct Chain {
+    static constexpr int THREADS = 448, PANEL = C * 128;
+    static constexpr int K_ = 0, Q_ = K_ + DK / 64 * PANEL, V_ = Q_ + (KEEP ? 0 : DK / 64 * PANEL);
+    static constexpr int REC = V_ + DV / 64 * PANEL, STAGE = (REC + REC_BYTES + 1023) / 1024 * 1024;
+    static constexpr int OUT = 2 * STAGE;                     // [64][DV] bf16
+    static constexpr int BAR = OUT + (KEEP ? 0 : C * DV * 2);
+    // the base is aligned up to 1024 bytes; more than half of an SM's, since each CTA takes all of its
+    // tensor memory
+    static constexpr int SMEM = BAR + 256 + 1024 > 116 * 1024 ? BAR + 256 + 1024 : 116 * 1024;
+    // tensor memory columns
+    static constexpr int M_ = 0, SP_ = DK, R_ = 2 * DK, U_ = R_ + 128, O_ = U_ + 64;
+};
+// plane p of Y (or decayed U), k-step x of 16 tokens: planes 0 and 1 whole, plane 2 in the place of the
+// warpgroup's half of K S
+__host__ __device__ constexpr int y_at(int p, int x) { return p < 2 ? p * 32 + x * 8 : 64 + (x >> 1) * 32 + (x & 1) * 8; }
+
+// 16 columns of 32 fp32 values of a thread (32 tokens) as N bf16 planes
+template <int N>
+__device__ __forceinline__ void planes_of(const float (&x)[32], uint32_t (&p)[N][16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        uint32_t q[N];
+        split<N>(x[2 * i], x[2 * i + 1], q);
+#pragma unroll
+        for (int n = 0; n < N; ++n) p[n][i] = q[n];
+    }
+}
+__device__ __forceinline__ void store64(void* dst, const uint32_t (&p)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ((uint4*)dst)[i] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+template <int DK, int DV, bool KEEP>
+__global__ void __launch_bounds__(448, 1)
+gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv,
+                 GdnArgs a, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status)
+{
+    using L = Chain<DK, DV, KEEP>;
+    extern __shared__ char raw[];
+    char* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t base = smem_addr(sm);
+    uint64_t* bars = (uint64_t*)(sm + L::BAR);
+    uint64_t *full = bars, *empty = full + 2, *landed = empty + 2, *ks_done = landed + 1, *qs_done = ks_done + 1, *ty_done = qs_done + 1;
+    uint64_t *s_done = ty_done + 1, *o_done = s_done + 1, *y_ready = o_done + 1, *u_ready = y_ready + 1, *s_ready = u_ready + 1;
+    uint64_t *o_scaled = s_ready + 1, *o_read = o_scaled + 1, *drain = o_read + 1;
+    uint32_t* tm_ptr = (uint32_t*)(drain + 1);
+    const Guard guard{(volatile int*)(tm_ptr + 1), status};
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
+    const int h = blockIdx.x, seq = blockIdx.y, hk = h / (a.Hv / a.Hk);
+    const int len = seqs.len(seq), nch = (len + C - 1) / C;
+    const int64_t t0 = seqs.start(seq);
+    const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * REC_BYTES;
+
+    if (warp == 13) {
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(full + i, 1);
+                mbar_init(empty + i, KEEP ? 9 : 13);   // the MMAs, and each warp that reads the stage
+            }
+            for (uint64_t* b : {landed, ks_done, qs_done, ty_done, s_done, o_done, drain}) mbar_init(b, 1);
+            for (uint64_t* b : {y_ready, u_ready, s_ready}) mbar_init(b, 8);
+            mbar_init(o_scaled, 4);
+            mbar_init(o_read, 4);
+            *guard.flag = 0;
+            fence_mbar_init();
+            fence_async_smem();
+        }
+    } else if (warp == 12) {
+        tmem_alloc(tm_ptr, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tm_ptr;
+
+    if (warp == 13) {
+        int issued = 0;
+        for (int c = 0; c < nch; ++c) {
+            char* st = sm + (c & 1) * L::STAGE;
+            const int valid = min(C, len - c * C);
+            if (c >= 2) wait(empty + (c & 1), ((c >> 1) & 1) ^ 1, guard);
+            if (warp_up(guard)) break;
+            uint64_t* bar = valid < C ? landed : full + (c & 1);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, (KEEP ? 1 : 2) * C * DK * 2 + C * DV * 2 + REC_BYTES);
+                for (int p = 0; p < DK / 64; ++p) {
+                    tma_load_3d(st + L::K_ + p * L::PANEL, &mk, bar, p * 64, hk, (int)t0 + c * C);
+                    if (!KEEP) tma_load_3d(st + L::Q_ + p * L::PANEL, &mq, bar, p * 64, hk, (int)t0 + c * C);
+                }
+                for (int p = 0; p < DV / 64; ++p) tma_load_3d(st + L::V_ + p * L::PANEL, &mv, bar, p * 64, h, (int)t0 + c * C);
+                bulk_load(st + L::REC, rec + (int64_t)c * a.Hv * REC_BYTES, REC_BYTES, bar);
+            }
+            ++issued;
+            if (valid < C) {
+                // the rows behind the sequence belong to another one, or to none: they are zeros here
+                __syncwarp();
+                wait(landed, 0, guard);
+                constexpr int TILES = (L::REC - L::K_) / L::PANEL;
+                for (int e = lane; e < TILES * (C - valid) * 8; e += 32)
+                    *(uint4*)(st + e / (8 * (C - valid)) * L::PANEL + (valid + e / 8 % (C - valid)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                warp_arrive(full + (c & 1));
+            }
+        }
+        if (warp_up(guard))   // whole chunks still on their way
+            for (int c = max(0, issued - 2); c < issued; ++c)
+                if (len - c * C >= C) mbar_wait_bounded(full + (c & 1), (c >> 1) & 1, kWaitNs);
+    } else if (warp == 12) {
+        const uint64_t dk = desc_rows(base + L::K_), dq = desc_rows(base + L::Q_), dkc = desc_cols(base + L::K_, L::PANEL);
+        const uint64_t dt = sdesc(base + L::REC, 128, 256);   // core matrices: halves 128 bytes apart along K, rows 256
+        for (int c = 0; c < nch; ++c) {
+            const uint32_t so = (c & 1) * (L::STAGE >> 4);
+            wait(full + (c & 1), (c >> 1) & 1, guard);
+            wait(s_ready, c & 1, guard);
+            tc_fence_after();
+            constexpr uint32_t id_ks = idesc_f16(128, C, false, false, false, true);
+            if (elect()) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int x = 0; x < DK / 16; ++x)
+                        umma_f16_ts(tmem + L::R_ + 64, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(dk + so, x, L::PANEL), id_ks, p + x > 0);
+                umma_commit(ks_done);
+            }
+            if (!KEEP) {
+                if (c > 0) wait(o_read, (c - 1) & 1, guard);
+                tc_fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+#pragma unroll
+                        for (int x = 0; x < DK / 16; ++x)
+                            umma_f16_ts(tmem + L::O_, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(dq + so, x, L::PANEL), id_ks, p + x > 0);
+                    umma_commit(qs_done);
+                }
+            }
+            wait(y_ready, c & 1, guard);
+            tc_fence_after();
+            if (elect()) {
+                // every product of planes but T1 Y2; T's block column x starts at row 16 x
+#pragma unroll
+                for (int q = 0; q < TPL; ++q)
+#pragma unroll
+                    for (int p = 0; p < PLANES - q; ++p)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            umma_f16_ts(tmem + L::U_ + 16 * x, tmem + L::R_ + y_at(p, x), dt + so + ((q * TRI + blk(x, x)) >> 4),
+                                        idesc_f16(128, C - 16 * x, false, false, false, true), p + q + x > 0);
+                umma_commit(ty_done);
+            }
+            wait(u_ready, c & 1, guard);
+            tc_fence_after();
+            if (elect()) {
+#pragma unroll
+                for (int p = PLANES - 1; p >= 0; --p)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        umma_f16_ts(tmem + L::M_, tmem + L::R_ + y_at(p, x), step_cols(dkc + so, x),
+                                    idesc_f16(128, DK, false, true, false, true), 1);
+                umma_commit(s_done);
+            }
+            if (!KEEP) {
+                wait(o_scaled, c & 1, guard);
+                tc_fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int q = 0; q < PPL; ++q)
+#pragma unroll
+                        for (int p = 0; p < 2 - q; ++p)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            umma_f16_ts(tmem + L::O_ + 16 * x, tmem + L::U_ + (x >> 1) * 32 + p * 16 + (x & 1) * 8,
+                                        dt + so + ((REC_P + q * TRI + blk(x, x)) >> 4),
+                                        idesc_f16(128, C - 16 * x, false, false, false, true), 1);
+                    umma_commit(o_done);
+                }
+            }
+            if (elect()) umma_commit(empty + (c & 1));
+        }
+        if (warp_up(guard)) {
+            if (elect()) umma_commit(drain);
+            mbar_wait_bounded(drain, 0, kWaitNs);
+        }
+    } else if (warp < 8) {
+        constexpr int HK = DK / 2;   // key channels of a warpgroup's half of the state
+        const int hf = warp >> 2, row = tid & 127;   // row: value column
+        const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16);
+        const bool real = row < DV;
+        const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * DV + (int64_t)hf * HK * DV + row;
+        const uint32_t v_at = base + L::V_ + (row >> 6) * L::PANEL + (row & 7) * 2, v_piece = (uint32_t)(row >> 3 & 7) << 4;
+        const Kept keep{DK, DV};
+        auto scal_of = [&](int c) { return (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL); };
+        // 32 of the half's channels: to the planes, and decayed for chunk c
+        auto put = [&](int i, const float (&s)[32], int c, char* dst) {
+            uint32_t p[2][16];
+            planes_of<2>(s, p);
+            tmem_st16u_nowait(at + L::SP_ + hf * (HK / 2) + i * 16, p[0]);
+            tmem_st16u_nowait(at + L::SP_ + DK / 2 + hf * (HK / 2) + i * 16, p[1]);
+            if (KEEP && real) {
+                store64(dst + keep.s() + (row * DK + hf * HK + i * 32) * 2, p[0]);
+                store64(dst + keep.s() + keep.state() + (row * DK + hf * HK + i * 32) * 2, p[1]);
+            }
+            const float gam = scal_of(c)[C - 1];
+            uint32_t m[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) m[x] = __float_as_uint(s[x] * gam);
+            tmem_st32u_nowait(at + L::M_ + hf * HK + i * 32, m);
+        };
+        char* mine = KEEP ? kept + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * keep.bytes() : nullptr;
+        const int64_t next = KEEP ? (int64_t)a.Hv * keep.bytes() : 0;
+        if (nch > 0) {
+            wait(full, 0, guard);
+#pragma unroll
+            for (int i = 0; i < HK / 32; ++i) {
+                float s[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[x] = a.S0 && real ? a.S0[soff + (int64_t)(i * 32 + x) * DV] : 0.f;
+                put(i, s, 0, mine);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(s_ready);
+        } else if (a.ST && real) {
+            for (int x = 0; x < HK; ++x) a.ST[soff + (int64_t)x * DV] = a.S0 ? a.S0[soff + (int64_t)x * DV] : 0.f;
+        }
+        for (int c = 0; c < nch; ++c) {
+            const float* scal = scal_of(c);
+            const uint32_t st = (c & 1) * L::STAGE;
+            char* dst = KEEP ? mine + c * next : nullptr;
+            wait(full + (c & 1), (c >> 1) & 1, guard);
+            float x[32];
+            uint32_t p[3][16];
+            // Y = beta o (V - e^cum o (K S)), 32 tokens
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                uint16_t b;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(v_at + st + (hf * 32 + i) * 128 + (v_piece ^ ((i & 7) << 4))));
+                v[i] = real ? __uint_as_float((uint32_t)b << 16) : 0.f;
+            }
+            wait(ks_done, c & 1, guard);
+            tc_fence_after();
+            tmem_ld32(at + L::R_ + 64 + hf * 32, x);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 g = *(const float4*)&scal[hf * 32 + i];
+                x[i] = fmaf(-g.x, x[i], v[i]);
+                x[i + 1] = fmaf(-g.y, x[i + 1], v[i + 1]);
+                x[i + 2] = fmaf(-g.z, x[i + 2], v[i + 2]);
+                x[i + 3] = fmaf(-g.w, x[i + 3], v[i + 3]);
+            }
+            if (KEEP && real) {
+                uint32_t r[1][16];
+                planes_of<1>(x, r);
+                store64(dst + keep.r() + (row * C + hf * 32) * 2, r[0]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 b = *(const float4*)&scal[2 * C + hf * 32 + i];
+                x[i] *= b.x; x[i + 1] *= b.y; x[i + 2] *= b.z; x[i + 3] *= b.w;
+            }
+            auto put_y = [&] {
+                planes_of<3>(x, p);
+#pragma unroll
+                for (int q = 0; q < 3; ++q) tmem_st16u_nowait(at + L::R_ + y_at(q, 2 * hf), p[q]);
+            };
+            put_y();
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(y_ready);
+            // U, its planes, and decayed
+            wait(ty_done, c & 1, guard);
+            tc_fence_after();
+            tmem_ld32(at + L::U_ + hf * 32, x);
+            {
+                uint32_t u[2][16];
+                planes_of<2>(x, u);
+                if (KEEP) {
+                    if (real) {
+                        store64(dst + keep.u() + (row * C + hf * 32) * 2, u[0]);
+                        store64(dst + keep.u() + keep.rows() + (row * C + hf * 32) * 2, u[1]);
+                    }
+                } else {
+                    tmem_st16u_nowait(at + L::U_ + hf * 32, u[0]);
+                    tmem_st16u_nowait(at + L::U_ + hf * 32 + 16, u[1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 e = *(const float4*)&scal[C + hf * 32 + i];
+                x[i] *= e.x; x[i + 1] *= e.y; x[i + 2] *= e.z; x[i + 3] *= e.w;
+            }
+            put_y();
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(u_ready);
+            warp_arrive(empty + (c & 1));
+            if (c + 1 < nch) wait(full + ((c + 1) & 1), ((c + 1) >> 1) & 1, guard);
+            if (!KEEP) wait(qs_done, c & 1, guard);   // its planes of S
+            wait(s_done, c & 1, guard);
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < HK / 32; ++i) {
+                float s[32];
+                tmem_ld32(at + L::M_ + hf * HK + i * 32, s);
+                if (c + 1 < nch) {
+                    put(i, s, c + 1, KEEP ? dst + next : nullptr);
+                } else if (a.ST && real) {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) a.ST[soff + (int64_t)(i * 32 + y) * DV] = s[y];
+                }
+            }
+            if (c + 1 < nch) {
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(s_ready);
+            }
+        }
+    } else if (!KEEP) {
+        const int row = tid & 127, t = tid - 256;
+        const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16) + L::O_;
+        __nv_bfloat16* op = (__nv_bfloat16*)a.o + (t0 * a.Hv + h) * DV;
+        __nv_bfloat16* out = (__nv_bfloat16*)(sm + L::OUT);
+        for (int c = 0; c < nch; ++c) {
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL);
+            wait(full + (c & 1), (c >> 1) & 1, guard);
+            wait(qs_done, c & 1, guard);
+            tc_fence_after();
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float x[32];
+                tmem_ld32(at + hf * 32, x);
+                uint32_t y[32];
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 g = *(const float4*)&scal[hf * 32 + i];
+                    y[i] = __float_as_uint(x[i] * g.x);
+                    y[i + 1] = __float_as_uint(x[i + 1] * g.y);
+                    y[i + 2] = __float_as_uint(x[i + 2] * g.z);
+                    y[i + 3] = __float_as_uint(x[i + 3] * g.w);
+                }
+                tmem_st32u_nowait(at + hf * 32, y);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(o_scaled);
+            warp_arrive(empty + (c & 1));
+            wait(o_done, c & 1, guard);
+            tc_fence_after();
+            asm volatile("bar.sync 1, 128;" ::: "memory");   // the last chunk's rows have been stored
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float x[32];
+                tmem_ld32(at + hf * 32, x);
+                if (row < DV)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) out[(hf * 32 + i) * DV + row] = __float2bfloat16_rn(x[i]);
+            }
+            tc_fence_before();
+            warp_arrive(o_read);
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int valid = min(C, len - c * C);
+            for (int e = t; e < valid * (DV / 8); e += 128)
+                *(uint4*)(op + ((int64_t)c * C + e / (DV / 8)) * a.Hv * DV + e % (DV / 8) * 8) = *(const uint4*)(out + e * 8);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+template <int DK, int DV, bool KEEP>
+cudaError_t chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st)
+{
+    using L = Chain<DK, DV, KEEP>;
+    CUtensorMap k{}, q{}, v{};
+    const int64_t T = s.tokens();
+    if (T > 0 && (!make_map(&k, a.k, T, a.Hk, DK, 64, 1, C) || !make_map(&q, a.q, T, a.Hk, DK, 64, 1, C) ||
+                  !make_map(&v, a.v, T, a.Hv, DV, 64, 1, C)))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = allow_smem<gdn_chain_kernel<DK, DV, KEEP>>(L::SMEM);
+    if (e != cudaSuccess) return e;
+    ProfileScope prof(KEEP ? "gdn_chain_keep" : "gdn_chain", st);
+    count_launch();
+    gdn_chain_kernel<DK, DV, KEEP><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, v, a, s, (const char*)records, (char*)kept, status);
+    return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st)
+{
+#define KDA_CHAIN(DK, DV) (kept ? chain<DK, DV, true>(a, s, records, kept, status, st) : chain<DK, DV, false>(a, s, records, kept, status, st))
+    if (a.Dk == 64) return a.Dv == 64 ? KDA_CHAIN(64, 64) : KDA_CHAIN(64, 128);
+    return a.Dv == 64 ? KDA_CHAIN(128, 64) : KDA_CHAIN(128, 128);
+#undef KDA_CHAIN
+}
+
+}  // namespace gdn
+}  // namespace kda

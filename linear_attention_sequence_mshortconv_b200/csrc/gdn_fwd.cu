@@ -15,9 +15,8 @@
 //
 // Precision.  The state and every sum are fp32.  MMA operands that are not inputs (S, Y, U, T)
 // are split over bf16 planes: three planes carry 24 bits and keep bf16's range (fp16 would need
-// fewer, but overflows at 65504), so the state that is handed on is as exact as fp32
-// arithmetic makes it.  What only reaches o, which is rounded to bf16, takes two planes (S and U in
-// Q S and P U) or one (P).
+// fewer, but overflows at 65504), two 16 to 17; gdn_tc.cuh says which take how many.  The state that
+// is handed on is within 1e-6 of the recurrence's.
 
 #include "gdn_tc.cuh"
 
@@ -66,7 +65,7 @@ __device__ __forceinline__ void small_mm(const float (*A)[ALD], const float (*B)
     }
 }
 
-template <int DK, int PP>
+template <int DK>
 __global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const __grid_constant__ Seqs seqs, char* records)
 {
     extern __shared__ __align__(128) char sm[];
@@ -86,7 +85,7 @@ __global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const _
 
     // a warp per head: inclusive sum of the gates in 64 bits, two tokens a lane
     auto sum_gates = [&](int h) {
-        float* scal = (float*)(records + ((int64_t)blockIdx.x * a.Hv + h) * rec_bytes(PP) + rec_scal(PP));
+        float* scal = (float*)(records + ((int64_t)blockIdx.x * a.Hv + h) * REC_BYTES + REC_SCAL);
         double s[2];
         float b[2];
 #pragma unroll
@@ -117,10 +116,8 @@ __global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const _
             scal[t] = exp2f(hi);
             scal[C + t] = exp2f((float)(last - cum[i]));
             scal[2 * C + t] = b[i];
-            if (PP == 2) {
-                scal[3 * C + t] = hi;
-                scal[4 * C + t] = lo;
-            }
+            scal[3 * C + t] = hi;
+            scal[4 * C + t] = lo;
         }
     };
     // heads hk r .. hk r + r - 1 in groups that share h / 4: slot h & 3 of `gates`, warp h & 3
@@ -154,7 +151,7 @@ __global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const _
     __syncthreads();   // K and Q have been read: A and T take their place
     const int g4 = lane >> 2, t2 = (lane & 3) * 2;
     for (int h = hk * r; h < hk * r + r; ++h) {
-        char* rec = records + ((int64_t)blockIdx.x * a.Hv + h) * rec_bytes(PP);
+        char* rec = records + ((int64_t)blockIdx.x * a.Hv + h) * REC_BYTES;
         if (h > hk * r && (h & 3) == 0) {
             gates_from(h);
             __syncthreads();
@@ -181,12 +178,12 @@ __global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const _
                 *(float2*)&A[i0][j] = make_float2(b0 * d[0] * kk[n][0], b0 * d[1] * kk[n][1]);
                 *(float2*)&A[i1][j] = make_float2(b1 * d[2] * kk[n][2], b1 * d[3] * kk[n][3]);
             }
-            uint32_t lo[PP], hi[PP];
-            split<PP>(d[0] * qk[n][0], d[1] * qk[n][1], lo);
-            split<PP>(d[2] * qk[n][2], d[3] * qk[n][3], hi);
-            char* dst = rec + rec_p(PP) + blk(w, n >> 1) + (n & 1) * 128 + g4 * 16 + t2 * 2;
+            uint32_t lo[PPL], hi[PPL];
+            split<PPL>(d[0] * qk[n][0], d[1] * qk[n][1], lo);
+            split<PPL>(d[2] * qk[n][2], d[3] * qk[n][3], hi);
+            char* dst = rec + REC_P + blk(w, n >> 1) + (n & 1) * 128 + g4 * 16 + t2 * 2;
 #pragma unroll
-            for (int q = 0; q < PP; ++q) {
+            for (int q = 0; q < PPL; ++q) {
                 *(uint32_t*)(dst + q * TRI) = lo[q];
                 *(uint32_t*)(dst + q * TRI + 256) = hi[q];
             }
@@ -252,7 +249,7 @@ __global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const _
     }
 }
 
-cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int PP, cudaStream_t st)
+cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, cudaStream_t st)
 {
     const dim3 grid(s.slots(C), a.Hk);
     ProfileScope prof("gdn_prologue", st);
@@ -262,10 +259,8 @@ cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int 
         kern<<<grid, 128, smem, st>>>(a, s, (char*)records);
         return cudaGetLastError();
     };
-#define KDA_PROLOGUE(DK, PP) go(gdn_prologue_kernel<DK, PP>, allow_smem<gdn_prologue_kernel<DK, PP>>(pro_smem<DK>()), pro_smem<DK>())
-    if (a.Dk == 64) return PP == 1 ? KDA_PROLOGUE(64, 1) : KDA_PROLOGUE(64, 2);
-    return PP == 1 ? KDA_PROLOGUE(128, 1) : KDA_PROLOGUE(128, 2);
-#undef KDA_PROLOGUE
+    if (a.Dk == 64) return go(gdn_prologue_kernel<64>, allow_smem<gdn_prologue_kernel<64>>(pro_smem<64>()), pro_smem<64>());
+    return go(gdn_prologue_kernel<128>, allow_smem<gdn_prologue_kernel<128>>(pro_smem<128>()), pro_smem<128>());
 }
 
 // ---- scan ---------------------------------------------------------------------------------
@@ -282,13 +277,12 @@ cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int 
 // chunk (the planes of S and U and R) in place of the output.
 template <int DK, int MT, bool KEEP>
 struct Scan {
-    static constexpr int PP = KEEP ? 2 : 1;
     static constexpr int THREADS = 256 * MT;
     static constexpr int VROW = 32 * MT + 16;        // bytes of a staged row of V: odd multiple of 16
     static constexpr int SROW = 2 * DK + 16;         // of a row of the S planes
     static constexpr int TROW = 2 * C + 16;          // of a row of the Y and U planes
     static constexpr int K_ = 0, Q_ = K_ + C * DK * 2, REC = Q_ + (KEEP ? 0 : C * DK * 2);
-    static constexpr int V_ = REC + rec_bytes(PP), STAGE = V_ + C * VROW;
+    static constexpr int V_ = REC + REC_BYTES, STAGE = V_ + C * VROW;
     static constexpr int SP = 2 * STAGE;                               // [plane][16 MT][SROW]
     static constexpr int YP = SP + SPL * 16 * MT * SROW;            // [plane][16 MT][TROW]
     static constexpr int UP = YP + PLANES * 16 * MT * TROW;            // decayed U
@@ -347,7 +341,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
         for (int c = 0; c < nch; ++c) {
             __syncthreads();   // chunk c has landed and S is in place
             const uint32_t st = base + (c & 1) * L::STAGE;
-            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(L::PP));
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL);
             // K S of the warp's 16 tokens (two 8-token tiles), transposed
             float ks[2][SPL][4] = {};
 #pragma unroll
@@ -462,7 +456,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
         const __nv_bfloat16* qp = (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK;
         const __nv_bfloat16* vp = (const __nv_bfloat16*)a.v + (t0 * a.Hv + h) * a.Dv + v0;
         __nv_bfloat16* op = (__nv_bfloat16*)a.o + (t0 * a.Hv + h) * a.Dv + v0;
-        const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * rec_bytes(L::PP);
+        const char* rec = records + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * REC_BYTES;
         const Kept keep{DK, a.Dv};
         auto load = [&](int c) {
             const uint32_t st = base + (c & 1) * L::STAGE;
@@ -474,8 +468,8 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
                 const bool in = row < valid;
                 cp16(st + L::V_ + row * L::VROW + piece * 16, vp + ((int64_t)c * C + (in ? row : 0)) * a.Hv * a.Dv + piece * 8, in);
             }
-            const char* src = rec + (int64_t)c * a.Hv * rec_bytes(L::PP);
-            for (int e = lt; e < rec_bytes(L::PP) / 16; e += LOADERS) cp16(st + L::REC + e * 16, src + e * 16, true);
+            const char* src = rec + (int64_t)c * a.Hv * REC_BYTES;
+            for (int e = lt; e < REC_BYTES / 16; e += LOADERS) cp16(st + L::REC + e * 16, src + e * 16, true);
             cp_async_commit();
         };
         if (nch > 0) load(0);
@@ -500,7 +494,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
                 }
                 continue;
             }
-            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + rec_scal(L::PP));
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL);
             float qs[2][2][4] = {};
 #pragma unroll
             for (int s = 0; s < DK / 16; ++s) {
@@ -524,13 +518,16 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
 #pragma unroll
             for (int jb = 0; jb < 4; ++jb) {
                 if (jb > f) break;
-                uint32_t x[2][4], b[4];
-                ldsm(b, st + L::REC + rec_p(L::PP) + blk(f, jb) + lane * 16);
+                uint32_t x[2][4], b[PPL][4];
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
+                    ldsm(b[p], st + L::REC + REC_P + p * TRI + blk(f, jb) + lane * 16);
                     ldsm(x[p], base + L::WP + p * 16 * MT * L::TROW + a_row * L::TROW + jb * 32 + a_piece);
-                    mma(o[0], x[p], b[0], b[1]);
-                    mma(o[1], x[p], b[2], b[3]);
+                }
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {   // P0 U0, P0 U1, P1 U0
+                    mma(o[0], x[p & 1], b[p >> 1][0], b[p >> 1][1]);
+                    mma(o[1], x[p & 1], b[p >> 1][2], b[p >> 1][3]);
                 }
             }
             // 16 tokens x 16 columns, turned over in the warp's own 512 bytes
@@ -576,6 +573,15 @@ cudaError_t launch_scan(const GdnArgs& a, const Seqs& s, const void* records, vo
 }
 }  // namespace gdn
 
+namespace gdn {
+// Which scan: whole heads (gdn_chain.cu) or columns of heads.
+bool whole_heads(const GdnArgs& a, const Seqs& s, int sms)
+{
+    (void)s; (void)sms;
+    return a.Dv != 32;
+}
+}  // namespace gdn
+
 // The tensor-core path copies rows in 16-byte pieces.
 bool gdn_tc_supported(const GdnArgs& a)
 {
@@ -583,14 +589,15 @@ bool gdn_tc_supported(const GdnArgs& a)
            gdn::aligned16(a.v) && gdn::aligned16(a.o);
 }
 
-size_t gdn_tc_workspace(const Seqs& s, int Hv) { return (size_t)s.slots(gdn::C) * Hv * gdn::rec_bytes(1); }
+size_t gdn_tc_workspace(const Seqs& s, int Hv) { return (size_t)s.slots(gdn::C) * Hv * gdn::REC_BYTES; }
 
 cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st)
 {
     cudaError_t e = cudaSuccess;
-    if (s.tokens() > 0) e = gdn::launch_prologue(a, s, ws, 1, st);
+    const bool whole = gdn::whole_heads(a, s, sms);
+    if (s.tokens() > 0) e = gdn::launch_prologue(a, s, ws, st);
     if (e != cudaSuccess) return e;
-    return gdn::launch_scan(a, s, ws, nullptr, sms, st);
+    return whole ? gdn::launch_chain(a, s, ws, nullptr, status, st) : gdn::launch_scan(a, s, ws, nullptr, sms, st);
 }
 
 }  // namespace kda

@@ -15,7 +15,9 @@ constexpr int C = 64;          // tokens per chunk
 // What enters the state directly (Y = beta o R and U) has three.  Two are enough for S in K S and
 // for T: their rounding (2^-18) reaches U only through K S, a fraction of V, and through T's
 // off-diagonal entries, beta k_i.k_j.
-constexpr int PLANES = 3, SPL = 2, TPL = 2;
+// P and U in P U have two as well: the sum over a chunk's tokens may cancel (with keys that repeat, U
+// holds the differences of successive values).
+constexpr int PLANES = 3, SPL = 2, TPL = 2, PPL = 2;
 
 // D(16x8, fp32) += A(16x16, bf16, rows) * B(16x8, bf16, columns)
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -86,16 +88,14 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src
 }
 
 // A chunk's factors for one value head, written by the prologue kernel and read by the scans:
-// T = (I + A)^-1 in TPL planes and P = lower(e^{cum_i - cum_j} q_i.k_j) in PP planes, each
+// T = (I + A)^-1 in TPL planes and P = lower(e^{cum_i - cum_j} q_i.k_j) in PPL planes, each
 // the ten 16x16 blocks on and below the diagonal, a block as four 8x8 core matrices of 128
-// contiguous bytes; then e^cum, e^{cum_C - cum}, beta and, with PP = 2 (the backward), cum
-// log2(e) as a sum of two floats.
+// contiguous bytes; then e^cum, e^{cum_C - cum}, beta, and cum log2(e) as a sum of two floats.
 constexpr int BLK = 512;
 constexpr int TRI = 10 * BLK;
-__host__ __device__ constexpr int rec_p(int) { return TPL * TRI; }
-__host__ __device__ constexpr int rec_scal(int PP) { return (TPL + PP) * TRI; }
-__host__ __device__ constexpr int rec_bytes(int PP) { return rec_scal(PP) + (PP == 2 ? 5 : 3) * C * 4; }
-__device__ __forceinline__ int blk(int ib, int jb) { return (ib * (ib + 1) / 2 + jb) * BLK; }
+constexpr int REC_P = TPL * TRI, REC_SCAL = (TPL + PPL) * TRI, REC_BYTES = REC_SCAL + 5 * C * 4;
+// blocks column by column: those of one column are evenly spaced, as an MMA's descriptor needs
+__host__ __device__ constexpr int blk(int ib, int jb) { return (ib + jb * 3 - jb * (jb - 1) / 2) * BLK; }
 
 // What the backward keeps of each chunk and value head, bf16: the entry state S^T and the
 // gradient D^T of the exit state, [Dv][Dk] in two planes each; U^T and dY^T, [Dv][64] in two
@@ -113,11 +113,21 @@ struct Kept {
     __host__ __device__ size_t bytes() const { return (exit() + Dv + 255) / 256 * 256; }
 };
 
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// The same scan with all value columns of a head in one CTA (Dv = 64 or 128)
+cudaError_t launch_chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st);
+bool whole_heads(const GdnArgs& a, const Seqs& s, int sms);   // which of the two
 // launch of the forward scan: o and S_T (kept null), or what the backward needs (kept and, if
 // not null, S_T; o unused)
 cudaError_t launch_scan(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int sms, cudaStream_t st);
 // launch of the prologue kernel: one record per (slot, value head)
-cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, int PP, cudaStream_t st);
+cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, cudaStream_t st);
 
 }  // namespace gdn
 }  // namespace kda
