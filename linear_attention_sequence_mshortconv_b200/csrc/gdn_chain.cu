@@ -14,9 +14,11 @@
 //   warp 12    issues the MMAs: K S, Q S | T Y | K^T U, P U
 //   warp 13    the loads of the next chunk
 //
-// Tensor memory (512 columns): S (fp32, Dk), its two planes (Dk), R (128: K S, then the planes of Y,
-// then of decayed U), U (64: the product, then its planes), O (64).  A warpgroup writes planes only
-// where its own half of a product was or where nothing is, so the two need no barrier between them.
+// Tensor memory (512 columns): S (fp32, Dk), its two planes (Dk), R (128: V^T and K S, then the planes of
+// Y, then of decayed U), U (64: the product, then its planes), O (64).  A warpgroup writes planes only
+// where its own half of a product was, so the two need no barrier between them.  V comes in by a
+// product with the identity (exact), which turns it over: two-byte reads of its columns took the
+// threads longer than K S takes.
 //
 // Every wait is bounded; after one runs out the chain runs to its end on whatever is there.
 
@@ -35,27 +37,61 @@ struct Chain {
     static constexpr int K_ = 0, Q_ = K_ + DK / 64 * PANEL, V_ = Q_ + (KEEP ? 0 : DK / 64 * PANEL);
     static constexpr int REC = V_ + DV / 64 * PANEL, STAGE = (REC + REC_BYTES + 1023) / 1024 * 1024;
     static constexpr int OUT = 2 * STAGE;                     // [64][DV] bf16
-    static constexpr int BAR = OUT + (KEEP ? 0 : C * DV * 2);
+    static constexpr int EYE = OUT + (KEEP ? 0 : C * DV * 2); // 64x64 identity, bf16, a panel
+    static constexpr int BAR = EYE + PANEL;
     // the base is aligned up to 1024 bytes; more than half of an SM's, since each CTA takes all of its
     // tensor memory
     static constexpr int SMEM = BAR + 256 + 1024 > 116 * 1024 ? BAR + 256 + 1024 : 116 * 1024;
     // tensor memory columns
     static constexpr int M_ = 0, SP_ = DK, R_ = 2 * DK, U_ = R_ + 128, O_ = U_ + 64;
 };
-// plane p of Y (or decayed U), k-step x of 16 tokens: planes 0 and 1 whole, plane 2 in the place of the
-// warpgroup's half of K S
-__host__ __device__ constexpr int y_at(int p, int x) { return p < 2 ? p * 32 + x * 8 : 64 + (x >> 1) * 32 + (x & 1) * 8; }
+// plane p of Y (or decayed U), k-step x of 16 tokens: planes 0 and 1 where the warpgroup's half of V was,
+// plane 2 where its half of K S was
+__host__ __device__ constexpr int y_at(int p, int x) { return (p < 2 ? p * 16 : 64) + (x >> 1) * 32 + (x & 1) * 8; }
 
-// 16 columns of 32 fp32 values of a thread (32 tokens) as N bf16 planes
+// 32 fp32 values of a thread (16 pairs) as N bf16 planes
 template <int N>
-__device__ __forceinline__ void planes_of(const float (&x)[32], uint32_t (&p)[N][16])
+__device__ __forceinline__ void planes_of(const uint64_t (&x)[16], uint32_t (&p)[N][16])
 {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        uint32_t q[N];
-        split<N>(x[2 * i], x[2 * i + 1], q);
+        uint64_t rest = x[i];
 #pragma unroll
-        for (int n = 0; n < N; ++n) p[n][i] = q[n];
+        for (int n = 0; n < N; ++n) {
+            float lo, hi;
+            unpair(rest, lo, hi);
+            p[n][i] = pack(lo, hi);
+            if (n + 1 < N) rest = fma2(pair(low(p[n][i]), high(p[n][i])), pair(-1.f, -1.f), rest);
+        }
+    }
+}
+__device__ __forceinline__ void load32(uint32_t taddr, uint64_t (&x)[16])
+{
+    float v[32];
+    tmem_ld32(taddr, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = pair(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void store32(uint32_t taddr, const uint64_t (&x)[16])
+{
+    uint32_t m[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        unpair(x[i], lo, hi);
+        m[2 * i] = __float_as_uint(lo);
+        m[2 * i + 1] = __float_as_uint(hi);
+    }
+    tmem_st32u_nowait(taddr, m);
+}
+// x *= 32 factors in shared memory
+__device__ __forceinline__ void scale32(uint64_t (&x)[16], const float* f)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const ulonglong2 v = *(const ulonglong2*)(f + 2 * i);
+        x[i] = mul2(x[i], v.x);
+        x[i + 1] = mul2(x[i + 1], v.y);
     }
 }
 __device__ __forceinline__ void store64(void* dst, const uint32_t (&p)[16])
@@ -108,6 +144,10 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     } else if (warp == 12) {
         tmem_alloc(tm_ptr, 512);
         tmem_relinquish();
+    } else if (tid < 64) {
+        for (int i = 0; i < 8; ++i) *(uint4*)(sm + L::EYE + tid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+        *(uint16_t*)(sm + L::EYE + piece_at(tid, tid >> 3) + (tid & 7) * 2) = 0x3f80;
+        fence_async_smem();
     }
     tc_fence_before();
     __syncthreads();
@@ -148,14 +188,20 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 if (len - c * C >= C) mbar_wait_bounded(full + (c & 1), (c >> 1) & 1, kWaitNs);
     } else if (warp == 12) {
         const uint64_t dk = desc_rows(base + L::K_), dq = desc_rows(base + L::Q_), dkc = desc_cols(base + L::K_, L::PANEL);
+        const uint64_t dv = desc_cols(base + L::V_, L::PANEL), de = desc_rows(base + L::EYE);
         const uint64_t dt = sdesc(base + L::REC, 128, 256);   // core matrices: halves 128 bytes apart along K, rows 256
         for (int c = 0; c < nch; ++c) {
             const uint32_t so = (c & 1) * (L::STAGE >> 4);
             wait(full + (c & 1), (c >> 1) & 1, guard);
             wait(s_ready, c & 1, guard);
             tc_fence_after();
-            constexpr uint32_t id_ks = idesc_f16(128, C, false, false, false, true);
+            constexpr uint32_t id_qs = idesc_f16(128, C, false, false, false, true);
+            constexpr uint32_t id_ks = idesc_f16(128, C, false, false, true, true);     // -K S
+            // (with Dv = 64 rows 64 on read the record behind V; they are not used)
+            constexpr uint32_t id_v = idesc_f16(128, C, true, false, false, true);
             if (elect()) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) umma_f16(tmem + L::R_, step_cols(dv + so, x), step_rows(de, x, L::PANEL), id_v, x > 0);
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -171,7 +217,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     for (int p = 0; p < 2; ++p)
 #pragma unroll
                         for (int x = 0; x < DK / 16; ++x)
-                            umma_f16_ts(tmem + L::O_, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(dq + so, x, L::PANEL), id_ks, p + x > 0);
+                            umma_f16_ts(tmem + L::O_, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(dq + so, x, L::PANEL), id_qs, p + x > 0);
                     umma_commit(qs_done);
                 }
             }
@@ -228,11 +274,10 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16);
         const bool real = row < DV;
         const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * DV + (int64_t)hf * HK * DV + row;
-        const uint32_t v_at = base + L::V_ + (row >> 6) * L::PANEL + (row & 7) * 2, v_piece = (uint32_t)(row >> 3 & 7) << 4;
         const Kept keep{DK, DV};
         auto scal_of = [&](int c) { return (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL); };
         // 32 of the half's channels: to the planes, and decayed for chunk c
-        auto put = [&](int i, const float (&s)[32], int c, char* dst) {
+        auto put = [&](int i, uint64_t (&s)[16], int c, char* dst) {
             uint32_t p[2][16];
             planes_of<2>(s, p);
             tmem_st16u_nowait(at + L::SP_ + hf * (HK / 2) + i * 16, p[0]);
@@ -242,10 +287,9 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 store64(dst + keep.s() + keep.state() + (row * DK + hf * HK + i * 32) * 2, p[1]);
             }
             const float gam = scal_of(c)[C - 1];
-            uint32_t m[32];
 #pragma unroll
-            for (int x = 0; x < 32; ++x) m[x] = __float_as_uint(s[x] * gam);
-            tmem_st32u_nowait(at + L::M_ + hf * HK + i * 32, m);
+            for (int x = 0; x < 16; ++x) s[x] = mul2(s[x], pair(gam, gam));
+            store32(at + L::M_ + hf * HK + i * 32, s);
         };
         char* mine = KEEP ? kept + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * keep.bytes() : nullptr;
         const int64_t next = KEEP ? (int64_t)a.Hv * keep.bytes() : 0;
@@ -253,9 +297,12 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             wait(full, 0, guard);
 #pragma unroll
             for (int i = 0; i < HK / 32; ++i) {
-                float s[32];
+                uint64_t s[16];
 #pragma unroll
-                for (int x = 0; x < 32; ++x) s[x] = a.S0 && real ? a.S0[soff + (int64_t)(i * 32 + x) * DV] : 0.f;
+                for (int x = 0; x < 16; ++x) {
+                    const int64_t off = soff + (int64_t)(i * 32 + 2 * x) * DV;
+                    s[x] = a.S0 && real ? pair(a.S0[off], a.S0[off + DV]) : 0;
+                }
                 put(i, s, 0, mine);
             }
             tmem_wait_st();
@@ -269,42 +316,37 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const uint32_t st = (c & 1) * L::STAGE;
             char* dst = KEEP ? mine + c * next : nullptr;
             wait(full + (c & 1), (c >> 1) & 1, guard);
-            float x[32];
+            uint64_t x[16];
             uint32_t p[3][16];
-            // Y = beta o (V - e^cum o (K S)), 32 tokens
-            float v[32];
+            auto put_y = [&] {
+                planes_of<3>(x, p);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                uint16_t b;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(v_at + st + (hf * 32 + i) * 128 + (v_piece ^ ((i & 7) << 4))));
-                v[i] = real ? __uint_as_float((uint32_t)b << 16) : 0.f;
-            }
+                for (int q = 0; q < 3; ++q) tmem_st16u_nowait(at + L::R_ + y_at(q, 2 * hf), p[q]);
+            };
+            // Y = beta o (V - e^cum o (K S)), 32 tokens
             wait(ks_done, c & 1, guard);
             tc_fence_after();
-            tmem_ld32(at + L::R_ + 64 + hf * 32, x);
+            {
+                uint64_t ks[16];
+                load32(at + L::R_ + hf * 32, x);
+                load32(at + L::R_ + 64 + hf * 32, ks);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 g = *(const float4*)&scal[hf * 32 + i];
-                x[i] = fmaf(-g.x, x[i], v[i]);
-                x[i + 1] = fmaf(-g.y, x[i + 1], v[i + 1]);
-                x[i + 2] = fmaf(-g.z, x[i + 2], v[i + 2]);
-                x[i + 3] = fmaf(-g.w, x[i + 3], v[i + 3]);
+                for (int i = 0; i < 16; i += 2) {
+                    const ulonglong2 g = *(const ulonglong2*)&scal[hf * 32 + 2 * i];
+                    x[i] = fma2(g.x, ks[i], x[i]);
+                    x[i + 1] = fma2(g.y, ks[i + 1], x[i + 1]);
+                }
+            }
+            if (DV < 128 && !real) {   // rows that no column of V fills
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = 0;
             }
             if (KEEP && real) {
                 uint32_t r[1][16];
                 planes_of<1>(x, r);
                 store64(dst + keep.r() + (row * C + hf * 32) * 2, r[0]);
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 b = *(const float4*)&scal[2 * C + hf * 32 + i];
-                x[i] *= b.x; x[i + 1] *= b.y; x[i + 2] *= b.z; x[i + 3] *= b.w;
-            }
-            auto put_y = [&] {
-                planes_of<3>(x, p);
-#pragma unroll
-                for (int q = 0; q < 3; ++q) tmem_st16u_nowait(at + L::R_ + y_at(q, 2 * hf), p[q]);
-            };
+            scale32(x, scal + 2 * C + hf * 32);
             put_y();
             tmem_wait_st();
             tc_fence_before();
@@ -312,7 +354,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             // U, its planes, and decayed
             wait(ty_done, c & 1, guard);
             tc_fence_after();
-            tmem_ld32(at + L::U_ + hf * 32, x);
+            load32(at + L::U_ + hf * 32, x);
             {
                 uint32_t u[2][16];
                 planes_of<2>(x, u);
@@ -326,11 +368,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     tmem_st16u_nowait(at + L::U_ + hf * 32 + 16, u[1]);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 e = *(const float4*)&scal[C + hf * 32 + i];
-                x[i] *= e.x; x[i + 1] *= e.y; x[i + 2] *= e.z; x[i + 3] *= e.w;
-            }
+            scale32(x, scal + C + hf * 32);
             put_y();
             tmem_wait_st();
             tc_fence_before();
@@ -342,13 +380,18 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < HK / 32; ++i) {
-                float s[32];
-                tmem_ld32(at + L::M_ + hf * HK + i * 32, s);
+                uint64_t s[16];
+                load32(at + L::M_ + hf * HK + i * 32, s);
                 if (c + 1 < nch) {
                     put(i, s, c + 1, KEEP ? dst + next : nullptr);
                 } else if (a.ST && real) {
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) a.ST[soff + (int64_t)(i * 32 + y) * DV] = s[y];
+                    for (int y = 0; y < 16; ++y) {
+                        float lo, hi;
+                        unpair(s[y], lo, hi);
+                        a.ST[soff + (int64_t)(i * 32 + 2 * y) * DV] = lo;
+                        a.ST[soff + (int64_t)(i * 32 + 2 * y + 1) * DV] = hi;
+                    }
                 }
             }
             if (c + 1 < nch) {
@@ -369,18 +412,10 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             tc_fence_after();
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                float x[32];
-                tmem_ld32(at + hf * 32, x);
-                uint32_t y[32];
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 g = *(const float4*)&scal[hf * 32 + i];
-                    y[i] = __float_as_uint(x[i] * g.x);
-                    y[i + 1] = __float_as_uint(x[i + 1] * g.y);
-                    y[i + 2] = __float_as_uint(x[i + 2] * g.z);
-                    y[i + 3] = __float_as_uint(x[i + 3] * g.w);
-                }
-                tmem_st32u_nowait(at + hf * 32, y);
+                uint64_t x[16];
+                load32(at + hf * 32, x);
+                scale32(x, scal + hf * 32);
+                store32(at + hf * 32, x);
             }
             tmem_wait_st();
             tc_fence_before();
