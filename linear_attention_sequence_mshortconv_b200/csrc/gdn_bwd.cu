@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
             float part = 0.f;
             for (int e = lt; e < 16 * MT * DK / 8; e += LOADERS) {
                 const int piece = e % (DK / 8), row = e / (DK / 8);
-                const int64_t off = ((v0 + row) * DK + piece * 8) * 2;
+                const uint32_t off = tile_at<DK>(v0 + row, piece);
                 const uint4 d0 = *(const uint4*)(sm + L::DP + row * L::SROW + piece * 16);
                 const uint4 d1 = *(const uint4*)(sm + L::DP + (16 * MT + row) * L::SROW + piece * 16);
                 *(uint4*)(dst + keep.d() + off) = d0;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
             for (int i = 0; i < MT; ++i) bar_sync(1 + 2 * MT + i, 128 + LOADERS);
             for (int e = lt; e < 2 * 16 * MT * 8; e += LOADERS) {
                 const int piece = e & 7, row = e / 8 % (16 * MT), p = e / 8 / (16 * MT);
-                *(uint4*)(dst + keep.y() + p * keep.rows() + ((v0 + row) * C + piece * 8) * 2) =
+                *(uint4*)(dst + keep.y() + p * keep.rows() + tile_at<C>(v0 + row, piece)) =
                     *(const uint4*)(sm + L::YP + (p * 16 * MT + row) * L::TROW + piece * 16);
             }
             // dV: 16 tokens x 16 columns of the chain warp of the same place
@@ -383,15 +383,15 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
     for (int h = hk * r; h < hk * r + r; ++h) {
         const char* mine = kept + ((int64_t)blockIdx.x * a.Hv + h) * keep.bytes();
         const char* rec = records + ((int64_t)blockIdx.x * a.Hv + h) * REC_BYTES;
-        auto plane = [&](uint32_t dst, size_t off) { load_tile<DK, 256, DV>(dst, (const __nv_bfloat16*)(mine + off), DK, DV, tid); };
+        auto take = [&](uint32_t dst, size_t off, int bytes) {   // kept tiles are laid out as they are read
+            for (int e = tid; e < bytes / 16; e += 256) cp16(dst + e * 16, mine + off + e * 16, true);
+        };
         load_tile<DV, 256>(base + L::G_, (const __nv_bfloat16*)b.dout + (t0 * a.Hv + h) * DV, (int64_t)a.Hv * DV, valid, tid);
-        for (int p = 0; p < 2; ++p) {
-            load_tile<C, 256, DV>(base + L::U_ + p * DV * C * 2, (const __nv_bfloat16*)(mine + keep.u() + p * keep.rows()), C, DV, tid);
-            load_tile<C, 256, DV>(base + L::Y_ + p * DV * C * 2, (const __nv_bfloat16*)(mine + keep.y() + p * keep.rows()), C, DV, tid);
-        }
+        take(base + L::U_, keep.u(), 2 * DV * C * 2);
+        take(base + L::Y_, keep.y(), 2 * DV * C * 2);
         for (int e = tid; e < 5 * C / 4; e += 256) cp16(base + L::SC + e * 16, rec + REC_SCAL + e * 16, true);
         cp_async_commit();
-        for (int p = 0; p < 2; ++p) plane(base + L::SB + p * DV * DK * 2, keep.s() + p * keep.state());
+        take(base + L::SB, keep.s(), 2 * DV * DK * 2);
         cp_async_commit();
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
             const int pc = tid & 7;
             float acc[8] = {};
             for (int row = tid >> 3; row < DV; row += 32) {
-                const uint4 rr = *(const uint4*)(mine + keep.r() + (row * C + pc * 8) * 2);
+                const uint4 rr = *(const uint4*)(mine + keep.r() + tile_at<C>(row, pc));
                 const uint4 y0 = *(const uint4*)(sm + L::Y_ + tile_at<C>(row, pc));
                 const uint4 y1 = *(const uint4*)(sm + L::Y_ + DV * C * 2 + tile_at<C>(row, pc));
                 const uint32_t rv[4] = {rr.x, rr.y, rr.z, rr.w}, a0[4] = {y0.x, y0.y, y0.z, y0.w}, a1[4] = {y1.x, y1.y, y1.z, y1.w};
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
                 for (int e = 0; e < 4; ++e) sk[n][e] += x[n][e];
         }
         __syncthreads();   // S has been read
-        for (int p = 0; p < 2; ++p) plane(base + L::SB + p * DV * DK * 2, keep.d() + p * keep.state());
+        take(base + L::SB, keep.d(), 2 * DV * DK * 2);
         cp_async_commit();
         cp_async_wait_all();
         __syncthreads();

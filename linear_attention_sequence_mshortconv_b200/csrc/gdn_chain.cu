@@ -35,9 +35,13 @@ template <int DK, int DV, bool KEEP>
 struct Chain {
     static constexpr int THREADS = 448, PANEL = C * 128;
     static constexpr int K_ = 0, Q_ = K_ + DK / 64 * PANEL, V_ = Q_ + (KEEP ? 0 : DK / 64 * PANEL);
-    static constexpr int REC = V_ + DV / 64 * PANEL, STAGE = (REC + REC_BYTES + 1023) / 1024 * 1024;
-    static constexpr int OUT = 2 * STAGE;                     // [64][DV] bf16
-    static constexpr int EYE = OUT + (KEEP ? 0 : C * DV * 2); // 64x64 identity, bf16, a panel
+    // the record; what is kept needs no P
+    static constexpr int REC = V_ + DV / 64 * PANEL, SCAL = REC + (KEEP ? REC_P : REC_SCAL);
+    static constexpr int STAGE = (SCAL + REC_BYTES - REC_SCAL + 1023) / 1024 * 1024;
+    static constexpr int OUT = 2 * STAGE;                     // the output [64][DV] bf16; or what is kept: two planes
+    static constexpr int OUT_U = OUT + 2 * DV * DK * 2;       // of S, of U, and R, as tiles
+    static constexpr int OUT_R = OUT_U + 2 * DV * C * 2;
+    static constexpr int EYE = KEEP ? OUT_R + DV * C * 2 : OUT + C * DV * 2;   // 64x64 identity, bf16, a panel
     static constexpr int BAR = EYE + PANEL;
     // the base is aligned up to 1024 bytes; more than half of an SM's, since each CTA takes all of its
     // tensor memory
@@ -49,55 +53,62 @@ struct Chain {
 // plane 2 where its half of K S was
 __host__ __device__ constexpr int y_at(int p, int x) { return (p < 2 ? p * 16 : 64) + (x >> 1) * 32 + (x & 1) * 8; }
 
-// 32 fp32 values of a thread (16 pairs) as N bf16 planes
+// 32 fp32 values of a thread as N bf16 planes, x = p0 - p1 (+ p2): the second has the opposite sign (its
+// MMAs negate it)
 template <int N>
-__device__ __forceinline__ void planes_of(const uint64_t (&x)[16], uint32_t (&p)[N][16])
+__device__ __forceinline__ void planes_of(const float (&x)[32], uint32_t (&p)[N][16])
 {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        uint64_t rest = x[i];
+        float a = x[2 * i], b = x[2 * i + 1];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            float lo, hi;
-            unpair(rest, lo, hi);
-            p[n][i] = pack(lo, hi);
-            if (n + 1 < N) rest = fma2(pair(low(p[n][i]), high(p[n][i])), pair(-1.f, -1.f), rest);
+            p[n][i] = pack(a, b);
+            if (n + 1 < N) {
+                a = less((uint16_t)p[n][i], a);
+                b = less((uint16_t)(p[n][i] >> 16), b);
+            }
         }
     }
 }
-__device__ __forceinline__ void load32(uint32_t taddr, uint64_t (&x)[16])
-{
-    float v[32];
-    tmem_ld32(taddr, v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = pair(v[2 * i], v[2 * i + 1]);
-}
-__device__ __forceinline__ void store32(uint32_t taddr, const uint64_t (&x)[16])
+__device__ __forceinline__ void store32(uint32_t taddr, const float (&x)[32])
 {
     uint32_t m[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float lo, hi;
-        unpair(x[i], lo, hi);
-        m[2 * i] = __float_as_uint(lo);
-        m[2 * i + 1] = __float_as_uint(hi);
-    }
+    for (int i = 0; i < 32; ++i) m[i] = __float_as_uint(x[i]);
     tmem_st32u_nowait(taddr, m);
 }
 // x *= 32 factors in shared memory
-__device__ __forceinline__ void scale32(uint64_t (&x)[16], const float* f)
+__device__ __forceinline__ void scale32(float (&x)[32], const float* f)
 {
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        const ulonglong2 v = *(const ulonglong2*)(f + 2 * i);
-        x[i] = mul2(x[i], v.x);
-        x[i + 1] = mul2(x[i + 1], v.y);
+    for (int i = 0; i < 32; i += 4) {
+        const float4 v = *(const float4*)(f + i);
+        x[i] *= v.x; x[i + 1] *= v.y; x[i + 2] *= v.z; x[i + 3] *= v.w;
     }
 }
-__device__ __forceinline__ void store64(void* dst, const uint32_t (&p)[16])
+// 32 bf16 values of a row, to a tile (sign: 0x80008000 to negate them)
+template <int W>
+__device__ __forceinline__ void to_tile(char* tile, int row, int piece, const uint32_t (&p)[16], uint32_t sign = 0)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ((uint4*)dst)[i] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+    for (int i = 0; i < 4; ++i)
+        *(uint4*)(tile + tile_at<W>(row, piece + i)) =
+            make_uint4(p[4 * i] ^ sign, p[4 * i + 1] ^ sign, p[4 * i + 2] ^ sign, p[4 * i + 3] ^ sign);
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),
+                 "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void prefetch(const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar)
 {
@@ -115,9 +126,12 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     char* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const uint32_t base = smem_addr(sm);
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
-    uint64_t *full = bars, *empty = full + 2, *landed = empty + 2, *ks_done = landed + 1, *qs_done = ks_done + 1, *ty_done = qs_done + 1;
-    uint64_t *s_done = ty_done + 1, *o_done = s_done + 1, *y_ready = o_done + 1, *u_ready = y_ready + 1, *s_ready = u_ready + 1;
-    uint64_t *o_scaled = s_ready + 1, *o_read = o_scaled + 1, *drain = o_read + 1;
+    // [2]: by stage (full, empty), or of the two warpgroups
+    uint64_t *full = bars, *empty = full + 2, *ks_done = empty + 2, *ty_done = ks_done + 2, *s_done = ty_done + 2;
+    uint64_t *y_ready = s_done + 2, *u_ready = y_ready + 2, *s_ready = u_ready + 2;
+    uint64_t *landed = s_ready + 2, *qs_done = landed + 1;
+    uint64_t *o_done = qs_done + 1, *o_scaled = o_done + 1, *o_read = o_scaled + 1;
+    uint64_t *s_kept = o_read + 1, *u_kept = s_kept + 1, *s_free = u_kept + 1, *u_free = s_free + 1, *drain = u_free + 1;
     uint32_t* tm_ptr = (uint32_t*)(drain + 1);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
@@ -132,11 +146,12 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             for (int i = 0; i < 2; ++i) {
                 mbar_init(full + i, 1);
                 mbar_init(empty + i, KEEP ? 9 : 13);   // the MMAs, and each warp that reads the stage
+                for (uint64_t* b : {ks_done, ty_done, s_done}) mbar_init(b + i, 1);
+                for (uint64_t* b : {y_ready, u_ready, s_ready}) mbar_init(b + i, 4);
             }
-            for (uint64_t* b : {landed, ks_done, qs_done, ty_done, s_done, o_done, drain}) mbar_init(b, 1);
-            for (uint64_t* b : {y_ready, u_ready, s_ready}) mbar_init(b, 8);
-            mbar_init(o_scaled, 4);
-            mbar_init(o_read, 4);
+            for (uint64_t* b : {landed, qs_done, o_done, s_free, u_free, drain}) mbar_init(b, 1);
+            for (uint64_t* b : {o_scaled, o_read}) mbar_init(b, 4);
+            for (uint64_t* b : {s_kept, u_kept}) mbar_init(b, 8);
             *guard.flag = 0;
             fence_mbar_init();
             fence_async_smem();
@@ -163,13 +178,30 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             if (warp_up(guard)) break;
             uint64_t* bar = valid < C ? landed : full + (c & 1);
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, (KEEP ? 1 : 2) * C * DK * 2 + C * DV * 2 + REC_BYTES);
+                mbar_arrive_expect_tx(bar, (KEEP ? 1 : 2) * C * DK * 2 + C * DV * 2 + REC_BYTES - (KEEP ? REC_SCAL - REC_P : 0));
                 for (int p = 0; p < DK / 64; ++p) {
                     tma_load_3d(st + L::K_ + p * L::PANEL, &mk, bar, p * 64, hk, (int)t0 + c * C);
                     if (!KEEP) tma_load_3d(st + L::Q_ + p * L::PANEL, &mq, bar, p * 64, hk, (int)t0 + c * C);
                 }
                 for (int p = 0; p < DV / 64; ++p) tma_load_3d(st + L::V_ + p * L::PANEL, &mv, bar, p * 64, h, (int)t0 + c * C);
-                bulk_load(st + L::REC, rec + (int64_t)c * a.Hv * REC_BYTES, REC_BYTES, bar);
+                const char* src = rec + (int64_t)c * a.Hv * REC_BYTES;
+                if (KEEP) {
+                    bulk_load(st + L::REC, src, REC_P, bar);
+                    bulk_load(st + L::SCAL, src + REC_SCAL, REC_BYTES - REC_SCAL, bar);
+                } else {
+                    bulk_load(st + L::REC, src, REC_BYTES, bar);
+                }
+                // The stage after next is still in use: its data come as far as L2 meanwhile, or the
+                // chain would wait for memory once a chunk.
+                if (c + 2 < nch) {
+                    const int y = (int)t0 + (c + 2) * C;
+                    for (int p = 0; p < DK / 64; ++p) {
+                        prefetch_3d(&mk, p * 64, hk, y);
+                        if (!KEEP) prefetch_3d(&mq, p * 64, hk, y);
+                    }
+                    for (int p = 0; p < DV / 64; ++p) prefetch_3d(&mv, p * 64, h, y);
+                    prefetch(src + 2 * (int64_t)a.Hv * REC_BYTES, REC_BYTES);
+                }
             }
             ++issued;
             if (valid < C) {
@@ -190,75 +222,103 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         const uint64_t dk = desc_rows(base + L::K_), dq = desc_rows(base + L::Q_), dkc = desc_cols(base + L::K_, L::PANEL);
         const uint64_t dv = desc_cols(base + L::V_, L::PANEL), de = desc_rows(base + L::EYE);
         const uint64_t dt = sdesc(base + L::REC, 128, 256);   // core matrices: halves 128 bytes apart along K, rows 256
+        // MMAs that follow one another on the same columns have the same shape, which is what orders
+        // them.  The halves of the tokens (32 columns of a product) and of the key channels are the
+        // warpgroups': each starts on its half while the other's is computed.
+        constexpr uint32_t id_t = idesc_f16(128, 32, false, false, false, true);
+        constexpr uint32_t id_ks = idesc_f16(128, 32, false, false, true, true);     // -K S
+        constexpr uint32_t id_qs = idesc_f16(128, C, false, false, false, true);
+        // (with Dv = 64 rows 64 on read what is behind V; they are not used)
+        constexpr uint32_t id_v = idesc_f16(128, C, true, false, false, true);
+        constexpr uint32_t id_s = idesc_f16(128, 64, false, true, false, true);
+        constexpr uint32_t NEG = 1u << 13;   // a second plane has the opposite sign
+        constexpr int KH = DK / 32;          // k-steps of half of the key channels
+        auto by_s = [&](uint32_t to, uint64_t desc, uint32_t id, int kh) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int x = kh * KH; x < kh * KH + KH; ++x)
+                    umma_f16_ts(to, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(desc, x, L::PANEL), id ^ (p ? NEG : 0), kh + p + (x - kh * KH) > 0);
+        };
+        // rows 32 th .. 32 th + 31 of a plane of T or P, times the tokens of k-step x
+        auto tri = [&](uint32_t so, int plane, int th, int x) { return dt + so + ((plane * TRI + blk(2 * th, x)) >> 4); };
         for (int c = 0; c < nch; ++c) {
             const uint32_t so = (c & 1) * (L::STAGE >> 4);
             wait(full + (c & 1), (c >> 1) & 1, guard);
+            if (c > 0) wait(s_done + 1, (c - 1) & 1, guard);   // decayed U is where K S goes
             wait(s_ready, c & 1, guard);
             tc_fence_after();
-            constexpr uint32_t id_qs = idesc_f16(128, C, false, false, false, true);
-            constexpr uint32_t id_ks = idesc_f16(128, C, false, false, true, true);     // -K S
-            // (with Dv = 64 rows 64 on read the record behind V; they are not used)
-            constexpr uint32_t id_v = idesc_f16(128, C, true, false, false, true);
             if (elect()) {
+                by_s(tmem + L::R_ + 64, dk + so, id_ks, 0);
+                by_s(tmem + L::R_ + 96, dk + so + (4096 >> 4), id_ks, 0);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) umma_f16(tmem + L::R_, step_cols(dv + so, x), step_rows(de, x, L::PANEL), id_v, x > 0);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int x = 0; x < DK / 16; ++x)
-                        umma_f16_ts(tmem + L::R_ + 64, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(dk + so, x, L::PANEL), id_ks, p + x > 0);
-                umma_commit(ks_done);
             }
-            if (!KEEP) {
-                if (c > 0) wait(o_read, (c - 1) & 1, guard);
+            wait(s_ready + 1, c & 1, guard);
+            tc_fence_after();
+            if (elect()) {
+                by_s(tmem + L::R_ + 64, dk + so, id_ks, 1);
+                umma_commit(ks_done);
+                by_s(tmem + L::R_ + 96, dk + so + (4096 >> 4), id_ks, 1);
+                umma_commit(ks_done + 1);
+            }
+            if (!KEEP && c > 0) wait(o_done, (c - 1) & 1, guard);   // the planes of U are where T Y goes
+#pragma unroll
+            for (int th = 0; th < 2; ++th) {   // T Y: every product of planes but T1 Y2
+                wait(y_ready + th, c & 1, guard);
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
-                    for (int p = 0; p < 2; ++p)
+                    for (int q = 0; q < TPL; ++q)
 #pragma unroll
-                        for (int x = 0; x < DK / 16; ++x)
-                            umma_f16_ts(tmem + L::O_, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(dq + so, x, L::PANEL), id_qs, p + x > 0);
+                        for (int p = 0; p < PLANES - q; ++p)
+#pragma unroll
+                            for (int x = 0; x < 2 * th + 2; ++x)
+                                umma_f16_ts(tmem + L::U_ + 32 * th, tmem + L::R_ + y_at(p, x), tri(so, q, th, x), id_t ^ (p == 1 ? NEG : 0), p + q + x > 0);
+                    umma_commit(ty_done + th);
+                }
+            }
+            if (!KEEP) {   // while U is turned into its planes
+                if (c > 0) wait(o_read, (c - 1) & 1, guard);
+                tc_fence_after();
+                if (elect()) {
+                    by_s(tmem + L::O_, dq + so, id_qs, 0);
+                    by_s(tmem + L::O_, dq + so, id_qs, 1);
                     umma_commit(qs_done);
                 }
             }
-            wait(y_ready, c & 1, guard);
-            tc_fence_after();
-            if (elect()) {
-                // every product of planes but T1 Y2; T's block column x starts at row 16 x
 #pragma unroll
-                for (int q = 0; q < TPL; ++q)
+            for (int th = 0; th < 2; ++th) {
+                wait(u_ready + th, c & 1, guard);
+                tc_fence_after();
+                if (elect()) {
 #pragma unroll
-                    for (int p = 0; p < PLANES - q; ++p)
+                    for (int n = 0; n < DK / 64; ++n) {   // 64 key channels
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            umma_f16_ts(tmem + L::U_ + 16 * x, tmem + L::R_ + y_at(p, x), dt + so + ((q * TRI + blk(x, x)) >> 4),
-                                        idesc_f16(128, C - 16 * x, false, false, false, true), p + q + x > 0);
-                umma_commit(ty_done);
-            }
-            wait(u_ready, c & 1, guard);
-            tc_fence_after();
-            if (elect()) {
+                        for (int p = PLANES - 1; p >= 0; --p)
 #pragma unroll
-                for (int p = PLANES - 1; p >= 0; --p)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        umma_f16_ts(tmem + L::M_, tmem + L::R_ + y_at(p, x), step_cols(dkc + so, x),
-                                    idesc_f16(128, DK, false, true, false, true), 1);
-                umma_commit(s_done);
+                            for (int x = 2 * th; x < 2 * th + 2; ++x)
+                                umma_f16_ts(tmem + L::M_ + 64 * n, tmem + L::R_ + y_at(p, x), step_cols(dkc + so, x) + (n * L::PANEL >> 4),
+                                            id_s ^ (p == 1 ? NEG : 0), 1);
+                        if (th) umma_commit(s_done + n);
+                    }
+                    if (th && DK == 64) umma_commit(s_done + 1);
+                }
             }
             if (!KEEP) {
                 wait(o_scaled, c & 1, guard);
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
-                    for (int q = 0; q < PPL; ++q)
+                    for (int th = 0; th < 2; ++th)
 #pragma unroll
-                        for (int p = 0; p < 2 - q; ++p)
+                        for (int q = 0; q < PPL; ++q)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            umma_f16_ts(tmem + L::O_ + 16 * x, tmem + L::U_ + (x >> 1) * 32 + p * 16 + (x & 1) * 8,
-                                        dt + so + ((REC_P + q * TRI + blk(x, x)) >> 4),
-                                        idesc_f16(128, C - 16 * x, false, false, false, true), 1);
+                            for (int p = 0; p < 2 - q; ++p)
+#pragma unroll
+                                for (int x = 0; x < 2 * th + 2; ++x)
+                                    umma_f16_ts(tmem + L::O_ + 32 * th, tmem + L::U_ + (x >> 1) * 32 + p * 16 + (x & 1) * 8, tri(so, TPL + q, th, x),
+                                                id_t ^ (p ? NEG : 0), 1);
                     umma_commit(o_done);
                 }
             }
@@ -274,49 +334,47 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16);
         const bool real = row < DV;
         const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * DV + (int64_t)hf * HK * DV + row;
-        const Kept keep{DK, DV};
-        auto scal_of = [&](int c) { return (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL); };
+        auto scal_of = [&](int c) { return (const float*)(sm + (c & 1) * L::STAGE + L::SCAL); };
         // 32 of the half's channels: to the planes, and decayed for chunk c
-        auto put = [&](int i, uint64_t (&s)[16], int c, char* dst) {
+        auto put = [&](int i, float (&s)[32], int c) {
             uint32_t p[2][16];
             planes_of<2>(s, p);
             tmem_st16u_nowait(at + L::SP_ + hf * (HK / 2) + i * 16, p[0]);
             tmem_st16u_nowait(at + L::SP_ + DK / 2 + hf * (HK / 2) + i * 16, p[1]);
             if (KEEP && real) {
-                store64(dst + keep.s() + (row * DK + hf * HK + i * 32) * 2, p[0]);
-                store64(dst + keep.s() + keep.state() + (row * DK + hf * HK + i * 32) * 2, p[1]);
+                to_tile<DK>(sm + L::OUT, row, hf * (HK / 8) + i * 4, p[0]);
+                to_tile<DK>(sm + L::OUT + DV * DK * 2, row, hf * (HK / 8) + i * 4, p[1], 0x80008000u);
             }
             const float gam = scal_of(c)[C - 1];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) s[x] = mul2(s[x], pair(gam, gam));
+            for (int x = 0; x < 32; ++x) s[x] *= gam;
             store32(at + L::M_ + hf * HK + i * 32, s);
         };
-        char* mine = KEEP ? kept + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * keep.bytes() : nullptr;
-        const int64_t next = KEEP ? (int64_t)a.Hv * keep.bytes() : 0;
+        auto state_ready = [&] {
+            if (KEEP) {
+                fence_async_smem();
+                warp_arrive(s_kept);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(s_ready + hf);
+        };
         if (nch > 0) {
             wait(full, 0, guard);
 #pragma unroll
             for (int i = 0; i < HK / 32; ++i) {
-                uint64_t s[16];
+                float s[32];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int64_t off = soff + (int64_t)(i * 32 + 2 * x) * DV;
-                    s[x] = a.S0 && real ? pair(a.S0[off], a.S0[off + DV]) : 0;
-                }
-                put(i, s, 0, mine);
+                for (int x = 0; x < 32; ++x) s[x] = a.S0 && real ? a.S0[soff + (int64_t)(i * 32 + x) * DV] : 0.f;
+                put(i, s, 0);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(s_ready);
+            state_ready();
         } else if (a.ST && real) {
             for (int x = 0; x < HK; ++x) a.ST[soff + (int64_t)x * DV] = a.S0 ? a.S0[soff + (int64_t)x * DV] : 0.f;
         }
         for (int c = 0; c < nch; ++c) {
             const float* scal = scal_of(c);
-            const uint32_t st = (c & 1) * L::STAGE;
-            char* dst = KEEP ? mine + c * next : nullptr;
-            wait(full + (c & 1), (c >> 1) & 1, guard);
-            uint64_t x[16];
+            float x[32];
             uint32_t p[3][16];
             auto put_y = [&] {
                 planes_of<3>(x, p);
@@ -324,96 +382,113 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 for (int q = 0; q < 3; ++q) tmem_st16u_nowait(at + L::R_ + y_at(q, 2 * hf), p[q]);
             };
             // Y = beta o (V - e^cum o (K S)), 32 tokens
-            wait(ks_done, c & 1, guard);
+            wait(ks_done + hf, c & 1, guard);
             tc_fence_after();
             {
-                uint64_t ks[16];
-                load32(at + L::R_ + hf * 32, x);
-                load32(at + L::R_ + 64 + hf * 32, ks);
+                float ks[32];
+                tmem_ld32(at + L::R_ + hf * 32, x);
+                tmem_ld32(at + L::R_ + 64 + hf * 32, ks);
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const ulonglong2 g = *(const ulonglong2*)&scal[hf * 32 + 2 * i];
-                    x[i] = fma2(g.x, ks[i], x[i]);
-                    x[i + 1] = fma2(g.y, ks[i + 1], x[i + 1]);
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 g = *(const float4*)&scal[hf * 32 + i];
+                    x[i] = fmaf(g.x, ks[i], x[i]);
+                    x[i + 1] = fmaf(g.y, ks[i + 1], x[i + 1]);
+                    x[i + 2] = fmaf(g.z, ks[i + 2], x[i + 2]);
+                    x[i + 3] = fmaf(g.w, ks[i + 3], x[i + 3]);
                 }
             }
             if (DV < 128 && !real) {   // rows that no column of V fills
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = 0;
+                for (int i = 0; i < 32; ++i) x[i] = 0.f;
             }
-            if (KEEP && real) {
+            if (KEEP) {
+                if (c > 0) wait(u_free, (c - 1) & 1, guard);
                 uint32_t r[1][16];
                 planes_of<1>(x, r);
-                store64(dst + keep.r() + (row * C + hf * 32) * 2, r[0]);
+                if (real) to_tile<C>(sm + L::OUT_R, row, hf * 4, r[0]);
             }
             scale32(x, scal + 2 * C + hf * 32);
             put_y();
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(y_ready);
+            warp_arrive(y_ready + hf);
             // U, its planes, and decayed
-            wait(ty_done, c & 1, guard);
+            if (c + 1 < nch) wait(full + ((c + 1) & 1), ((c + 1) >> 1) & 1, guard);
+            if (KEEP) wait(s_free, c & 1, guard);
+            wait(ty_done + hf, c & 1, guard);
             tc_fence_after();
-            load32(at + L::U_ + hf * 32, x);
+            tmem_ld32(at + L::U_ + hf * 32, x);
             {
                 uint32_t u[2][16];
                 planes_of<2>(x, u);
                 if (KEEP) {
                     if (real) {
-                        store64(dst + keep.u() + (row * C + hf * 32) * 2, u[0]);
-                        store64(dst + keep.u() + keep.rows() + (row * C + hf * 32) * 2, u[1]);
+                        to_tile<C>(sm + L::OUT_U, row, hf * 4, u[0]);
+                        to_tile<C>(sm + L::OUT_U + DV * C * 2, row, hf * 4, u[1], 0x80008000u);
                     }
+                    fence_async_smem();
+                    warp_arrive(u_kept);
                 } else {
                     tmem_st16u_nowait(at + L::U_ + hf * 32, u[0]);
                     tmem_st16u_nowait(at + L::U_ + hf * 32 + 16, u[1]);
                 }
             }
             scale32(x, scal + C + hf * 32);
+            wait(ty_done + 1, c & 1, guard);   // the second half of T Y reads both halves' planes of Y
+            tc_fence_after();
             put_y();
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(u_ready);
+            warp_arrive(u_ready + hf);
             warp_arrive(empty + (c & 1));
-            if (c + 1 < nch) wait(full + ((c + 1) & 1), ((c + 1) >> 1) & 1, guard);
             if (!KEEP) wait(qs_done, c & 1, guard);   // its planes of S
-            wait(s_done, c & 1, guard);
+            wait(s_done + hf, c & 1, guard);
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < HK / 32; ++i) {
-                uint64_t s[16];
-                load32(at + L::M_ + hf * HK + i * 32, s);
+                float s[32];
+                tmem_ld32(at + L::M_ + hf * HK + i * 32, s);
                 if (c + 1 < nch) {
-                    put(i, s, c + 1, KEEP ? dst + next : nullptr);
+                    put(i, s, c + 1);
                 } else if (a.ST && real) {
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        float lo, hi;
-                        unpair(s[y], lo, hi);
-                        a.ST[soff + (int64_t)(i * 32 + 2 * y) * DV] = lo;
-                        a.ST[soff + (int64_t)(i * 32 + 2 * y + 1) * DV] = hi;
-                    }
+                    for (int y = 0; y < 32; ++y) a.ST[soff + (int64_t)(i * 32 + y) * DV] = s[y];
                 }
             }
-            if (c + 1 < nch) {
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(s_ready);
-            }
+            if (c + 1 < nch) state_ready();
         }
-    } else if (!KEEP) {
+    } else if (KEEP) {
+        if (warp == 8 && lane == 0) {   // what the gradients need goes out by the copy engine
+            const Kept keep{DK, DV};
+            char* dst = kept + ((int64_t)seqs.slot0(seq, C) * a.Hv + h) * keep.bytes();
+            for (int c = 0; c < nch; ++c, dst += (int64_t)a.Hv * keep.bytes()) {
+                wait(s_kept, c & 1, guard);
+                bulk_store(dst + keep.s(), sm + L::OUT, 2 * DV * DK * 2);
+                bulk_commit();
+                bulk_wait_read0();
+                mbar_arrive(s_free);
+                wait(u_kept, c & 1, guard);
+                bulk_store(dst + keep.u(), sm + L::OUT_U, 3 * DV * C * 2);   // U and, behind it, R
+                bulk_commit();
+                bulk_wait_read0();
+                mbar_arrive(u_free);
+            }
+            bulk_wait0();
+        }
+    } else {
         const int row = tid & 127, t = tid - 256;
         const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16) + L::O_;
         __nv_bfloat16* op = (__nv_bfloat16*)a.o + (t0 * a.Hv + h) * DV;
         __nv_bfloat16* out = (__nv_bfloat16*)(sm + L::OUT);
         for (int c = 0; c < nch; ++c) {
-            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::REC + REC_SCAL);
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::SCAL);
             wait(full + (c & 1), (c >> 1) & 1, guard);
             wait(qs_done, c & 1, guard);
             tc_fence_after();
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                uint64_t x[16];
-                load32(at + hf * 32, x);
+                float x[32];
+                tmem_ld32(at + hf * 32, x);
                 scale32(x, scal + hf * 32);
                 store32(at + hf * 32, x);
             }

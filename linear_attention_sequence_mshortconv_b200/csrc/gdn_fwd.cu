@@ -233,7 +233,9 @@ __global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const _
             *(float4*)&T[48 + i2][c2] = make_float4(-x[1][0], -x[1][1], -x[1][2], -x[1][3]);
         }
         __syncthreads();
-        // the ten blocks, 128 pairs each, as planes
+        // the ten blocks, 128 pairs each, as planes; and the zeros
+        for (int e = tid; e < 2 * (TPL + PPL) * BLK / 16; e += 128)
+            *(uint4*)(rec + e / (2 * BLK / 16) * TRI + (e & (BLK / 16) ? blk(2, 3) : blk(0, 1)) + e % (BLK / 16) * 16) = make_uint4(0, 0, 0, 0);
         const int ii = ((tid >> 6) << 3) + ((tid >> 2) & 7), jj = (((tid >> 5) & 1) << 3) + (tid & 3) * 2;
 #pragma unroll
         for (int ib = 0; ib < 4; ++ib)
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
                 char* dst = kept + ((int64_t)(seqs.slot0(seq, C) + c) * a.Hv + h) * keep.bytes();
                 for (int e = lt; e < SPL * 16 * MT * DK / 8; e += LOADERS) {
                     const int piece = e % (DK / 8), row = e / (DK / 8) % (16 * MT), p = e / (DK / 8) / (16 * MT);
-                    *(uint4*)(dst + keep.s() + p * keep.state() + ((v0 + row) * DK + piece * 8) * 2) =
+                    *(uint4*)(dst + keep.s() + p * keep.state() + tile_at<DK>(v0 + row, piece)) =
                         *(const uint4*)(sm + L::SP + (p * 16 * MT + row) * L::SROW + piece * 16);
                 }
 #pragma unroll
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
                 for (int e = lt; e < 3 * 16 * MT * 8; e += LOADERS) {
                     const int piece = e & 7, row = e / 8 % (16 * MT), p = e / 8 / (16 * MT);
                     const uint4 x = *(const uint4*)(sm + (p < 2 ? L::WP + (p * 16 * MT + row) * L::TROW : L::OS + row * L::TROW) + piece * 16);
-                    *(uint4*)(dst + (p < 2 ? keep.u() + p * keep.rows() : keep.r()) + ((v0 + row) * C + piece * 8) * 2) = x;
+                    *(uint4*)(dst + (p < 2 ? keep.u() + p * keep.rows() : keep.r()) + tile_at<C>(v0 + row, piece)) = x;
                 }
                 continue;
             }
@@ -575,11 +577,7 @@ cudaError_t launch_scan(const GdnArgs& a, const Seqs& s, const void* records, vo
 
 namespace gdn {
 // Which scan: whole heads (gdn_chain.cu) or columns of heads.
-bool whole_heads(const GdnArgs& a, const Seqs& s, int sms)
-{
-    (void)s; (void)sms;
-    return a.Dv != 32;
-}
+bool whole_heads(const GdnArgs& a, const Seqs& s, int sms) { return a.Dv != 32 && (int64_t)s.n * a.Hv * (a.Dv / 32) > sms; }
 }  // namespace gdn
 
 // The tensor-core path copies rows in 16-byte pieces.

@@ -38,15 +38,24 @@ __device__ __forceinline__ float low(uint32_t p) { return __uint_as_float(p << 1
 __device__ __forceinline__ float high(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 // A pair of fp32 values as N bf16 planes: x = p0 + p1 + ..., each plane the rounded rest of
 // the ones before, so N planes leave 2^-(9N) of x (N = 3: less than fp32's own half step).
+__device__ __forceinline__ float less(uint16_t a, float b)   // a - b, in one instruction
+{
+    float r;
+    asm("sub.rn.f32.bf16 %0, %1, %2;" : "=f"(r) : "h"(a), "f"(b));
+    return r;
+}
 template <int N>
 __device__ __forceinline__ void split(float a, float b, uint32_t (&p)[N])
 {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         p[i] = pack(a, b);
-        a -= low(p[i]);
-        b -= high(p[i]);
+        if (i + 1 < N) {   // minus the rest
+            a = less((uint16_t)p[i], a);
+            b = less((uint16_t)(p[i] >> 16), b);
+        }
     }
+    if (N > 1) p[1] ^= 0x80008000u;
 }
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) { ldsm_x4(r, addr); }
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) { ldsm_x4_t(r, addr); }
@@ -90,16 +99,18 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src
 // A chunk's factors for one value head, written by the prologue kernel and read by the scans:
 // T = (I + A)^-1 in TPL planes and P = lower(e^{cum_i - cum_j} q_i.k_j) in PPL planes, each
 // the ten 16x16 blocks on and below the diagonal, a block as four 8x8 core matrices of 128
-// contiguous bytes; then e^cum, e^{cum_C - cum}, beta, and cum log2(e) as a sum of two floats.
+// contiguous bytes, and two of zeros; then e^cum, e^{cum_C - cum}, beta, and cum log2(e) as a sum of two floats.
 constexpr int BLK = 512;
-constexpr int TRI = 10 * BLK;
+constexpr int TRI = 12 * BLK;
 constexpr int REC_P = TPL * TRI, REC_SCAL = (TPL + PPL) * TRI, REC_BYTES = REC_SCAL + 5 * C * 4;
-// blocks column by column: those of one column are evenly spaced, as an MMA's descriptor needs
-__host__ __device__ constexpr int blk(int ib, int jb) { return (ib + jb * 3 - jb * (jb - 1) / 2) * BLK; }
+// Blocks column by column, with zeros before (1, 1) and (3, 3), that is, as (0, 1) and (2, 3): the two
+// blocks that any column has in one half of the rows lie side by side, as an MMA needs.
+__host__ __device__ constexpr int blk(int ib, int jb) { return (ib + (jb ? 2 + 2 * jb : 0)) * BLK; }
 
 // What the backward keeps of each chunk and value head, bf16: the entry state S^T and the
-// gradient D^T of the exit state, [Dv][Dk] in two planes each; U^T and dY^T, [Dv][64] in two
-// planes each; R^T, [Dv][64].  Then per-warp parts of <exit state, D>, fp32, Dv / 4.
+// gradient D^T of the exit state, [Dv][Dk] in two planes each; U^T, [Dv][64] in two planes, R^T,
+// [Dv][64], and dY^T, [Dv][64] in two planes; every plane as the tile (tile_at) that the gradients' kernel reads.
+// Then per-warp parts of <exit state, D>, fp32, Dv / 4.
 struct Kept {
     int Dk, Dv;
     __host__ __device__ size_t state() const { return (size_t)Dv * Dk * 2; }     // bytes of a plane
@@ -107,9 +118,9 @@ struct Kept {
     __host__ __device__ size_t s() const { return 0; }
     __host__ __device__ size_t d() const { return 2 * state(); }
     __host__ __device__ size_t u() const { return 4 * state(); }
-    __host__ __device__ size_t y() const { return u() + 2 * rows(); }
-    __host__ __device__ size_t r() const { return y() + 2 * rows(); }
-    __host__ __device__ size_t exit() const { return r() + rows(); }
+    __host__ __device__ size_t r() const { return u() + 2 * rows(); }
+    __host__ __device__ size_t y() const { return r() + rows(); }
+    __host__ __device__ size_t exit() const { return y() + 2 * rows(); }
     __host__ __device__ size_t bytes() const { return (exit() + Dv + 255) / 256 * 256; }
 };
 
