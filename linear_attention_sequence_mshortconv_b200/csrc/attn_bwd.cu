@@ -323,9 +323,14 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 // ---- dq -------------------------------------------------------------------------------------
 // The forward's layout: two tiles of 128 rows in turn over blocks of 64 keys, S = Q K^T and
 // dP = dO V^T, then dQ += dS K.  Tensor memory: dQ0, dQ1 (D each), 2 x (S 64, dP 64).
+//
+// delta = do.o is as exact as the rounded o.  For a row that sees few keys o is as large as a value, and
+// its rounding (2^-8) weighs as much in dS as dS's own: rows of the first SHORT blocks take
+// delta = sum_j p_ij (do_i.v_j) from a pass of their own over their keys (a few blocks), and leave it
+// for the keys' kernel, which runs after this one.  For longer rows o is an average, and smaller.
 template <int D>
 struct Dq {
-    static constexpr int QR = 128, KB = 64;
+    static constexpr int QR = 128, KB = 64, SHORT = 4;
     static constexpr int QPANEL = QR * 128, QTILE = D / 64 * QPANEL;
     static constexpr int KPANEL = KB * 128, KTILE = D / 64 * KPANEL;
     static constexpr int STAGES = D == 64 ? 6 : 2;
@@ -337,7 +342,7 @@ struct Dq {
 template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnBwdArgs b,
-                     const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, const float* ndelta, int* status)
+                     const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, float* ndelta, int* status)
 {
     using L = Dq<D>;
     const AttnArgs& a = b.f;
@@ -362,14 +367,15 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     };
     const int n0 = blocks(0), n1 = blocks(1), n = max(n0, n1);
     const int tail = len - (n - 1) * L::KB;   // keys of the last block
+    const int passes = n <= L::SHORT ? 2 : 1, total = passes * n;   // blocks that go through the ring
 
     const RowAt row_at{t0, a.H, hk * (int)r, (int)r, D};
     auto load = [&](int j) {
-        const int s = j % L::STAGES;
+        const int s = j % L::STAGES, y = (int)t0 + j % n * L::KB;
         mbar_arrive_expect_tx(full + s, 2 * L::KTILE);
         for (int p = 0; p < D / 64; ++p) {
-            tma_load_3d(sm + L::K_ + s * L::KTILE + p * L::KPANEL, &tm_k, full + s, p * 64, hk, (int)t0 + j * L::KB);
-            tma_load_3d(sm + L::V_ + s * L::KTILE + p * L::KPANEL, &tm_v, full + s, p * 64, hk, (int)t0 + j * L::KB);
+            tma_load_3d(sm + L::K_ + s * L::KTILE + p * L::KPANEL, &tm_k, full + s, p * 64, hk, y);
+            tma_load_3d(sm + L::V_ + s * L::KTILE + p * L::KPANEL, &tm_v, full + s, p * 64, hk, y);
         }
     };
     if (warp == 10) {
@@ -389,7 +395,7 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             *guard.flag = 0;
             fence_mbar_init();
             fence_async_smem();
-            for (int j = 0; j < n && j < L::STAGES; ++j) load(j);
+            for (int j = 0; j < total && j < L::STAGES; ++j) load(j);
         }
     } else if (warp == 8) {
         tmem_alloc(tm_ptr, 512);
@@ -414,8 +420,8 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 
     if (warp >= 10) {
         if (warp == 10 && lane == 0) {
-            int issued = min(n, L::STAGES);
-            for (; issued < n; ++issued) {
+            int issued = min(total, L::STAGES);
+            for (; issued < total; ++issued) {
                 wait(empty + issued % L::STAGES, ((issued / L::STAGES) & 1) ^ 1, guard);
                 if (guard.up()) break;
                 load(issued);
@@ -424,8 +430,8 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         __syncwarp();
         if (warp == 10 && tail < L::KB && !guard.up()) {   // keys past the end (dS is 0 there): K must be finite
-            const int s = (n - 1) % L::STAGES;
-            wait(full + s, ((n - 1) / L::STAGES) & 1, guard);
+            const int s = (total - 1) % L::STAGES;
+            wait(full + s, ((total - 1) / L::STAGES) & 1, guard);
             for (int e = lane; e < (L::KB - tail) * (D / 8); e += 32) {
                 const int row = tail + e / (D / 8), piece = e % (D / 8);
                 *(uint4*)(sm + L::K_ + s * L::KTILE + (piece >> 3) * L::KPANEL + piece_at(row, piece & 7)) = make_uint4(0, 0, 0, 0);
@@ -441,10 +447,18 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const uint32_t ts = tmem + L::S_ + t * L::BUF, tp = tmem + L::P_ + t * L::BUF, to = tmem + L::DQ_ + t * D;
         const uint64_t dq = desc_rows(base + L::Q_ + t * L::QTILE), dg = desc_rows(base + L::G_ + t * L::QTILE);
         const uint64_t dk = desc_rows(base + L::K_), dv = desc_rows(base + L::V_), dkc = desc_cols(base + L::K_, L::KPANEL);
-        for (int j = 0; j < nt; ++j) {
-            const int s = j % L::STAGES;
-            wait(full + s, (j / L::STAGES) & 1, guard);
-            if (j > 0) wait(done + t, (j - 1) & 1, guard);   // dS is in dP's place
+        for (int g = 0, it = 0, j = 0; g < total; ++g, j = j + 1 == n ? 0 : j + 1) {   // g: block of the ring, it: of this tile
+            const int s = g % L::STAGES;
+            if (j >= nt) {   // a block that only the other tile sees (as in the forward)
+                if (lane == 0) {
+                    wait(empty + s, ((g / L::STAGES) & 1) ^ 1, guard);
+                    mbar_arrive(empty + s);
+                }
+                __syncwarp();
+                continue;
+            }
+            wait(full + s, (g / L::STAGES) & 1, guard);
+            if (it > 0) wait(done + t, (it - 1) & 1, guard);   // dS is in dP's place
             tc_fence_after();
             if (elect()) {
 #pragma unroll
@@ -456,22 +470,19 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     umma_f16(tp, step_rows(dg, x, L::QPANEL), step_rows(dv + (s * L::KTILE >> 4), x, L::KPANEL), id_g, x > 0);
                 umma_commit(gfull + t);
             }
-            if (j == n - 1 && tail < L::KB) wait(fix, 0, guard);
-            wait(dready + t, j & 1, guard);
+            if (g == total - 1 && tail < L::KB) wait(fix, 0, guard);
+            wait(dready + t, it & 1, guard);
             tc_fence_after();
             if (elect()) {
+                if (g >= total - n)   // (the pass for delta has no dS)
 #pragma unroll
-                for (int x = 0; x < L::KB / 16; ++x)
-                    umma_f16_ts(to, tp + x * 8, step_cols(dkc + (s * L::KTILE >> 4), x), id_o, j > 0 || x > 0);
+                    for (int x = 0; x < L::KB / 16; ++x)
+                        umma_f16_ts(to, tp + x * 8, step_cols(dkc + (s * L::KTILE >> 4), x), id_o, j > 0 || x > 0);
                 umma_commit(empty + s);
                 umma_commit(done + t);
             }
+            ++it;
         }
-        if (lane == 0)   // blocks that only the other tile sees (as in the forward)
-            for (int j = nt; j < n && !guard.up(); ++j) {
-                wait(empty + j % L::STAGES, ((j / L::STAGES) & 1) ^ 1, guard);
-                mbar_arrive(empty + j % L::STAGES);
-            }
         __syncwarp();
         drain_mma(drain + t, guard);
     } else {
@@ -485,9 +496,11 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const int least = (int)(min(first + t * L::QR + (warp & 3) * 32, all - 1) / r);
         const int64_t rd = ((int64_t)hk * seqs.tokens() + t0) * r + i;
         const float nl = real ? nlse[rd] : 0.f, nd = real ? ndelta[rd] : 0.f;
-        const uint64_t sl2 = pair(sl, sl), nl2 = pair(nl, nl), nd2 = pair(nd, nd);
-        for (int j = 0; j < nt; ++j) {
-            wait(sfull + t, j & 1, guard);
+        const uint64_t sl2 = pair(sl, sl), nl2 = pair(nl, nl);
+        uint64_t nd2 = pair(nd, nd), sum = 0;
+        for (int it = 0, j = 0; it < passes * nt; ++it, j = j + 1 == nt ? 0 : j + 1) {
+            const bool last = it >= (passes - 1) * nt;
+            wait(sfull + t, it & 1, guard);
             tc_fence_after();
             float p[64];
             tmem_ld64(ts, p);
@@ -497,7 +510,7 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 p[x] = ex2_approx(p[x]);
                 p[x + 1] = ex2_approx(p[x + 1]);
             }
-            wait(gfull + t, j & 1, guard);
+            wait(gfull + t, it & 1, guard);
             tc_fence_after();
             const bool edge = j * L::KB + L::KB - 1 > least;
             const int seen = token - j * L::KB;
@@ -506,23 +519,35 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             for (int hlf = 0; hlf < 2; ++hlf) {
                 float g[32];
                 tmem_ld32(tp + hlf * 32, g);
+                const uint64_t off = last ? nd2 : 0;
 #pragma unroll
                 for (int x = 0; x < 32; x += 2)
-                    unpair(mul2(pair(p[hlf * 32 + x], p[hlf * 32 + x + 1]), add2(pair(g[x], g[x + 1]), nd2)), g[x], g[x + 1]);
+                    unpair(mul2(pair(p[hlf * 32 + x], p[hlf * 32 + x + 1]), add2(pair(g[x], g[x + 1]), off)), g[x], g[x + 1]);
                 if (edge)
 #pragma unroll
                     for (int x = 0; x < 32; ++x)
                         if (hlf * 32 + x > seen) g[x] = 0.f;
+                if (!last)
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) sum = add2(sum, pair(g[x], g[x + 1]));
 #pragma unroll
                 for (int x = 0; x < 16; ++x) q[hlf * 16 + x] = pack_bf16(g[2 * x], g[2 * x + 1]);
             }
-            tmem_st32u_nowait(tp, q);
-            tmem_wait_st();
+            if (last) {
+                tmem_st32u_nowait(tp, q);
+                tmem_wait_st();
+            }
             tc_fence_before();
             mbar_arrive(dready + t);
+            if (!last && j == nt - 1) {
+                float lo, hi;
+                unpair(sum, lo, hi);
+                nd2 = pair(-(lo + hi), -(lo + hi));
+                if (real) ndelta[rd] = -(lo + hi);
+            }
         }
         if (nt > 0) {
-            wait(done + t, (nt - 1) & 1, guard);
+            wait(done + t, (passes * nt - 1) & 1, guard);
             tc_fence_after();
             if (!warp_up(guard)) {
                 store_rows<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)b.dq,
@@ -559,16 +584,16 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float* nlse, int* stat
         attn_delta_kernel<D><<<(unsigned)((T * a.H + PER - 1) / PER), 256, 0, st>>>(a, (const __nv_bfloat16*)b.dout, nlse, ndelta, T);
     }
     {
-        ProfileScope prof("attn_bwd_keys", st);
-        count_launch();
-        const int64_t ctas = make_tiles(tiles, s, a.Hkv, 1, 128);
-        attn_bwd_keys_kernel<D><<<(unsigned)ctas, 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, tiles, nlse, ndelta, status);
-    }
-    {
         ProfileScope prof("attn_bwd_rows", st);
         count_launch();
         const int64_t ctas = make_tiles(tiles, s, a.Hkv, r, 256);
         attn_bwd_rows_kernel<D><<<(unsigned)ctas, 384, Dq<D>::SMEM, st>>>(k64, v64, b, s, tiles, nlse, ndelta, status);
+    }
+    {
+        ProfileScope prof("attn_bwd_keys", st);
+        count_launch();
+        const int64_t ctas = make_tiles(tiles, s, a.Hkv, 1, 128);
+        attn_bwd_keys_kernel<D><<<(unsigned)ctas, 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, tiles, nlse, ndelta, status);
     }
     return cudaGetLastError();
 }
