@@ -334,10 +334,15 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
 }
 
 // ---- gradients of q, k, g and beta ----------------------------------------------------------
-// One CTA per chunk and key head: 8 warps, warp (mt, half) owns 16 tokens and half the columns of
-// every product; the value heads of the group follow one another and are summed in registers.
+// One CTA per chunk and key head: 16 warps, warp (mt, qt) owns 16 tokens and a quarter of the columns
+// of every product; the value heads of the group follow one another and are summed in registers.
+// The tiles take most of shared memory (221 KB at Dk = Dv = 128), so an SM holds one CTA: its 16 warps
+// have to hide each other's latency (8 took 0.56 ms at the image stream, 16 take 0.49; the rate of mma.sync
+// alone would be about 0.37), and D comes in where S was while the
+// pair products are taken.
 template <int DK, int DV>
 struct Grads {
+    static constexpr int THREADS = 512;
     static constexpr int NROW = 2 * C + 16;
     static constexpr int K_ = 0, Q_ = K_ + C * DK * 2;
     static constexpr int SB = Q_ + C * DK * 2;              // planes of S^T, then of D^T [2][DV][DK]
@@ -347,25 +352,25 @@ struct Grads {
     static constexpr int N_ = Y_ + 2 * DV * C * 2;          // of N [2][64][NROW], then of beta M
     static constexpr int M_ = N_ + 2 * C * NROW;
     static constexpr int SC = M_ + 2 * C * NROW;            // grow, end, beta, cum
-    static constexpr int RED = SC + 5 * C * 4;              // fp32 [10][64]
-    static constexpr int SMEM = RED + 10 * C * 4;
+    static constexpr int RED = SC + 5 * C * 4;              // fp32 [20][64]
+    static constexpr int SMEM = RED + 20 * C * 4;
 };
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records,
+__global__ void __launch_bounds__(512) gdn_grads_kernel(GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records,
                                                         const char* kept)
 {
     using L = Grads<DK, DV>;
     const GdnArgs& a = b.f;
-    constexpr int NK = DK / 16;   // 8-column tiles of half the key channels
+    constexpr int NT = L::THREADS, NK = DK / 32;   // 8-column tiles of a quarter of the key channels
     extern __shared__ __align__(128) char sm[];
     const uint32_t base = smem_addr(sm);
     int seq, c;
     if (!seqs.locate(blockIdx.x, C, seq, c)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // of the lower triangle the two halves have 1, 2, 3, 4 and 0, 0, 1, 2 blocks: put them
-    // opposite on the SM partitions
-    const int half = warp >> 2, mt = half ? 3 - (warp & 3) : (warp & 3);
+    // the triangular products have mt + 1 steps (or 4 - mt): the quarters put the tokens on different
+    // SM partitions
+    const int qt = warp >> 2, mt = (warp + qt) & 3;
     const int hk = blockIdx.y, r = a.Hv / a.Hk;
     const int valid = min(C, seqs.len(seq) - c * C);
     const int64_t t0 = (int64_t)seqs.start(seq) + c * C;
@@ -377,105 +382,128 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
     const int krow = (lane & 7) + ((lane >> 4) << 3), tpc = (lane >> 3) & 1;              // A, stored [k][row]
     const int brow = lane & 15, bpc = lane >> 4;                                          // B, stored [k][column]
 
-    load_tile<DK, 256>(base + L::K_, (const __nv_bfloat16*)a.k + (t0 * a.Hk + hk) * DK, (int64_t)a.Hk * DK, valid, tid);
-    load_tile<DK, 256>(base + L::Q_, (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK, (int64_t)a.Hk * DK, valid, tid);
+    load_tile<DK, NT>(base + L::K_, (const __nv_bfloat16*)a.k + (t0 * a.Hk + hk) * DK, (int64_t)a.Hk * DK, valid, tid);
+    load_tile<DK, NT>(base + L::Q_, (const __nv_bfloat16*)a.q + (t0 * a.Hk + hk) * DK, (int64_t)a.Hk * DK, valid, tid);
     float sq[NK][4] = {}, sk[NK][4] = {};
     for (int h = hk * r; h < hk * r + r; ++h) {
         const char* mine = kept + ((int64_t)blockIdx.x * a.Hv + h) * keep.bytes();
         const char* rec = records + ((int64_t)blockIdx.x * a.Hv + h) * REC_BYTES;
         auto take = [&](uint32_t dst, size_t off, int bytes) {   // kept tiles are laid out as they are read
-            for (int e = tid; e < bytes / 16; e += 256) cp16(dst + e * 16, mine + off + e * 16, true);
+            for (int e = tid; e < bytes / 16; e += NT) cp16(dst + e * 16, mine + off + e * 16, true);
         };
-        load_tile<DV, 256>(base + L::G_, (const __nv_bfloat16*)b.dout + (t0 * a.Hv + h) * DV, (int64_t)a.Hv * DV, valid, tid);
-        take(base + L::U_, keep.u(), 2 * DV * C * 2);
-        take(base + L::Y_, keep.y(), 2 * DV * C * 2);
-        for (int e = tid; e < 5 * C / 4; e += 256) cp16(base + L::SC + e * 16, rec + REC_SCAL + e * 16, true);
-        cp_async_commit();
+        for (int e = tid; e < C * DV / 8; e += NT) {
+            const int row = e / (DV / 8), piece = e % (DV / 8);
+            const bool in = row < valid;
+            cp16(base + L::G_ + tile_at<DV>(row, piece), (const __nv_bfloat16*)b.dout + ((t0 + (in ? row : 0)) * a.Hv + h) * DV + piece * 8, in);
+        }
         take(base + L::SB, keep.s(), 2 * DV * DK * 2);
+        take(base + L::Y_, keep.y(), 2 * DV * C * 2);
+        cp_async_commit();
+        take(base + L::U_, keep.u(), 2 * DV * C * 2);
+        for (int e = tid; e < 5 * C / 4; e += NT) cp16(base + L::SC + e * 16, rec + REC_SCAL + e * 16, true);
         cp_async_commit();
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        // dO U^T, dY U^T and K K^T, the warp's 16 rows and 32 columns, on and below the diagonal
-        float n4[4][4] = {}, m4[4][2][4] = {}, kk[4][4] = {};
-        const int jbs = min(2, mt - 2 * half + 1);   // 16-column blocks
-        if (jbs > 0) {
+        // dO S^T and dY S^T, the warp's 16 tokens and quarter of the channels
+        float xq[NK][4] = {}, xr[NK][4] = {};
 #pragma unroll
-            for (int s = 0; s < DV / 16; ++s) {
-                uint32_t g[4], y[2][4];
-                ldsm(g, base + L::G_ + tile_at<DV>(arow, 2 * s + apc));
+        for (int s = 0; s < DV / 16; ++s) {
+            uint32_t g[4], y[2][4];
+            ldsm(g, base + L::G_ + tile_at<DV>(arow, 2 * s + apc));
+#pragma unroll
+            for (int p = 0; p < 2; ++p) ldsm_t(y[p], base + L::Y_ + p * DV * C * 2 + tile_at<C>(s * 16 + krow, mt * 2 + tpc));
+#pragma unroll
+            for (int n = 0; n < NK; n += 2) {
+                uint32_t t[2][4];
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
+                    ldsm_t(t[p], base + L::SB + p * DV * DK * 2 + tile_at<DK>(s * 16 + brow, qt * NK + n + bpc));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(xq[n + e], g, t[0][2 * e], t[0][2 * e + 1]);
+                    mma(xr[n + e], y[0], t[0][2 * e], t[0][2 * e + 1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(xq[n + e], g, t[1][2 * e], t[1][2 * e + 1]);
+                    mma(xr[n + e], y[1], t[0][2 * e], t[0][2 * e + 1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mma(xr[n + e], y[0], t[1][2 * e], t[1][2 * e + 1]);
+            }
+        }
+        cp_async_wait_all();
+        __syncthreads();   // S has been read; U and the gates are in
+        take(base + L::SB, keep.d(), 2 * DV * DK * 2);
+        cp_async_commit();
+        // dO U^T, dY U^T and K K^T, the warp's 16 rows and 16 columns, on and below the diagonal
+        float db[2] = {0.f, 0.f};   // sum_j M_ij k_i.k_j, rows i0 and i0 + 8
+        if (qt <= mt) {
+            float n4[2][4] = {}, m4[2][2][4] = {}, kk[2][4] = {};
+#pragma unroll
+            for (int s = 0; s < DV / 16; ++s) {
+                uint32_t g[4], y[2][4], u[2][4];
+                ldsm(g, base + L::G_ + tile_at<DV>(arow, 2 * s + apc));
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
                     ldsm_t(y[p], base + L::Y_ + p * DV * C * 2 + tile_at<C>(s * 16 + krow, mt * 2 + tpc));
+                    ldsm_t(u[p], base + L::U_ + p * DV * C * 2 + tile_at<C>(s * 16 + brow, qt * 2 + bpc));
+                }
 #pragma unroll
-                for (int jb = 0; jb < 2; ++jb) {
-                    if (jb >= jbs) break;
-                    uint32_t u[2][4];
+                for (int n = 0; n < 2; ++n) {
+                    mma(n4[n], g, u[0][2 * n], u[0][2 * n + 1]);
+                    mma(m4[n][0], y[0], u[0][2 * n], u[0][2 * n + 1]);
+                    mma(m4[n][1], y[1], u[0][2 * n], u[0][2 * n + 1]);
+                }
 #pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        ldsm_t(u[p], base + L::U_ + p * DV * C * 2 + tile_at<C>(s * 16 + brow, half * 4 + jb * 2 + bpc));
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma(n4[2 * jb + n], g, u[0][2 * n], u[0][2 * n + 1]);
-                        mma(m4[2 * jb + n][0], y[0], u[0][2 * n], u[0][2 * n + 1]);
-                        mma(m4[2 * jb + n][1], y[1], u[0][2 * n], u[0][2 * n + 1]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma(n4[2 * jb + n], g, u[1][2 * n], u[1][2 * n + 1]);
-                        mma(m4[2 * jb + n][1], y[0], u[1][2 * n], u[1][2 * n + 1]);
-                    }
+                for (int n = 0; n < 2; ++n) {
+                    mma(n4[n], g, u[1][2 * n], u[1][2 * n + 1]);
+                    mma(m4[n][1], y[0], u[1][2 * n], u[1][2 * n + 1]);
                 }
             }
 #pragma unroll
             for (int s = 0; s < DK / 16; ++s) {
-                uint32_t x[4];
+                uint32_t x[4], k4[4];
                 ldsm(x, base + L::K_ + tile_at<DK>(arow, 2 * s + apc));
-#pragma unroll
-                for (int jb = 0; jb < 2; ++jb) {
-                    if (jb >= jbs) break;
-                    uint32_t k4[4];
-                    ldsm(k4, base + L::K_ + tile_at<DK>(half * 32 + jb * 16 + krow, 2 * s + tpc));
-                    mma(kk[2 * jb], x, k4[0], k4[1]);
-                    mma(kk[2 * jb + 1], x, k4[2], k4[3]);
-                }
+                ldsm(k4, base + L::K_ + tile_at<DK>(qt * 16 + krow, 2 * s + tpc));
+                mma(kk[0], x, k4[0], k4[1]);
+                mma(kk[1], x, k4[2], k4[3]);
             }
-        }
-        float db[2] = {0.f, 0.f};   // sum_j M_ij k_i.k_j, rows i0 and i0 + 8
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            if (n >= 2 * jbs) break;
-            const int j = half * 32 + n * 8 + t2;
-            const float2 hj = *(const float2*)&scal[3 * C + j], lj = *(const float2*)&scal[4 * C + j];
+            for (int n = 0; n < 2; ++n) {
+                const int j = qt * 16 + n * 8 + t2;
+                const float2 hj = *(const float2*)&scal[3 * C + j], lj = *(const float2*)&scal[4 * C + j];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = i0 + 8 * e;
-                const float hi = scal[3 * C + i], li = scal[4 * C + i], be = scal[2 * C + i];
-                const float d0 = j <= i ? exp2f((hi - hj.x) + (li - lj.x)) : 0.f;
-                const float d1 = j + 1 <= i ? exp2f((hi - hj.y) + (li - lj.y)) : 0.f;
-                const float m0 = j < i ? -d0 * (m4[n][0][2 * e] + m4[n][1][2 * e]) : 0.f;
-                const float m1 = j + 1 < i ? -d1 * (m4[n][0][2 * e + 1] + m4[n][1][2 * e + 1]) : 0.f;
-                db[e] = fmaf(m0, kk[n][2 * e], fmaf(m1, kk[n][2 * e + 1], db[e]));
-                uint32_t p[2];
-                const uint32_t off = i * L::NROW + j * 2;
-                split<2>(d0 * n4[n][2 * e], d1 * n4[n][2 * e + 1], p);
-                st_shared_b32(base + L::N_ + off, p[0]);
-                st_shared_b32(base + L::N_ + C * L::NROW + off, p[1]);
-                split<2>(be * m0, be * m1, p);
-                st_shared_b32(base + L::M_ + off, p[0]);
-                st_shared_b32(base + L::M_ + C * L::NROW + off, p[1]);
+                for (int e = 0; e < 2; ++e) {
+                    const int i = i0 + 8 * e;
+                    const float hi = scal[3 * C + i], li = scal[4 * C + i], be = scal[2 * C + i];
+                    const float d0 = j <= i ? ex2_approx((hi - hj.x) + (li - lj.x)) : 0.f;
+                    const float d1 = j + 1 <= i ? ex2_approx((hi - hj.y) + (li - lj.y)) : 0.f;
+                    const float m0 = j < i ? -d0 * (m4[n][0][2 * e] + m4[n][1][2 * e]) : 0.f;
+                    const float m1 = j + 1 < i ? -d1 * (m4[n][0][2 * e + 1] + m4[n][1][2 * e + 1]) : 0.f;
+                    db[e] = fmaf(m0, kk[n][2 * e], fmaf(m1, kk[n][2 * e + 1], db[e]));
+                    uint32_t p[2];
+                    const uint32_t off = i * L::NROW + j * 2;
+                    split<2>(d0 * n4[n][2 * e], d1 * n4[n][2 * e + 1], p);
+                    st_shared_b32(base + L::N_ + off, p[0]);
+                    st_shared_b32(base + L::N_ + C * L::NROW + off, p[1]);
+                    split<2>(be * m0, be * m1, p);
+                    st_shared_b32(base + L::M_ + off, p[0]);
+                    st_shared_b32(base + L::M_ + C * L::NROW + off, p[1]);
+                }
             }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             db[e] += __shfl_xor_sync(~0u, db[e], 1);
             db[e] += __shfl_xor_sync(~0u, db[e], 2);
-            if ((lane & 3) == 0) red[half * C + i0 + 8 * e] = db[e];
+            if ((lane & 3) == 0) red[qt * C + i0 + 8 * e] = db[e];
         }
-        // dY . R: 8 tokens a thread, its rows strided by 32
+        // dY . R: 8 tokens a thread, its rows strided by 64
         {
             const int pc = tid & 7;
             float acc[8] = {};
-            for (int row = tid >> 3; row < DV; row += 32) {
+            for (int row = tid >> 3; row < DV; row += NT / 8) {
                 const uint4 rr = *(const uint4*)(mine + keep.r() + tile_at<C>(row, pc));
                 const uint4 y0 = *(const uint4*)(sm + L::Y_ + tile_at<C>(row, pc));
                 const uint4 y1 = *(const uint4*)(sm + L::Y_ + DV * C * 2 + tile_at<C>(row, pc));
@@ -490,15 +518,14 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
             for (int i = 0; i < 8; ++i) {
                 acc[i] += __shfl_xor_sync(~0u, acc[i], 8);
                 acc[i] += __shfl_xor_sync(~0u, acc[i], 16);
-                if (lane < 8) red[(2 + warp) * C + pc * 8 + i] = acc[i];
+                if (lane < 8) red[(4 + warp) * C + pc * 8 + i] = acc[i];
             }
         }
-        cp_async_wait_all();
         __syncthreads();
         if (tid < valid) {
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < 10; ++w) s += red[w * C + tid];
+            for (int w = 0; w < 20; ++w) s += red[w * C + tid];
             ((__nv_bfloat16*)b.dbeta)[(t0 + tid) * a.Hv + h] = __float2bfloat16_rn(s);
         }
         float dc[2] = {0.f, 0.f};   // the warp's part of dcum, rows i0 and i0 + 8
@@ -507,181 +534,119 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
             for (int n = 0; n < NK; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t v = *(const uint32_t*)(sm + tile + tile_at<DK>(i0 + 8 * e, half * NK + n) + t2 * 2);
+                    const uint32_t v = *(const uint32_t*)(sm + tile + tile_at<DK>(i0 + 8 * e, qt * NK + n) + t2 * 2);
                     dc[e] += sign * fmaf(low(v), x[n][2 * e], high(v) * x[n][2 * e + 1]);
                 }
         };
-        // dQ = e^cum o (dO S^T) + N K
-        {
-            float x[NK][4] = {};
-#pragma unroll
-            for (int s = 0; s < DV / 16; ++s) {
-                uint32_t g[4];
-                ldsm(g, base + L::G_ + tile_at<DV>(arow, 2 * s + apc));
-#pragma unroll
-                for (int n = 0; n < NK; n += 2)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t t[4];
-                        ldsm_t(t, base + L::SB + p * DV * DK * 2 + tile_at<DK>(s * 16 + brow, half * NK + n + bpc));
-                        mma(x[n], g, t[0], t[1]);
-                        mma(x[n + 1], g, t[2], t[3]);
-                    }
-            }
-            const float ga = scal[i0], gb = scal[i0 + 8];
+        auto scale = [&](float (&x)[NK][4], float f0, float f1) {
 #pragma unroll
             for (int n = 0; n < NK; ++n) {
-                x[n][0] *= ga; x[n][1] *= ga; x[n][2] *= gb; x[n][3] *= gb;
+                x[n][0] *= f0; x[n][1] *= f0; x[n][2] *= f1; x[n][3] *= f1;
+            }
+        };
+        // dQ = e^cum o (dO S^T) + N K;  row part of dK: -beta e^cum o (dY S^T) + (beta M) K
+        scale(xq, scal[i0], scal[i0 + 8]);
+        scale(xr, -scal[i0] * scal[2 * C + i0], -scal[i0 + 8] * scal[2 * C + i0 + 8]);
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+            if (jb > mt) break;
+            uint32_t w[2][2][4];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t off = p * C * L::NROW + arow * L::NROW + jb * 32 + apc * 16;
+                ldsm(w[0][p], base + L::N_ + off);
+                ldsm(w[1][p], base + L::M_ + off);
             }
 #pragma unroll
-            for (int jb = 0; jb < 4; ++jb) {
-                if (jb > mt) break;
-                uint32_t w[2][4];
+            for (int n = 0; n < NK; n += 2) {
+                uint32_t t[4];
+                ldsm_t(t, base + L::K_ + tile_at<DK>(jb * 16 + brow, qt * NK + n + bpc));
 #pragma unroll
-                for (int p = 0; p < 2; ++p) ldsm(w[p], base + L::N_ + p * C * L::NROW + arow * L::NROW + jb * 32 + apc * 16);
+                for (int p = 1; p >= 0; --p)
 #pragma unroll
-                for (int n = 0; n < NK; n += 2) {
-                    uint32_t t[4];
-                    ldsm_t(t, base + L::K_ + tile_at<DK>(jb * 16 + brow, half * NK + n + bpc));
-#pragma unroll
-                    for (int p = 1; p >= 0; --p) {
-                        mma(x[n], w[p], t[0], t[1]);
-                        mma(x[n + 1], w[p], t[2], t[3]);
+                    for (int e = 0; e < 2; ++e) {
+                        mma(xq[n + e], w[0][p], t[2 * e], t[2 * e + 1]);
+                        mma(xr[n + e], w[1][p], t[2 * e], t[2 * e + 1]);
                     }
-                }
             }
-            dot(L::Q_, x, 1.f);
-#pragma unroll
-            for (int n = 0; n < NK; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sq[n][e] += x[n][e];
         }
-        // row part of dK: -beta e^cum o (dY S^T) + (beta M) K
-        {
-            float x[NK][4] = {};
+        dot(L::Q_, xq, 1.f);
+        dot(L::K_, xr, 1.f);
 #pragma unroll
-            for (int s = 0; s < DV / 16; ++s) {
-                uint32_t y[2][4];
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    ldsm_t(y[p], base + L::Y_ + p * DV * C * 2 + tile_at<C>(s * 16 + krow, mt * 2 + tpc));
-#pragma unroll
-                for (int n = 0; n < NK; n += 2)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t t[4];
-                        ldsm_t(t, base + L::SB + p * DV * DK * 2 + tile_at<DK>(s * 16 + brow, half * NK + n + bpc));
-                        mma(x[n], y[0], t[0], t[1]);
-                        mma(x[n + 1], y[0], t[2], t[3]);
-                        if (p == 0) {
-                            mma(x[n], y[1], t[0], t[1]);
-                            mma(x[n + 1], y[1], t[2], t[3]);
-                        }
-                    }
+            for (int e = 0; e < 4; ++e) {
+                sq[n][e] += xq[n][e];
+                sk[n][e] += xr[n][e];
             }
-            const float ga = -scal[i0] * scal[2 * C + i0], gb = -scal[i0 + 8] * scal[2 * C + i0 + 8];
-#pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                x[n][0] *= ga; x[n][1] *= ga; x[n][2] *= gb; x[n][3] *= gb;
-            }
-#pragma unroll
-            for (int jb = 0; jb < 4; ++jb) {
-                if (jb > mt) break;
-                uint32_t w[2][4];
-#pragma unroll
-                for (int p = 0; p < 2; ++p) ldsm(w[p], base + L::M_ + p * C * L::NROW + arow * L::NROW + jb * 32 + apc * 16);
-#pragma unroll
-                for (int n = 0; n < NK; n += 2) {
-                    uint32_t t[4];
-                    ldsm_t(t, base + L::K_ + tile_at<DK>(jb * 16 + brow, half * NK + n + bpc));
-#pragma unroll
-                    for (int p = 1; p >= 0; --p) {
-                        mma(x[n], w[p], t[0], t[1]);
-                        mma(x[n + 1], w[p], t[2], t[3]);
-                    }
-                }
-            }
-            dot(L::K_, x, 1.f);
-#pragma unroll
-            for (int n = 0; n < NK; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sk[n][e] += x[n][e];
-        }
-        __syncthreads();   // S has been read
-        take(base + L::SB, keep.d(), 2 * DV * DK * 2);
-        cp_async_commit();
+        // column part of dK: e^{cum_C - cum} o (U D^T) + (beta M)^T K + N^T Q
+        float x[NK][4] = {};
         cp_async_wait_all();
         __syncthreads();
-        // column part of dK: e^{cum_C - cum} o (U D^T) + (beta M)^T K + N^T Q
-        {
-            float x[NK][4] = {};
 #pragma unroll
-            for (int s = 0; s < DV / 16; ++s) {
-                uint32_t u[2][4];
+        for (int s = 0; s < DV / 16; ++s) {
+            uint32_t u[2][4];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) ldsm_t(u[p], base + L::U_ + p * DV * C * 2 + tile_at<C>(s * 16 + krow, mt * 2 + tpc));
+#pragma unroll
+            for (int n = 0; n < NK; n += 2) {
+                uint32_t t[2][4];
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    ldsm_t(u[p], base + L::U_ + p * DV * C * 2 + tile_at<C>(s * 16 + krow, mt * 2 + tpc));
+                    ldsm_t(t[p], base + L::SB + p * DV * DK * 2 + tile_at<DK>(s * 16 + brow, qt * NK + n + bpc));
 #pragma unroll
-                for (int n = 0; n < NK; n += 2)
+                for (int p = 0; p < 3; ++p)   // U0 D0, U1 D0, U0 D1
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t t[4];
-                        ldsm_t(t, base + L::SB + p * DV * DK * 2 + tile_at<DK>(s * 16 + brow, half * NK + n + bpc));
-                        mma(x[n], u[0], t[0], t[1]);
-                        mma(x[n + 1], u[0], t[2], t[3]);
-                        if (p == 0) {
-                            mma(x[n], u[1], t[0], t[1]);
-                            mma(x[n + 1], u[1], t[2], t[3]);
-                        }
-                    }
+                    for (int e = 0; e < 2; ++e) mma(x[n + e], u[p & 1], t[p >> 1][2 * e], t[p >> 1][2 * e + 1]);
             }
-            const float ga = scal[C + i0], gb = scal[C + i0 + 8];
-#pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                x[n][0] *= ga; x[n][1] *= ga; x[n][2] *= gb; x[n][3] *= gb;
-            }
-#pragma unroll
-            for (int ib = 0; ib < 4; ++ib) {
-                if (ib < mt) continue;
-                uint32_t w[2][2][4];
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const uint32_t off = p * C * L::NROW + (ib * 16 + krow) * L::NROW + mt * 32 + tpc * 16;
-                    ldsm_t(w[0][p], base + L::M_ + off);
-                    ldsm_t(w[1][p], base + L::N_ + off);
-                }
-#pragma unroll
-                for (int n = 0; n < NK; n += 2)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        uint32_t t[4];
-                        ldsm_t(t, base + (z ? L::Q_ : L::K_) + tile_at<DK>(ib * 16 + brow, half * NK + n + bpc));
-#pragma unroll
-                        for (int p = 1; p >= 0; --p) {
-                            mma(x[n], w[z][p], t[0], t[1]);
-                            mma(x[n + 1], w[z][p], t[2], t[3]);
-                        }
-                    }
-            }
-            dot(L::K_, x, -1.f);
-#pragma unroll
-            for (int n = 0; n < NK; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sk[n][e] += x[n][e];
         }
+        scale(x, scal[C + i0], scal[C + i0 + 8]);
+#pragma unroll
+        for (int ib = 0; ib < 4; ++ib) {
+            if (ib < mt) continue;
+            uint32_t w[2][2][4];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t off = p * C * L::NROW + (ib * 16 + krow) * L::NROW + mt * 32 + tpc * 16;
+                ldsm_t(w[0][p], base + L::M_ + off);
+                ldsm_t(w[1][p], base + L::N_ + off);
+            }
+#pragma unroll
+            for (int n = 0; n < NK; n += 2)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    uint32_t t[4];
+                    ldsm_t(t, base + (z ? L::Q_ : L::K_) + tile_at<DK>(ib * 16 + brow, qt * NK + n + bpc));
+#pragma unroll
+                    for (int p = 1; p >= 0; --p) {
+                        mma(x[n], w[z][p], t[0], t[1]);
+                        mma(x[n + 1], w[z][p], t[2], t[3]);
+                    }
+                }
+        }
+        dot(L::K_, x, -1.f);
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sk[n][e] += x[n][e];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             dc[e] += __shfl_xor_sync(~0u, dc[e], 1);
             dc[e] += __shfl_xor_sync(~0u, dc[e], 2);
-            if ((lane & 3) == 0) red[half * C + i0 + 8 * e] = dc[e];
+            if ((lane & 3) == 0) red[qt * C + i0 + 8 * e] = dc[e];
         }
         __syncthreads();
         if (warp == 0) {   // dg: suffix sums of dcum, two tokens a lane, and the exit term
-            float x = 0.f;
-            for (int i = lane; i < DV / 4; i += 32) x += *(const float*)(mine + keep.exit() + i * 4);
+            float ex = 0.f;
+            for (int i = lane; i < DV / 4; i += 32) ex += *(const float*)(mine + keep.exit() + i * 4);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-            const float d0 = red[2 * lane] + red[C + 2 * lane], d1 = red[2 * lane + 1] + red[C + 2 * lane + 1];
+            for (int o = 16; o > 0; o >>= 1) ex += __shfl_xor_sync(~0u, ex, o);
+            float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                d0 += red[w * C + 2 * lane];
+                d1 += red[w * C + 2 * lane + 1];
+            }
             float s = d0 + d1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -689,8 +654,8 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
                 if (lane + o < 32) s += y;
             }
             __nv_bfloat16* dg = (__nv_bfloat16*)b.dg + t0 * a.Hv + h;
-            if (2 * lane < valid) dg[(int64_t)(2 * lane) * a.Hv] = __float2bfloat16_rn(s + x);
-            if (2 * lane + 1 < valid) dg[(int64_t)(2 * lane + 1) * a.Hv] = __float2bfloat16_rn(s - d0 + x);
+            if (2 * lane < valid) dg[(int64_t)(2 * lane) * a.Hv] = __float2bfloat16_rn(s + ex);
+            if (2 * lane + 1 < valid) dg[(int64_t)(2 * lane + 1) * a.Hv] = __float2bfloat16_rn(s - d0 + ex);
         }
         __syncthreads();   // the next head's tiles overwrite these
     }
@@ -701,7 +666,7 @@ __global__ void __launch_bounds__(256) gdn_grads_kernel(GdnBwdArgs b, const __gr
         for (int e = 0; e < 2; ++e) {
             const int i = i0 + 8 * e;
             if (i >= valid) continue;
-            const int64_t off = ((t0 + i) * a.Hk + hk) * DK + half * (DK / 2) + n * 8 + t2;
+            const int64_t off = ((t0 + i) * a.Hk + hk) * DK + qt * (DK / 4) + n * 8 + t2;
             *(uint32_t*)((__nv_bfloat16*)b.dq + off) = pack(sq[n][2 * e], sq[n][2 * e + 1]);
             *(uint32_t*)((__nv_bfloat16*)b.dk + off) = pack(sk[n][2 * e], sk[n][2 * e + 1]);
         }
@@ -729,7 +694,7 @@ cudaError_t grads(const GdnBwdArgs& a, const Seqs& s, const void* records, const
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_grads", st);
     count_launch();
-    kern<<<dim3(s.slots(C), a.f.Hk), 256, L::SMEM, st>>>(a, s, (const char*)records, (const char*)kept);
+    kern<<<dim3(s.slots(C), a.f.Hk), L::THREADS, L::SMEM, st>>>(a, s, (const char*)records, (const char*)kept);
     return cudaGetLastError();
 }
 
