@@ -576,8 +576,22 @@ cudaError_t launch_scan(const GdnArgs& a, const Seqs& s, const void* records, vo
 }  // namespace gdn
 
 namespace gdn {
-// Which scan: whole heads (gdn_chain.cu) or columns of heads.
-bool whole_heads(const GdnArgs& a, const Seqs& s, int sms) { return a.Dv != 32 && (int64_t)s.n * a.Hv * (a.Dv / 32) > sms; }
+// Which scan: whole heads (gdn_chain.cu) or columns of heads.  Columns make Dv / 32 times as many CTAs, whose
+// steps are shorter (1.5 us alone on an SM against 2.6) but read the head's chunk records once each.  So they are
+// for calls whose time is set by the longest sample's steps in a row, and whole heads for those where
+// the columns' steps, shared out over the SMs, are more than that.
+// Measured (Dk = Dv = 128): 4 x 68 chunks, 16 heads (117 steps of work an SM against 68 in a row): columns
+// 333 us, whole heads 179; 107 chunks in 12 ragged samples, 8 heads (23 against 33): 86 and 94.
+bool whole_heads(const GdnArgs& a, const Seqs& s, int sms)
+{
+    int64_t longest = 0, all = 0;
+    for (int i = 0; i < s.n; ++i) {
+        const int chunks = (s.len(i) + C - 1) / C;
+        longest = max(longest, (int64_t)chunks);
+        all += chunks;
+    }
+    return a.Dv != 32 && all * a.Hv * (a.Dv / 32) > sms * longest;
+}
 }  // namespace gdn
 
 // The tensor-core path copies rows in 16-byte pieces.
