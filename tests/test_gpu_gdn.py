@@ -255,6 +255,132 @@ def test_workspace_of_the_stated_size():
                 call(buf[:need - 256])
 
 
+# ---- many heads or samples: whole heads to a CTA in the scan, two column tiles in the reverse one ----------------------
+WIDE = [  # lens, Hk, Hv, Dk, Dv
+    ([64] * 10, 4, 8, 128, 128), ([130, 70, 0, 1, 129], 16, 32, 128, 64), ([65] * 6 + [3], 2, 6, 64, 128),
+    ([63, 1, 200, 64, 130], 32, 32, 64, 64), ([191] + [128, 127] * 5, 2, 6, 128, 128)]
+NARROW = [([40, 65] * 10, 4, 8, 64, 32), ([1, 129, 64] * 6, 1, 9, 128, 32)]   # Dv = 32: columns of heads, two tiles to a CTA
+
+
+def kernels(names, call):
+    """The call's result, and which of the named kernels it launched."""
+    for n in names:
+        kda.profile_collect(n)
+    kda.profile_enable(True)
+    try:
+        out = call()
+        torch.cuda.synchronize()
+    finally:
+        kda.profile_enable(False)
+    return out, {n for n in names if kda.profile_collect(n)}
+
+
+@pytest.mark.parametrize("with_states", [False, True])
+@pytest.mark.parametrize("case", WIDE + NARROW, ids=str)
+def test_many_heads(case, with_states):
+    lens, Hk, Hv, Dk, Dv = case
+    x, S0, do, dS = make(lens, Hk, Hv, Dk, Dv, torch.bfloat16, seed=40 + len(lens))
+    states = (S0, dS) if with_states else ()
+    cu, whole = R.offsets(lens), Dv > 32
+    ref_o, ref_S = R.gdn(*map(R.f64, x), lens, *map(R.f64, states[:1]))
+    (o, S), ran = kernels(["gdn_chain", "gdn_scan"], lambda: gdn.forward_varlen(*cuda(x), cu, *cuda(states[:1])))
+    assert ran == {"gdn_chain" if whole else "gdn_scan"}
+    assert R.norm_error(o, ref_o) <= BF16_TOL and R.norm_error(S, ref_S) <= FP32_TOL
+    ref = R.gdn_backward(*map(R.f64, x), R.f64(do), lens, *map(R.f64, states))
+    got, ran = kernels(["gdn_chain_keep", "gdn_scan_keep"], lambda: gdn.backward_varlen(*cuda(x), do.cuda(), cu, *cuda(states)))
+    assert ran == {"gdn_chain_keep" if whole else "gdn_scan_keep"}
+    check_grads(got, ref, x, BF16_GRAD_TOL)
+    assert kda.last_device_error() == 0
+
+
+@pytest.mark.parametrize("g", [-0.5, -8.0, -90.0, float("-inf")])
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64)])
+def test_many_heads_strong_gates(Dk, Dv, g):
+    lens, Hk, Hv = [150, 70, 130], 16, 32
+    x, S0, do, dS = make(lens, Hk, Hv, Dk, Dv, torch.bfloat16, seed=11)
+    x[3][::7] = g
+    x[3][150:] = g
+    ref_o, ref_S = R.gdn(*map(R.f64, x), lens, R.f64(S0))
+    o, S = gdn.forward_varlen(*cuda(x), R.offsets(lens), S0.cuda())
+    assert R.norm_error(o, ref_o) <= BF16_TOL and R.norm_error(S, ref_S) <= FP32_TOL
+    ref = R.gdn_backward(*map(R.f64, x), R.f64(do), lens, R.f64(S0), R.f64(dS))
+    got = gdn.backward_varlen(*cuda(x), do.cuda(), R.offsets(lens), S0.cuda(), dS.cuda())
+    check_grads(got, ref, x, BF16_GRAD_TOL)
+
+
+def test_many_heads_repeated_keys_without_decay():
+    T, H, D = 192, 48, 128
+    k = torch.zeros(T, H, D)
+    k[:, :, 3] = 1.0
+    v = torch.randn(T, H, D, generator=torch.Generator().manual_seed(2))
+    x = cuda([t.to(torch.bfloat16) for t in (k, k, v, torch.zeros(T, H), torch.ones(T, H))])
+    o, S = gdn.forward_varlen(*x, [0, T])
+    assert R.norm_error(o, R.f64(x[2])) <= BF16_TOL
+    assert R.norm_error(S[0, :, 3], R.f64(x[2][-1])) <= FP32_TOL
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64), (128, 32)])
+def test_many_heads_samples_do_not_touch_each_other_nor_the_rows_behind(Dk, Dv):
+    lens, spare = [65, 1, 130], 70
+    x, S0, do, dS = make(lens, 16, 64, Dk, Dv, torch.bfloat16, seed=4, spare=spare)
+    x, do, cu, S0, dS = cuda(x), do.cuda(), R.offsets(lens), S0.cuda(), dS.cuda()
+    want_o, want_S = gdn.forward_varlen(*x, cu, S0)
+    want_g = gdn.backward_varlen(*x, do, cu, S0, dS)
+    for lo, hi in ((66, None), (0, 66)):   # the third sample and the spare rows; the first two
+        bad = [t.clone() for t in x]
+        for t in bad:
+            t[lo:hi] = float("nan")
+        keep, seqs = (slice(0, 66), slice(0, 2)) if lo else (slice(66, 196), slice(2, 3))
+        o, S = torch.full_like(want_o, 7.0), torch.full_like(want_S, 7.0)
+        gdn.forward_varlen(*bad, cu, S0, o=o, S_T=S)
+        assert torch.equal(o[keep], want_o[keep]) and torch.equal(S[seqs], want_S[seqs])
+        assert bool((o[sum(lens):] == 7.0).all())
+        out = tuple(torch.full_like(t, 7.0) for t in want_g)
+        gdn.backward_varlen(*bad, do, cu, S0, dS, out=out)
+        for a, b in zip(out[:5], want_g):
+            assert torch.equal(a[keep], b[keep]) and bool((a[sum(lens):] == 7.0).all())
+        assert torch.equal(out[5][seqs], want_g[5][seqs])
+
+
+def test_many_heads_captured_and_on_two_streams():
+    lens = [100, 65, 64]
+    cu = R.offsets(lens)
+    sets = [make(lens, 16, 32, 128, 128, torch.bfloat16, seed=50 + i) for i in range(2)]
+    sets = [cuda(x) + [S0.cuda(), do.cuda(), dS.cuda()] for x, S0, do, dS in sets]
+    call = lambda s, **kw: (*gdn.forward_varlen(*s[:5], cu, s[5], **kw), *gdn.backward_varlen(*s[:5], s[6], cu, s[5], s[7], **kw))   # noqa: E731
+    want = [call(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [call(s, stream=st) for s, st in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(u, w) for u, w in zip(a, b))
+    static = [t.clone() for t in sets[0]]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(static)
+    for s, t in zip(static, sets[1]):
+        s.copy_(t)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, w) for u, w in zip(out, want[1]))
+    assert kda.last_device_error() == 0
+
+
+def test_many_heads_workspace_of_the_stated_size():
+    lens = [130, 64]
+    x, S0, do, _ = make(lens, 16, 64, 128, 128, torch.bfloat16, seed=12)
+    x, do, cu = cuda(x), do.cuda(), R.offsets(lens)
+    for need, call in ((gdn.varlen_workspace_size(cu, 16, 64, 128, 128), lambda w: gdn.forward_varlen(*x, cu, workspace=w)),
+                       (gdn.backward_varlen_workspace_size(cu, 16, 64, 128, 128), lambda w: gdn.backward_varlen(*x, do, cu, workspace=w))):
+        buf = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        got, want = call(buf[:need]), call(None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert bool((buf[need:] == 0xA5).all())
+
+
 # ---- one token per request --------------------------------------------------------------------------------------
 def make_step(n, slots, Hk, Hv, Dk, Dv, dtype, seed=0):
     x, _, _, _ = make([n], Hk, Hv, Dk, Dv, dtype, seed=seed)
