@@ -70,6 +70,20 @@ def test_backward_varlen(case, dtype):
     assert kda.last_device_error() == 0
 
 
+@pytest.mark.parametrize("case", [([1100, 5, 300], 3, 1, 64), ([900, 70], 5, 1, 128), ([40, 1, 33], 64, 1, 128),
+                                  ([40, 1, 33], 65, 1, 64), ([130, 2], 128, 1, 64), ([1500], 10, 2, 64)], ids=str)
+def test_shared_heads(case):
+    """Group sizes that no tile is a multiple of, large ones, and more heads than a tile has rows."""
+    lens, H, Hkv, D = case
+    q, k, v, do = make(lens, H, Hkv, D, torch.bfloat16, seed=60 + H)
+    o, lse = attention.forward_varlen(*cuda((q, k, v)), R.offsets(lens))
+    check_forward(o, lse, q, k, v, lens, torch.bfloat16)
+    got = attention.backward_varlen(*cuda((q, k, v)), o, lse, do.cuda(), R.offsets(lens))
+    for a, b in zip(got, R.attention_backward(*map(R.f64, (q, k, v, do)), lens)):
+        assert R.norm_error(a, b) <= GRAD
+    assert kda.last_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("B,T,H,Hkv,D", [(2, 200, 4, 2, 64), (1, 1, 2, 1, 128), (3, 128, 2, 2, 128), (2, 77, 1, 1, 32)])
 def test_rows_equal_packed_samples(B, T, H, Hkv, D, dtype):
