@@ -722,17 +722,19 @@ cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& b, const Seqs& s, void* ws, int 
     char* records = (char*)ws;
     char* kept = records + rec_part(s, b.f.Hv);
     float* ST = b.dST ? (float*)(kept + kept_part(s, b.f.Hv, b.f.Dk, b.f.Dv)) : nullptr;
+    const bool whole = whole_heads(b.f, s, sms);
     cudaError_t e = cudaSuccess;
     if (s.tokens() > 0) {
         GdnArgs f = b.f;
         f.ST = ST;
         e = launch_prologue(f, s, records, st);
-        if (e == cudaSuccess) e = whole_heads(f, s, sms) ? launch_chain(f, s, records, kept, status, st) : launch_scan(f, s, records, kept, sms, st);
+        if (e == cudaSuccess) e = whole ? launch_chain(f, s, records, kept, status, st) : launch_scan(f, s, records, kept, sms, st);
     }
     const bool wide = (int64_t)s.n * b.f.Hv * (b.f.Dv / 32) >= sms;   // as in the forward scan
     if (e == cudaSuccess)
-        e = b.f.Dk == 64 ? (wide ? rscan<64, 2>(b, s, records, kept, ST, st) : rscan<64, 1>(b, s, records, kept, ST, st))
-                         : (wide ? rscan<128, 2>(b, s, records, kept, ST, st) : rscan<128, 1>(b, s, records, kept, ST, st));
+        e = whole          ? launch_rchain(b, s, records, kept, ST, status, st)
+            : b.f.Dk == 64 ? (wide ? rscan<64, 2>(b, s, records, kept, ST, st) : rscan<64, 1>(b, s, records, kept, ST, st))
+                           : (wide ? rscan<128, 2>(b, s, records, kept, ST, st) : rscan<128, 1>(b, s, records, kept, ST, st));
     if (e != cudaSuccess || s.tokens() == 0) return e;
     switch (b.f.Dk * 1000 + b.f.Dv) {
         case 64032: return grads<64, 32>(b, s, records, kept, st);

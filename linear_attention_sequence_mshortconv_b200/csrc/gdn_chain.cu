@@ -22,18 +22,15 @@
 //
 // Every wait is bounded; after one runs out the chain runs to its end on whatever is there.
 
-#include "gdn_tc.cuh"
-#include "tc.cuh"
+#include "gdn_whole.cuh"
 
 namespace kda {
 namespace gdn {
 namespace {
 
-using namespace tc;
-
 template <int DK, int DV, bool KEEP>
 struct Chain {
-    static constexpr int THREADS = 448, PANEL = C * 128;
+    static constexpr int THREADS = 448;
     static constexpr int K_ = 0, Q_ = K_ + DK / 64 * PANEL, V_ = Q_ + (KEEP ? 0 : DK / 64 * PANEL);
     // the record; what is kept needs no P
     static constexpr int REC = V_ + DV / 64 * PANEL, SCAL = REC + (KEEP ? REC_P : REC_SCAL);
@@ -52,69 +49,6 @@ struct Chain {
 // plane p of Y (or decayed U), k-step x of 16 tokens: planes 0 and 1 where the warpgroup's half of V was,
 // plane 2 where its half of K S was
 __host__ __device__ constexpr int y_at(int p, int x) { return (p < 2 ? p * 16 : 64) + (x >> 1) * 32 + (x & 1) * 8; }
-
-// 32 fp32 values of a thread as N bf16 planes, x = p0 - p1 (+ p2): the second has the opposite sign (its
-// MMAs negate it)
-template <int N>
-__device__ __forceinline__ void planes_of(const float (&x)[32], uint32_t (&p)[N][16])
-{
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float a = x[2 * i], b = x[2 * i + 1];
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            p[n][i] = pack(a, b);
-            if (n + 1 < N) {
-                a = less((uint16_t)p[n][i], a);
-                b = less((uint16_t)(p[n][i] >> 16), b);
-            }
-        }
-    }
-}
-__device__ __forceinline__ void store32(uint32_t taddr, const float (&x)[32])
-{
-    uint32_t m[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) m[i] = __float_as_uint(x[i]);
-    tmem_st32u_nowait(taddr, m);
-}
-// x *= 32 factors in shared memory
-__device__ __forceinline__ void scale32(float (&x)[32], const float* f)
-{
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        const float4 v = *(const float4*)(f + i);
-        x[i] *= v.x; x[i + 1] *= v.y; x[i + 2] *= v.z; x[i + 3] *= v.w;
-    }
-}
-// 32 bf16 values of a row, to a tile (sign: 0x80008000 to negate them)
-template <int W>
-__device__ __forceinline__ void to_tile(char* tile, int row, int piece, const uint32_t (&p)[16], uint32_t sign = 0)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *(uint4*)(tile + tile_at<W>(row, piece + i)) =
-            make_uint4(p[4 * i] ^ sign, p[4 * i + 1] ^ sign, p[4 * i + 2] ^ sign, p[4 * i + 3] ^ sign);
-}
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),
-                 "r"(c1), "r"(c2)
-                 : "memory");
-}
-__device__ __forceinline__ void prefetch(const void* src, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void warp_arrive(uint64_t* bar)
-{
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
 
 template <int DK, int DV, bool KEEP>
 __global__ void __launch_bounds__(448, 1)
@@ -180,10 +114,10 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar, (KEEP ? 1 : 2) * C * DK * 2 + C * DV * 2 + REC_BYTES - (KEEP ? REC_SCAL - REC_P : 0));
                 for (int p = 0; p < DK / 64; ++p) {
-                    tma_load_3d(st + L::K_ + p * L::PANEL, &mk, bar, p * 64, hk, (int)t0 + c * C);
-                    if (!KEEP) tma_load_3d(st + L::Q_ + p * L::PANEL, &mq, bar, p * 64, hk, (int)t0 + c * C);
+                    tma_load_3d(st + L::K_ + p * PANEL, &mk, bar, p * 64, hk, (int)t0 + c * C);
+                    if (!KEEP) tma_load_3d(st + L::Q_ + p * PANEL, &mq, bar, p * 64, hk, (int)t0 + c * C);
                 }
-                for (int p = 0; p < DV / 64; ++p) tma_load_3d(st + L::V_ + p * L::PANEL, &mv, bar, p * 64, h, (int)t0 + c * C);
+                for (int p = 0; p < DV / 64; ++p) tma_load_3d(st + L::V_ + p * PANEL, &mv, bar, p * 64, h, (int)t0 + c * C);
                 const char* src = rec + (int64_t)c * a.Hv * REC_BYTES;
                 if (KEEP) {
                     bulk_load(st + L::REC, src, REC_P, bar);
@@ -208,9 +142,9 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 // the rows behind the sequence belong to another one, or to none: they are zeros here
                 __syncwarp();
                 wait(landed, 0, guard);
-                constexpr int TILES = (L::REC - L::K_) / L::PANEL;
+                constexpr int TILES = (L::REC - L::K_) / PANEL;
                 for (int e = lane; e < TILES * (C - valid) * 8; e += 32)
-                    *(uint4*)(st + e / (8 * (C - valid)) * L::PANEL + (valid + e / 8 % (C - valid)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    *(uint4*)(st + e / (8 * (C - valid)) * PANEL + (valid + e / 8 % (C - valid)) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
                 warp_arrive(full + (c & 1));
             }
@@ -219,8 +153,8 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             for (int c = max(0, issued - 2); c < issued; ++c)
                 if (len - c * C >= C) mbar_wait_bounded(full + (c & 1), (c >> 1) & 1, kWaitNs);
     } else if (warp == 12) {
-        const uint64_t dk = desc_rows(base + L::K_), dq = desc_rows(base + L::Q_), dkc = desc_cols(base + L::K_, L::PANEL);
-        const uint64_t dv = desc_cols(base + L::V_, L::PANEL), de = desc_rows(base + L::EYE);
+        const uint64_t dk = desc_rows(base + L::K_), dq = desc_rows(base + L::Q_), dkc = desc_cols(base + L::K_, PANEL);
+        const uint64_t dv = desc_cols(base + L::V_, PANEL), de = desc_rows(base + L::EYE);
         const uint64_t dt = sdesc(base + L::REC, 128, 256);   // core matrices: halves 128 bytes apart along K, rows 256
         // MMAs that follow one another on the same columns have the same shape, which is what orders
         // them.  The halves of the tokens (32 columns of a product) and of the key channels are the
@@ -231,14 +165,13 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         // (with Dv = 64 rows 64 on read what is behind V; they are not used)
         constexpr uint32_t id_v = idesc_f16(128, C, true, false, false, true);
         constexpr uint32_t id_s = idesc_f16(128, 64, false, true, false, true);
-        constexpr uint32_t NEG = 1u << 13;   // a second plane has the opposite sign
         constexpr int KH = DK / 32;          // k-steps of half of the key channels
         auto by_s = [&](uint32_t to, uint64_t desc, uint32_t id, int kh) {
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int x = kh * KH; x < kh * KH + KH; ++x)
-                    umma_f16_ts(to, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(desc, x, L::PANEL), id ^ (p ? NEG : 0), kh + p + (x - kh * KH) > 0);
+                    umma_f16_ts(to, tmem + L::SP_ + p * (DK / 2) + x * 8, step_rows(desc, x, PANEL), id ^ (p ? NEG : 0), kh + p + (x - kh * KH) > 0);
         };
         // rows 32 th .. 32 th + 31 of a plane of T or P, times the tokens of k-step x
         auto tri = [&](uint32_t so, int plane, int th, int x) { return dt + so + ((plane * TRI + blk(2 * th, x)) >> 4); };
@@ -252,7 +185,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 by_s(tmem + L::R_ + 64, dk + so, id_ks, 0);
                 by_s(tmem + L::R_ + 96, dk + so + (4096 >> 4), id_ks, 0);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) umma_f16(tmem + L::R_, step_cols(dv + so, x), step_rows(de, x, L::PANEL), id_v, x > 0);
+                for (int x = 0; x < 4; ++x) umma_f16(tmem + L::R_, step_cols(dv + so, x), step_rows(de, x, PANEL), id_v, x > 0);
             }
             wait(s_ready + 1, c & 1, guard);
             tc_fence_after();
@@ -298,7 +231,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         for (int p = PLANES - 1; p >= 0; --p)
 #pragma unroll
                             for (int x = 2 * th; x < 2 * th + 2; ++x)
-                                umma_f16_ts(tmem + L::M_ + 64 * n, tmem + L::R_ + y_at(p, x), step_cols(dkc + so, x) + (n * L::PANEL >> 4),
+                                umma_f16_ts(tmem + L::M_ + 64 * n, tmem + L::R_ + y_at(p, x), step_cols(dkc + so, x) + (n * PANEL >> 4),
                                             id_s ^ (p == 1 ? NEG : 0), 1);
                         if (th) umma_commit(s_done + n);
                     }

@@ -133,6 +133,8 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // The same scan with all value columns of a head in one CTA (Dv = 64 or 128)
 cudaError_t launch_chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st);
+// and the reverse scan (D and dY kept; ST: the final states, where there are gradients of them)
+cudaError_t launch_rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, const float* ST, int* status, cudaStream_t st);
 bool whole_heads(const GdnArgs& a, const Seqs& s, int sms);   // which of the two
 // launch of the forward scan: o and S_T (kept null), or what the backward needs (kept and, if
 // not null, S_T; o unused)
