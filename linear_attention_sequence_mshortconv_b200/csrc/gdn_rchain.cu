@@ -8,12 +8,12 @@
 //   warps 0-7  (two warpgroups, each with half of the columns of every operand) what the chain computes
 //              between its products: K D -> dU, T^T dU -> dY and dV, D -> planes
 //   warps 8-11 dO^T, turned over and split into planes for the two products that do not wait for the
-//              chain; <exit state, D>; the rows of dV
+//              chain; <exit state, D>
 //   warp 12    issues the MMAs: P^T dO, K D, half of Q^T (e^cum o dO), T^T dU, the other half,
 //              -K^T (e^cum o dV)
 //   warp 13    the loads.  K, T and the gates are double-buffered; Q, dO and P, which only the products aside
 //              from the chain read, come in when those of the chunk before are done.
-//   warp 14    D and dY out to memory, by the copy engine
+//   warp 14    D, dY and dV out to memory, by the copy engine
 //
 // Tensor memory (512 columns): D (fp32, Dk), its two planes (Dk), X (64: K D, then the planes of dU),
 // Y (64: dO^T, then T^T dU, then the planes of e^cum o dV), W (64: P^T dO), G (64: planes of e^cum o dO).  A
@@ -35,7 +35,7 @@ struct RChain {
     static constexpr int Q_ = 2 * STAGE, G_ = Q_ + DK / 64 * PANEL, P_ = G_ + DV / 64 * PANEL;
     static constexpr int OUT_D = P_ + PPL * TRI;               // planes of D, two tiles
     static constexpr int OUT_Y = OUT_D + 2 * DV * DK * 2;      // of dY
-    static constexpr int OUT_V = OUT_Y + 2 * DV * C * 2;       // dV [64][DV]
+    static constexpr int OUT_V = OUT_Y + 2 * DV * C * 2;       // dV, panels of 64 columns
     static constexpr int BAR = OUT_V + C * DV * 2;
     // the base is aligned up to 1024 bytes; more than half of an SM's, since each CTA takes all of its
     // tensor memory
@@ -48,7 +48,7 @@ __host__ __device__ constexpr int half_at(int p, int x) { return (x >> 1) * 32 +
 template <int DK, int DV>
 __global__ void __launch_bounds__(480, 1)
 gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
-                  GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, const float* ST, int* status)
+                  const __grid_constant__ CUtensorMap mv, GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, const float* ST, int* status)
 {
     using L = RChain<DK, DV>;
     const GdnArgs& a = b.f;
@@ -80,9 +80,9 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 for (uint64_t* x : {kd_done, ty_done, d_done}) mbar_init(x + i, 1);
                 for (uint64_t* x : {u_ready, v_ready, d_ready}) mbar_init(x + i, 4);
             }
-            for (uint64_t* x : {g_full, landed, w_done, drain}) mbar_init(x, 1);
+            for (uint64_t* x : {g_full, landed, w_done, y_free, drain}) mbar_init(x, 1);
             mbar_init(g_ready, 4);
-            for (uint64_t* x : {d_free, y_free, g_empty}) mbar_init(x, 5);   // warps 8-11, and the copies out or the MMAs
+            for (uint64_t* x : {d_free, g_empty}) mbar_init(x, 5);   // warps 8-11, and the copy out or the MMAs
             for (uint64_t* x : {d_kept, y_kept}) mbar_init(x, 8);
             *guard.flag = 0;
             fence_mbar_init();
@@ -272,14 +272,14 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16);
         const bool real = row < DV;
         const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * DV + (int64_t)hf * HK * DV + row;
-        __nv_bfloat16* out = (__nv_bfloat16*)(sm + L::OUT_V);
+        char* out = sm + L::OUT_V + (DV > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2;
         auto scal_of = [&](int it) { return (const float*)(sm + (it & 1) * L::STAGE + L::SCAL); };
-        uint32_t dp[NI][2][16];
         // 32 of the half's channels for step it: to the planes, and decayed
         auto put = [&](int i, float (&s)[32], int it) {
-            planes_of<2>(s, dp[i]);
-            tmem_st16u_nowait(at + L::DP + hf * (HK / 2) + i * 16, dp[i][0]);
-            tmem_st16u_nowait(at + L::DP + DK / 2 + hf * (HK / 2) + i * 16, dp[i][1]);
+            uint32_t p[2][16];
+            planes_of<2>(s, p);
+            tmem_st16u_nowait(at + L::DP + hf * (HK / 2) + i * 16, p[0]);
+            tmem_st16u_nowait(at + L::DP + DK / 2 + hf * (HK / 2) + i * 16, p[1]);
             const float gam = scal_of(it)[C - 1];
 #pragma unroll
             for (int x = 0; x < 32; ++x) s[x] *= gam;
@@ -290,12 +290,8 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             tc_fence_before();
             warp_arrive(d_ready + hf);
             if (it > 0) wait(d_free, (it - 1) & 1, guard);   // while K D runs
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (real) {
-                    to_tile<DK>(sm + L::OUT_D, row, hf * (HK / 8) + i * 4, dp[i][0]);
-                    to_tile<DK>(sm + L::OUT_D + DV * DK * 2, row, hf * (HK / 8) + i * 4, dp[i][1], 0x80008000u);
-                }
+            planes_to_tile<DK, HK / 2>(at + L::DP + hf * (HK / 2), sm + L::OUT_D, row, hf * (HK / 8), real, 0);
+            planes_to_tile<DK, HK / 2>(at + L::DP + DK / 2 + hf * (HK / 2), sm + L::OUT_D + DV * DK * 2, row, hf * (HK / 8), real, 0x80008000u);
             fence_async_smem();
             warp_arrive(d_kept);
         };
@@ -343,36 +339,37 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(u_ready + hf);
-            // dY; dV = beta o dY, and -e^cum o dV
+            // dY, and -e^cum o dV = -e^cum o beta o dY
             if (it + 1 < nch) wait(full + ((it + 1) & 1), ((it + 1) >> 1) & 1, guard);
             if (it > 0) wait(y_free, (it - 1) & 1, guard);
             wait(ty_done + hf, it & 1, guard);
             tc_fence_after();
             tmem_ld32(at + L::Y_ + hf * 32, x);
-            uint32_t y[2][16];
-            planes_of<2>(x, y);
-            scale32(x, scal + 2 * C + hf * 32);
-            uint32_t v[16];
+            {
+                float z[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = pack(x[2 * i], x[2 * i + 1]);
-            scale32(x, scal + hf * 32);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = -x[i];
-            planes_of<2>(x, p);
+                for (int i = 0; i < 32; ++i) z[i] = -x[i];
+                scale32(z, scal + 2 * C + hf * 32);
+                scale32(z, scal + hf * 32);
+                planes_of<2>(z, p);
+            }
             tmem_st16u_nowait(at + L::Y_ + hf * 32, p[0]);
             tmem_st16u_nowait(at + L::Y_ + hf * 32 + 16, p[1]);
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(v_ready + hf);
-            warp_arrive(empty + (it & 1));
             // while K^T (e^cum o dV) runs: dY and dV to where they are copied from
+            planes_of<2>(x, p);
+            scale32(x, scal + 2 * C + hf * 32);
+            warp_arrive(empty + (it & 1));
             if (real) {
-                to_tile<C>(sm + L::OUT_Y, row, hf * 4, y[0]);
-                to_tile<C>(sm + L::OUT_Y + DV * C * 2, row, hf * 4, y[1], 0x80008000u);
+                to_tile<C>(sm + L::OUT_Y, row, hf * 4, p[0]);
+                to_tile<C>(sm + L::OUT_Y + DV * C * 2, row, hf * 4, p[1], 0x80008000u);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    ((uint16_t*)out)[(hf * 32 + 2 * i) * DV + row] = (uint16_t)v[i];
-                    ((uint16_t*)out)[(hf * 32 + 2 * i + 1) * DV + row] = (uint16_t)(v[i] >> 16);
+                    const uint32_t v = pack(x[2 * i], x[2 * i + 1]);
+                    *(uint16_t*)(out + piece_at(hf * 32 + 2 * i, (row & 63) >> 3)) = (uint16_t)v;
+                    *(uint16_t*)(out + piece_at(hf * 32 + 2 * i + 1, (row & 63) >> 3)) = (uint16_t)(v >> 16);
                 }
             }
             fence_async_smem();
@@ -393,51 +390,54 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             if (it + 1 < nch) state_ready(it + 1);
         }
     } else if (warp == 14) {
-        if (lane == 0) {
-            for (int it = 0; it < nch; ++it) {
-                char* dst = mine + (nch - 1 - it) * next;
-                wait(d_kept, it & 1, guard);
+        __nv_bfloat16* vp = (__nv_bfloat16*)b.dv + (t0 * a.Hv + h) * DV;
+        for (int it = 0; it < nch; ++it) {
+            const int c = nch - 1 - it, valid = min(C, len - c * C);
+            char* dst = mine + c * next;
+            wait(d_kept, it & 1, guard);
+            __syncwarp();
+            if (lane == 0) {
                 bulk_store(dst + keep.d(), sm + L::OUT_D, 2 * DV * DK * 2);
                 bulk_commit();
                 bulk_wait_read0();
                 mbar_arrive(d_free);
-                wait(y_kept, it & 1, guard);
+            }
+            wait(y_kept, it & 1, guard);
+            if (valid < C)   // the rows behind the sequence are not its own
+                for (int i = lane; i < valid * (DV / 8); i += 32) {
+                    const int tok = i / (DV / 8), piece = i % (DV / 8);
+                    *(uint4*)(vp + ((int64_t)c * C + tok) * a.Hv * DV + piece * 8) =
+                        *(const uint4*)(sm + L::OUT_V + piece / 8 * PANEL + piece_at(tok, piece & 7));
+                }
+            __syncwarp();
+            if (lane == 0) {
                 bulk_store(dst + keep.y(), sm + L::OUT_Y, 2 * DV * C * 2);
+                if (valid == C)
+                    for (int p = 0; p < DV / 64; ++p) store_3d(&mv, sm + L::OUT_V + p * PANEL, p * 64, h, (int)t0 + c * C);
                 bulk_commit();
                 bulk_wait_read0();
                 mbar_arrive(y_free);
             }
-            bulk_wait0();
         }
+        if (lane == 0) bulk_wait0();
     } else {
         const int row = tid & 127, t = tid - 256;
         const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16);
-        __nv_bfloat16* vp = (__nv_bfloat16*)b.dv + (t0 * a.Hv + h) * DV;
         const char* col = sm + L::G_ + (DV > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2;
         for (int it = 0; it < nch; ++it) {
             const int c = nch - 1 - it;
             const float* scal = (const float*)(sm + (it & 1) * L::STAGE + L::SCAL);
             wait(full + (it & 1), (it >> 1) & 1, guard);
             wait(g_full, it & 1, guard);
-            uint32_t g[2][16], e[2][2][16];   // dO^T, planes of e^cum o dO^T
+            uint32_t g[2][16];   // dO^T
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float x[32];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int tok = hf * 32 + 2 * i;
-                    // (with Dv = 64, rows 64 on repeat the others; they are not used)
-                    const uint32_t lo = *(const uint16_t*)(col + piece_at(tok, (row & 63) >> 3));
-                    const uint32_t hi = *(const uint16_t*)(col + piece_at(tok + 1, (row & 63) >> 3));
-                    g[hf][i] = lo | hi << 16;
-                    x[2 * i] = low(g[hf][i]);
-                    x[2 * i + 1] = high(g[hf][i]);
-                }
-                scale32(x, scal + hf * 32);
-                planes_of<2>(x, e[hf]);
+            for (int i = 0; i < 32; ++i) {
+                // (with Dv = 64, rows 64 on repeat the others; they are not used)
+                const uint32_t lo = *(const uint16_t*)(col + piece_at(2 * i, (row & 63) >> 3));
+                const uint32_t hi = *(const uint16_t*)(col + piece_at(2 * i + 1, (row & 63) >> 3));
+                g[i >> 4][i & 15] = lo | hi << 16;
             }
             warp_arrive(g_empty);
-            warp_arrive(empty + (it & 1));
             if (it > 0) {   // dV's planes and the last of e^cum o dO have been read
                 wait(d_done, (it - 1) & 1, guard);
                 wait(d_done + 1, (it - 1) & 1, guard);
@@ -446,39 +446,56 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 tmem_st16u_nowait(at + L::Y_ + hf * 16, g[hf]);
-                tmem_st16u_nowait(at + L::GE + hf * 16, e[hf][0]);
-                tmem_st16u_nowait(at + L::GE + 32 + hf * 16, e[hf][1]);
+                float x[32];
+                uint32_t e[2][16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[2 * i] = low(g[hf][i]);
+                    x[2 * i + 1] = high(g[hf][i]);
+                }
+                scale32(x, scal + hf * 32);
+                planes_of<2>(x, e);
+                tmem_st16u_nowait(at + L::GE + hf * 16, e[0]);
+                tmem_st16u_nowait(at + L::GE + 32 + hf * 16, e[1]);
             }
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(g_ready);
-            // <exit state, D>: the exit state is the next chunk's entry state
-            wait(d_kept, it & 1, guard);
-            if (it > 0) {
-                const char* s = mine + (c + 1) * next + keep.s();
-                const char* d = sm + L::OUT_D;
-                float part = 0.f;
-#pragma unroll 4
-                for (int i = t * 16; i < DV * DK * 2; i += 128 * 16) {
-                    const uint4 s0 = *(const uint4*)(s + i), s1 = *(const uint4*)(s + keep.state() + i);
-                    const uint4 d0 = *(const uint4*)(d + i), d1 = *(const uint4*)(d + DV * DK * 2 + i);
-                    const uint32_t ss[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
-                    const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
+            warp_arrive(empty + (it & 1));
+            // <exit state, D>: the exit state is the next chunk's entry state.  Its planes come from L2, the first
+            // pieces while the chain is at work.
+            constexpr int PIECES = DV * DK * 2 / (128 * 16), NB = PIECES < 8 ? PIECES : 8;
+            const char *s = mine + (c + 1) * next + keep.s() + t * 16, *d = sm + L::OUT_D + t * 16;
+            float part = 0.f;
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        part = fmaf(low(dd[0][z]) + low(dd[1][z]), low(ss[0][z]) + low(ss[1][z]),
-                                    fmaf(high(dd[0][z]) + high(dd[1][z]), high(ss[0][z]) + high(ss[1][z]), part));
-                }
+            for (int i0 = 0; i0 < PIECES; i0 += NB) {
+                uint4 sp[2][NB];
+                if (it > 0)
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        sp[0][i] = *(const uint4*)(s + (i0 + i) * 2048);
+                        sp[1][i] = *(const uint4*)(s + keep.state() + (i0 + i) * 2048);
+                    }
+                if (i0 == 0) wait(d_kept, it & 1, guard);
+                if (it > 0)
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        const uint4 s0 = sp[0][i], s1 = sp[1][i];
+                        const uint4 d0 = *(const uint4*)(d + (i0 + i) * 2048), d1 = *(const uint4*)(d + DV * DK * 2 + (i0 + i) * 2048);
+                        const uint32_t ss[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
+                        const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            part = fmaf(low(dd[0][z]) + low(dd[1][z]), low(ss[0][z]) + low(ss[1][z]),
+                                        fmaf(high(dd[0][z]) + high(dd[1][z]), high(ss[0][z]) + high(ss[1][z]), part));
+                    }
+            }
+            warp_arrive(d_free);
+            if (it > 0) {
                 constexpr int G = 512 / DV;   // lanes to a part: Dv / 16 parts a warp
                 for (int o = G / 2; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
                 if ((lane & (G - 1)) == 0) *(float*)(mine + c * next + keep.exit() + ((warp - 8) * (DV / 16) + lane / G) * 4) = part;
             }
-            warp_arrive(d_free);
-            wait(y_kept, it & 1, guard);
-            const int valid = min(C, len - c * C);
-            for (int i = t; i < valid * (DV / 8); i += 128)
-                *(uint4*)(vp + ((int64_t)c * C + i / (DV / 8)) * a.Hv * DV + i % (DV / 8) * 8) = *(const uint4*)(sm + L::OUT_V + i * 16);
-            warp_arrive(y_free);
         }
     }
     tc_fence_before();
@@ -491,17 +508,17 @@ template <int DK, int DV>
 cudaError_t rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, const float* ST, int* status, cudaStream_t st)
 {
     using L = RChain<DK, DV>;
-    CUtensorMap k{}, q{}, g{};
+    CUtensorMap k{}, q{}, g{}, v{};
     const GdnArgs& a = b.f;
     const int64_t T = s.tokens();
     if (T > 0 && (!make_map(&k, a.k, T, a.Hk, DK, 64, 1, C) || !make_map(&q, a.q, T, a.Hk, DK, 64, 1, C) ||
-                  !make_map(&g, b.dout, T, a.Hv, DV, 64, 1, C)))
+                  !make_map(&g, b.dout, T, a.Hv, DV, 64, 1, C) || !make_map(&v, b.dv, T, a.Hv, DV, 64, 1, C)))
         return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<gdn_rchain_kernel<DK, DV>>(L::SMEM);
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_rchain", st);
     count_launch();
-    gdn_rchain_kernel<DK, DV><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, g, b, s, (const char*)records, (char*)kept, ST, status);
+    gdn_rchain_kernel<DK, DV><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, g, v, b, s, (const char*)records, (char*)kept, ST, status);
     return cudaGetLastError();
 }
 }  // namespace

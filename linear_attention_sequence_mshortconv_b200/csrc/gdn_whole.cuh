@@ -56,9 +56,29 @@ __device__ __forceinline__ void to_tile(char* tile, int row, int piece, const ui
         *(uint4*)(tile + tile_at<W>(row, piece + i)) =
             make_uint4(p[4 * i] ^ sign, p[4 * i + 1] ^ sign, p[4 * i + 2] ^ sign, p[4 * i + 3] ^ sign);
 }
+// COLS columns of planes that the thread has put into tensor memory, to a tile of rows of W values
+template <int W, int COLS>
+__device__ __forceinline__ void planes_to_tile(uint32_t taddr, char* tile, int row, int piece, bool real, uint32_t sign)
+{
+#pragma unroll
+    for (int i = 0; i < COLS / 16; ++i) {
+        float x[16];
+        uint32_t p[16];
+        tmem_ld16(taddr + i * 16, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) p[j] = __float_as_uint(x[j]);
+        if (real) to_tile<W>(tile, row, piece + i * 4, p, sign);
+    }
+}
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
 {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
 }
 __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2)
 {
