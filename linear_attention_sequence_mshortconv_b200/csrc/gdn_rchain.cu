@@ -273,52 +273,58 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         const bool real = row < DV;
         const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * DV + (int64_t)hf * HK * DV + row;
         char* out = sm + L::OUT_V + (DV > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2;
-        auto scal_of = [&](int it) { return (const float*)(sm + (it & 1) * L::STAGE + L::SCAL); };
-        // 32 of the half's channels for step it: to the planes, and decayed
-        auto put = [&](int i, float (&s)[32], int it) {
-            uint32_t p[2][16];
-            planes_of<2>(s, p);
-            tmem_st16u_nowait(at + L::DP + hf * (HK / 2) + i * 16, p[0]);
-            tmem_st16u_nowait(at + L::DP + DK / 2 + hf * (HK / 2) + i * 16, p[1]);
-            const float gam = scal_of(it)[C - 1];
+        if (nch > 0) wait(full, 0, guard);
+        // (Loops over 32 channels stay loops here: unrolled, the kernel's roles fetched instructions for longer than
+        // they took to issue.)
+        for (int it = 0;; ++it) {
+            // D for step it: to the planes, and decayed; at the end, out
+            const float* scal = (const float*)(sm + (it & 1) * L::STAGE + L::SCAL);
+            float part = 0.f;   // <S_T, dS_T>
+#pragma unroll 1
+            for (int i = 0; i < NI; ++i) {
+                float x[32];
+                if (it == 0) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] *= gam;
-            store32(at + L::M_ + hf * HK + i * 32, s);
-        };
-        auto state_ready = [&](int it) {
+                    for (int z = 0; z < 32; ++z) {
+                        const int64_t off = soff + (int64_t)(i * 32 + z) * DV;
+                        x[z] = b.dST && real ? b.dST[off] : 0.f;
+                        if (b.dST && real && nch > 0) part = fmaf(x[z], ST[off], part);
+                    }
+                } else {
+                    tmem_ld32(at + L::M_ + hf * HK + i * 32, x);
+                }
+                if (it < nch) {
+                    uint32_t p[2][16];
+                    planes_of<2>(x, p);
+                    tmem_st16u_nowait(at + L::DP + hf * (HK / 2) + i * 16, p[0]);
+                    tmem_st16u_nowait(at + L::DP + DK / 2 + hf * (HK / 2) + i * 16, p[1]);
+                    const float gam = scal[C - 1];
+#pragma unroll
+                    for (int z = 0; z < 32; ++z) x[z] *= gam;
+                    store32(at + L::M_ + hf * HK + i * 32, x);
+                } else if (b.dS0 && real) {
+#pragma unroll
+                    for (int z = 0; z < 32; ++z) b.dS0[soff + (int64_t)(i * 32 + z) * DV] = x[z];
+                }
+            }
+            if (it == nch) break;
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(d_ready + hf);
-            if (it > 0) wait(d_free, (it - 1) & 1, guard);   // while K D runs
-            planes_to_tile<DK, HK / 2>(at + L::DP + hf * (HK / 2), sm + L::OUT_D, row, hf * (HK / 8), real, 0);
-            planes_to_tile<DK, HK / 2>(at + L::DP + DK / 2 + hf * (HK / 2), sm + L::OUT_D + DV * DK * 2, row, hf * (HK / 8), real, 0x80008000u);
+            if (it == 0) {   // Dv / 4 parts, four of each warp that has columns
+                for (int o = 4; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
+                if (real && (lane & 7) == 0)
+                    *(float*)(mine + (nch - 1) * next + keep.exit() + ((hf * (DV / 32) + (warp & 3)) * 4 + (lane >> 3)) * 4) = part;
+            } else {
+                wait(d_free, (it - 1) & 1, guard);
+            }
+            // while K D runs, the planes to where they are copied from
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p)
+                planes_to_tile<DK, HK / 2>(at + L::DP + p * (DK / 2) + hf * (HK / 2), sm + L::OUT_D + p * DV * DK * 2, row, hf * (HK / 8), real,
+                                           p ? 0x80008000u : 0u);
             fence_async_smem();
             warp_arrive(d_kept);
-        };
-        if (nch > 0) {
-            wait(full, 0, guard);
-            float part = 0.f;   // <S_T, dS_T>
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                float s[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const int64_t off = soff + (int64_t)(i * 32 + x) * DV;
-                    s[x] = b.dST && real ? b.dST[off] : 0.f;
-                    if (b.dST && real) part = fmaf(s[x], ST[off], part);
-                }
-                put(i, s, 0);
-            }
-            state_ready(0);
-            // Dv / 4 parts, four of each warp that has columns
-            for (int o = 4; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
-            if (real && (lane & 7) == 0)
-                *(float*)(mine + (nch - 1) * next + keep.exit() + ((hf * (DV / 32) + (warp & 3)) * 4 + (lane >> 3)) * 4) = part;
-        } else if (b.dS0 && real) {
-            for (int x = 0; x < HK; ++x) b.dS0[soff + (int64_t)x * DV] = b.dST ? b.dST[soff + (int64_t)x * DV] : 0.f;
-        }
-        for (int it = 0; it < nch; ++it) {
-            const float* scal = scal_of(it);
             float x[32];
             uint32_t p[2][16];
             // dU = P^T dO + e^{cum_C - cum} o (K D), 32 tokens
@@ -376,18 +382,6 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             warp_arrive(y_kept);
             wait(d_done + hf, it & 1, guard);
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                float s[32];
-                tmem_ld32(at + L::M_ + hf * HK + i * 32, s);
-                if (it + 1 < nch) {
-                    put(i, s, it + 1);
-                } else if (b.dS0 && real) {
-#pragma unroll
-                    for (int z = 0; z < 32; ++z) b.dS0[soff + (int64_t)(i * 32 + z) * DV] = s[z];
-                }
-            }
-            if (it + 1 < nch) state_ready(it + 1);
         }
     } else if (warp == 14) {
         __nv_bfloat16* vp = (__nv_bfloat16*)b.dv + (t0 * a.Hv + h) * DV;
@@ -429,30 +423,25 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             const float* scal = (const float*)(sm + (it & 1) * L::STAGE + L::SCAL);
             wait(full + (it & 1), (it >> 1) & 1, guard);
             wait(g_full, it & 1, guard);
-            uint32_t g[2][16];   // dO^T
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                // (with Dv = 64, rows 64 on repeat the others; they are not used)
-                const uint32_t lo = *(const uint16_t*)(col + piece_at(2 * i, (row & 63) >> 3));
-                const uint32_t hi = *(const uint16_t*)(col + piece_at(2 * i + 1, (row & 63) >> 3));
-                g[i >> 4][i & 15] = lo | hi << 16;
-            }
-            warp_arrive(g_empty);
             if (it > 0) {   // dV's planes and the last of e^cum o dO have been read
                 wait(d_done, (it - 1) & 1, guard);
                 wait(d_done + 1, (it - 1) & 1, guard);
                 tc_fence_after();
             }
-#pragma unroll
+#pragma unroll 1
             for (int hf = 0; hf < 2; ++hf) {
-                tmem_st16u_nowait(at + L::Y_ + hf * 16, g[hf]);
                 float x[32];
-                uint32_t e[2][16];
+                uint32_t g[16], e[2][16];   // dO^T, planes of e^cum o dO^T
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    x[2 * i] = low(g[hf][i]);
-                    x[2 * i + 1] = high(g[hf][i]);
+                    // (with Dv = 64, rows 64 on repeat the others; they are not used)
+                    const uint32_t lo = *(const uint16_t*)(col + hf * 4096 + piece_at(2 * i, (row & 63) >> 3));
+                    const uint32_t hi = *(const uint16_t*)(col + hf * 4096 + piece_at(2 * i + 1, (row & 63) >> 3));
+                    g[i] = lo | hi << 16;
+                    x[2 * i] = low(g[i]);
+                    x[2 * i + 1] = high(g[i]);
                 }
+                tmem_st16u_nowait(at + L::Y_ + hf * 16, g);
                 scale32(x, scal + hf * 32);
                 planes_of<2>(x, e);
                 tmem_st16u_nowait(at + L::GE + hf * 16, e[0]);
@@ -461,26 +450,36 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(g_ready);
+            warp_arrive(g_empty);
             warp_arrive(empty + (it & 1));
-            // <exit state, D>: the exit state is the next chunk's entry state.  Its planes come from L2, the first
-            // pieces while the chain is at work.
-            constexpr int PIECES = DV * DK * 2 / (128 * 16), NB = PIECES < 8 ? PIECES : 8;
+            // <exit state, D>: the exit state is the next chunk's entry state.  Its planes come from L2, each batch
+            // while the one before is at work.
+            constexpr int PIECES = DV * DK * 2 / (128 * 16), NB = 4;
             const char *s = mine + (c + 1) * next + keep.s() + t * 16, *d = sm + L::OUT_D + t * 16;
             float part = 0.f;
+            uint4 sp[2][NB];
+            auto fetch = [&](int i0) {
 #pragma unroll
-            for (int i0 = 0; i0 < PIECES; i0 += NB) {
-                uint4 sp[2][NB];
-                if (it > 0)
+                for (int i = 0; i < NB; ++i) {
+                    sp[0][i] = __ldcg((const uint4*)(s + (i0 + i) * 2048));
+                    sp[1][i] = __ldcg((const uint4*)(s + keep.state() + (i0 + i) * 2048));
+                }
+            };
+            if (it > 0) fetch(0);
+            wait(d_kept, it & 1, guard);
+            if (it > 0)
+#pragma unroll 1
+                for (int i0 = 0; i0 < PIECES; i0 += NB) {
+                    uint4 now[2][NB];
 #pragma unroll
                     for (int i = 0; i < NB; ++i) {
-                        sp[0][i] = *(const uint4*)(s + (i0 + i) * 2048);
-                        sp[1][i] = *(const uint4*)(s + keep.state() + (i0 + i) * 2048);
+                        now[0][i] = sp[0][i];
+                        now[1][i] = sp[1][i];
                     }
-                if (i0 == 0) wait(d_kept, it & 1, guard);
-                if (it > 0)
+                    if (i0 + NB < PIECES) fetch(i0 + NB);
 #pragma unroll
                     for (int i = 0; i < NB; ++i) {
-                        const uint4 s0 = sp[0][i], s1 = sp[1][i];
+                        const uint4 s0 = now[0][i], s1 = now[1][i];
                         const uint4 d0 = *(const uint4*)(d + (i0 + i) * 2048), d1 = *(const uint4*)(d + DV * DK * 2 + (i0 + i) * 2048);
                         const uint32_t ss[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
                         const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
@@ -489,7 +488,7 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                             part = fmaf(low(dd[0][z]) + low(dd[1][z]), low(ss[0][z]) + low(ss[1][z]),
                                         fmaf(high(dd[0][z]) + high(dd[1][z]), high(ss[0][z]) + high(ss[1][z]), part));
                     }
-            }
+                }
             warp_arrive(d_free);
             if (it > 0) {
                 constexpr int G = 512 / DV;   // lanes to a part: Dv / 16 parts a warp
