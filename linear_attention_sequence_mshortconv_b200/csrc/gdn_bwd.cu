@@ -15,7 +15,7 @@
 //   dcum_i = q_i.dQ_i + k_i.row_i - k_i.col_i,  dg_i = sum_{j >= i} dcum_j + <S', D>
 // where S' is the chunk's exit state: scaling it is what a gate of the chunk does to all that
 // follows, so <S', D> is the later chunks' share, and no sum of gates' gradients runs over more
-// than one chunk.
+// than one chunk.  It is e^{cum_C} <S, D> + sum_t k_t . (e^{cum_C - cum} o (U D^T))_t.
 //
 // Precision: sums and chains are fp32; operands that are not inputs are two bf16 planes (16 to 17
 // bits), R one.  Every gradient is rounded once, at the end.
@@ -49,7 +49,7 @@ struct RScan {
 
 template <int DK, int MT>
 __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records,
-                                                             char* kept, const float* ST)
+                                                             char* kept)
 {
     using L = RScan<DK, MT>;
     const GdnArgs& a = b.f;
@@ -77,18 +77,11 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
     if (chain) {
         float D[NS][4];
         const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * a.Dv + v0 + row0 + g4;
-        float part = 0.f;   // <S_T, dS_T>
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t off = soff + (int64_t)(f * (DK / 4) + n * 8 + t2 + (e & 1)) * a.Dv + (e >> 1) * 8;
-                D[n][e] = b.dST ? b.dST[off] : 0.f;
-                if (b.dST && nch > 0) part = fmaf(D[n][e], ST[off], part);
-            }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
-        if (lane == 0 && nch > 0) *(float*)(mine + (nch - 1) * next + keep.exit() + (v0 / 4 + warp) * 4) = part;
+            for (int e = 0; e < 4; ++e)
+                D[n][e] = b.dST ? b.dST[soff + (int64_t)(f * (DK / 4) + n * 8 + t2 + (e & 1)) * a.Dv + (e >> 1) * 8] : 0.f;
         auto put_state = [&] {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
@@ -291,30 +284,11 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
                         *(float2*)(sm + L::WS + ((row0 + g4 + 8 * e) * L::WROW + f * (DK / 4) + n * 8 + t2) * 4) =
                             make_float2(w[n][2 * e], w[n][2 * e + 1]);
             }
-            // the planes of D, and its product with the exit state (the next chunk's entry state)
-            float part = 0.f;
-            for (int e = lt; e < 16 * MT * DK / 8; e += LOADERS) {
+            for (int e = lt; e < 16 * MT * DK / 8; e += LOADERS) {   // the planes of D
                 const int piece = e % (DK / 8), row = e / (DK / 8);
                 const uint32_t off = tile_at<DK>(v0 + row, piece);
-                const uint4 d0 = *(const uint4*)(sm + L::DP + row * L::SROW + piece * 16);
-                const uint4 d1 = *(const uint4*)(sm + L::DP + (16 * MT + row) * L::SROW + piece * 16);
-                *(uint4*)(dst + keep.d() + off) = d0;
-                *(uint4*)(dst + keep.d() + keep.state() + off) = d1;
-                if (c + 1 < nch) {
-                    const uint4 s0 = *(const uint4*)(dst + next + keep.s() + off);
-                    const uint4 s1 = *(const uint4*)(dst + next + keep.s() + keep.state() + off);
-                    const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
-                    const uint32_t ss[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        part = fmaf(low(dd[0][i]) + low(dd[1][i]), low(ss[0][i]) + low(ss[1][i]),
-                                    fmaf(high(dd[0][i]) + high(dd[1][i]), high(ss[0][i]) + high(ss[1][i]), part));
-                }
-            }
-            if (c + 1 < nch) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
-                if (lane == 0) *(float*)(dst + keep.exit() + (v0 / 4 + warp - 4 * MT) * 4) = part;
+                *(uint4*)(dst + keep.d() + off) = *(const uint4*)(sm + L::DP + row * L::SROW + piece * 16);
+                *(uint4*)(dst + keep.d() + keep.state() + off) = *(const uint4*)(sm + L::DP + (16 * MT + row) * L::SROW + piece * 16);
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) bar_sync(1 + 2 * MT + i, 128 + LOADERS);
@@ -580,9 +554,18 @@ __global__ void __launch_bounds__(512) gdn_grads_kernel(GdnBwdArgs b, const __gr
                 sk[n][e] += xr[n][e];
             }
         // column part of dK: e^{cum_C - cum} o (U D^T) + (beta M)^T K + N^T Q
-        float x[NK][4] = {};
+        float x[NK][4] = {}, ex = 0.f;
         cp_async_wait_all();
         __syncthreads();
+        // S once more, 16 bytes of each plane a thread and round, while the product runs
+        constexpr int NP = (DV * DK + 4095) / 4096;
+        const bool has = DV * DK >= 4096 || tid < DV * DK / 8;
+        uint4 sp[2][NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                sp[p][i] = has ? __ldcg((const uint4*)(mine + keep.s() + p * keep.state() + tid * 16 + i * 8192)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int s = 0; s < DV / 16; ++s) {
             uint32_t u[2][4];
@@ -601,6 +584,26 @@ __global__ void __launch_bounds__(512) gdn_grads_kernel(GdnBwdArgs b, const __gr
             }
         }
         scale(x, scal[C + i0], scal[C + i0 + 8]);
+        // <S', D> = e^cum_C <S, D> + sum_t k_t . (e^{cum_C - cum_t} (U D^T)_t)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            if (!has) break;
+            const uint4 d0 = *(const uint4*)(sm + L::SB + tid * 16 + i * 8192), d1 = *(const uint4*)(sm + L::SB + DV * DK * 2 + tid * 16 + i * 8192);
+            const uint32_t ss[2][4] = {{sp[0][i].x, sp[0][i].y, sp[0][i].z, sp[0][i].w}, {sp[1][i].x, sp[1][i].y, sp[1][i].z, sp[1][i].w}};
+            const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                ex = fmaf(low(dd[0][z]) + low(dd[1][z]), low(ss[0][z]) + low(ss[1][z]),
+                          fmaf(high(dd[0][z]) + high(dd[1][z]), high(ss[0][z]) + high(ss[1][z]), ex));
+        }
+        ex *= scal[C - 1];
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t v = *(const uint32_t*)(sm + L::K_ + tile_at<DK>(i0 + 8 * e, qt * NK + n) + t2 * 2);
+                ex = fmaf(low(v), x[n][2 * e], fmaf(high(v), x[n][2 * e + 1], ex));
+            }
 #pragma unroll
         for (int ib = 0; ib < 4; ++ib) {
             if (ib < mt) continue;
@@ -635,12 +638,15 @@ __global__ void __launch_bounds__(512) gdn_grads_kernel(GdnBwdArgs b, const __gr
             dc[e] += __shfl_xor_sync(~0u, dc[e], 2);
             if ((lane & 3) == 0) red[qt * C + i0 + 8 * e] = dc[e];
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ex += __shfl_xor_sync(~0u, ex, o);
+        if (lane == 0) red[4 * C + warp] = ex;
         __syncthreads();
         if (warp == 0) {   // dg: suffix sums of dcum, two tokens a lane, and the exit term
-            float ex = 0.f;
-            for (int i = lane; i < DV / 4; i += 32) ex += *(const float*)(mine + keep.exit() + i * 4);
+            float all = lane < 16 ? red[4 * C + lane] : 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) ex += __shfl_xor_sync(~0u, ex, o);
+            for (int o = 8; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+            all = __shfl_sync(~0u, all, 0);
             float d0 = 0.f, d1 = 0.f;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -654,8 +660,8 @@ __global__ void __launch_bounds__(512) gdn_grads_kernel(GdnBwdArgs b, const __gr
                 if (lane + o < 32) s += y;
             }
             __nv_bfloat16* dg = (__nv_bfloat16*)b.dg + t0 * a.Hv + h;
-            if (2 * lane < valid) dg[(int64_t)(2 * lane) * a.Hv] = __float2bfloat16_rn(s + ex);
-            if (2 * lane + 1 < valid) dg[(int64_t)(2 * lane + 1) * a.Hv] = __float2bfloat16_rn(s - d0 + ex);
+            if (2 * lane < valid) dg[(int64_t)(2 * lane) * a.Hv] = __float2bfloat16_rn(s + all);
+            if (2 * lane + 1 < valid) dg[(int64_t)(2 * lane + 1) * a.Hv] = __float2bfloat16_rn(s - d0 + all);
         }
         __syncthreads();   // the next head's tiles overwrite these
     }
@@ -673,7 +679,7 @@ __global__ void __launch_bounds__(512) gdn_grads_kernel(GdnBwdArgs b, const __gr
 }
 
 template <int DK, int MT>
-cudaError_t rscan(const GdnBwdArgs& a, const Seqs& s, const void* records, void* kept, const float* ST, cudaStream_t st)
+cudaError_t rscan(const GdnBwdArgs& a, const Seqs& s, const void* records, void* kept, cudaStream_t st)
 {
     using L = RScan<DK, MT>;
     auto kern = gdn_rscan_kernel<DK, MT>;
@@ -681,7 +687,7 @@ cudaError_t rscan(const GdnBwdArgs& a, const Seqs& s, const void* records, void*
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_rscan", st);
     count_launch();
-    kern<<<dim3(a.f.Dv / (16 * MT), a.f.Hv, s.n), L::THREADS, L::SMEM, st>>>(a, s, (const char*)records, (char*)kept, ST);
+    kern<<<dim3(a.f.Dv / (16 * MT), a.f.Hv, s.n), L::THREADS, L::SMEM, st>>>(a, s, (const char*)records, (char*)kept);
     return cudaGetLastError();
 }
 
@@ -712,8 +718,7 @@ bool gdn_tc_bwd_supported(const GdnBwdArgs& a)
 
 size_t gdn_tc_bwd_workspace(const Seqs& s, int Hv, int Dk, int Dv)
 {
-    // records, kept tiles, and S_T for <S_T, dS_T>
-    return gdn::rec_part(s, Hv) + gdn::kept_part(s, Hv, Dk, Dv) + (size_t)s.n * Hv * Dk * Dv * sizeof(float);
+    return gdn::rec_part(s, Hv) + gdn::kept_part(s, Hv, Dk, Dv);
 }
 
 cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& b, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st)
@@ -721,20 +726,17 @@ cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& b, const Seqs& s, void* ws, int 
     using namespace gdn;
     char* records = (char*)ws;
     char* kept = records + rec_part(s, b.f.Hv);
-    float* ST = b.dST ? (float*)(kept + kept_part(s, b.f.Hv, b.f.Dk, b.f.Dv)) : nullptr;
     const bool whole = whole_heads(b.f, s, sms);
     cudaError_t e = cudaSuccess;
     if (s.tokens() > 0) {
-        GdnArgs f = b.f;
-        f.ST = ST;
-        e = launch_prologue(f, s, records, st);
-        if (e == cudaSuccess) e = whole ? launch_chain(f, s, records, kept, status, st) : launch_scan(f, s, records, kept, sms, st);
+        e = launch_prologue(b.f, s, records, st);
+        if (e == cudaSuccess) e = whole ? launch_chain(b.f, s, records, kept, status, st) : launch_scan(b.f, s, records, kept, sms, st);
     }
     const bool wide = (int64_t)s.n * b.f.Hv * (b.f.Dv / 32) >= sms;   // as in the forward scan
     if (e == cudaSuccess)
-        e = whole          ? launch_rchain(b, s, records, kept, ST, status, st)
-            : b.f.Dk == 64 ? (wide ? rscan<64, 2>(b, s, records, kept, ST, st) : rscan<64, 1>(b, s, records, kept, ST, st))
-                           : (wide ? rscan<128, 2>(b, s, records, kept, ST, st) : rscan<128, 1>(b, s, records, kept, ST, st));
+        e = whole          ? launch_rchain(b, s, records, kept, status, st)
+            : b.f.Dk == 64 ? (wide ? rscan<64, 2>(b, s, records, kept, st) : rscan<64, 1>(b, s, records, kept, st))
+                           : (wide ? rscan<128, 2>(b, s, records, kept, st) : rscan<128, 1>(b, s, records, kept, st));
     if (e != cudaSuccess || s.tokens() == 0) return e;
     switch (b.f.Dk * 1000 + b.f.Dv) {
         case 64032: return grads<64, 32>(b, s, records, kept, st);

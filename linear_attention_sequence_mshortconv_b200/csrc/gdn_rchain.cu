@@ -7,8 +7,7 @@
 //
 //   warps 0-7  (two warpgroups, each with half of the columns of every operand) what the chain computes
 //              between its products: K D -> dU, T^T dU -> dY and dV, D -> planes
-//   warps 8-11 dO^T, turned over and split into planes for the two products that do not wait for the
-//              chain; <exit state, D>
+//   warps 8-11 dO^T, turned over and split into planes, for the two products that do not wait for the chain
 //   warp 12    issues the MMAs: P^T dO, K D, half of Q^T (e^cum o dO), T^T dU, the other half,
 //              -K^T (e^cum o dV)
 //   warp 13    the loads.  K, T and the gates are double-buffered; Q, dO and P, which only the products aside
@@ -48,7 +47,7 @@ __host__ __device__ constexpr int half_at(int p, int x) { return (x >> 1) * 32 +
 template <int DK, int DV>
 __global__ void __launch_bounds__(480, 1)
 gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
-                  const __grid_constant__ CUtensorMap mv, GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, const float* ST, int* status)
+                  const __grid_constant__ CUtensorMap mv, GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status)
 {
     using L = RChain<DK, DV>;
     const GdnArgs& a = b.f;
@@ -80,9 +79,9 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 for (uint64_t* x : {kd_done, ty_done, d_done}) mbar_init(x + i, 1);
                 for (uint64_t* x : {u_ready, v_ready, d_ready}) mbar_init(x + i, 4);
             }
-            for (uint64_t* x : {g_full, landed, w_done, y_free, drain}) mbar_init(x, 1);
+            for (uint64_t* x : {g_full, landed, w_done, d_free, y_free, drain}) mbar_init(x, 1);
             mbar_init(g_ready, 4);
-            for (uint64_t* x : {d_free, g_empty}) mbar_init(x, 5);   // warps 8-11, and the copy out or the MMAs
+            mbar_init(g_empty, 5);   // warps 8-11 and the MMAs
             for (uint64_t* x : {d_kept, y_kept}) mbar_init(x, 8);
             *guard.flag = 0;
             fence_mbar_init();
@@ -124,9 +123,8 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 for (int p = 0; p < DV / 64; ++p) tma_load_3d(sm + L::G_ + p * PANEL, &mg, bar, p * 64, h, y);
                 bulk_load(sm + L::P_, src + REC_P, REC_SCAL - REC_P, bar);
                 for (int p = 0; p < DK / 64; ++p) tma_load_3d(sm + L::Q_ + p * PANEL, &mq, bar, p * 64, hk, y);
-                // The next chunks' data come as far as L2 meanwhile, or the chain would wait for memory
-                // once a chunk; so does this chunk's entry state, the exit state of the next step's chunk.
-                if (c > 0) prefetch(mine + c * next + keep.s(), 2 * DV * DK * 2);
+                // The data of the step after come as far as L2 meanwhile, or the chain would wait for memory
+                // once a chunk.
                 if (c >= 2) {
                     for (int p = 0; p < DK / 64; ++p) {
                         prefetch_3d(&mk, p * 64, hk, y - 2 * C);
@@ -279,7 +277,6 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         for (int it = 0;; ++it) {
             // D for step it: to the planes, and decayed; at the end, out
             const float* scal = (const float*)(sm + (it & 1) * L::STAGE + L::SCAL);
-            float part = 0.f;   // <S_T, dS_T>
 #pragma unroll 1
             for (int i = 0; i < NI; ++i) {
                 float x[32];
@@ -288,7 +285,6 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     for (int z = 0; z < 32; ++z) {
                         const int64_t off = soff + (int64_t)(i * 32 + z) * DV;
                         x[z] = b.dST && real ? b.dST[off] : 0.f;
-                        if (b.dST && real && nch > 0) part = fmaf(x[z], ST[off], part);
                     }
                 } else {
                     tmem_ld32(at + L::M_ + hf * HK + i * 32, x);
@@ -311,13 +307,7 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(d_ready + hf);
-            if (it == 0) {   // Dv / 4 parts, four of each warp that has columns
-                for (int o = 4; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
-                if (real && (lane & 7) == 0)
-                    *(float*)(mine + (nch - 1) * next + keep.exit() + ((hf * (DV / 32) + (warp & 3)) * 4 + (lane >> 3)) * 4) = part;
-            } else {
-                wait(d_free, (it - 1) & 1, guard);
-            }
+            if (it > 0) wait(d_free, (it - 1) & 1, guard);
             // while K D runs, the planes to where they are copied from
 #pragma unroll 1
             for (int p = 0; p < 2; ++p)
@@ -415,11 +405,10 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         }
         if (lane == 0) bulk_wait0();
     } else {
-        const int row = tid & 127, t = tid - 256;
+        const int row = tid & 127;
         const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16);
         const char* col = sm + L::G_ + (DV > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2;
         for (int it = 0; it < nch; ++it) {
-            const int c = nch - 1 - it;
             const float* scal = (const float*)(sm + (it & 1) * L::STAGE + L::SCAL);
             wait(full + (it & 1), (it >> 1) & 1, guard);
             wait(g_full, it & 1, guard);
@@ -452,49 +441,6 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             warp_arrive(g_ready);
             warp_arrive(g_empty);
             warp_arrive(empty + (it & 1));
-            // <exit state, D>: the exit state is the next chunk's entry state.  Its planes come from L2, each batch
-            // while the one before is at work.
-            constexpr int PIECES = DV * DK * 2 / (128 * 16), NB = 4;
-            const char *s = mine + (c + 1) * next + keep.s() + t * 16, *d = sm + L::OUT_D + t * 16;
-            float part = 0.f;
-            uint4 sp[2][NB];
-            auto fetch = [&](int i0) {
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    sp[0][i] = __ldcg((const uint4*)(s + (i0 + i) * 2048));
-                    sp[1][i] = __ldcg((const uint4*)(s + keep.state() + (i0 + i) * 2048));
-                }
-            };
-            if (it > 0) fetch(0);
-            wait(d_kept, it & 1, guard);
-            if (it > 0)
-#pragma unroll 1
-                for (int i0 = 0; i0 < PIECES; i0 += NB) {
-                    uint4 now[2][NB];
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        now[0][i] = sp[0][i];
-                        now[1][i] = sp[1][i];
-                    }
-                    if (i0 + NB < PIECES) fetch(i0 + NB);
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        const uint4 s0 = now[0][i], s1 = now[1][i];
-                        const uint4 d0 = *(const uint4*)(d + (i0 + i) * 2048), d1 = *(const uint4*)(d + DV * DK * 2 + (i0 + i) * 2048);
-                        const uint32_t ss[2][4] = {{s0.x, s0.y, s0.z, s0.w}, {s1.x, s1.y, s1.z, s1.w}};
-                        const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
-#pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            part = fmaf(low(dd[0][z]) + low(dd[1][z]), low(ss[0][z]) + low(ss[1][z]),
-                                        fmaf(high(dd[0][z]) + high(dd[1][z]), high(ss[0][z]) + high(ss[1][z]), part));
-                    }
-                }
-            warp_arrive(d_free);
-            if (it > 0) {
-                constexpr int G = 512 / DV;   // lanes to a part: Dv / 16 parts a warp
-                for (int o = G / 2; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
-                if ((lane & (G - 1)) == 0) *(float*)(mine + c * next + keep.exit() + ((warp - 8) * (DV / 16) + lane / G) * 4) = part;
-            }
         }
     }
     tc_fence_before();
@@ -504,7 +450,7 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 }
 
 template <int DK, int DV>
-cudaError_t rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, const float* ST, int* status, cudaStream_t st)
+cudaError_t rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st)
 {
     using L = RChain<DK, DV>;
     CUtensorMap k{}, q{}, g{}, v{};
@@ -517,15 +463,15 @@ cudaError_t rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_rchain", st);
     count_launch();
-    gdn_rchain_kernel<DK, DV><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, g, v, b, s, (const char*)records, (char*)kept, ST, status);
+    gdn_rchain_kernel<DK, DV><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, g, v, b, s, (const char*)records, (char*)kept, status);
     return cudaGetLastError();
 }
 }  // namespace
 
-cudaError_t launch_rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, const float* ST, int* status, cudaStream_t st)
+cudaError_t launch_rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st)
 {
-    if (b.f.Dk == 64) return b.f.Dv == 64 ? rchain<64, 64>(b, s, records, kept, ST, status, st) : rchain<64, 128>(b, s, records, kept, ST, status, st);
-    return b.f.Dv == 64 ? rchain<128, 64>(b, s, records, kept, ST, status, st) : rchain<128, 128>(b, s, records, kept, ST, status, st);
+    if (b.f.Dk == 64) return b.f.Dv == 64 ? rchain<64, 64>(b, s, records, kept, status, st) : rchain<64, 128>(b, s, records, kept, status, st);
+    return b.f.Dv == 64 ? rchain<128, 64>(b, s, records, kept, status, st) : rchain<128, 128>(b, s, records, kept, status, st);
 }
 
 }  // namespace gdn

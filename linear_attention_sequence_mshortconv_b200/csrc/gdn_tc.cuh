@@ -110,7 +110,6 @@ __host__ __device__ constexpr int blk(int ib, int jb) { return (ib + (jb ? 2 + 2
 // What the backward keeps of each chunk and value head, bf16: the entry state S^T and the
 // gradient D^T of the exit state, [Dv][Dk] in two planes each; U^T, [Dv][64] in two planes, R^T,
 // [Dv][64], and dY^T, [Dv][64] in two planes; every plane as the tile (tile_at) that the gradients' kernel reads.
-// Then per-warp parts of <exit state, D>, fp32, Dv / 4.
 struct Kept {
     int Dk, Dv;
     __host__ __device__ size_t state() const { return (size_t)Dv * Dk * 2; }     // bytes of a plane
@@ -120,8 +119,7 @@ struct Kept {
     __host__ __device__ size_t u() const { return 4 * state(); }
     __host__ __device__ size_t r() const { return u() + 2 * rows(); }
     __host__ __device__ size_t y() const { return r() + rows(); }
-    __host__ __device__ size_t exit() const { return y() + 2 * rows(); }
-    __host__ __device__ size_t bytes() const { return (exit() + Dv + 255) / 256 * 256; }
+    __host__ __device__ size_t bytes() const { return y() + 2 * rows(); }
 };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
@@ -133,8 +131,8 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // The same scan with all value columns of a head in one CTA (Dv = 64 or 128)
 cudaError_t launch_chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st);
-// and the reverse scan (D and dY kept; ST: the final states, where there are gradients of them)
-cudaError_t launch_rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, const float* ST, int* status, cudaStream_t st);
+// and the reverse scan (D and dY kept)
+cudaError_t launch_rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st);
 bool whole_heads(const GdnArgs& a, const Seqs& s, int sms);   // which of the two
 // launch of the forward scan: o and S_T (kept null), or what the backward needs (kept and, if
 // not null, S_T; o unused)
