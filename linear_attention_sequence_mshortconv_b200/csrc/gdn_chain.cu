@@ -267,46 +267,48 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16);
         const bool real = row < DV;
         const int64_t soff = ((int64_t)seq * a.Hv + h) * DK * DV + (int64_t)hf * HK * DV + row;
-        auto scal_of = [&](int c) { return (const float*)(sm + (c & 1) * L::STAGE + L::SCAL); };
-        // 32 of the half's channels: to the planes, and decayed for chunk c
-        auto put = [&](int i, float (&s)[32], int c) {
-            uint32_t p[2][16];
-            planes_of<2>(s, p);
-            tmem_st16u_nowait(at + L::SP_ + hf * (HK / 2) + i * 16, p[0]);
-            tmem_st16u_nowait(at + L::SP_ + DK / 2 + hf * (HK / 2) + i * 16, p[1]);
-            if (KEEP && real) {
-                to_tile<DK>(sm + L::OUT, row, hf * (HK / 8) + i * 4, p[0]);
-                to_tile<DK>(sm + L::OUT + DV * DK * 2, row, hf * (HK / 8) + i * 4, p[1], 0x80008000u);
-            }
-            const float gam = scal_of(c)[C - 1];
+        if (nch > 0) wait(full, 0, guard);
+        // (Loops over 32 channels stay loops here: unrolled, the kernel's roles fetched instructions for longer than
+        // they took to issue.)
+        for (int c = 0;; ++c) {
+            // S for chunk c: to the planes, and decayed; at the end, out
+            const float* scal = (const float*)(sm + (c & 1) * L::STAGE + L::SCAL);
+#pragma unroll 1
+            for (int i = 0; i < HK / 32; ++i) {
+                float s[32];
+                if (c == 0) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] *= gam;
-            store32(at + L::M_ + hf * HK + i * 32, s);
-        };
-        auto state_ready = [&] {
-            if (KEEP) {
-                fence_async_smem();
-                warp_arrive(s_kept);
+                    for (int z = 0; z < 32; ++z) s[z] = a.S0 && real ? a.S0[soff + (int64_t)(i * 32 + z) * DV] : 0.f;
+                } else {
+                    tmem_ld32(at + L::M_ + hf * HK + i * 32, s);
+                }
+                if (c < nch) {
+                    uint32_t p[2][16];
+                    planes_of<2>(s, p);
+                    tmem_st16u_nowait(at + L::SP_ + hf * (HK / 2) + i * 16, p[0]);
+                    tmem_st16u_nowait(at + L::SP_ + DK / 2 + hf * (HK / 2) + i * 16, p[1]);
+                    const float gam = scal[C - 1];
+#pragma unroll
+                    for (int z = 0; z < 32; ++z) s[z] *= gam;
+                    store32(at + L::M_ + hf * HK + i * 32, s);
+                } else if (a.ST && real) {
+#pragma unroll
+                    for (int z = 0; z < 32; ++z) a.ST[soff + (int64_t)(i * 32 + z) * DV] = s[z];
+                }
             }
+            if (c == nch) break;
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(s_ready + hf);
-        };
-        if (nch > 0) {
-            wait(full, 0, guard);
-#pragma unroll
-            for (int i = 0; i < HK / 32; ++i) {
-                float s[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) s[x] = a.S0 && real ? a.S0[soff + (int64_t)(i * 32 + x) * DV] : 0.f;
-                put(i, s, 0);
+            if (KEEP) {   // while K S runs, the planes to where they are copied from
+                if (c > 0) wait(s_free, (c - 1) & 1, guard);
+#pragma unroll 1
+                for (int p = 0; p < 2; ++p)
+                    planes_to_tile<DK, HK / 2>(at + L::SP_ + p * (DK / 2) + hf * (HK / 2), sm + L::OUT + p * DV * DK * 2, row, hf * (HK / 8), real,
+                                               p ? 0x80008000u : 0u);
+                fence_async_smem();
+                warp_arrive(s_kept);
             }
-            state_ready();
-        } else if (a.ST && real) {
-            for (int x = 0; x < HK; ++x) a.ST[soff + (int64_t)x * DV] = a.S0 ? a.S0[soff + (int64_t)x * DV] : 0.f;
-        }
-        for (int c = 0; c < nch; ++c) {
-            const float* scal = scal_of(c);
             float x[32];
             uint32_t p[3][16];
             auto put_y = [&] {
@@ -334,37 +336,27 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = 0.f;
             }
-            if (KEEP) {
-                if (c > 0) wait(u_free, (c - 1) & 1, guard);
-                uint32_t r[1][16];
-                planes_of<1>(x, r);
-                if (real) to_tile<C>(sm + L::OUT_R, row, hf * 4, r[0]);
-            }
+            uint32_t r[1][16];
+            if (KEEP) planes_of<1>(x, r);
             scale32(x, scal + 2 * C + hf * 32);
             put_y();
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(y_ready + hf);
+            if (KEEP) {   // R, and later U, while the next product runs
+                if (c > 0) wait(u_free, (c - 1) & 1, guard);
+                if (real) to_tile<C>(sm + L::OUT_R, row, hf * 4, r[0]);
+            }
             // U, its planes, and decayed
             if (c + 1 < nch) wait(full + ((c + 1) & 1), ((c + 1) >> 1) & 1, guard);
-            if (KEEP) wait(s_free, c & 1, guard);
             wait(ty_done + hf, c & 1, guard);
             tc_fence_after();
             tmem_ld32(at + L::U_ + hf * 32, x);
-            {
-                uint32_t u[2][16];
-                planes_of<2>(x, u);
-                if (KEEP) {
-                    if (real) {
-                        to_tile<C>(sm + L::OUT_U, row, hf * 4, u[0]);
-                        to_tile<C>(sm + L::OUT_U + DV * C * 2, row, hf * 4, u[1], 0x80008000u);
-                    }
-                    fence_async_smem();
-                    warp_arrive(u_kept);
-                } else {
-                    tmem_st16u_nowait(at + L::U_ + hf * 32, u[0]);
-                    tmem_st16u_nowait(at + L::U_ + hf * 32 + 16, u[1]);
-                }
+            uint32_t u[2][16];
+            planes_of<2>(x, u);
+            if (!KEEP) {
+                tmem_st16u_nowait(at + L::U_ + hf * 32, u[0]);
+                tmem_st16u_nowait(at + L::U_ + hf * 32 + 16, u[1]);
             }
             scale32(x, scal + C + hf * 32);
             wait(ty_done + 1, c & 1, guard);   // the second half of T Y reads both halves' planes of Y
@@ -373,22 +365,18 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(u_ready + hf);
+            if (KEEP) {
+                if (real) {
+                    to_tile<C>(sm + L::OUT_U, row, hf * 4, u[0]);
+                    to_tile<C>(sm + L::OUT_U + DV * C * 2, row, hf * 4, u[1], 0x80008000u);
+                }
+                fence_async_smem();
+                warp_arrive(u_kept);
+            }
             warp_arrive(empty + (c & 1));
             if (!KEEP) wait(qs_done, c & 1, guard);   // its planes of S
             wait(s_done + hf, c & 1, guard);
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < HK / 32; ++i) {
-                float s[32];
-                tmem_ld32(at + L::M_ + hf * HK + i * 32, s);
-                if (c + 1 < nch) {
-                    put(i, s, c + 1);
-                } else if (a.ST && real) {
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) a.ST[soff + (int64_t)(i * 32 + y) * DV] = s[y];
-                }
-            }
-            if (c + 1 < nch) state_ready();
         }
     } else if (KEEP) {
         if (warp == 8 && lane == 0) {   // what the gradients need goes out by the copy engine
