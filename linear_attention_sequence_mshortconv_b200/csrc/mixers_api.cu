@@ -137,6 +137,7 @@ size_t gdn_fwd_need(const GdnArgs& a, const Batch& b)
 kda_status run_gdn_forward(const GdnArgs& a, const Batch& b, void* workspace, size_t workspace_bytes,
                            kda_stream_t stream)
 {
+    if (b.n == 0) return KDA_OK;
     Scratch ws;
     const kda_status st = ws.acquire(workspace, workspace_bytes, gdn_fwd_need(a, b), (cudaStream_t)stream);
     if (st != KDA_OK) return st;
@@ -168,6 +169,7 @@ size_t gdn_bwd_need(const GdnArgs& a, const Batch& b)
 kda_status run_gdn_backward(const GdnBwdArgs& a, const Batch& b, void* workspace, size_t workspace_bytes,
                             kda_stream_t stream)
 {
+    if (b.n == 0) return KDA_OK;
     Scratch ws;
     kda_status st = ws.acquire(workspace, workspace_bytes, gdn_bwd_need(a.f, b), (cudaStream_t)stream);
     if (st != KDA_OK) return st;

@@ -18,20 +18,22 @@ import torch
 from .kda import _check, _code, _cu_array, _dtype_code, load_library
 
 # The current stream's handle without building a Stream object (some 3 us of a call whose
-# kernel may take 5); torch's public way where a version lacks it.
+# kernel may take 5), and the current device; torch's public ways where a version lacks them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_Tensor = torch.Tensor
 
 
 def check_tensors(first, named):
     """The tensors of a call, (name, tensor or None, shape, dtype), are contiguous CUDA tensors of the
     first one's device and of the shape and type given; None passes.  Returns the device's index."""
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+    if not isinstance(first, _Tensor) or not first.is_cuda:
         raise TypeError("q must be a CUDA tensor")
     index = first.get_device()
     for name, t, shape, dtype in named:
-        if t is None or (isinstance(t, torch.Tensor) and t.get_device() == index and t.shape == shape
-                         and t.dtype is dtype and t.is_contiguous()):
+        if t is None or (isinstance(t, _Tensor) and t.shape == shape and t.dtype is dtype
+                         and t.get_device() == index and t.is_contiguous()):
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
@@ -53,7 +55,7 @@ def launch(index, stream, body):
     """body(stream handle) with the tensors' device and the launching stream current, so that what a
     call allocates belongs to the stream it runs on."""
     if stream is None:
-        if torch.cuda.current_device() == index:
+        if _device() == index:
             return body(_raw_stream(index))
         with torch.cuda.device(index):
             return body(_raw_stream(index))
@@ -76,18 +78,18 @@ def scratch(workspace, need, like):
 
 
 def _sizes(q, v, tokens_dims):
-    if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor) or q.dim() != tokens_dims + 2 \
-            or v.dim() != tokens_dims + 2:
+    if not isinstance(q, _Tensor) or not isinstance(v, _Tensor) or q.ndim != tokens_dims + 2 or v.ndim != tokens_dims + 2:
         raise ValueError(f"q and v must have {tokens_dims + 2} dimensions")
-    (Hk, Dk), (Hv, Dv) = q.shape[-2:], v.shape[-2:]
+    (*_, Hk, Dk), (*_, Hv, Dv) = q.shape, v.shape
     if Hk == 0 or Hv % Hk:
         raise ValueError(f"{Hv} value heads cannot share {Hk} query/key heads")
     return Hk, Hv, Dk, Dv
 
 
 def _inputs(q, k, v, g, beta, lead, Hv):
-    return [("q", q, q.shape, q.dtype), ("k", k, q.shape, q.dtype), ("v", v, v.shape, q.dtype),
-            ("g", g, (*lead, Hv), q.dtype), ("beta", beta, (*lead, Hv), q.dtype)]
+    shape, gates, dtype = q.shape, (*lead, Hv), q.dtype
+    return [("q", q, shape, dtype), ("k", k, shape, dtype), ("v", v, (*lead, *v.shape[-2:]), dtype),
+            ("g", g, gates, dtype), ("beta", beta, gates, dtype)]
 
 
 def _packed(cu_seqlens, T):
@@ -217,17 +219,18 @@ def step(q, k, v, g, beta, state, slots=None, *, o=None, stream=None):
     Hk, Hv, Dk, Dv = _sizes(q, v, 1)
     dt = _dtype_code(q)
     n = q.shape[0]
-    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+    if not isinstance(state, _Tensor) or state.ndim != 4:
         raise ValueError("state must be [n_slots,Hv,Dk,Dv]")
+    n_slots = state.shape[0]
     index = check_tensors(q, _inputs(q, k, v, g, beta, (n,), Hv) + [
-        ("state", state, (state.shape[0], Hv, Dk, Dv), torch.float32), ("slots", slots, (n,), torch.int32),
-        ("o", o, v.shape, q.dtype)])
+        ("state", state, (n_slots, Hv, Dk, Dv), torch.float32), ("slots", slots, (n,), torch.int32),
+        ("o", o, (n, Hv, Dv), q.dtype)])
     lib = load_library()
 
     def body(s):
         out = torch.empty_like(v) if o is None else o
         _check("gdn_step", lib.gdn_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                        state.data_ptr(), ptr(slots), out.data_ptr(), n, state.shape[0], Hk, Hv, Dk, Dv,
+                                        state.data_ptr(), ptr(slots), out.data_ptr(), n, n_slots, Hk, Hv, Dk, Dv,
                                         dt, s))
         return out
 

@@ -56,6 +56,8 @@ _lock = threading.Lock()
 def load_library(path: str = LIB_PATH):
     """Loads libkda.so and declares its signatures (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

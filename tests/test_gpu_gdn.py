@@ -255,6 +255,19 @@ def test_workspace_of_the_stated_size():
                 call(buf[:need - 256])
 
 
+@pytest.mark.parametrize("which", [1, 2, 3, 4])
+def test_inputs_of_fewer_tokens_are_refused(which):
+    """k, v, g or beta one token shorter than q."""
+    x, S0, do, _ = make([8], 1, 2, 64, 64, torch.bfloat16)
+    x, do = cuda(x), do.cuda()
+    bad = [t[:-1].contiguous() if i == which else t for i, t in enumerate(x)]
+    rows = [t[None] for t in bad]
+    for call in (lambda: gdn.forward_varlen(*bad, [0, 7]), lambda: gdn.forward(*rows), lambda: gdn.step(*bad, torch.zeros(8, 2, 64, 64, device="cuda")),
+                 lambda: gdn.backward_varlen(*bad, do, [0, 7]), lambda: gdn.backward(*rows, do[None])):
+        with pytest.raises(ValueError):
+            call()
+
+
 # ---- many heads or samples: whole heads to a CTA in the scan, two column tiles in the reverse one ----------------------
 WIDE = [  # lens, Hk, Hv, Dk, Dv
     ([64] * 10, 4, 8, 128, 128), ([130, 70, 0, 1, 129], 16, 32, 128, 64), ([65] * 6 + [3], 2, 6, 64, 128),
