@@ -28,17 +28,22 @@ namespace kda {
 namespace gdn {
 namespace {
 
-template <int DK, int DV, bool KEEP>
+// What a launch gives: o (and S_T); what the backward keeps; S_T alone; or the transition of the whole
+// sequence, that is, S_T with S_0 = 1 and V = 0 (Dv = Dk).
+enum { CHAIN_OUT, CHAIN_KEEP, CHAIN_STATE, CHAIN_TRANSITION };
+
+template <int DK, int DV, int MODE>
 struct Chain {
+    static constexpr bool KEEP = MODE == CHAIN_KEEP, READ = MODE == CHAIN_OUT, HAS_V = MODE != CHAIN_TRANSITION;
     static constexpr int THREADS = 448;
-    static constexpr int K_ = 0, Q_ = K_ + DK / 64 * PANEL, V_ = Q_ + (KEEP ? 0 : DK / 64 * PANEL);
-    // the record; what is kept needs no P
-    static constexpr int REC = V_ + DV / 64 * PANEL, SCAL = REC + (KEEP ? REC_P : REC_SCAL);
+    static constexpr int K_ = 0, Q_ = K_ + DK / 64 * PANEL, V_ = Q_ + (READ ? DK / 64 * PANEL : 0);
+    // the record; only o needs P
+    static constexpr int REC = V_ + (HAS_V ? DV / 64 * PANEL : 0), SCAL = REC + (READ ? REC_SCAL : REC_P);
     static constexpr int STAGE = (SCAL + REC_BYTES - REC_SCAL + 1023) / 1024 * 1024;
     static constexpr int OUT = 2 * STAGE;                     // the output [64][DV] bf16; or what is kept: two planes
     static constexpr int OUT_U = OUT + 2 * DV * DK * 2;       // of S, of U, and R, as tiles
     static constexpr int OUT_R = OUT_U + 2 * DV * C * 2;
-    static constexpr int EYE = KEEP ? OUT_R + DV * C * 2 : OUT + C * DV * 2;   // 64x64 identity, bf16, a panel
+    static constexpr int EYE = KEEP ? OUT_R + DV * C * 2 : OUT + (READ ? C * DV * 2 : 0);   // 64x64 identity, bf16, a panel
     static constexpr int BAR = EYE + PANEL;
     // the base is aligned up to 1024 bytes; more than half of an SM's, since each CTA takes all of its
     // tensor memory
@@ -50,12 +55,13 @@ struct Chain {
 // plane 2 where its half of K S was
 __host__ __device__ constexpr int y_at(int p, int x) { return (p < 2 ? p * 16 : 64) + (x >> 1) * 32 + (x & 1) * 8; }
 
-template <int DK, int DV, bool KEEP>
+template <int DK, int DV, int MODE>
 __global__ void __launch_bounds__(448, 1)
 gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv,
                  GdnArgs a, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status)
 {
-    using L = Chain<DK, DV, KEEP>;
+    using L = Chain<DK, DV, MODE>;
+    constexpr bool KEEP = L::KEEP, READ = L::READ, HAS_V = L::HAS_V;
     extern __shared__ char raw[];
     char* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const uint32_t base = smem_addr(sm);
@@ -79,7 +85,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         if (lane == 0) {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(full + i, 1);
-                mbar_init(empty + i, KEEP ? 9 : 13);   // the MMAs, and each warp that reads the stage
+                mbar_init(empty + i, READ ? 13 : 9);   // the MMAs, and each warp that reads the stage
                 for (uint64_t* b : {ks_done, ty_done, s_done}) mbar_init(b + i, 1);
                 for (uint64_t* b : {y_ready, u_ready, s_ready}) mbar_init(b + i, 4);
             }
@@ -112,18 +118,18 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             if (warp_up(guard)) break;
             uint64_t* bar = valid < C ? landed : full + (c & 1);
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, (KEEP ? 1 : 2) * C * DK * 2 + C * DV * 2 + REC_BYTES - (KEEP ? REC_SCAL - REC_P : 0));
+                mbar_arrive_expect_tx(bar, (READ ? 2 : 1) * C * DK * 2 + (HAS_V ? C * DV * 2 : 0) + REC_BYTES - (READ ? 0 : REC_SCAL - REC_P));
                 for (int p = 0; p < DK / 64; ++p) {
                     tma_load_3d(st + L::K_ + p * PANEL, &mk, bar, p * 64, hk, (int)t0 + c * C);
-                    if (!KEEP) tma_load_3d(st + L::Q_ + p * PANEL, &mq, bar, p * 64, hk, (int)t0 + c * C);
+                    if (READ) tma_load_3d(st + L::Q_ + p * PANEL, &mq, bar, p * 64, hk, (int)t0 + c * C);
                 }
-                for (int p = 0; p < DV / 64; ++p) tma_load_3d(st + L::V_ + p * PANEL, &mv, bar, p * 64, h, (int)t0 + c * C);
+                for (int p = 0; HAS_V && p < DV / 64; ++p) tma_load_3d(st + L::V_ + p * PANEL, &mv, bar, p * 64, h, (int)t0 + c * C);
                 const char* src = rec + (int64_t)c * a.Hv * REC_BYTES;
-                if (KEEP) {
+                if (READ) {
+                    bulk_load(st + L::REC, src, REC_BYTES, bar);
+                } else {
                     bulk_load(st + L::REC, src, REC_P, bar);
                     bulk_load(st + L::SCAL, src + REC_SCAL, REC_BYTES - REC_SCAL, bar);
-                } else {
-                    bulk_load(st + L::REC, src, REC_BYTES, bar);
                 }
                 // The stage after next is still in use: its data come as far as L2 meanwhile, or the
                 // chain would wait for memory once a chunk.
@@ -131,9 +137,9 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     const int y = (int)t0 + (c + 2) * C;
                     for (int p = 0; p < DK / 64; ++p) {
                         prefetch_3d(&mk, p * 64, hk, y);
-                        if (!KEEP) prefetch_3d(&mq, p * 64, hk, y);
+                        if (READ) prefetch_3d(&mq, p * 64, hk, y);
                     }
-                    for (int p = 0; p < DV / 64; ++p) prefetch_3d(&mv, p * 64, h, y);
+                    for (int p = 0; HAS_V && p < DV / 64; ++p) prefetch_3d(&mv, p * 64, h, y);
                     prefetch(src + 2 * (int64_t)a.Hv * REC_BYTES, REC_BYTES);
                 }
             }
@@ -185,7 +191,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 by_s(tmem + L::R_ + 64, dk + so, id_ks, 0);
                 by_s(tmem + L::R_ + 96, dk + so + (4096 >> 4), id_ks, 0);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) umma_f16(tmem + L::R_, step_cols(dv + so, x), step_rows(de, x, PANEL), id_v, x > 0);
+                for (int x = 0; HAS_V && x < 4; ++x) umma_f16(tmem + L::R_, step_cols(dv + so, x), step_rows(de, x, PANEL), id_v, x > 0);
             }
             wait(s_ready + 1, c & 1, guard);
             tc_fence_after();
@@ -195,7 +201,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 by_s(tmem + L::R_ + 96, dk + so + (4096 >> 4), id_ks, 1);
                 umma_commit(ks_done + 1);
             }
-            if (!KEEP && c > 0) wait(o_done, (c - 1) & 1, guard);   // the planes of U are where T Y goes
+            if (READ && c > 0) wait(o_done, (c - 1) & 1, guard);   // the planes of U are where T Y goes
 #pragma unroll
             for (int th = 0; th < 2; ++th) {   // T Y: every product of planes but T1 Y2
                 wait(y_ready + th, c & 1, guard);
@@ -211,7 +217,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     umma_commit(ty_done + th);
                 }
             }
-            if (!KEEP) {   // while U is turned into its planes
+            if (READ) {   // while U is turned into its planes
                 if (c > 0) wait(o_read, (c - 1) & 1, guard);
                 tc_fence_after();
                 if (elect()) {
@@ -238,7 +244,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     if (th && DK == 64) umma_commit(s_done + 1);
                 }
             }
-            if (!KEEP) {
+            if (READ) {
                 wait(o_scaled, c & 1, guard);
                 tc_fence_after();
                 if (elect()) {
@@ -278,7 +284,10 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 float s[32];
                 if (c == 0) {
 #pragma unroll
-                    for (int z = 0; z < 32; ++z) s[z] = a.S0 && real ? a.S0[soff + (int64_t)(i * 32 + z) * DV] : 0.f;
+                    for (int z = 0; z < 32; ++z) {
+                        if (HAS_V) s[z] = a.S0 && real ? a.S0[soff + (int64_t)(i * 32 + z) * DV] : 0.f;
+                        else s[z] = hf * HK + i * 32 + z == row ? 1.f : 0.f;
+                    }
                 } else {
                     tmem_ld32(at + L::M_ + hf * HK + i * 32, s);
                 }
@@ -321,7 +330,12 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             tc_fence_after();
             {
                 float ks[32];
-                tmem_ld32(at + L::R_ + hf * 32, x);
+                if (HAS_V) {
+                    tmem_ld32(at + L::R_ + hf * 32, x);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                }
                 tmem_ld32(at + L::R_ + 64 + hf * 32, ks);
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
@@ -354,7 +368,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             tmem_ld32(at + L::U_ + hf * 32, x);
             uint32_t u[2][16];
             planes_of<2>(x, u);
-            if (!KEEP) {
+            if (READ) {
                 tmem_st16u_nowait(at + L::U_ + hf * 32, u[0]);
                 tmem_st16u_nowait(at + L::U_ + hf * 32 + 16, u[1]);
             }
@@ -374,7 +388,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 warp_arrive(u_kept);
             }
             warp_arrive(empty + (c & 1));
-            if (!KEEP) wait(qs_done, c & 1, guard);   // its planes of S
+            if (READ) wait(qs_done, c & 1, guard);   // its planes of S
             wait(s_done + hf, c & 1, guard);
             tc_fence_after();
         }
@@ -396,7 +410,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
             bulk_wait0();
         }
-    } else {
+    } else if (READ) {
         const int row = tid & 127, t = tid - 256;
         const uint32_t at = tmem + ((uint32_t)(warp & 3) * 32u << 16) + L::O_;
         __nv_bfloat16* op = (__nv_bfloat16*)a.o + (t0 * a.Hv + h) * DV;
@@ -442,30 +456,183 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-template <int DK, int DV, bool KEEP>
+template <int DK, int DV, int MODE>
 cudaError_t chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st)
 {
-    using L = Chain<DK, DV, KEEP>;
+    using L = Chain<DK, DV, MODE>;
     CUtensorMap k{}, q{}, v{};
     const int64_t T = s.tokens();
-    if (T > 0 && (!make_map(&k, a.k, T, a.Hk, DK, 64, 1, C) || !make_map(&q, a.q, T, a.Hk, DK, 64, 1, C) ||
-                  !make_map(&v, a.v, T, a.Hv, DV, 64, 1, C)))
+    if (T > 0 && (!make_map(&k, a.k, T, a.Hk, DK, 64, 1, C) || (L::READ && !make_map(&q, a.q, T, a.Hk, DK, 64, 1, C)) ||
+                  (L::HAS_V && !make_map(&v, a.v, T, a.Hv, DV, 64, 1, C))))
         return cudaErrorInvalidValue;
-    const cudaError_t e = allow_smem<gdn_chain_kernel<DK, DV, KEEP>>(L::SMEM);
+    const cudaError_t e = allow_smem<gdn_chain_kernel<DK, DV, MODE>>(L::SMEM);
     if (e != cudaSuccess) return e;
-    ProfileScope prof(KEEP ? "gdn_chain_keep" : "gdn_chain", st);
+    ProfileScope prof(MODE == CHAIN_OUT ? "gdn_chain" : MODE == CHAIN_KEEP ? "gdn_chain_keep" : MODE == CHAIN_STATE ? "gdn_chain_state" : "gdn_chain_transition", st);
     count_launch();
-    gdn_chain_kernel<DK, DV, KEEP><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, v, a, s, (const char*)records, (char*)kept, status);
+    gdn_chain_kernel<DK, DV, MODE><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, v, a, s, (const char*)records, (char*)kept, status);
+    return cudaGetLastError();
+}
+template <int MODE>
+cudaError_t chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st)
+{
+    if (a.Dk == 64) return a.Dv == 64 ? chain<64, 64, MODE>(a, s, records, kept, status, st) : chain<64, 128, MODE>(a, s, records, kept, status, st);
+    return a.Dv == 64 ? chain<128, 64, MODE>(a, s, records, kept, status, st) : chain<128, 128, MODE>(a, s, records, kept, status, st);
+}
+
+// ---- pieces of long samples ---------------------------------------------------------------------
+// Where few heads have many chunks in a row, the samples are cut into pieces of equal length that run at
+// once.  The state is linear in the one before, S_out = M S_in + B: one launch gives every piece's B (from
+// a state of zero), one its M (from the identity, without V), this kernel carries the states from piece
+// to piece, and a last launch runs every piece from the right state: three times the work, on more SMs than
+// that.  (16 heads of 512 chunks in 9 pieces: 139, 129, 38 and 171 us; one chain of columns takes 770.)
+//
+// A CTA has 16 columns of a head's states; thread (i, j) has rows i, i + 32, ... and columns 4j .. 4j + 3.  The next
+// piece's M is on its way while one is used.
+template <int DK>
+struct Carry {
+    static constexpr int THREADS = 128, COLS = 16, MROW = DK + 4;   // floats; rows 16 bytes apart in banks
+    static constexpr int S_ = 2 * DK * MROW, SMEM = (S_ + DK * COLS) * 4;
+};
+struct Pieces {
+    int16_t first[kMaxSeqs + 1];   // a sample's first piece
+};
+template <int DK>
+__global__ void __launch_bounds__(128) gdn_carry_kernel(const __grid_constant__ Pieces pieces, const float* M, const float* B, const float* S0, float* in,
+                                                        float* ST, int Hv, int Dv)
+{
+    using L = Carry<DK>;
+    extern __shared__ float fm[];
+    float* S = fm + L::S_;
+    const int tid = threadIdx.x, ri = tid >> 2, j = (tid & 3) * 4;
+    const int h = blockIdx.x, seq = blockIdx.y, col = blockIdx.z * L::COLS + j;
+    const int p0 = pieces.first[seq], p1 = pieces.first[seq + 1];
+    constexpr int R = DK / 32;
+    auto fetch = [&](int p) {
+        const float* src = M + ((int64_t)p * Hv + h) * DK * DK;
+        const uint32_t dst = smem_addr(fm + (p & 1) * DK * L::MROW);
+        for (int e = tid; e < DK * DK / 4; e += L::THREADS)
+            cp16(dst + (e / (DK / 4) * L::MROW + e % (DK / 4) * 4) * 4, src + e * 4, true);
+        cp_async_commit();
+    };
+    float4 s[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        s[i] = S0 ? *(const float4*)(S0 + (((int64_t)seq * Hv + h) * DK + ri + 32 * i) * Dv + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // (the last piece's is for S_T alone)
+    if (p0 + (ST ? 0 : 1) < p1) fetch(p0);
+    for (int p = p0; p < p1; ++p) {
+        const int64_t off = ((int64_t)p * Hv + h) * DK * Dv + col;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            *(float4*)(in + off + (int64_t)(ri + 32 * i) * Dv) = s[i];
+            *(float4*)(S + (ri + 32 * i) * L::COLS + j) = s[i];
+        }
+        if (p + 1 == p1 && !ST) break;
+        cp_async_wait_all();
+        __syncthreads();
+        if (p + (ST ? 1 : 2) < p1) fetch(p + 1);
+#pragma unroll
+        for (int i = 0; i < R; ++i) s[i] = *(const float4*)(B + off + (int64_t)(ri + 32 * i) * Dv);
+        const float* m = fm + (p & 1) * DK * L::MROW + ri * L::MROW;
+#pragma unroll 4
+        for (int k = 0; k < DK; k += 4) {
+            float4 x[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) x[z] = *(const float4*)(S + (k + z) * L::COLS + j);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float4 w = *(const float4*)(m + 32 * i * L::MROW + k);
+                const float ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    s[i].x = fmaf(ww[z], x[z].x, s[i].x);
+                    s[i].y = fmaf(ww[z], x[z].y, s[i].y);
+                    s[i].z = fmaf(ww[z], x[z].z, s[i].z);
+                    s[i].w = fmaf(ww[z], x[z].w, s[i].w);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (ST)
+#pragma unroll
+        for (int i = 0; i < R; ++i) *(float4*)(ST + (((int64_t)seq * Hv + h) * DK + ri + 32 * i) * Dv + col) = s[i];
+}
+template <int DK>
+cudaError_t carry(const GdnArgs& a, const Seqs& s, const Pieces& pieces, const float* M, const float* B, float* in, cudaStream_t st)
+{
+    using L = Carry<DK>;
+    const cudaError_t e = allow_smem<gdn_carry_kernel<DK>>(L::SMEM);
+    if (e != cudaSuccess) return e;
+    ProfileScope prof("gdn_carry", st);
+    count_launch();
+    gdn_carry_kernel<DK><<<dim3(a.Hv, s.n, a.Dv / L::COLS), L::THREADS, L::SMEM, st>>>(pieces, M, B, a.S0, in, a.ST, a.Hv, a.Dv);
     return cudaGetLastError();
 }
 }  // namespace
 
 cudaError_t launch_chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st)
 {
-#define KDA_CHAIN(DK, DV) (kept ? chain<DK, DV, true>(a, s, records, kept, status, st) : chain<DK, DV, false>(a, s, records, kept, status, st))
-    if (a.Dk == 64) return a.Dv == 64 ? KDA_CHAIN(64, 64) : KDA_CHAIN(64, 128);
-    return a.Dv == 64 ? KDA_CHAIN(128, 64) : KDA_CHAIN(128, 128);
-#undef KDA_CHAIN
+    return kept ? chain<CHAIN_KEEP>(a, s, records, kept, status, st) : chain<CHAIN_OUT>(a, s, records, nullptr, status, st);
+}
+
+int piece_chunks(const Seqs& s, int Hv, int Dk, int Dv, int sms)
+{
+    if (Dv == 32 || Dk == 32) return 0;
+    int64_t longest = 0;
+    for (int i = 0; i < s.n; ++i) longest = max(longest, ((int64_t)s.len(i) + C - 1) / C);
+    auto pieces = [&](int64_t per) {
+        int64_t n = 0;
+        for (int i = 0; i < s.n; ++i) n += ((s.len(i) + C - 1) / C + per - 1) / per;
+        return n;
+    };
+    // the shortest pieces that the SMs take at once
+    int64_t lo = 1, hi = longest;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (pieces(mid) * Hv <= sms && pieces(mid) <= kMaxSeqs) hi = mid; else lo = mid + 1;
+    }
+    const int64_t per = max(lo, (int64_t)8);
+    if (pieces(per) * Hv > sms || pieces(per) > kMaxSeqs) return 0;
+    // Steps in a row, in units of 0.1 us: 15 a chunk with columns of heads; 26 a chunk and launch, 40 a piece
+    // carried, 150 for the launches.  Measured (Dk = Dv = 128; columns, then pieces): one head pair of 6016 tokens 155
+    // and 128 us, of 12288 303 and 170; 16 heads of 8192 241 and 218, of 32768 920 and 620.
+    const int64_t steps = (longest + per - 1) / per;
+    return 3 * 26 * per + 40 * steps + 150 < 15 * longest ? (int)per : 0;
+}
+size_t pieces_workspace(const Seqs& s, int Hv, int Dk, int Dv, int per)
+{
+    int64_t n = 0;
+    for (int i = 0; i < s.n; ++i) n += ((s.len(i) + C - 1) / C + per - 1) / per;
+    return (size_t)(s.tokens() / C + n) * Hv * REC_BYTES + (size_t)n * Hv * Dk * (Dk + 2 * Dv) * sizeof(float);
+}
+cudaError_t launch_pieces(const GdnArgs& a, const Seqs& s, void* ws, int per, int* status, cudaStream_t st)
+{
+    Seqs cut;
+    Pieces pieces;
+    cut.n = 0;
+    cut.T = -1;
+    for (int i = 0; i < s.n; ++i) {
+        pieces.first[i] = (int16_t)cut.n;
+        for (int at = 0; at < s.len(i); at += per * C) cut.cu[cut.n++] = s.start(i) + at;
+    }
+    pieces.first[s.n] = (int16_t)cut.n;
+    cut.cu[cut.n] = s.tokens();
+    const size_t states = (size_t)cut.n * a.Hv * a.Dk;
+    float* M = (float*)((char*)ws + (size_t)cut.slots(C) * a.Hv * REC_BYTES);
+    float *B = M + states * a.Dk, *in = B + states * a.Dv;
+    cudaError_t e = launch_prologue(a, cut, ws, st);
+    GdnArgs x = a;
+    x.S0 = nullptr;
+    x.ST = B;
+    if (e == cudaSuccess) e = chain<CHAIN_STATE>(x, cut, ws, nullptr, status, st);
+    x.ST = M;
+    if (e == cudaSuccess) e = a.Dk == 64 ? chain<64, 64, CHAIN_TRANSITION>(x, cut, ws, nullptr, status, st) : chain<128, 128, CHAIN_TRANSITION>(x, cut, ws, nullptr, status, st);
+    if (e == cudaSuccess) e = a.Dk == 64 ? carry<64>(a, s, pieces, M, B, in, st) : carry<128>(a, s, pieces, M, B, in, st);
+    x.S0 = in;
+    x.ST = nullptr;
+    if (e == cudaSuccess) e = chain<CHAIN_OUT>(x, cut, ws, nullptr, status, st);
+    return e;
 }
 
 }  // namespace gdn

@@ -601,10 +601,15 @@ bool gdn_tc_supported(const GdnArgs& a)
            gdn::aligned16(a.v) && gdn::aligned16(a.o);
 }
 
-size_t gdn_tc_workspace(const Seqs& s, int Hv) { return (size_t)s.slots(gdn::C) * Hv * gdn::REC_BYTES; }
+size_t gdn_tc_workspace(const GdnArgs& a, const Seqs& s, int sms)
+{
+    const int per = gdn::piece_chunks(s, a.Hv, a.Dk, a.Dv, sms);
+    return per ? gdn::pieces_workspace(s, a.Hv, a.Dk, a.Dv, per) : (size_t)s.slots(gdn::C) * a.Hv * gdn::REC_BYTES;
+}
 
 cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st)
 {
+    if (const int per = gdn::piece_chunks(s, a.Hv, a.Dk, a.Dv, sms)) return gdn::launch_pieces(a, s, ws, per, status, st);
     cudaError_t e = cudaSuccess;
     const bool whole = gdn::whole_heads(a, s, sms);
     if (s.tokens() > 0) e = gdn::launch_prologue(a, s, ws, st);

@@ -134,6 +134,10 @@ cudaError_t launch_chain(const GdnArgs& a, const Seqs& s, const void* records, v
 // and the reverse scan (D and dY kept)
 cudaError_t launch_rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st);
 bool whole_heads(const GdnArgs& a, const Seqs& s, int sms);   // which of the two
+// The forward over pieces of long samples: chunks to a piece (0: not worth it), bytes, launch
+int piece_chunks(const Seqs& s, int Hv, int Dk, int Dv, int sms);
+size_t pieces_workspace(const Seqs& s, int Hv, int Dk, int Dv, int per);
+cudaError_t launch_pieces(const GdnArgs& a, const Seqs& s, void* ws, int per, int* status, cudaStream_t st);
 // launch of the forward scan: o and S_T (kept null), or what the backward needs (kept and, if
 // not null, S_T; o unused)
 cudaError_t launch_scan(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int sms, cudaStream_t st);

@@ -87,7 +87,7 @@ struct GdnBwdArgs {
 cudaError_t launch_gdn_recurrent(const GdnArgs& a, const Seqs& s, cudaStream_t st);
 // tensor cores (bf16, Dk = 64 or 128, 16-byte aligned tensors)
 bool gdn_tc_supported(const GdnArgs& a);
-size_t gdn_tc_workspace(const Seqs& s, int Hv);
+size_t gdn_tc_workspace(const GdnArgs& a, const Seqs& s, int sms);
 cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st);
 bool gdn_tc_bwd_supported(const GdnBwdArgs& a);
 size_t gdn_tc_bwd_workspace(const Seqs& s, int Hv, int Dk, int Dv);

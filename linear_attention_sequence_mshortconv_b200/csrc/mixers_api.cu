@@ -127,8 +127,9 @@ size_t gdn_fwd_need(const GdnArgs& a, const Batch& b)
     x.q = x.k = x.v = x.o = nullptr;
     if (!gdn_tc_supported(x)) return 0;
     size_t need = 0;
+    const int sms = num_sms();
     each_group(b, [&](const Seqs& s, int, int64_t) {
-        if (s.tokens() > 0) need = max_of(need, gdn_tc_workspace(s, a.Hv));
+        if (s.tokens() > 0) need = max_of(need, gdn_tc_workspace(a, s, sms));
         return KDA_OK;
     });
     return need;

@@ -394,6 +394,91 @@ def test_many_heads_workspace_of_the_stated_size():
         assert bool((buf[need:] == 0xA5).all())
 
 
+# ---- few heads and long samples: the samples cut into pieces ------------------------------------------------------------
+LONG = [([6000, 0, 70, 3001], 1, 2, 64, 128), ([6107], 2, 2, 128, 64), ([5120, 64], 1, 1, 128, 128), ([9000], 2, 6, 64, 64)]
+PIECES = {"gdn_chain", "gdn_chain_state", "gdn_chain_transition", "gdn_carry"}
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_samples(case):
+    lens, Hk, Hv, Dk, Dv = case
+    x, S0, _, _ = make(lens, Hk, Hv, Dk, Dv, torch.bfloat16, seed=70 + len(lens), g_scale=0.02)
+    cu = R.offsets(lens)
+    ref_o, ref_S = R.gdn(*map(R.f64, x), lens, R.f64(S0))
+    x, S0 = cuda(x), S0.cuda()
+    (o, S), ran = kernels([*PIECES, "gdn_scan"], lambda: gdn.forward_varlen(*x, cu, S0))
+    assert ran == PIECES
+    assert R.norm_error(o, ref_o) <= BF16_TOL and R.norm_error(S, ref_S) <= FP32_TOL
+    o2, none = gdn.forward_varlen(*x, cu, S0, want_state=False)
+    assert none is None and torch.equal(o, o2)
+    need = gdn.varlen_workspace_size(cu, Hk, Hv, Dk, Dv)
+    buf = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    o3, S3 = gdn.forward_varlen(*x, cu, S0, workspace=buf[:need])
+    assert torch.equal(o, o3) and torch.equal(S, S3) and bool((buf[need:] == 0xA5).all())
+    assert kda.last_device_error() == 0
+
+
+@pytest.mark.parametrize("g", [-0.5, -90.0, float("-inf")])
+def test_long_samples_strong_gates(g):
+    lens = [6000]
+    x, S0, _, _ = make(lens, 1, 2, 64, 64, torch.bfloat16, seed=13, g_scale=0.01)
+    x[3][::701] = g
+    ref_o, ref_S = R.gdn(*map(R.f64, x), lens, R.f64(S0))
+    (o, S), ran = kernels(PIECES, lambda: gdn.forward(*[t[None].cuda() for t in x], S0.cuda()))
+    assert ran == PIECES
+    assert R.norm_error(o[0], ref_o) <= BF16_TOL and R.norm_error(S, ref_S) <= FP32_TOL
+
+
+def test_long_samples_without_decay():
+    """No gate closes and every key is one of eight: what the pieces hand on is all there is."""
+    T, D = 6016, 64
+    k = torch.zeros(T, 1, D)
+    at = torch.randint(0, 8, (T,), generator=torch.Generator().manual_seed(3))
+    k[torch.arange(T), 0, at] = 1.0
+    k[:64] = 0.0
+    k[torch.arange(64), 0, torch.arange(64)] = 1.0   # the other keys are written once, in the first chunk
+    v = torch.randn(T, 1, D, generator=torch.Generator().manual_seed(2))
+    x = [t.to(torch.bfloat16) for t in (k, k, v, torch.zeros(T, 1), torch.ones(T, 1))]
+    ref_o, ref_S = R.gdn(*map(R.f64, x), [T])
+    o, S = gdn.forward_varlen(*cuda(x), [0, T])
+    assert R.norm_error(o, ref_o) <= BF16_TOL and R.norm_error(S, ref_S) <= FP32_TOL
+
+
+def test_long_samples_do_not_touch_each_other_nor_the_rows_behind():
+    lens, spare = [6000, 5000, 1], 70
+    x, S0, _, _ = make(lens, 1, 2, 128, 64, torch.bfloat16, seed=4, spare=spare, g_scale=0.02)
+    x, cu, S0 = cuda(x), R.offsets(lens), S0.cuda()
+    want_o, want_S = gdn.forward_varlen(*x, cu, S0)
+    for bad_rows, good in (((6000, 11000), [0, 2]), ((0, 6000), [1, 2])):
+        bad = [t.clone() for t in x]
+        for t in bad:
+            t[bad_rows[0]:bad_rows[1]] = float("nan")
+            t[sum(lens):] = float("nan")
+        o, S = torch.full_like(want_o, 7.0), torch.full_like(want_S, 7.0)
+        gdn.forward_varlen(*bad, cu, S0, o=o, S_T=S)
+        for i in good:
+            assert torch.equal(o[cu[i]:cu[i + 1]], want_o[cu[i]:cu[i + 1]]) and torch.equal(S[i], want_S[i])
+        assert bool((o[sum(lens):] == 7.0).all())
+
+
+def test_long_samples_captured():
+    x, S0, _, _ = make([6000], 2, 2, 64, 64, torch.bfloat16, seed=8, g_scale=0.02)
+    y, S1, _, _ = make([6000], 2, 2, 64, 64, torch.bfloat16, seed=9, g_scale=0.02)
+    static, other = cuda(x) + [S0.cuda()], cuda(y) + [S1.cuda()]
+    call = lambda s: gdn.forward_varlen(*s[:5], [0, 6000], s[5])   # noqa: E731
+    want = call(other)
+    call(static)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(static)
+    for s, t in zip(static, other):
+        s.copy_(t)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, w) for u, w in zip(out, want))
+
+
 # ---- one token per request --------------------------------------------------------------------------------------
 def make_step(n, slots, Hk, Hv, Dk, Dv, dtype, seed=0):
     x, _, _, _ = make([n], Hk, Hv, Dk, Dv, dtype, seed=seed)
