@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
             }
             for (int e = lt; e < 16 * MT * DK / 8; e += LOADERS) {   // the planes of D
                 const int piece = e % (DK / 8), row = e / (DK / 8);
-                const uint32_t off = tile_at<DK>(v0 + row, piece);
+                const uint32_t off = state_at(v0 + row, piece, a.Dv);
                 *(uint4*)(dst + keep.d() + off) = *(const uint4*)(sm + L::DP + row * L::SROW + piece * 16);
                 *(uint4*)(dst + keep.d() + keep.state() + off) = *(const uint4*)(sm + L::DP + (16 * MT + row) * L::SROW + piece * 16);
             }
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(512) gdn_grads_kernel(GdnBwdArgs b, const __gr
                 uint32_t t[2][4];
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    ldsm_t(t[p], base + L::SB + p * DV * DK * 2 + tile_at<DK>(s * 16 + brow, qt * NK + n + bpc));
+                    ldsm_t(t[p], base + L::SB + p * DV * DK * 2 + state_at(s * 16 + brow, qt * NK + n + bpc, DV));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(xq[n + e], g, t[0][2 * e], t[0][2 * e + 1]);
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(512) gdn_grads_kernel(GdnBwdArgs b, const __gr
                 uint32_t t[2][4];
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    ldsm_t(t[p], base + L::SB + p * DV * DK * 2 + tile_at<DK>(s * 16 + brow, qt * NK + n + bpc));
+                    ldsm_t(t[p], base + L::SB + p * DV * DK * 2 + state_at(s * 16 + brow, qt * NK + n + bpc, DV));
 #pragma unroll
                 for (int p = 0; p < 3; ++p)   // U0 D0, U1 D0, U0 D1
 #pragma unroll
@@ -698,7 +698,7 @@ cudaError_t grads(const GdnBwdArgs& a, const Seqs& s, const void* records, const
     auto kern = gdn_grads_kernel<DK, DV>;
     const cudaError_t e = allow_smem<gdn_grads_kernel<DK, DV>>(L::SMEM);
     if (e != cudaSuccess) return e;
-    ProfileScope prof("gdn_grads", st);
+    ProfileScope prof("gdn_grads_narrow", st);
     count_launch();
     kern<<<dim3(s.slots(C), a.f.Hk), L::THREADS, L::SMEM, st>>>(a, s, (const char*)records, (const char*)kept);
     return cudaGetLastError();
@@ -738,14 +738,8 @@ cudaError_t launch_gdn_tc_bwd(const GdnBwdArgs& b, const Seqs& s, void* ws, int 
             : b.f.Dk == 64 ? (wide ? rscan<64, 2>(b, s, records, kept, st) : rscan<64, 1>(b, s, records, kept, st))
                            : (wide ? rscan<128, 2>(b, s, records, kept, st) : rscan<128, 1>(b, s, records, kept, st));
     if (e != cudaSuccess || s.tokens() == 0) return e;
-    switch (b.f.Dk * 1000 + b.f.Dv) {
-        case 64032: return grads<64, 32>(b, s, records, kept, st);
-        case 64064: return grads<64, 64>(b, s, records, kept, st);
-        case 64128: return grads<64, 128>(b, s, records, kept, st);
-        case 128032: return grads<128, 32>(b, s, records, kept, st);
-        case 128064: return grads<128, 64>(b, s, records, kept, st);
-        default: return grads<128, 128>(b, s, records, kept, st);
-    }
+    if (b.f.Dv != 32) return launch_grads(b, s, records, kept, sms, status, st);
+    return b.f.Dk == 64 ? grads<64, 32>(b, s, records, kept, st) : grads<128, 32>(b, s, records, kept, st);
 }
 
 }  // namespace kda

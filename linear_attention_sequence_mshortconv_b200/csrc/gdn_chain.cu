@@ -313,7 +313,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 if (c > 0) wait(s_free, (c - 1) & 1, guard);
 #pragma unroll 1
                 for (int p = 0; p < 2; ++p)
-                    planes_to_tile<DK, HK / 2>(at + L::SP_ + p * (DK / 2) + hf * (HK / 2), sm + L::OUT + p * DV * DK * 2, row, hf * (HK / 8), real,
+                    planes_to_tile<DV, HK / 2>(at + L::SP_ + p * (DK / 2) + hf * (HK / 2), sm + L::OUT + p * DV * DK * 2, row, hf * (HK / 8), real,
                                                p ? 0x80008000u : 0u);
                 fence_async_smem();
                 warp_arrive(s_kept);
@@ -359,7 +359,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             warp_arrive(y_ready + hf);
             if (KEEP) {   // R, and later U, while the next product runs
                 if (c > 0) wait(u_free, (c - 1) & 1, guard);
-                if (real) to_tile<C>(sm + L::OUT_R, row, hf * 4, r[0]);
+                if (real) to_tile<DV>(sm + L::OUT_R, row, hf * 4, r[0]);
             }
             // U, its planes, and decayed
             if (c + 1 < nch) wait(full + ((c + 1) & 1), ((c + 1) >> 1) & 1, guard);
@@ -381,8 +381,8 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             warp_arrive(u_ready + hf);
             if (KEEP) {
                 if (real) {
-                    to_tile<C>(sm + L::OUT_U, row, hf * 4, u[0]);
-                    to_tile<C>(sm + L::OUT_U + DV * C * 2, row, hf * 4, u[1], 0x80008000u);
+                    to_tile<DV>(sm + L::OUT_U, row, hf * 4, u[0]);
+                    to_tile<DV>(sm + L::OUT_U + DV * C * 2, row, hf * 4, u[1], 0x80008000u);
                 }
                 fence_async_smem();
                 warp_arrive(u_kept);

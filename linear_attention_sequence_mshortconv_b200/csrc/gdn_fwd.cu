@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(256 * MT) gdn_scan_kernel(GdnArgs a, const __g
                 char* dst = kept + ((int64_t)(seqs.slot0(seq, C) + c) * a.Hv + h) * keep.bytes();
                 for (int e = lt; e < SPL * 16 * MT * DK / 8; e += LOADERS) {
                     const int piece = e % (DK / 8), row = e / (DK / 8) % (16 * MT), p = e / (DK / 8) / (16 * MT);
-                    *(uint4*)(dst + keep.s() + p * keep.state() + tile_at<DK>(v0 + row, piece)) =
+                    *(uint4*)(dst + keep.s() + p * keep.state() + state_at(v0 + row, piece, a.Dv)) =
                         *(const uint4*)(sm + L::SP + (p * 16 * MT + row) * L::SROW + piece * 16);
                 }
 #pragma unroll

@@ -311,7 +311,7 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             // while K D runs, the planes to where they are copied from
 #pragma unroll 1
             for (int p = 0; p < 2; ++p)
-                planes_to_tile<DK, HK / 2>(at + L::DP + p * (DK / 2) + hf * (HK / 2), sm + L::OUT_D + p * DV * DK * 2, row, hf * (HK / 8), real,
+                planes_to_tile<DV, HK / 2>(at + L::DP + p * (DK / 2) + hf * (HK / 2), sm + L::OUT_D + p * DV * DK * 2, row, hf * (HK / 8), real,
                                            p ? 0x80008000u : 0u);
             fence_async_smem();
             warp_arrive(d_kept);
@@ -359,8 +359,8 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             scale32(x, scal + 2 * C + hf * 32);
             warp_arrive(empty + (it & 1));
             if (real) {
-                to_tile<C>(sm + L::OUT_Y, row, hf * 4, p[0]);
-                to_tile<C>(sm + L::OUT_Y + DV * C * 2, row, hf * 4, p[1], 0x80008000u);
+                to_tile<DV>(sm + L::OUT_Y, row, hf * 4, p[0]);
+                to_tile<DV>(sm + L::OUT_Y + DV * C * 2, row, hf * 4, p[1], 0x80008000u);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const uint32_t v = pack(x[2 * i], x[2 * i + 1]);

@@ -84,6 +84,12 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece)
 {
     return row * (2 * W) + ((piece ^ (W == 32 ? (row >> 1) & 3 : row & 7)) << 4);
 }
+// A tile of a state, `rows` rows of W values: panels of 64 values, a row of a panel 128 bytes, its pieces
+// permuted as above (the 128-byte swizzle of the copy engine and of tcgen05's operands).
+__device__ __forceinline__ uint32_t state_at(int row, int piece, int rows)
+{
+    return ((piece >> 3) * rows + row) * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
 template <int W, int THREADS, int ROWS = C>
 __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16* src, int64_t row_stride, int valid, int tid)
 {
@@ -109,7 +115,8 @@ __host__ __device__ constexpr int blk(int ib, int jb) { return (ib + (jb ? 2 + 2
 
 // What the backward keeps of each chunk and value head, bf16: the entry state S^T and the
 // gradient D^T of the exit state, [Dv][Dk] in two planes each; U^T, [Dv][64] in two planes, R^T,
-// [Dv][64], and dY^T, [Dv][64] in two planes; every plane as the tile (tile_at) that the gradients' kernel reads.
+// [Dv][64], and dY^T, [Dv][64] in two planes; every plane as the tile (state_at; of 64 values tile_at, which is
+// the same) that the gradients' kernel reads.
 struct Kept {
     int Dk, Dv;
     __host__ __device__ size_t state() const { return (size_t)Dv * Dk * 2; }     // bytes of a plane
@@ -133,6 +140,8 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 cudaError_t launch_chain(const GdnArgs& a, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st);
 // and the reverse scan (D and dY kept)
 cudaError_t launch_rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st);
+// the gradients of q, k, g and beta (Dv = 64 or 128)
+cudaError_t launch_grads(const GdnBwdArgs& b, const Seqs& s, const void* records, const void* kept, int sms, int* status, cudaStream_t st);
 bool whole_heads(const GdnArgs& a, const Seqs& s, int sms);   // which of the two
 // The forward over pieces of long samples: chunks to a piece (0: not worth it), bytes, launch
 int piece_chunks(const Seqs& s, int Hv, int Dk, int Dv, int sms);

@@ -47,17 +47,17 @@ __device__ __forceinline__ void scale32(float (&x)[32], const float* f)
         x[i] *= v.x; x[i + 1] *= v.y; x[i + 2] *= v.z; x[i + 3] *= v.w;
     }
 }
-// 32 bf16 values of a row, to a tile (sign: 0x80008000 to negate them)
-template <int W>
+// 32 bf16 values of a row, to a tile of ROWS rows (sign: 0x80008000 to negate them)
+template <int ROWS>
 __device__ __forceinline__ void to_tile(char* tile, int row, int piece, const uint32_t (&p)[16], uint32_t sign = 0)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *(uint4*)(tile + tile_at<W>(row, piece + i)) =
+        *(uint4*)(tile + state_at(row, piece + i, ROWS)) =
             make_uint4(p[4 * i] ^ sign, p[4 * i + 1] ^ sign, p[4 * i + 2] ^ sign, p[4 * i + 3] ^ sign);
 }
-// COLS columns of planes that the thread has put into tensor memory, to a tile of rows of W values
-template <int W, int COLS>
+// COLS columns of planes that the thread has put into tensor memory, to a tile of ROWS rows
+template <int ROWS, int COLS>
 __device__ __forceinline__ void planes_to_tile(uint32_t taddr, char* tile, int row, int piece, bool real, uint32_t sign)
 {
 #pragma unroll
@@ -67,7 +67,7 @@ __device__ __forceinline__ void planes_to_tile(uint32_t taddr, char* tile, int r
         tmem_ld16(taddr + i * 16, x);
 #pragma unroll
         for (int j = 0; j < 16; ++j) p[j] = __float_as_uint(x[j]);
-        if (real) to_tile<W>(tile, row, piece + i * 4, p, sign);
+        if (real) to_tile<ROWS>(tile, row, piece + i * 4, p, sign);
     }
 }
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes)
