@@ -8,13 +8,17 @@
 // and all operands lie as the copy engine brought them: what is kept of a chunk (S, D, U, dY) has its rows (value
 // columns) as K.  Only N and beta M are written by the threads, two planes each.
 //
+// The other part of dbeta, sum_j M_ij k_i.k_j, is k_i . (beta M K)_i / beta_i; so that this holds for beta = 0 as well,
+// betas below 2^-24 count as 2^-24 in beta M (less than the planes' rounding), and as themselves in dK's row part.
+//
 // One CTA per SM takes chunks of key heads in turn, and the value heads of each one after another.
 //
-//   warps 0-15 (four warpgroups) E1 -> N, E2 -> beta M and its part of dbeta; dY . R; <S, D>; then all
-//              sums over the key channels, a channel a lane, 16 tokens a warpgroup
-//   warp 16    issues the MMAs
-//   warp 17    the loads: S and then D share a buffer; each goes on as soon as its buffer is free, into the next
-//              head and chunk
+//   warps 0-3   E1 -> N, E2 -> beta M; then dY . R and <S, D>
+//   warps 4-19  (four warpgroups) the sums over the key channels, a channel a lane, 16 tokens a warpgroup;
+//               these and the first four warps are a head apart
+//   warp 20     issues the MMAs
+//   warp 21     the loads: S and then D share a buffer; each goes on as soon as its buffer is free, into the
+//               next head and chunk
 //
 // What bounds it: the tiles of a chunk and value head are 208 KB at Dk = Dv = 128, 0.14 ms of HBM at the image stream.
 //
@@ -28,8 +32,7 @@ namespace {
 
 template <int DK, int DV>
 struct TGrads {
-    static constexpr int THREADS = 576;
-    // (Q before K: with the rows of K as the lower half of a product's, the upper half reads Q's panels)
+    static constexpr int THREADS = 704;
     static constexpr int Q_ = 0, K_ = Q_ + DK / 64 * PANEL;
     static constexpr int SD = K_ + DK / 64 * PANEL;          // planes of S^T, then of D^T [2][DK / 64][DV][64]
     static constexpr int U_ = SD + 2 * DV * DK * 2;          // planes of U^T [2][DV][64]
@@ -37,8 +40,9 @@ struct TGrads {
     static constexpr int G_ = Y_ + 2 * DV * C * 2;           // dO
     static constexpr int N_ = G_ + DV / 64 * PANEL;          // planes of N^T [2][64][64], then of beta M^T
     static constexpr int SC = N_ + 4 * PANEL;                // grow, end, beta, cum, of two heads
-    static constexpr int RED = SC + 2 * 5 * C * 4;               // fp32: dY.R [16][64], dbeta [2][64], dcum [4][64], exit [16]
-    static constexpr int BAR = RED + 22 * C * 4 + 64;
+    static constexpr int RED = SC + 2 * 5 * C * 4;               // fp32: of two heads dY.R [4][64] and <S, D> [4]; dbeta [4][64], dcum [4][64], exit [16]
+    static constexpr int RY = 4 * C + 4, DB = 2 * RY, DC = DB + 4 * C, EX = DC + 4 * C;
+    static constexpr int BAR = RED + (EX + 16) * 4;
     static constexpr int SMEM = BAR + 256 + 1024 > 116 * 1024 ? BAR + 256 + 1024 : 116 * 1024;   // one CTA to an SM
     static constexpr int XQ = 0, XR = 64, XC = 128, CC = 192, NK = 256, MK = 320, E1 = 384, E2 = 448;   // tensor memory
 };
@@ -57,17 +61,20 @@ __device__ __forceinline__ float transpose_sum(float (&v)[16], int lane)
     }
     return v[0] + __shfl_xor_sync(~0u, v[0], 16);
 }
-__device__ __forceinline__ void load16(float (&x)[16], const float* f)
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
 {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        const float4 v = *(const float4*)(f + i);
-        x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ float at_least(float beta) { return fabsf(beta) < 5.9604644775390625e-8f ? 5.9604644775390625e-8f : beta; }
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(576, 1)
+__global__ void __launch_bounds__(704, 1)
 gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
                   const __grid_constant__ CUtensorMap mdq, const __grid_constant__ CUtensorMap mdk, GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, const char* kept, int* status)
 {
@@ -78,7 +85,7 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     const uint32_t base = smem_addr(sm);
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
     uint64_t *kq_full = bars, *kq_empty = bars + 1, *y_full = bars + 2, *y_empty = bars + 3, *s_full = bars + 4, *s_done = bars + 5;
-    uint64_t *d_full = bars + 6, *d_empty = bars + 7, *landed = bars + 8, *e_done = bars + 9, *kk_done = bars + 10, *kk_read = bars + 11;
+    uint64_t *d_full = bars + 6, *d_empty = bars + 7, *landed = bars + 8, *e_done = bars + 9, *ry_ready = bars + 10, *sum_free = bars + 11;
     uint64_t *nm_ready = bars + 12, *out_done = bars + 13, *acc_free = bars + 14, *drain = bars + 15, *u_full = bars + 16, *u_empty = bars + 17;
     uint32_t* tm_ptr = (uint32_t*)(bars + 18);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
@@ -87,17 +94,18 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     const int r = a.Hv / a.Hk, items = seqs.slots(C) * a.Hk;
     const Kept keep{DK, DV};
 
-    if (warp == 17) {
+    if (warp == 21) {
         if (lane == 0) {
-            for (uint64_t* x : {kq_full, y_full, u_full, u_empty, s_full, s_done, d_full, landed, e_done, kk_done, out_done, drain}) mbar_init(x, 1);
-            for (uint64_t* x : {kq_empty, y_empty, d_empty}) mbar_init(x, 17);   // the MMAs and warps 0-15
-            for (uint64_t* x : {nm_ready, acc_free}) mbar_init(x, 16);
-            mbar_init(kk_read, 8);
+            for (uint64_t* x : {kq_full, y_full, u_full, u_empty, s_full, s_done, d_full, landed, e_done, drain}) mbar_init(x, 1);
+            for (uint64_t* x : {y_empty, d_empty, out_done}) mbar_init(x, 5);   // the MMAs and warps 0-3
+            mbar_init(kq_empty, 2);                                             // the MMAs, and dq and dk out of the same place
+            for (uint64_t* x : {nm_ready, ry_ready}) mbar_init(x, 4);
+            for (uint64_t* x : {acc_free, sum_free}) mbar_init(x, 16);
             *guard.flag = 0;
             fence_mbar_init();
             fence_async_smem();
         }
-    } else if (warp == 16) {
+    } else if (warp == 20) {
         tmem_alloc(tm_ptr, 512);
         tmem_relinquish();
     }
@@ -107,7 +115,7 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     const uint32_t tmem = *tm_ptr;
     int n = 0, hd = 0;   // chunks and value heads so far
 
-    if (warp == 17) {
+    if (warp == 21) {
         int ragged = 0, kq_in = 0, y_in = 0, u_in = 0, s_in = 0, d_in = 0;   // copies issued
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             int seq, c;
@@ -192,14 +200,13 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             if (s_in > 0) mbar_wait_bounded(s_full, (s_in - 1) & 1, kWaitNs);
             if (d_in > 0) mbar_wait_bounded(d_full, (d_in - 1) & 1, kWaitNs);
         }
-    } else if (warp == 16) {
+    } else if (warp == 20) {
         constexpr uint32_t id_rows = idesc_f16(128, C, true, false, false, true);    // right operand: its values are K
         constexpr uint32_t id_cols = idesc_f16(128, C, true, true, false, true);     // its rows are K
-        constexpr uint32_t id_kk = idesc_f16(128, 32, false, false, false, true);
         constexpr int ST = DV * 128, KV = DV / 16;   // bytes of a panel of S, k-steps of the value columns
         const uint64_t ds = desc_cols(base + L::SD, ST), du = desc_cols(base + L::U_, ST), dy = desc_cols(base + L::Y_, ST);
         const uint64_t dg = desc_rows(base + L::G_), dkc = desc_cols(base + L::K_, PANEL), dqc = desc_cols(base + L::Q_, PANEL);
-        const uint64_t dnc = desc_cols(base + L::N_, PANEL), dnr = desc_rows(base + L::N_), dk = desc_rows(base + L::K_);
+        const uint64_t dnc = desc_cols(base + L::N_, PANEL), dnr = desc_rows(base + L::N_);
         constexpr int S1 = DV * DK * 2 >> 4, U1 = DV * C * 2 >> 4, P1 = PANEL >> 4;   // second planes
         // products of planes 0 0, 0 1 and (all) 1 0, their rows as K; `left1` and U1: the second planes
         auto planes = [&](uint32_t to, uint64_t left, uint64_t right, int left1, bool all) {
@@ -233,43 +240,28 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 tc_fence_after();
                 if (elect()) {
                     planes(tmem + L::XR, ds, dy, S1, true);
-                }
-                if (i == 0) {   // K K^T: columns 0-31 for rows 0-63, 32-63 for rows 64-127, where the threads want them
-                    wait(kq_full, n & 1, guard);
-                    tc_fence_after();
-                    if (elect()) {
-#pragma unroll 1
-                        for (int z = 0; z < 2; ++z)
-#pragma unroll
-                            for (int x = 0; x < DK / 16; ++x)
-                                umma_f16(tmem + L::XQ + 32 * z, step_rows(dk - z * P1, x, PANEL), step_rows(dk + (z * 4096 >> 4), x, PANEL), id_kk, x > 0);
-                        umma_commit(kk_done);
-                    }
-                    wait(kk_read, n & 1, guard);
-                    tc_fence_after();
-                }
-                if (elect()) {
                     by_dout(tmem + L::XQ, ds, 2);
                     umma_commit(s_done);
                     umma_commit(y_empty);
                 }
+                if (i == 0) wait(kq_full, n & 1, guard);
                 wait(nm_ready, hd & 1, guard);
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll 1
-                    for (int p = 0; p < 2; ++p)
+                    for (int m = 0; m < 2; ++m)   // NK, MK
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            umma_f16(tmem + L::NK, step_cols(dkc, x), step_cols(dnc + p * P1, x), id_cols, p + x > 0);
-                            umma_f16(tmem + L::MK, step_cols(dkc, x), step_cols(dnc + (2 + p) * P1, x), id_cols, p + x > 0);
-                        }
+                        for (int p = 0; p < 2; ++p)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                umma_f16(tmem + L::NK + 64 * m, step_cols(dkc, x), step_cols(dnc + (2 * m + p) * P1, x), id_cols, p + x > 0);
 #pragma unroll 1
-                    for (int p = 0; p < 2; ++p)
+                    for (int m = 1; m >= 0; --m)   // CC: K by beta M, Q by N
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            umma_f16(tmem + L::CC, step_cols(dkc, x), step_rows(dnr + (2 + p) * P1, x, PANEL), id_rows, p + x > 0);
-                            umma_f16(tmem + L::CC, step_cols(dqc, x), step_rows(dnr + p * P1, x, PANEL), id_rows, 1);
-                        }
+                        for (int p = 0; p < 2; ++p)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                umma_f16(tmem + L::CC, step_cols(m ? dkc : dqc, x), step_rows(dnr + (2 * m + p) * P1, x, PANEL), id_rows, (1 - m) + p + x > 0);
                 }
                 wait(d_full, hd & 1, guard);
                 tc_fence_after();
@@ -287,222 +279,249 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             if (elect()) umma_commit(drain);
             mbar_wait_bounded(drain, 0, kWaitNs);
         }
-    } else {
-        // Warpgroup g: of the pairs, N (0, 1) or M (2, 3), columns 16 z .. of either half of the tokens; of the
-        // sums over the channels, tokens 16 g ..
-        const int g = warp >> 2, m = g >> 1, w4 = warp & 3, row = tid & 127, j = row & 63, own = 32 * (w4 >> 1) + 16 * (g & 1), other = own ^ 32;
-        const uint32_t at = tmem + ((uint32_t)w4 * 32u << 16);
+    } else if (warp < 4) {
+        const int j = tid & 63, own = 32 * (warp >> 1);   // token of U, and 32 of the others
+        const uint32_t at = tmem + ((uint32_t)warp * 32u << 16);
+        char *sums = sm + L::N_ + tid * 128, *theirs = sm + L::N_ + (tid ^ 64) * 128;   // 128 rows of 32 sums, twice
         float* red = (float*)(sm + L::RED);
-        const bool real = row < DK;
-        const int ch = (DK > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2, pc = (row & 63) >> 3;   // a channel's column of K and Q
-        char* planes = sm + L::N_ + m * 2 * PANEL;            // N's or beta M's
-        char* sums = sm + L::N_ + g * PANEL;                  // before them, 128 x 16 sums
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+            int seq, c;
+            if (!seqs.locate(item / a.Hk, C, seq, c)) continue;
+            const int hk = item % a.Hk;
+            for (int i = 0; i < r; ++i, ++hd) {
+                const float* scal = (const float*)(sm + L::SC + (hd & 1) * 5 * C * 4);
+                const char* mine = kept + ((int64_t)(item / a.Hk) * a.Hv + hk * r + i) * keep.bytes();
+                float x[32];
+                if (hd > 0) wait(out_done, (hd - 1) & 1, guard);   // the planes have been read
+                wait(y_full, hd & 1, guard);
+                wait(e_done, hd & 1, guard);
+                tc_fence_after();
+                // The planes' sums: each of the two threads of a token hands over the columns that are not its own.
+#pragma unroll 1
+                for (int m = 0; m < 2; ++m) {
+                    tmem_ld32(at + L::E1 + 64 * m + (own ^ 32), x);
+#pragma unroll
+                    for (int z = 0; z < 8; ++z)
+                        *(float4*)(sums + m * 2 * PANEL + ((z ^ (tid & 7)) << 4)) = make_float4(x[4 * z], x[4 * z + 1], x[4 * z + 2], x[4 * z + 3]);
+                }
+                bar_sync(1, 128);
+                const float hj = scal[3 * C + j], lj = scal[4 * C + j];
+#pragma unroll 1
+                for (int m = 0; m < 2; ++m) {   // N, beta M
+                    tmem_ld32(at + L::E1 + 64 * m + own, x);
+#pragma unroll
+                    for (int z = 0; z < 32; z += 4) {
+                        const float4 v = *(const float4*)(theirs + m * 2 * PANEL + (((z >> 2) ^ (tid & 7)) << 4));
+                        const float4 hi = *(const float4*)&scal[3 * C + own + z], li = *(const float4*)&scal[4 * C + own + z], be = *(const float4*)&scal[2 * C + own + z];
+                        const float vv[4] = {v.x, v.y, v.z, v.w}, hh[4] = {hi.x, hi.y, hi.z, hi.w}, ll[4] = {li.x, li.y, li.z, li.w}, bb[4] = {be.x, be.y, be.z, be.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float d = ex2_approx((hh[e] - hj) + (ll[e] - lj));
+                            x[z + e] = j + m <= own + z + e ? (m ? -at_least(bb[e]) : 1.f) * (d * (x[z + e] + vv[e])) : 0.f;
+                        }
+                    }
+                    bar_sync(1, 128);   // the sums have been read: the planes take their place
+                    uint32_t p[2][16];
+                    planes_of<2>(x, p);
+                    to_tile<C>(sm + L::N_ + m * 2 * PANEL, j, own / 8, p[0]);
+                    to_tile<C>(sm + L::N_ + m * 2 * PANEL + PANEL, j, own / 8, p[1], 0x80008000u);
+                }
+                tc_fence_before();
+                fence_async_smem();
+                warp_arrive(nm_ready);
+                warp_arrive(out_done);   // (whoever waits for it sees the gates as well)
+                // dY . R: 8 tokens a thread, its rows strided by 16
+                {
+                    const int row = tid >> 3, piece = tid & 7;
+                    float acc[8] = {};
+#pragma unroll 1
+                    for (int z0 = 0; z0 < DV / 16; z0 += 4) {
+                        uint4 rr[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) rr[z] = __ldcg((const uint4*)(mine + keep.r() + tile_at<C>(row + 16 * (z0 + z), piece)));
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const uint32_t off = L::Y_ + tile_at<C>(row + 16 * (z0 + z), piece);
+                            const uint4 y0 = *(const uint4*)(sm + off), y1 = *(const uint4*)(sm + DV * C * 2 + off);
+                            const uint32_t rv[4] = {rr[z].x, rr[z].y, rr[z].z, rr[z].w}, a0[4] = {y0.x, y0.y, y0.z, y0.w}, a1[4] = {y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                acc[2 * e] = fmaf(low(a0[e]) + low(a1[e]), low(rv[e]), acc[2 * e]);
+                                acc[2 * e + 1] = fmaf(high(a0[e]) + high(a1[e]), high(rv[e]), acc[2 * e + 1]);
+                            }
+                        }
+                    }
+                    warp_arrive(y_empty);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        acc[e] += __shfl_xor_sync(~0u, acc[e], 8);
+                        acc[e] += __shfl_xor_sync(~0u, acc[e], 16);
+                        if (lane < 8) red[(hd & 1) * L::RY + warp * C + piece * 8 + e] = acc[e];
+                    }
+                }
+                // <S, D>, 16 bytes of each plane a thread and round; S once more from L2
+                {
+                    constexpr int PIECES = DV * DK * 2 / (128 * 16), NB = 2;
+                    const char *s = mine + keep.s() + tid * 16, *d = sm + L::SD + tid * 16;
+                    float ex = 0.f;
+                    uint4 sp[2][NB];
+                    auto fetch = [&](int i0) {
+#pragma unroll
+                        for (int z = 0; z < NB; ++z) {
+                            sp[0][z] = __ldcg((const uint4*)(s + (i0 + z) * 2048));
+                            sp[1][z] = __ldcg((const uint4*)(s + keep.state() + (i0 + z) * 2048));
+                        }
+                    };
+                    fetch(0);
+                    wait(d_full, hd & 1, guard);
+#pragma unroll 1
+                    for (int i0 = 0; i0 < PIECES; i0 += NB) {
+                        uint4 now[2][NB];
+#pragma unroll
+                        for (int z = 0; z < NB; ++z) {
+                            now[0][z] = sp[0][z];
+                            now[1][z] = sp[1][z];
+                        }
+                        if (i0 + NB < PIECES) fetch(i0 + NB);
+#pragma unroll
+                        for (int z = 0; z < NB; ++z) {
+                            const uint4 d0 = *(const uint4*)(d + (i0 + z) * 2048), d1 = *(const uint4*)(d + DV * DK * 2 + (i0 + z) * 2048);
+                            const uint32_t ss[2][4] = {{now[0][z].x, now[0][z].y, now[0][z].z, now[0][z].w}, {now[1][z].x, now[1][z].y, now[1][z].z, now[1][z].w}};
+                            const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                ex = fmaf(low(dd[0][e]) + low(dd[1][e]), low(ss[0][e]) + low(ss[1][e]),
+                                          fmaf(high(dd[0][e]) + high(dd[1][e]), high(ss[0][e]) + high(ss[1][e]), ex));
+                        }
+                    }
+                    warp_arrive(d_empty);
+                    ex *= scal[C - 1];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) ex += __shfl_xor_sync(~0u, ex, o);
+                    if (lane == 0) red[(hd & 1) * L::RY + 4 * C + warp] = ex;
+                }
+                if (hd > 0) wait(sum_free, (hd - 1) & 1, guard);   // two heads' sums at most are on their way
+                warp_arrive(ry_ready);
+            }
+            ++n;
+        }
+    } else {
+        const int tok = 16 * ((warp - 4) >> 2), w4 = warp & 3, row = tid & 127;   // 16 tokens from tok on, channel
+        const uint32_t at = tmem + ((uint32_t)w4 * 32u << 16) + tok;
+        float* red = (float*)(sm + L::RED);
+        const bool real = DK == 128 || row < DK;
+        char* ch = sm + (DK > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2;   // the channel's column of Q and K
+        const int pc = (row & 63) >> 3;
+        auto value = [&](int tile, int t) { return __uint_as_float((uint32_t)*(const uint16_t*)(ch + tile + piece_at(tok + t, pc)) << 16); };
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             int seq, c;
             if (!seqs.locate(item / a.Hk, C, seq, c)) continue;
             const int hk = item % a.Hk, valid = min(C, seqs.len(seq) - c * C);
             const int64_t t0 = (int64_t)seqs.start(seq) + c * C;
-            float sq[16] = {}, sk[16] = {}, kk[16] = {};
+            float sq[16] = {}, sk[16] = {};
+            wait(kq_full, n & 1, guard);
             for (int i = 0; i < r; ++i, ++hd) {
                 const int h = hk * r + i;
-                const float* scal = (const float*)(sm + L::SC + (hd & 1) * 5 * C * 4);
-                const char* mine = kept + ((int64_t)(item / a.Hk) * a.Hv + h) * keep.bytes();
-                // dY . R: 8 tokens a thread, its rows strided by 64
-                {
-                    uint4 rr[DV / 64];
-                    const int at_row = tid >> 3, piece = tid & 7;
-#pragma unroll
-                    for (int z = 0; z < DV / 64; ++z) rr[z] = __ldcg((const uint4*)(mine + keep.r() + tile_at<C>(at_row + 64 * z, piece)));
-                    wait(y_full, hd & 1, guard);
-                    float acc[8] = {};
-#pragma unroll
-                    for (int z = 0; z < DV / 64; ++z) {
-                        const uint4 y0 = *(const uint4*)(sm + L::Y_ + tile_at<C>(at_row + 64 * z, piece));
-                        const uint4 y1 = *(const uint4*)(sm + L::Y_ + DV * C * 2 + tile_at<C>(at_row + 64 * z, piece));
-                        const uint32_t rv[4] = {rr[z].x, rr[z].y, rr[z].z, rr[z].w}, a0[4] = {y0.x, y0.y, y0.z, y0.w}, a1[4] = {y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            acc[2 * e] = fmaf(low(a0[e]) + low(a1[e]), low(rv[e]), acc[2 * e]);
-                            acc[2 * e + 1] = fmaf(high(a0[e]) + high(a1[e]), high(rv[e]), acc[2 * e + 1]);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        acc[e] += __shfl_xor_sync(~0u, acc[e], 8);
-                        acc[e] += __shfl_xor_sync(~0u, acc[e], 16);
-                        if (lane < 8) red[warp * C + piece * 8 + e] = acc[e];
-                    }
-                    warp_arrive(y_empty);
-                }
-                if (i == 0 && m) {
-                    wait(kk_done, n & 1, guard);
-                    tc_fence_after();
-                    tmem_ld16(at + L::XQ + own, kk);
-                    tc_fence_before();
-                    warp_arrive(kk_read);
-                }
-                if (i == 0) {   // dq and dk of the chunk before have been read from where the sums go
-                    if (tid == 0) bulk_wait_read0();
-                    bar_sync(3, 512);
-                }
-                // E: token j of U, 16 of the other tokens.  The planes' sums: each of the two threads of a token hands
-                // over the columns that are not its own.
-                wait(e_done, hd & 1, guard);
-                tc_fence_after();
-                float x[16];
-                const uint32_t e = at + (m ? L::E2 : L::E1);
-                tmem_ld16(e + other, x);
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    *(float4*)(sums + row * 64 + ((z ^ ((row >> 1) & 3)) << 4)) = make_float4(x[4 * z], x[4 * z + 1], x[4 * z + 2], x[4 * z + 3]);
-                tmem_ld16(e + own, x);
-                bar_sync(1 + m, 256);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const float4 v = *(const float4*)(sums + (row ^ 64) * 64 + ((z ^ ((row >> 1) & 3)) << 4));
-                    x[4 * z] += v.x; x[4 * z + 1] += v.y; x[4 * z + 2] += v.z; x[4 * z + 3] += v.w;
-                }
-                {
-                    float hi[16], li[16];
-                    load16(hi, scal + 3 * C + own);
-                    load16(li, scal + 4 * C + own);
-                    const float hj = scal[3 * C + j], lj = scal[4 * C + j];
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const float d = ex2_approx((hi[t] - hj) + (li[t] - lj));
-                        x[t] = m ? (j < own + t ? -d * x[t] : 0.f) : (j <= own + t ? d * x[t] : 0.f);
-                    }
-                }
-                if (m) {   // M: its part of dbeta, then beta M
-                    float v[16];
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) v[t] = j < own + t ? x[t] * kk[t] : 0.f;
-                    const float s = transpose_sum(v, lane);
-                    if (lane < 16) red[(16 + (w4 & 1)) * C + own + lane] = s;
-                    load16(v, scal + 2 * C + own);
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) x[t] *= v[t];
-                }
-                bar_sync(1 + m, 256);   // the sums have been read: the planes take their place
-                {
-                    uint32_t p[2][8];
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        uint32_t w[2];
-                        split<2>(x[2 * t], x[2 * t + 1], w);
-                        p[0][t] = w[0];
-                        p[1][t] = w[1];
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int z = 0; z < 2; ++z)
-                            *(uint4*)(planes + q * PANEL + piece_at(j, (own >> 3) + z)) = make_uint4(p[q][4 * z], p[q][4 * z + 1], p[q][4 * z + 2], p[q][4 * z + 3]);
-                }
-                tc_fence_before();
-                fence_async_smem();
-                warp_arrive(nm_ready);
-                // <S, D>, 16 bytes of each plane a thread and round; S once more from L2
-                float ex = 0.f;
-                {
-                    constexpr int PIECES = DV * DK * 2 / (512 * 16);
-                    const char *s = mine + keep.s() + tid * 16, *d = sm + L::SD + tid * 16;
-                    uint4 sp[2][PIECES];
-#pragma unroll
-                    for (int z = 0; z < PIECES; ++z) {
-                        sp[0][z] = __ldcg((const uint4*)(s + z * 8192));
-                        sp[1][z] = __ldcg((const uint4*)(s + keep.state() + z * 8192));
-                    }
-                    wait(d_full, hd & 1, guard);
-#pragma unroll
-                    for (int z = 0; z < PIECES; ++z) {
-                        const uint4 d0 = *(const uint4*)(d + z * 8192), d1 = *(const uint4*)(d + DV * DK * 2 + z * 8192);
-                        const uint32_t ss[2][4] = {{sp[0][z].x, sp[0][z].y, sp[0][z].z, sp[0][z].w}, {sp[1][z].x, sp[1][z].y, sp[1][z].z, sp[1][z].w}};
-                        const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            ex = fmaf(low(dd[0][y]) + low(dd[1][y]), low(ss[0][y]) + low(ss[1][y]),
-                                      fmaf(high(dd[0][y]) + high(dd[1][y]), high(ss[0][y]) + high(ss[1][y]), ex));
-                    }
-                    ex *= scal[C - 1];
-                }
-                warp_arrive(d_empty);
-                // channel `row`, 16 tokens
-                if (i == 0) wait(kq_full, n & 1, guard);
+                const float* scal = (const float*)(sm + L::SC + (hd & 1) * 5 * C * 4) + tok;
+                float ex = 0.f, dc[16], db[16];
                 wait(out_done, hd & 1, guard);
                 tc_fence_after();
-                const int tok = 16 * g;
-                float dc[16];
+#pragma unroll
+                for (int z = 0; z < 16; z += 8) {
+                    float u[8], v[8];
+                    // row part of dK: (beta M) K - beta e^cum o (dY S^T), and k . (beta M K)
+                    tmem_ld8(at + L::XR + z, u);
+                    tmem_ld8(at + L::MK + z, v);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        const float be = scal[2 * C + z + t];
+                        const float k = real ? value(L::K_, z + t) : 0.f, mk = real ? v[t] : 0.f;
+                        const float f = real ? fmaf(-be * scal[z + t], u[t], at_least(be) == be ? mk : mk * (be * 16777216.f)) : 0.f;   // (2^24)
+                        sk[z + t] += f;
+                        dc[z + t] = k * f;
+                        db[z + t] = k * mk;
+                    }
+                }
                 {
-                    float u[16], v[16], f[16], k[16];
-                    auto value = [&](int tile, int t) { return __uint_as_float((uint32_t)*(const uint16_t*)(sm + tile + ch + piece_at(tok + t, pc)) << 16); };
+                    const float s = transpose_sum(db, lane);
+                    if (lane < 16) red[L::DB + w4 * C + tok + lane] = s / at_least(scal[2 * C + lane]);
+                }
+#pragma unroll
+                for (int z = 0; z < 16; z += 8) {
+                    float u[8], v[8];
                     // dQ = e^cum o (dO S^T) + N K
-                    tmem_ld16(at + L::XQ + tok, u);
-                    tmem_ld16(at + L::NK + tok, v);
-                    load16(f, scal + tok);
+                    tmem_ld8(at + L::XQ + z, u);
+                    tmem_ld8(at + L::NK + z, v);
 #pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const float w = fmaf(f[t], u[t], v[t]);
-                        sq[t] += w;
-                        dc[t] = real ? value(L::Q_, t) * w : 0.f;
-                    }
-                    // row part of dK: (beta M) K - beta e^cum o (dY S^T)
-                    load16(k, scal + 2 * C + tok);
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        f[t] *= -k[t];
-                        k[t] = value(L::K_, t);
-                    }
-                    tmem_ld16(at + L::XR + tok, u);
-                    tmem_ld16(at + L::MK + tok, v);
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const float w = fmaf(f[t], u[t], v[t]);
-                        sk[t] += w;
-                        if (real) dc[t] = fmaf(k[t], w, dc[t]);
+                    for (int t = 0; t < 8; ++t) {
+                        const float f = real ? fmaf(scal[z + t], u[t], v[t]) : 0.f;
+                        sq[z + t] += f;
+                        if (real) dc[z + t] = fmaf(value(L::Q_, z + t), f, dc[z + t]);
                     }
                     // column part: e^{cum_C - cum} o (U D^T) + (beta M)^T K + N^T Q
-                    tmem_ld16(at + L::XC + tok, u);
-                    tmem_ld16(at + L::CC + tok, v);
-                    tc_fence_before();
-                    warp_arrive(acc_free);
-                    load16(f, scal + C + tok);
+                    tmem_ld8(at + L::XC + z, u);
+                    tmem_ld8(at + L::CC + z, v);
+                    if (z == 8) {
+                        tc_fence_before();
+                        warp_arrive(acc_free);
+                    }
 #pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const float y = f[t] * u[t], w = y + v[t];
-                        sk[t] += w;
-                        if (real) {
-                            ex = fmaf(k[t], y, ex);
-                            dc[t] = fmaf(-k[t], w, dc[t]);
-                        }
+                    for (int t = 0; t < 8; ++t) {
+                        const float k = real ? value(L::K_, z + t) : 0.f, g = real ? scal[C + z + t] * u[t] : 0.f, f = real ? g + v[t] : 0.f;
+                        sk[z + t] += f;
+                        ex = fmaf(k, g, ex);
+                        dc[z + t] = fmaf(-k, f, dc[z + t]);
                     }
                 }
-                if (i + 1 == r) warp_arrive(kq_empty);
-                const float s = transpose_sum(dc, lane);
-                if (lane < 16) red[(18 + w4) * C + tok + lane] = s;
+                if (i + 1 == r) {   // dq and dk take the place of Q and K, which no one else reads any more
+                    if (real)
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) ex += __shfl_xor_sync(~0u, ex, o);
-                if (lane == 0) red[22 * C + warp] = ex;
-                if (i + 1 == r && real) {   // dq and dk, as tiles in the place of N and M
-                    const int col = (DK > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2;
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        *(__nv_bfloat16*)(sm + L::N_ + col + piece_at(tok + t, pc)) = __float2bfloat16_rn(sq[t]);
-                        *(__nv_bfloat16*)(sm + L::N_ + 2 * PANEL + col + piece_at(tok + t, pc)) = __float2bfloat16_rn(sk[t]);
-                    }
+                        for (int t = 0; t < 16; ++t) {
+                            *(__nv_bfloat16*)(ch + L::Q_ + piece_at(tok + t, pc)) = __float2bfloat16_rn(sq[t]);
+                            *(__nv_bfloat16*)(ch + L::K_ + piece_at(tok + t, pc)) = __float2bfloat16_rn(sk[t]);
+                        }
                     fence_async_smem();
                 }
-                bar_sync(3, 512);
-                if (warp == 0) {   // dg: suffix sums of dcum, two tokens a lane, and the exit term
-                    float all = lane < 16 ? red[22 * C + lane] : 0.f;
+                {
+                    const float s = transpose_sum(dc, lane);
+                    if (lane < 16) red[L::DC + w4 * C + tok + lane] = s;
+                }
 #pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+                for (int o = 16; o > 0; o >>= 1) ex += __shfl_xor_sync(~0u, ex, o);
+                if (lane == 0) red[L::EX + warp - 4] = ex;
+                wait(ry_ready, hd & 1, guard);
+                bar_sync(2, 512);
+                if (i + 1 == r) {
+                    if (valid < C) {   // the rows behind the sequence are not its own
+                        for (int z = tid - 128; z < 2 * valid * (DK / 8); z += 512) {
+                            const int piece = (z >> 1) % (DK / 8), t = (z >> 1) / (DK / 8);
+                            *(uint4*)((__nv_bfloat16*)(z & 1 ? b.dk : b.dq) + ((t0 + t) * a.Hk + hk) * DK + piece * 8) =
+                                *(const uint4*)(sm + (z & 1 ? L::K_ : L::Q_) + piece / 8 * PANEL + piece_at(t, piece & 7));
+                        }
+                        bar_sync(2, 512);
+                    }
+                    if (warp == 19 && lane == 0) {
+                        if (valid == C) {
+                            for (int p = 0; p < DK / 64; ++p) {
+                                store_3d(&mdq, sm + L::Q_ + p * PANEL, p * 64, hk, (int)t0);
+                                store_3d(&mdk, sm + L::K_ + p * PANEL, p * 64, hk, (int)t0);
+                            }
+                            bulk_commit();
+                            bulk_wait_read0();
+                        }
+                        mbar_arrive(kq_empty);
+                    }
+                }
+                if (warp == 4) {   // dg: suffix sums of dcum, two tokens a lane, and the exit term
+                    float all = lane < 16 ? red[L::EX + lane] : lane < 20 ? red[(hd & 1) * L::RY + 4 * C + lane - 16] : 0.f;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
                     all = __shfl_sync(~0u, all, 0);
                     float d0 = 0.f, d1 = 0.f;
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        d0 += red[(18 + w) * C + 2 * lane];
-                        d1 += red[(18 + w) * C + 2 * lane + 1];
+                        d0 += red[L::DC + w * C + 2 * lane];
+                        d1 += red[L::DC + w * C + 2 * lane + 1];
                     }
                     float sum = d0 + d1;
 #pragma unroll
@@ -513,40 +532,24 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     __nv_bfloat16* dst = (__nv_bfloat16*)b.dg + t0 * a.Hv + h;
                     if (2 * lane < valid) dst[(int64_t)(2 * lane) * a.Hv] = __float2bfloat16_rn(sum + all);
                     if (2 * lane + 1 < valid) dst[(int64_t)(2 * lane + 1) * a.Hv] = __float2bfloat16_rn(sum - d0 + all);
-                } else if (warp >= 4 && warp < 6) {
+                } else if (warp >= 8 && warp < 10) {
                     const int t = tid & 63;
                     float sum = 0.f;
 #pragma unroll
-                    for (int w = 0; w < 18; ++w) sum += red[w * C + t];
+                    for (int w = 0; w < 4; ++w) sum += red[(hd & 1) * L::RY + w * C + t] + red[L::DB + w * C + t];
                     if (t < valid) ((__nv_bfloat16*)b.dbeta)[(t0 + t) * a.Hv + h] = __float2bfloat16_rn(sum);
                 }
-                if (i + 1 == r) {
-                    if (valid == C) {
-                        if (tid == 0) {
-                            for (int p = 0; p < DK / 64; ++p) {
-                                store_3d(&mdq, sm + L::N_ + p * PANEL, p * 64, hk, (int)t0);
-                                store_3d(&mdk, sm + L::N_ + (2 + p) * PANEL, p * 64, hk, (int)t0);
-                            }
-                            bulk_commit();
-                        }
-                    } else {   // the rows behind the sequence are not its own
-                        for (int z = tid; z < 2 * valid * (DK / 8); z += 512) {
-                            const int which = z & 1, piece = (z >> 1) % (DK / 8), t = (z >> 1) / (DK / 8);
-                            *(uint4*)((__nv_bfloat16*)(which ? b.dk : b.dq) + ((t0 + t) * a.Hk + hk) * DK + piece * 8) =
-                                *(const uint4*)(sm + L::N_ + which * 2 * PANEL + piece / 8 * PANEL + piece_at(t, piece & 7));
-                        }
-                    }
-                }
-                bar_sync(3, 512);   // the next head's sums take these' place
+                warp_arrive(sum_free);
+                bar_sync(2, 512);   // the next head's sums take these' place
             }
             ++n;
         }
-        if (tid == 0) bulk_wait0();
+        if (warp == 19 && lane == 0) bulk_wait0();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 16) tmem_dealloc(tmem, 512);
+    if (warp == 20) tmem_dealloc(tmem, 512);
 }
 
 template <int DK, int DV>
