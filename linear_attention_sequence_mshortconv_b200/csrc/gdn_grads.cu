@@ -13,9 +13,9 @@
 //
 // One CTA per SM takes chunks of key heads in turn, and the value heads of each one after another.
 //
-//   warps 0-3   E1 -> N, E2 -> beta M; then dY . R and <S, D>
-//   warps 4-19  (four warpgroups) the sums over the key channels, a channel a lane, 16 tokens a warpgroup;
-//               these and the first four warps are a head apart
+//   warps 0-3   E1 -> N, E2 -> beta M; then dY . R
+//   warps 4-19  (four warpgroups) <S, D>, and the sums over the key channels, a channel a lane, 16 tokens a
+//               warpgroup; these and the first four warps are a head apart
 //   warp 20     issues the MMAs
 //   warp 21     the loads: S and then D share a buffer; each goes on as soon as its buffer is free, into the
 //               next head and chunk
@@ -39,19 +39,19 @@ struct TGrads {
     static constexpr int Y_ = U_ + 2 * DV * C * 2;           // of dY^T
     static constexpr int G_ = Y_ + 2 * DV * C * 2;           // dO
     static constexpr int N_ = G_ + DV / 64 * PANEL;          // planes of N^T [2][64][64], then of beta M^T
-    static constexpr int SC = N_ + 4 * PANEL;                // grow, end, beta, cum, of two heads
-    static constexpr int RED = SC + 2 * 5 * C * 4;               // fp32: of two heads dY.R [4][64] and <S, D> [4]; dbeta [4][64], dcum [4][64], exit [16]
-    static constexpr int RY = 4 * C + 4, DB = 2 * RY, DC = DB + 4 * C, EX = DC + 4 * C;
+    static constexpr int SC = N_ + 4 * PANEL;                // grow, end, beta, cum, of three heads: the loads are two ahead of the last reader
+    static constexpr int RED = SC + 3 * 5 * C * 4;               // fp32: of two heads dY.R [4][64]; dbeta [4][64], dcum [4][64], exit [16]
+    static constexpr int RY = 4 * C, DB = 2 * RY, DC = DB + 4 * C, EX = DC + 4 * C;
     static constexpr int BAR = RED + (EX + 16) * 4;
     static constexpr int SMEM = BAR + 256 + 1024 > 116 * 1024 ? BAR + 256 + 1024 : 116 * 1024;   // one CTA to an SM
     static constexpr int XQ = 0, XR = 64, XC = 128, CC = 192, NK = 256, MK = 320, E1 = 384, E2 = 448;   // tensor memory
 };
 
-// v[c], c = 0 .. 15, summed over the warp: lanes c and c + 16 get the sum of v[c]
-__device__ __forceinline__ float transpose_sum(float (&v)[16], int lane)
+// v[c], c = 0 .. 7, summed over the warp: lane l gets the sum of v[l & 7]
+__device__ __forceinline__ float transpose_sum(float (&v)[8], int lane)
 {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
+    for (int o = 4; o > 0; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int k = 0; k < o; ++k) {
@@ -59,6 +59,7 @@ __device__ __forceinline__ float transpose_sum(float (&v)[16], int lane)
             v[k] = keep + __shfl_xor_sync(~0u, give, o);
         }
     }
+    v[0] += __shfl_xor_sync(~0u, v[0], 8);
     return v[0] + __shfl_xor_sync(~0u, v[0], 16);
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
@@ -76,7 +77,7 @@ __device__ __forceinline__ float at_least(float beta) { return fabsf(beta) < 5.9
 template <int DK, int DV>
 __global__ void __launch_bounds__(704, 1)
 gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
-                  const __grid_constant__ CUtensorMap mdq, const __grid_constant__ CUtensorMap mdk, GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, const char* kept, int* status)
+                  GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status)
 {
     using L = TGrads<DK, DV>;
     const GdnArgs& a = b.f;
@@ -97,8 +98,8 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
     if (warp == 21) {
         if (lane == 0) {
             for (uint64_t* x : {kq_full, y_full, u_full, u_empty, s_full, s_done, d_full, landed, e_done, drain}) mbar_init(x, 1);
-            for (uint64_t* x : {y_empty, d_empty, out_done}) mbar_init(x, 5);   // the MMAs and warps 0-3
-            mbar_init(kq_empty, 2);                                             // the MMAs, and dq and dk out of the same place
+            for (uint64_t* x : {y_empty, out_done}) mbar_init(x, 5);            // the MMAs and warps 0-3
+            for (uint64_t* x : {d_empty, kq_empty}) mbar_init(x, 17);           // the MMAs and warps 4-19
             for (uint64_t* x : {nm_ready, ry_ready}) mbar_init(x, 4);
             for (uint64_t* x : {acc_free, sum_free}) mbar_init(x, 16);
             *guard.flag = 0;
@@ -133,6 +134,11 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 warp_arrive(full);
                 __syncwarp();
             };
+            if (lane == 0)   // K and Q come late: as far as L2 meanwhile
+                for (int p = 0; p < DK / 64; ++p) {
+                    prefetch_3d(&mk, p * 64, hk, y);
+                    prefetch_3d(&mq, p * 64, hk, y);
+                }
             for (int h = hk * r; h < hk * r + r; ++h, ++hd) {
                 const char* mine = kept + ((int64_t)(item / a.Hk) * a.Hv + h) * keep.bytes();
                 const char* rec = records + ((int64_t)(item / a.Hk) * a.Hv + h) * REC_BYTES;
@@ -143,7 +149,7 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     mbar_arrive_expect_tx(bar, C * DV * 2 + 2 * DV * C * 2 + 5 * C * 4);
                     bulk_load(sm + L::Y_, mine + keep.y(), 2 * DV * C * 2, bar);
                     for (int p = 0; p < DV / 64; ++p) tma_load_3d(sm + L::G_ + p * PANEL, &mg, bar, p * 64, h, y);
-                    bulk_load(sm + L::SC + (hd & 1) * 5 * C * 4, rec + REC_SCAL, 5 * C * 4, bar);
+                    bulk_load(sm + L::SC + hd % 3 * 5 * C * 4, rec + REC_SCAL, 5 * C * 4, bar);
                 }
                 ++y_in;
                 __syncwarp();
@@ -289,7 +295,7 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             if (!seqs.locate(item / a.Hk, C, seq, c)) continue;
             const int hk = item % a.Hk;
             for (int i = 0; i < r; ++i, ++hd) {
-                const float* scal = (const float*)(sm + L::SC + (hd & 1) * 5 * C * 4);
+                const float* scal = (const float*)(sm + L::SC + hd % 3 * 5 * C * 4);
                 const char* mine = kept + ((int64_t)(item / a.Hk) * a.Hv + hk * r + i) * keep.bytes();
                 float x[32];
                 if (hd > 0) wait(out_done, (hd - 1) & 1, guard);   // the planes have been read
@@ -359,47 +365,6 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                         if (lane < 8) red[(hd & 1) * L::RY + warp * C + piece * 8 + e] = acc[e];
                     }
                 }
-                // <S, D>, 16 bytes of each plane a thread and round; S once more from L2
-                {
-                    constexpr int PIECES = DV * DK * 2 / (128 * 16), NB = 2;
-                    const char *s = mine + keep.s() + tid * 16, *d = sm + L::SD + tid * 16;
-                    float ex = 0.f;
-                    uint4 sp[2][NB];
-                    auto fetch = [&](int i0) {
-#pragma unroll
-                        for (int z = 0; z < NB; ++z) {
-                            sp[0][z] = __ldcg((const uint4*)(s + (i0 + z) * 2048));
-                            sp[1][z] = __ldcg((const uint4*)(s + keep.state() + (i0 + z) * 2048));
-                        }
-                    };
-                    fetch(0);
-                    wait(d_full, hd & 1, guard);
-#pragma unroll 1
-                    for (int i0 = 0; i0 < PIECES; i0 += NB) {
-                        uint4 now[2][NB];
-#pragma unroll
-                        for (int z = 0; z < NB; ++z) {
-                            now[0][z] = sp[0][z];
-                            now[1][z] = sp[1][z];
-                        }
-                        if (i0 + NB < PIECES) fetch(i0 + NB);
-#pragma unroll
-                        for (int z = 0; z < NB; ++z) {
-                            const uint4 d0 = *(const uint4*)(d + (i0 + z) * 2048), d1 = *(const uint4*)(d + DV * DK * 2 + (i0 + z) * 2048);
-                            const uint32_t ss[2][4] = {{now[0][z].x, now[0][z].y, now[0][z].z, now[0][z].w}, {now[1][z].x, now[1][z].y, now[1][z].z, now[1][z].w}};
-                            const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                ex = fmaf(low(dd[0][e]) + low(dd[1][e]), low(ss[0][e]) + low(ss[1][e]),
-                                          fmaf(high(dd[0][e]) + high(dd[1][e]), high(ss[0][e]) + high(ss[1][e]), ex));
-                        }
-                    }
-                    warp_arrive(d_empty);
-                    ex *= scal[C - 1];
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) ex += __shfl_xor_sync(~0u, ex, o);
-                    if (lane == 0) red[(hd & 1) * L::RY + 4 * C + warp] = ex;
-                }
                 if (hd > 0) wait(sum_free, (hd - 1) & 1, guard);   // two heads' sums at most are on their way
                 warp_arrive(ry_ready);
             }
@@ -410,7 +375,7 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
         const uint32_t at = tmem + ((uint32_t)w4 * 32u << 16) + tok;
         float* red = (float*)(sm + L::RED);
         const bool real = DK == 128 || row < DK;
-        char* ch = sm + (DK > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2;   // the channel's column of Q and K
+        const char* ch = sm + (DK > 64 ? row >> 6 : 0) * PANEL + (row & 7) * 2;   // the channel's column of Q and K
         const int pc = (row & 63) >> 3;
         auto value = [&](int tile, int t) { return __uint_as_float((uint32_t)*(const uint16_t*)(ch + tile + piece_at(tok + t, pc)) << 16); };
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -418,45 +383,59 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             if (!seqs.locate(item / a.Hk, C, seq, c)) continue;
             const int hk = item % a.Hk, valid = min(C, seqs.len(seq) - c * C);
             const int64_t t0 = (int64_t)seqs.start(seq) + c * C;
-            float sq[16] = {}, sk[16] = {};
-            wait(kq_full, n & 1, guard);
+            // the sums over the value heads so far, fp32 [2][64][Dk], in the place of the first one's S and D
+            float* so_far = (float*)(kept + ((int64_t)(item / a.Hk) * a.Hv + hk * r) * keep.bytes()) + tok * DK + row;
             for (int i = 0; i < r; ++i, ++hd) {
                 const int h = hk * r + i;
-                const float* scal = (const float*)(sm + L::SC + (hd & 1) * 5 * C * 4) + tok;
-                float ex = 0.f, dc[16], db[16];
-                wait(out_done, hd & 1, guard);
-                tc_fence_after();
+                const float* scal = (const float*)(sm + L::SC + hd % 3 * 5 * C * 4) + tok;
+                const char* mine = kept + ((int64_t)(item / a.Hk) * a.Hv + h) * keep.bytes();
+                float ex = 0.f;
+                {   // <S, D>, 16 bytes of each plane a thread and round; S once more from L2
+                    constexpr int PIECES = DV * DK * 2 / (512 * 16);
+                    const char *s = mine + keep.s() + (tid - 128) * 16, *d = sm + L::SD + (tid - 128) * 16;
+                    uint4 sp[2][PIECES];
 #pragma unroll
-                for (int z = 0; z < 16; z += 8) {
-                    float u[8], v[8];
+                    for (int z = 0; z < PIECES; ++z)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) sp[q][z] = __ldcg((const uint4*)(s + q * keep.state() + z * 8192));
+                    wait(d_full, hd & 1, guard);
+#pragma unroll
+                    for (int z = 0; z < PIECES; ++z) {
+                        const uint4 d0 = *(const uint4*)(d + z * 8192), d1 = *(const uint4*)(d + DV * DK * 2 + z * 8192);
+                        const uint32_t ss[2][4] = {{sp[0][z].x, sp[0][z].y, sp[0][z].z, sp[0][z].w}, {sp[1][z].x, sp[1][z].y, sp[1][z].z, sp[1][z].w}};
+                        const uint32_t dd[2][4] = {{d0.x, d0.y, d0.z, d0.w}, {d1.x, d1.y, d1.z, d1.w}};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            ex = fmaf(low(dd[0][e]) + low(dd[1][e]), low(ss[0][e]) + low(ss[1][e]),
+                                      fmaf(high(dd[0][e]) + high(dd[1][e]), high(ss[0][e]) + high(ss[1][e]), ex));
+                    }
+                    warp_arrive(d_empty);
+                }
+                if (i == 0) wait(kq_full, n & 1, guard);
+                wait(out_done, hd & 1, guard);
+                ex *= scal[C - 1 - tok];
+                tc_fence_after();
+#pragma unroll 1
+                for (int z = 0; z < 16; z += 8) {   // (a loop: see the scans)
+                    float u[8], v[8], k[8], dq[8], dk[8], dc[8], db[8];
                     // row part of dK: (beta M) K - beta e^cum o (dY S^T), and k . (beta M K)
                     tmem_ld8(at + L::XR + z, u);
                     tmem_ld8(at + L::MK + z, v);
 #pragma unroll
                     for (int t = 0; t < 8; ++t) {
-                        const float be = scal[2 * C + z + t];
-                        const float k = real ? value(L::K_, z + t) : 0.f, mk = real ? v[t] : 0.f;
-                        const float f = real ? fmaf(-be * scal[z + t], u[t], at_least(be) == be ? mk : mk * (be * 16777216.f)) : 0.f;   // (2^24)
-                        sk[z + t] += f;
-                        dc[z + t] = k * f;
-                        db[z + t] = k * mk;
+                        const float be = scal[2 * C + z + t], mk = real ? v[t] : 0.f;
+                        k[t] = real ? value(L::K_, z + t) : 0.f;
+                        dk[t] = real ? fmaf(-be * scal[z + t], u[t], at_least(be) == be ? mk : mk * (be * 16777216.f)) : 0.f;   // (2^24)
+                        dc[t] = k[t] * dk[t];
+                        db[t] = k[t] * mk;
                     }
-                }
-                {
-                    const float s = transpose_sum(db, lane);
-                    if (lane < 16) red[L::DB + w4 * C + tok + lane] = s / at_least(scal[2 * C + lane]);
-                }
-#pragma unroll
-                for (int z = 0; z < 16; z += 8) {
-                    float u[8], v[8];
                     // dQ = e^cum o (dO S^T) + N K
                     tmem_ld8(at + L::XQ + z, u);
                     tmem_ld8(at + L::NK + z, v);
 #pragma unroll
                     for (int t = 0; t < 8; ++t) {
-                        const float f = real ? fmaf(scal[z + t], u[t], v[t]) : 0.f;
-                        sq[z + t] += f;
-                        if (real) dc[z + t] = fmaf(value(L::Q_, z + t), f, dc[z + t]);
+                        dq[t] = real ? fmaf(scal[z + t], u[t], v[t]) : 0.f;
+                        if (real) dc[t] = fmaf(value(L::Q_, z + t), dq[t], dc[t]);
                     }
                     // column part: e^{cum_C - cum} o (U D^T) + (beta M)^T K + N^T Q
                     tmem_ld8(at + L::XC + z, u);
@@ -464,58 +443,56 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     if (z == 8) {
                         tc_fence_before();
                         warp_arrive(acc_free);
+                        if (i + 1 == r) warp_arrive(kq_empty);
                     }
 #pragma unroll
                     for (int t = 0; t < 8; ++t) {
-                        const float k = real ? value(L::K_, z + t) : 0.f, g = real ? scal[C + z + t] * u[t] : 0.f, f = real ? g + v[t] : 0.f;
-                        sk[z + t] += f;
-                        ex = fmaf(k, g, ex);
-                        dc[z + t] = fmaf(-k, f, dc[z + t]);
+                        const float g = real ? scal[C + z + t] * u[t] : 0.f, f = real ? g + v[t] : 0.f;
+                        dk[t] += f;
+                        ex = fmaf(k[t], g, ex);
+                        dc[t] = fmaf(-k[t], f, dc[t]);
                     }
-                }
-                if (i + 1 == r) {   // dq and dk take the place of Q and K, which no one else reads any more
-                    if (real)
+                    const float s0 = transpose_sum(db, lane), s1 = transpose_sum(dc, lane);
+                    if (lane < 8) {
+                        red[L::DB + w4 * C + tok + z + lane] = s0 / at_least(scal[2 * C + z + lane]);
+                        red[L::DC + w4 * C + tok + z + lane] = s1;
+                    }
+                    if (i > 0 && real)
 #pragma unroll
-                        for (int t = 0; t < 16; ++t) {
-                            *(__nv_bfloat16*)(ch + L::Q_ + piece_at(tok + t, pc)) = __float2bfloat16_rn(sq[t]);
-                            *(__nv_bfloat16*)(ch + L::K_ + piece_at(tok + t, pc)) = __float2bfloat16_rn(sk[t]);
+                        for (int t = 0; t < 8; ++t) {
+                            dq[t] += so_far[(z + t) * DK];
+                            dk[t] += so_far[(C + z + t) * DK];
                         }
-                    fence_async_smem();
-                }
-                {
-                    const float s = transpose_sum(dc, lane);
-                    if (lane < 16) red[L::DC + w4 * C + tok + lane] = s;
+                    if (i + 1 < r) {
+                        if (real)
+#pragma unroll
+                            for (int t = 0; t < 8; ++t) {
+                                so_far[(z + t) * DK] = dq[t];
+                                so_far[(C + z + t) * DK] = dk[t];
+                            }
+                    } else {
+                        // even lanes take the even tokens of their channel and the next, odd lanes the odd ones
+                        const bool odd = lane & 1;
+                        const int64_t off = ((t0 + tok + z + odd) * a.Hk + hk) * DK + row - odd, step = 2 * (int64_t)a.Hk * DK;
+#pragma unroll
+                        for (int t = 0; t < 8; t += 2) {
+                            const float q1 = __shfl_xor_sync(~0u, odd ? dq[t] : dq[t + 1], 1), k1 = __shfl_xor_sync(~0u, odd ? dk[t] : dk[t + 1], 1);
+                            if (real && tok + z + t + odd < valid) {
+                                *(uint32_t*)((__nv_bfloat16*)b.dq + off + t / 2 * step) = odd ? pack(q1, dq[t + 1]) : pack(dq[t], q1);
+                                *(uint32_t*)((__nv_bfloat16*)b.dk + off + t / 2 * step) = odd ? pack(k1, dk[t + 1]) : pack(dk[t], k1);
+                            }
+                        }
+                    }
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) ex += __shfl_xor_sync(~0u, ex, o);
                 if (lane == 0) red[L::EX + warp - 4] = ex;
                 wait(ry_ready, hd & 1, guard);
                 bar_sync(2, 512);
-                if (i + 1 == r) {
-                    if (valid < C) {   // the rows behind the sequence are not its own
-                        for (int z = tid - 128; z < 2 * valid * (DK / 8); z += 512) {
-                            const int piece = (z >> 1) % (DK / 8), t = (z >> 1) / (DK / 8);
-                            *(uint4*)((__nv_bfloat16*)(z & 1 ? b.dk : b.dq) + ((t0 + t) * a.Hk + hk) * DK + piece * 8) =
-                                *(const uint4*)(sm + (z & 1 ? L::K_ : L::Q_) + piece / 8 * PANEL + piece_at(t, piece & 7));
-                        }
-                        bar_sync(2, 512);
-                    }
-                    if (warp == 19 && lane == 0) {
-                        if (valid == C) {
-                            for (int p = 0; p < DK / 64; ++p) {
-                                store_3d(&mdq, sm + L::Q_ + p * PANEL, p * 64, hk, (int)t0);
-                                store_3d(&mdk, sm + L::K_ + p * PANEL, p * 64, hk, (int)t0);
-                            }
-                            bulk_commit();
-                            bulk_wait_read0();
-                        }
-                        mbar_arrive(kq_empty);
-                    }
-                }
                 if (warp == 4) {   // dg: suffix sums of dcum, two tokens a lane, and the exit term
-                    float all = lane < 16 ? red[L::EX + lane] : lane < 20 ? red[(hd & 1) * L::RY + 4 * C + lane - 16] : 0.f;
+                    float all = lane < 16 ? red[L::EX + lane] : 0.f;
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+                    for (int o = 8; o > 0; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
                     all = __shfl_sync(~0u, all, 0);
                     float d0 = 0.f, d1 = 0.f;
 #pragma unroll
@@ -544,7 +521,6 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             ++n;
         }
-        if (warp == 19 && lane == 0) bulk_wait0();
     }
     tc_fence_before();
     __syncthreads();
@@ -553,25 +529,24 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
 }
 
 template <int DK, int DV>
-cudaError_t tgrads(const GdnBwdArgs& b, const Seqs& s, const void* records, const void* kept, int sms, int* status, cudaStream_t st)
+cudaError_t tgrads(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int sms, int* status, cudaStream_t st)
 {
     using L = TGrads<DK, DV>;
-    CUtensorMap k{}, q{}, g{}, dq{}, dk{};
+    CUtensorMap k{}, q{}, g{};
     const GdnArgs& a = b.f;
     const int64_t T = s.tokens(), items = (int64_t)s.slots(C) * a.Hk;
-    if (!make_map(&k, a.k, T, a.Hk, DK, 64, 1, C) || !make_map(&q, a.q, T, a.Hk, DK, 64, 1, C) || !make_map(&g, b.dout, T, a.Hv, DV, 64, 1, C) ||
-        !make_map(&dq, b.dq, T, a.Hk, DK, 64, 1, C) || !make_map(&dk, b.dk, T, a.Hk, DK, 64, 1, C))
+    if (!make_map(&k, a.k, T, a.Hk, DK, 64, 1, C) || !make_map(&q, a.q, T, a.Hk, DK, 64, 1, C) || !make_map(&g, b.dout, T, a.Hv, DV, 64, 1, C))
         return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<gdn_tgrads_kernel<DK, DV>>(L::SMEM);
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_grads", st);
     count_launch();
-    gdn_tgrads_kernel<DK, DV><<<(unsigned)min(items, (int64_t)sms), L::THREADS, L::SMEM, st>>>(k, q, g, dq, dk, b, s, (const char*)records, (const char*)kept, status);
+    gdn_tgrads_kernel<DK, DV><<<(unsigned)min(items, (int64_t)sms), L::THREADS, L::SMEM, st>>>(k, q, g, b, s, (const char*)records, (char*)kept, status);
     return cudaGetLastError();
 }
 }  // namespace
 
-cudaError_t launch_grads(const GdnBwdArgs& b, const Seqs& s, const void* records, const void* kept, int sms, int* status, cudaStream_t st)
+cudaError_t launch_grads(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int sms, int* status, cudaStream_t st)
 {
     if (b.f.Dk == 64) return b.f.Dv == 64 ? tgrads<64, 64>(b, s, records, kept, sms, status, st) : tgrads<64, 128>(b, s, records, kept, sms, status, st);
     return b.f.Dv == 64 ? tgrads<128, 64>(b, s, records, kept, sms, status, st) : tgrads<128, 128>(b, s, records, kept, sms, status, st);

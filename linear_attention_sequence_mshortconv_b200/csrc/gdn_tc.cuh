@@ -141,7 +141,7 @@ cudaError_t launch_chain(const GdnArgs& a, const Seqs& s, const void* records, v
 // and the reverse scan (D and dY kept)
 cudaError_t launch_rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int* status, cudaStream_t st);
 // the gradients of q, k, g and beta (Dv = 64 or 128)
-cudaError_t launch_grads(const GdnBwdArgs& b, const Seqs& s, const void* records, const void* kept, int sms, int* status, cudaStream_t st);
+cudaError_t launch_grads(const GdnBwdArgs& b, const Seqs& s, const void* records, void* kept, int sms, int* status, cudaStream_t st);
 bool whole_heads(const GdnArgs& a, const Seqs& s, int sms);   // which of the two
 // The forward over pieces of long samples: chunks to a piece (0: not worth it), bytes, launch
 int piece_chunks(const Seqs& s, int Hv, int Dk, int Dv, int sms);

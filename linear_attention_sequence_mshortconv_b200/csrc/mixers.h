@@ -33,7 +33,7 @@ struct Seqs {
         int lo = 0, hi = n - 1;   // the last sequence whose first slot is <= slot
         if (T >= 0) {
             // first slots are i * T / C + i: a guess from the mean spacing, corrected
-            lo = min(hi, (int)((long long)slot * C / (T + C)));
+            lo = min(hi, (int)((float)slot * (float)C / (float)(T + C)));
             while (lo > 0 && slot0(lo, C) > slot) --lo;
             while (lo < hi && slot0(lo + 1, C) <= slot) ++lo;
         } else {
