@@ -150,6 +150,8 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                     bulk_load(sm + L::Y_, mine + keep.y(), 2 * DV * C * 2, bar);
                     for (int p = 0; p < DV / 64; ++p) tma_load_3d(sm + L::G_ + p * PANEL, &mg, bar, p * 64, h, y);
                     bulk_load(sm + L::SC + hd % 3 * 5 * C * 4, rec + REC_SCAL, 5 * C * 4, bar);
+                    prefetch(mine + keep.u(), 3 * DV * C * 2);   // and R
+                    prefetch(mine + keep.s(), 2 * DV * DK * 2);
                 }
                 ++y_in;
                 __syncwarp();
@@ -159,7 +161,6 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 if (lane == 0) {
                     mbar_arrive_expect_tx(u_full, 2 * DV * C * 2);
                     bulk_load(sm + L::U_, mine + keep.u(), 2 * DV * C * 2, u_full);
-                    prefetch(mine + keep.r(), DV * C * 2);
                 }
                 ++u_in;
                 __syncwarp();
@@ -297,7 +298,6 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             for (int i = 0; i < r; ++i, ++hd) {
                 const float* scal = (const float*)(sm + L::SC + hd % 3 * 5 * C * 4);
                 const char* mine = kept + ((int64_t)(item / a.Hk) * a.Hv + hk * r + i) * keep.bytes();
-                float x[32];
                 if (hd > 0) wait(out_done, (hd - 1) & 1, guard);   // the planes have been read
                 wait(y_full, hd & 1, guard);
                 wait(e_done, hd & 1, guard);
@@ -305,6 +305,7 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 // The planes' sums: each of the two threads of a token hands over the columns that are not its own.
 #pragma unroll 1
                 for (int m = 0; m < 2; ++m) {
+                    float x[32];
                     tmem_ld32(at + L::E1 + 64 * m + (own ^ 32), x);
 #pragma unroll
                     for (int z = 0; z < 8; ++z)
@@ -314,23 +315,34 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 const float hj = scal[3 * C + j], lj = scal[4 * C + j];
 #pragma unroll 1
                 for (int m = 0; m < 2; ++m) {   // N, beta M
-                    tmem_ld32(at + L::E1 + 64 * m + own, x);
+                    uint32_t p[2][16];
 #pragma unroll
-                    for (int z = 0; z < 32; z += 4) {
-                        const float4 v = *(const float4*)(theirs + m * 2 * PANEL + (((z >> 2) ^ (tid & 7)) << 4));
-                        const float4 hi = *(const float4*)&scal[3 * C + own + z], li = *(const float4*)&scal[4 * C + own + z], be = *(const float4*)&scal[2 * C + own + z];
-                        const float vv[4] = {v.x, v.y, v.z, v.w}, hh[4] = {hi.x, hi.y, hi.z, hi.w}, ll[4] = {li.x, li.y, li.z, li.w}, bb[4] = {be.x, be.y, be.z, be.w};
+                    for (int w = 0; w < 32; w += 16) {
+                        float y[16];
+                        tmem_ld16(at + L::E1 + 64 * m + own + w, y);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float d = ex2_approx((hh[e] - hj) + (ll[e] - lj));
-                            x[z + e] = j + m <= own + z + e ? (m ? -at_least(bb[e]) : 1.f) * (d * (x[z + e] + vv[e])) : 0.f;
+                        for (int z = 0; z < 16; z += 4) {
+                            const int i0 = own + w + z;
+                            const float4 v = *(const float4*)(theirs + m * 2 * PANEL + ((((w + z) >> 2) ^ (tid & 7)) << 4));
+                            const float4 hi = *(const float4*)&scal[3 * C + i0], li = *(const float4*)&scal[4 * C + i0], be = *(const float4*)&scal[2 * C + i0];
+                            const float vv[4] = {v.x, v.y, v.z, v.w}, hh[4] = {hi.x, hi.y, hi.z, hi.w}, ll[4] = {li.x, li.y, li.z, li.w}, bb[4] = {be.x, be.y, be.z, be.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float d = ex2_approx((hh[e] - hj) + (ll[e] - lj));
+                                y[z + e] = j + m <= i0 + e ? (m ? -at_least(bb[e]) : 1.f) * (d * (y[z + e] + vv[e])) : 0.f;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                uint32_t q[2];
+                                split<2>(y[z + e], y[z + e + 1], q);
+                                p[0][(w + z + e) / 2] = q[0];
+                                p[1][(w + z + e) / 2] = q[1];
+                            }
                         }
                     }
                     bar_sync(1, 128);   // the sums have been read: the planes take their place
-                    uint32_t p[2][16];
-                    planes_of<2>(x, p);
                     to_tile<C>(sm + L::N_ + m * 2 * PANEL, j, own / 8, p[0]);
-                    to_tile<C>(sm + L::N_ + m * 2 * PANEL + PANEL, j, own / 8, p[1], 0x80008000u);
+                    to_tile<C>(sm + L::N_ + m * 2 * PANEL + PANEL, j, own / 8, p[1]);
                 }
                 tc_fence_before();
                 fence_async_smem();
