@@ -422,6 +422,7 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                                       fmaf(high(dd[0][e]) + high(dd[1][e]), high(ss[0][e]) + high(ss[1][e]), ex));
                     }
                     warp_arrive(d_empty);
+                    if (i == 0 && r > 1) bar_sync(2, 512);   // every warp has read S: the sums so far take its place
                 }
                 if (i == 0) wait(kq_full, n & 1, guard);
                 wait(out_done, hd & 1, guard);

@@ -306,6 +306,49 @@ def test_many_heads(case, with_states):
     assert kda.last_device_error() == 0
 
 
+@pytest.mark.parametrize("case", [([64, 65, 3] * 60, 2, 2, 64, 64), ([130, 1] * 20, 1, 8, 128, 128), ([100] * 80, 2, 6, 128, 64)], ids=str)
+def test_more_chunks_than_sms(case):
+    """The gradients' kernel takes several chunks to an SM, ragged ones among them, and groups of many heads."""
+    lens, Hk, Hv, Dk, Dv = case
+    x, S0, do, dS = make(lens, Hk, Hv, Dk, Dv, torch.bfloat16, seed=90 + Hv)
+    ref = R.gdn_backward(*map(R.f64, x), R.f64(do), lens, R.f64(S0), R.f64(dS))
+    got = gdn.backward_varlen(*cuda(x), do.cuda(), R.offsets(lens), S0.cuda(), dS.cuda())
+    check_grads(got, ref, x, BF16_GRAD_TOL)
+    assert kda.last_device_error() == 0
+
+
+@pytest.mark.parametrize("case", [([2000, 1, 777, 2048], 4, 4, 128, 128), ([700, 100, 1333], 2, 6, 128, 64), ([900] * 9, 2, 4, 64, 128),
+                                  ([12000], 2, 2, 64, 64)], ids=str)
+def test_the_same_call_gives_the_same_bits(case):
+    """Nothing depends on which warp, block or copy comes first."""
+    lens, Hk, Hv, Dk, Dv = case
+    x, S0, do, dS = make(lens, Hk, Hv, Dk, Dv, torch.bfloat16, seed=95)
+    x, S0, do, dS, cu = cuda(x), S0.cuda(), do.cuda(), dS.cuda(), R.offsets(lens)
+    call = lambda: (*gdn.forward_varlen(*x, cu, S0), *gdn.backward_varlen(*x, do, cu, S0, dS))   # noqa: E731
+    want = call()
+    for _ in range(15):
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    assert all(bool(torch.isfinite(t.float()).all()) for t in want)
+
+
+@pytest.mark.parametrize("Dv", [32, 64])
+def test_gradients_of_tokens_that_write_nothing(Dv):
+    """beta is 0, or far below any rounding, on some tokens and in whole samples."""
+    lens, Hk, Hv, Dk = [130, 70, 64], 1, 2, 64
+    x, S0, do, dS = make(lens, Hk, Hv, Dk, Dv, torch.bfloat16, seed=33)
+    x[4][::5] = 0.0
+    x[4][1::5] = 2.0 ** -40
+    x[4][2::7] = -2.0 ** -30
+    x[4][130:200] = 0.0
+    ref = R.gdn_backward(*map(R.f64, x), R.f64(do), lens, R.f64(S0), R.f64(dS))
+    got = gdn.backward_varlen(*cuda(x), do.cuda(), R.offsets(lens), S0.cuda(), dS.cuda())
+    check_grads(got, ref, x, BF16_GRAD_TOL)
+    # dbeta of the tokens with beta = 0 by themselves: it does not depend on their own beta
+    rows = np.arange(sum(lens)) % 5 == 0
+    a, b = R.f64(got[4])[rows], ref[4][rows]
+    assert np.linalg.norm(a - b) <= BF16_GRAD_TOL * np.linalg.norm(b)
+
+
 @pytest.mark.parametrize("g", [-0.5, -8.0, -90.0, float("-inf")])
 @pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64)])
 def test_many_heads_strong_gates(Dk, Dv, g):
