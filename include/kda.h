@@ -584,7 +584,11 @@ void kda_profile_enable(int on);
  * collection; clears that kernel's record.  Returns 0, or -1 if `name` has no
  * record.  Names: "kda_generic", "kda_tc_state", "kda_tc_combine",
  * "kda_tc_output", "kda_tc_output_first", "conv", "gate_norm", "kda_sp_fold",
- * "kda_bwd", "conv_bwd". */
+ * "kda_bwd", "conv_bwd"; "gdn_recurrent", "gdn_prologue", "gdn_scan", "gdn_chain",
+ * "gdn_chain_state", "gdn_chain_transition", "gdn_carry", "gdn_scan_keep",
+ * "gdn_chain_keep", "gdn_rscan", "gdn_rchain", "gdn_grads", "gdn_grads_narrow",
+ * "gdn_bwd_generic", "gdn_step"; "attn_generic", "attn_bwd_generic", "attn_fwd",
+ * "attn_delta", "attn_bwd_keys", "attn_bwd_rows". */
 int kda_profile_collect(const char* name, double* total_ms, int* launches);
 
 #ifdef __cplusplus

@@ -17,6 +17,9 @@
 // left the tensor cores idle half of the time (16384 tokens, 16 heads, width 128: 0.93 ms).
 // Tensor memory (512 columns): 2 x 2 x S (64 each), O0, O1 (D each).
 //
+// (16384 tokens, 16 heads to 4, width 128: 0.81 ms, 1.35 PFLOP/s or 82% of a large product's burst rate, at
+// the power limit 0.95 ms, 83% of its sustained one; the exponentials and the tensor cores are both nearly full.)
+//
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the reference of
 // its exponents was set (sums and weights then stay below 2^8 times their size, far from
 // overflow), which after the first blocks is rare; the result does not depend on the reference.

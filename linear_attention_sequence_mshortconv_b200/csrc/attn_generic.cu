@@ -4,7 +4,7 @@
 //   dv_j = sum_i p_ij do_i, ds_ij = scale p_ij (do_i.v_j - do_i.o_i), dq_i = sum_j ds_ij k_j,
 //   dk_j = sum_i ds_ij q_i, the sums of dk and dv running over the query heads of the group.
 // One warp owns a row (a query, or a key for dk and dv) and goes over the others 32 at a
-// time, one to a lane; the block's 8 rows share the staged tile.
+// time, one to a lane; the block's 8 rows share the staged tile.  Bound by the shared-memory reads of the staged tile.
 
 #include "mixers.h"
 

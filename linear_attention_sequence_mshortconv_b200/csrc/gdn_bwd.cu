@@ -1,7 +1,8 @@
 // Gradients of the gated delta rule on the tensor cores (bf16; Dk = 64 or 128).
 //
 // Four launches: the prologue (T, P, gates) and the forward scan again, which keeps every
-// chunk's entry state S, U and R; a reverse scan, a chain like the forward's,
+// chunk's entry state S, U and R; a reverse scan, a chain like the forward's (here by columns of heads, in
+// gdn_rchain.cu by whole heads; the forward scan's rule says which),
 //   dU = P^T dO + e^{cum_C - cum} o (K D),  dY = T^T dU,  dV = beta o dY,
 //   D' = e^{cum_C} D + Q^T (e^cum o dO) - K^T (e^cum o dV)
 // with D the gradient of the chunk's exit state and D' that of its entry state, which keeps D and
@@ -308,12 +309,11 @@ __global__ void __launch_bounds__(256 * MT) gdn_rscan_kernel(GdnBwdArgs b, const
 }
 
 // ---- gradients of q, k, g and beta ----------------------------------------------------------
-// One CTA per chunk and key head: 16 warps, warp (mt, qt) owns 16 tokens and a quarter of the columns
-// of every product; the value heads of the group follow one another and are summed in registers.
-// The tiles take most of shared memory (221 KB at Dk = Dv = 128), so an SM holds one CTA: its 16 warps
-// have to hide each other's latency (8 took 0.56 ms at the image stream, 16 take 0.49; the rate of mma.sync
-// alone would be about 0.37), and D comes in where S was while the
-// pair products are taken.
+// Dv = 32 (gdn_grads.cu has the others: half of an MMA's K = 64 panels would be empty).  One CTA per chunk and key
+// head: 16 warps, warp (mt, qt) owns 16 tokens and a quarter of the columns of every product; the value heads of
+// the group follow one another and are summed in registers.  D comes in where S was while the pair products
+// are taken.  Bound by the rate and latency of warp MMAs (at Dv = 128 it took 0.50 ms for 4352 chunks and heads, of which
+// their rate alone is 0.37; 8 warps took 0.56).
 template <int DK, int DV>
 struct Grads {
     static constexpr int THREADS = 512;

@@ -5,8 +5,10 @@
 // value columns, so a head's K, Q and factors are read once per 16 or 32 columns, and shared
 // memory bounds it as soon as the heads fill the SMs.  Here all Dv columns are the 128 rows of every
 // product: S, Y and U are left operands in tensor memory (lane = value column), and K, Q, T and P
-// are read from shared memory once per chunk and plane.  A chunk takes about as long as there
-// (both are a chain of three products), for 4 to 8 times the columns.
+// are read from shared memory once per chunk and plane.  A chunk takes 2.6 us against 1.5 there, for 4 to 8
+// times the columns (4 rows of 68 chunks, 16 heads, Dk = Dv = 128: 181 us, columns 333; what the backward keeps,
+// 208 KB a chunk less D and dY, comes out in 190).  Bound by the latency of the chain: three products in a row and
+// what the threads do between them, about 0.4 us each time.
 //
 //   warps 0-7  (two warpgroups, each with half of the columns of every operand): K S -> Y,
 //              U -> decayed U, S -> planes: what lies between the products, in fp32

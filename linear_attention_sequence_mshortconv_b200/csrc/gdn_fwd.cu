@@ -29,7 +29,8 @@ namespace gdn {
 // forward substitution, a warp each, a column to a lane; then twice T21 = -T22 (A21 T11), on
 // the two 32x32 and on the one 64x64 block.  Nothing here waits for another chunk, so what bounds
 // it is the latency of these steps against the warps an SM holds: A and T take the place of K and
-// Q, and 102 registers a thread let five CTAs share an SM.
+// Q, and 102 registers a thread let five CTAs share an SM.  (4352 chunks and heads, Dk = 128: 84 us, 0.25 GB of
+// factors and inputs; the shared-memory pipe is busy 72% of it.)
 constexpr int ALD = 68;   // row of A and T in floats: rows of a warp's reads fall in different banks
 template <int DK>
 constexpr int pro_smem()
@@ -273,7 +274,8 @@ cudaError_t launch_prologue(const GdnArgs& a, const Seqs& s, void* records, cuda
 //   output: next chunk's loads (cp.async, two stages), Q S | O = e^cum o (Q S) + P U
 // with a barrier at each bar, where Y, U and S pass through shared memory as planes.  The
 // chain is bound by latency (one warp a scheduler issues every fourth cycle), which the
-// output warps fill.
+// output warps fill: 1.5 us a chunk where a CTA has its SM to itself (16 heads of 512 chunks, 16 columns a CTA:
+// 0.77 ms), 88 us for 12 ragged samples of 33 chunks at most with 8 heads (Dk = Dv = 128).
 //
 // KEEP: the scan of the backward.  The output warps then write what the gradients need of each
 // chunk (the planes of S and U and R) in place of the output.
@@ -609,7 +611,9 @@ size_t gdn_tc_workspace(const GdnArgs& a, const Seqs& s, int sms)
 
 cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st)
 {
-    if (const int per = gdn::piece_chunks(s, a.Hv, a.Dk, a.Dv, sms)) return gdn::launch_pieces(a, s, ws, per, status, st);
+    // (states are carried from piece to piece 16 bytes at a time)
+    const int per = gdn::aligned16(a.S0) && gdn::aligned16(a.ST) ? gdn::piece_chunks(s, a.Hv, a.Dk, a.Dv, sms) : 0;
+    if (per) return gdn::launch_pieces(a, s, ws, per, status, st);
     cudaError_t e = cudaSuccess;
     const bool whole = gdn::whole_heads(a, s, sms);
     if (s.tokens() > 0) e = gdn::launch_prologue(a, s, ws, st);

@@ -20,7 +20,9 @@
 //   warp 21     the loads: S and then D share a buffer; each goes on as soon as its buffer is free, into the
 //               next head and chunk
 //
-// What bounds it: the tiles of a chunk and value head are 208 KB at Dk = Dv = 128, 0.14 ms of HBM at the image stream.
+// The tiles of a chunk and value head are 208 KB at Dk = Dv = 128, 0.14 ms of HBM for 4 rows of 68 chunks, 16 heads; the
+// kernel takes 0.26 ms there (warp MMAs, as gdn_bwd.cu has them for Dv = 32, 0.50).  What bounds it is the circle from one head
+// to the next, 7.7 us: U's load and E 2, the threads' N and M 3.4, the products that wait for them 2.3.
 //
 // Every wait is bounded; after one runs out all roles run to their end on whatever is there.
 

@@ -14,6 +14,11 @@
 //              from the chain read, come in when those of the chunk before are done.
 //   warp 14    D, dY and dV out to memory, by the copy engine
 //
+// Bound by the latency of that chain, 3.2 us a chunk (4 rows of 68 chunks, 16 heads, Dk = Dv = 128: 217 us; columns of
+// heads on warp MMAs take 608).  What made the difference here was code, not data: with every loop unrolled the
+// roles' 85 KB of instructions were fetched anew each chunk (370 us), and spilled registers came back from L2, since the tiles
+// leave the L1 cache little.
+//
 // Tensor memory (512 columns): D (fp32, Dk), its two planes (Dk), X (64: K D, then the planes of dU),
 // Y (64: dO^T, then T^T dU, then the planes of e^cum o dV), W (64: P^T dO), G (64: planes of e^cum o dO).  A
 // warpgroup writes planes only where its own half of a product was.

@@ -504,6 +504,19 @@ def test_long_samples_do_not_touch_each_other_nor_the_rows_behind():
         assert bool((o[sum(lens):] == 7.0).all())
 
 
+def test_long_samples_with_states_off_alignment():
+    """States one float into their storage: contiguous, but not 16-byte aligned."""
+    lens = [6000]
+    x, S0, _, _ = make(lens, 1, 2, 64, 64, torch.bfloat16, seed=14, g_scale=0.02)
+    ref_o, ref_S = R.gdn(*map(R.f64, x), lens, R.f64(S0))
+    buf = torch.zeros(2, S0.numel() + 1, device="cuda")
+    first, last = (b[1:].view(S0.shape) for b in buf)
+    first.copy_(S0)
+    for S, out in ((first, None), (S0.cuda(), last), (first, last)):
+        o, S_T = gdn.forward_varlen(*cuda(x), [0, 6000], S, S_T=out)
+        assert R.norm_error(o, ref_o) <= BF16_TOL and R.norm_error(S_T, ref_S) <= FP32_TOL
+
+
 def test_long_samples_captured():
     x, S0, _, _ = make([6000], 2, 2, 64, 64, torch.bfloat16, seed=8, g_scale=0.02)
     y, S1, _, _ = make([6000], 2, 2, 64, 64, torch.bfloat16, seed=9, g_scale=0.02)
