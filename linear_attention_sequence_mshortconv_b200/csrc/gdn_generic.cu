@@ -14,21 +14,25 @@ namespace {
 __device__ __forceinline__ double gate_of(float g) { return (double)fmaxf(g, -1000.f); }
 
 // ---- forward: one warp per 4 value columns, 8 lanes to a column ------------------------
-// A lane holds Dk / 8 entries of its column of S in registers, so a token costs Dk / 8 FMAs
-// for each of k^T S, q^T S and the update, and three xor-shuffle steps over the 8 lanes for
-// the sums (o = a q^T S + (q.k) u needs only the old S, so both sums go through the same
-// steps).  Tokens are staged 16 at a time in shared memory; the next 16 are read into
-// registers while these are computed.  Bound by the latency of the token chain, not by bytes.
-constexpr int RT = 16;       // tokens per stage
+// A lane holds Dk / 8 entries of its column of S in registers.  Four tokens at a time: their products with the
+// S before them, k_t^T S and q_t^T S, are summed over the 8 lanes together, and then go from token to
+// token without S, since after token s
+//   k_t^T S_s = a_s k_t^T S_{s-1} + (k_t.k_s) u_s   (and so for q_t),   u_s = beta_s (v_s - a_s k_s^T S_{s-1}).
+// So only three dependent operations a token are left in the chain, and the shuffles are once in four.  Tokens
+// are staged 16 to 64 at a time in shared memory, with the products k.k and q.k of each four; the next ones are
+// read into registers while these are computed.  Bound by the latency of the chain, not by bytes.
+constexpr int RB = 4;        // tokens at a time
 constexpr int RCOLS = 16;    // value columns per CTA (4 warps)
 
 template <typename T, int DK>
 __global__ void __launch_bounds__(128) gdn_recurrent_kernel(GdnArgs a, const __grid_constant__ Seqs seqs)
 {
     constexpr int NR = DK / 8;
+    constexpr int RT = 2048 / DK;        // tokens per stage
     constexpr int PER = RT * DK / 128;   // staged k (and q) values per thread
     __shared__ __align__(16) float sk[RT][DK], sq[RT][DK];
-    __shared__ float sv[RT][RCOLS], sa[RT], sb[RT], sqk[RT];
+    __shared__ float sv[RT][RCOLS], sa[RT], sb[RT];
+    __shared__ __align__(16) float sqk[RT][RB], skk[RT][RB];   // q_t.k_s and k_t.k_s with the tokens s of t's four
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int seq = blockIdx.z, h = blockIdx.y, c0 = blockIdx.x * RCOLS;
     const int col = wid * 4 + (lane >> 3), l8 = lane & 7;
@@ -48,7 +52,7 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(GdnArgs a, const __g
         const int i = (r >> 2) * 32 + l8 * 4 + (r & 3);
         S[r] = a.S0 ? a.S0[s_off + (int64_t)i * a.Dv] : 0.f;
     }
-    float pk[PER], pq[PER], pv[2], pg = 0.f, pb = 0.f;
+    float pk[PER], pq[PER], pv[RT * RCOLS / 128], pg = 0.f, pb = 0.f;
     auto fetch = [&](int base) {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
@@ -59,13 +63,14 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(GdnArgs a, const __g
             pq[j] = in ? to_f32(q[off]) : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < RT * RCOLS / 128; ++j) {
             const int e = j * 128 + tid, t = base + e / RCOLS;
             pv[j] = t < len ? to_f32(v[((t0 + t) * a.Hv + h) * a.Dv + c0 + e % RCOLS]) : 0.f;
         }
-        if (tid < RT && base + tid < len) {
-            pg = to_f32(g[(t0 + base + tid) * a.Hv + h]);
-            pb = to_f32(beta[(t0 + base + tid) * a.Hv + h]);
+        if (tid < RT) {   // (tokens behind the sequence change nothing: alpha = 1, beta = 0)
+            const bool in = base + tid < len;
+            pg = in ? to_f32(g[(t0 + base + tid) * a.Hv + h]) : 0.f;
+            pb = in ? to_f32(beta[(t0 + base + tid) * a.Hv + h]) : 0.f;
         }
     };
     if (len > 0) fetch(0);
@@ -78,7 +83,7 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(GdnArgs a, const __g
             sq[e / DK][e % DK] = pq[j];
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < RT * RCOLS / 128; ++j) {
             const int e = j * 128 + tid;
             sv[e / RCOLS][e % RCOLS] = pv[j];
         }
@@ -89,37 +94,61 @@ __global__ void __launch_bounds__(128) gdn_recurrent_kernel(GdnArgs a, const __g
         __syncthreads();
         if (base + RT < len) fetch(base + RT);
         const int n = min(RT, len - base);
-        // q . k of every token, 8 lanes to a token
-        {
-            const int t = tid >> 3;
+        // two threads to a pair of tokens, each with one of the products
+        for (int z = tid; z < RT * 8; z += 128) {
+            const int t = z >> 3, j = (z >> 1) & 3, other = (t & ~3) + j;
+            const float* x = (tid & 1) ? sk[t] : sq[t];
             float s = 0.f;
-            for (int i = l8; i < DK; i += 8) s = fmaf(sq[t][i], sk[t][i], s);
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
-            if (l8 == 0) sqk[t] = s;
+#pragma unroll 4
+            for (int i0 = 0; i0 < DK; i0 += 4) {
+                const int i = (i0 + (tid >> 1) * 4) % DK;   // the threads of a warp in different banks
+                const float4 u = *(const float4*)&x[i], w = *(const float4*)&sk[other][i];
+                s = fmaf(u.x, w.x, fmaf(u.y, w.y, fmaf(u.z, w.z, fmaf(u.w, w.w, s))));
+            }
+            ((tid & 1) ? skk : sqk)[t][j] = s;
         }
         __syncthreads();
-        for (int t = 0; t < n; ++t) {
-            float kr[NR], ks = 0.f, qs = 0.f;
+        for (int t = 0; t < n; t += RB) {
+            float ks[RB] = {}, qs[RB] = {};
 #pragma unroll
-            for (int r = 0; r < NR; r += 4) {
-                const float4 kv = *(const float4*)&sk[t][r * 8 + l8 * 4];
-                const float4 qv = *(const float4*)&sq[t][r * 8 + l8 * 4];
-                kr[r] = kv.x; kr[r + 1] = kv.y; kr[r + 2] = kv.z; kr[r + 3] = kv.w;
-                ks = fmaf(kv.x, S[r], fmaf(kv.y, S[r + 1], fmaf(kv.z, S[r + 2], fmaf(kv.w, S[r + 3], ks))));
-                qs = fmaf(qv.x, S[r], fmaf(qv.y, S[r + 1], fmaf(qv.z, S[r + 2], fmaf(qv.w, S[r + 3], qs))));
+            for (int r = 0; r < NR; r += 4)
+#pragma unroll
+                for (int j = 0; j < RB; ++j) {
+                    const float4 kv = *(const float4*)&sk[t + j][r * 8 + l8 * 4];
+                    const float4 qv = *(const float4*)&sq[t + j][r * 8 + l8 * 4];
+                    ks[j] = fmaf(kv.x, S[r], fmaf(kv.y, S[r + 1], fmaf(kv.z, S[r + 2], fmaf(kv.w, S[r + 3], ks[j]))));
+                    qs[j] = fmaf(qv.x, S[r], fmaf(qv.y, S[r + 1], fmaf(qv.z, S[r + 2], fmaf(qv.w, S[r + 3], qs[j]))));
+                }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+                for (int j = 0; j < RB; ++j) {
+                    ks[j] += __shfl_xor_sync(~0u, ks[j], o);
+                    qs[j] += __shfl_xor_sync(~0u, qs[j], o);
+                }
+            float al[RB], u[RB];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                al[i] = sa[t + i];
+                u[i] = sb[t + i] * (sv[t + i][col] - al[i] * ks[i]);
+#pragma unroll
+                for (int j = i; j < RB; ++j) {
+                    ks[j] = fmaf(skk[t + j][i], u[i], al[i] * ks[j]);
+                    qs[j] = fmaf(sqk[t + j][i], u[i], al[i] * qs[j]);
+                }
             }
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                ks += __shfl_xor_sync(~0u, ks, o);
-                qs += __shfl_xor_sync(~0u, qs, o);
-            }
-            const float al = sa[t];
-            const float u = sb[t] * (sv[t][col] - al * ks);
+            for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int r = 0; r < NR; ++r) S[r] = fmaf(kr[r], u, al * S[r]);
-            if (l8 == 0)
-                ((T*)a.o)[((t0 + base + t) * a.Hv + h) * a.Dv + c0 + col] = from_f32<T>(fmaf(sqk[t], u, al * qs));
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 kv = *(const float4*)&sk[t + i][r * 8 + l8 * 4];
+                    S[r] = fmaf(kv.x, u[i], al[i] * S[r]);
+                    S[r + 1] = fmaf(kv.y, u[i], al[i] * S[r + 1]);
+                    S[r + 2] = fmaf(kv.z, u[i], al[i] * S[r + 2]);
+                    S[r + 3] = fmaf(kv.w, u[i], al[i] * S[r + 3]);
+                }
+            const float out = l8 == 0 ? qs[0] : l8 == 1 ? qs[1] : l8 == 2 ? qs[2] : qs[3];   // (qs[j] is that of S_j by now)
+            if (l8 < RB && t + l8 < n) ((T*)a.o)[((t0 + base + t + l8) * a.Hv + h) * a.Dv + c0 + col] = from_f32<T>(out);
         }
     }
     if (a.ST) {
