@@ -18,6 +18,8 @@
 // fewer, but overflows at 65504), two 16 to 17; gdn_tc.cuh says which take how many.  The state that
 // is handed on is within 1e-6 of the recurrence's.
 
+#include <algorithm>
+
 #include "gdn_tc.cuh"
 
 namespace kda {
@@ -605,8 +607,10 @@ bool gdn_tc_supported(const GdnArgs& a)
 
 size_t gdn_tc_workspace(const GdnArgs& a, const Seqs& s, int sms)
 {
+    // (enough for either way: which one is taken depends on the states' alignment as well)
     const int per = gdn::piece_chunks(s, a.Hv, a.Dk, a.Dv, sms);
-    return per ? gdn::pieces_workspace(s, a.Hv, a.Dk, a.Dv, per) : (size_t)s.slots(gdn::C) * a.Hv * gdn::REC_BYTES;
+    const size_t records = (size_t)s.slots(gdn::C) * a.Hv * gdn::REC_BYTES;
+    return per ? std::max(records, gdn::pieces_workspace(s, a.Hv, a.Dk, a.Dv, per)) : records;
 }
 
 cudaError_t launch_gdn_tc(const GdnArgs& a, const Seqs& s, void* ws, int sms, int* status, cudaStream_t st)

@@ -506,15 +506,18 @@ def test_long_samples_do_not_touch_each_other_nor_the_rows_behind():
 
 def test_long_samples_with_states_off_alignment():
     """States one float into their storage: contiguous, but not 16-byte aligned."""
-    lens = [6000]
+    lens = [0] * 100 + [6000]
     x, S0, _, _ = make(lens, 1, 2, 64, 64, torch.bfloat16, seed=14, g_scale=0.02)
     ref_o, ref_S = R.gdn(*map(R.f64, x), lens, R.f64(S0))
     buf = torch.zeros(2, S0.numel() + 1, device="cuda")
     first, last = (b[1:].view(S0.shape) for b in buf)
     first.copy_(S0)
-    for S, out in ((first, None), (S0.cuda(), last), (first, last)):
-        o, S_T = gdn.forward_varlen(*cuda(x), [0, 6000], S, S_T=out)
+    need = gdn.varlen_workspace_size(R.offsets(lens), 1, 2, 64, 64)
+    for S, out in ((first, None), (S0.cuda(), last), (first, last), (S0.cuda(), None)):
+        ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        o, S_T = gdn.forward_varlen(*cuda(x), R.offsets(lens), S, S_T=out, workspace=ws[:need])
         assert R.norm_error(o, ref_o) <= BF16_TOL and R.norm_error(S_T, ref_S) <= FP32_TOL
+        assert bool((ws[need:] == 0xA5).all())
 
 
 def test_long_samples_captured():
