@@ -61,7 +61,8 @@ __device__ __forceinline__ float max_of(const float (&s)[64])
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
-attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnArgs a,
+attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
+                const __grid_constant__ CUtensorMap tm_o, bool boxes, AttnArgs a,
                 const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, int* status)
 {
     using L = Fwd<D>;
@@ -71,7 +72,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
     uint64_t *kfull = bars, *kempty = kfull + L::STAGES, *vfull = kempty + L::STAGES, *vempty = vfull + L::STAGES;
     uint64_t *sfull = vempty + L::STAGES, *pready = sfull + 4, *pvdone = pready + 4, *vfix = pvdone + 4, *drain = vfix + 1;
-    uint32_t* tm_ptr = (uint32_t*)(drain + 2);
+    uint64_t* qfull = drain + 2;   // by tile, where Q comes in boxes
+    uint32_t* tm_ptr = (uint32_t*)(qfull + 2);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
@@ -117,9 +119,17 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             mbar_init(vfix, 32);
             mbar_init(drain, 1);
             mbar_init(drain + 1, 1);
+            mbar_init(qfull, 1);
+            mbar_init(qfull + 1, 1);
             *guard.flag = 0;
             fence_mbar_init();
             fence_async_smem();
+            // (rows past the sequence's end are another one's, or zeros: no other row sees them)
+            for (int t = 0; boxes && t < 2 && first + t * QR < all; ++t) {
+                mbar_arrive_expect_tx(qfull + t, L::QTILE);
+                for (int p = 0; p < D / 64; ++p)
+                    tma_load_3d(sm + L::Q_ + t * L::QTILE + p * L::QPANEL, &tm_q, qfull + t, p * 64, hk * r, (int)t0 + (first + t * QR) / r);
+            }
             for (int j = 0; j < n && j < L::STAGES; ++j) {
                 load_k(j);
                 load_v(j);
@@ -128,7 +138,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     } else if (warp == 8) {
         tmem_alloc(tm_ptr, 512);
         tmem_relinquish();
-    } else if (warp < 8) {
+    } else if (warp < 8 && !boxes) {
         // Q: rows past the sequence's end are zeros
         for (int e = tid; e < 2 * QR * (D / 8); e += 256) {
             const int piece = e % (D / 8), row = e / (D / 8);
@@ -160,6 +170,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 ++v_issued;
             }
             if (guard.up()) {
+                for (int t = 0; boxes && t < 2 && first + t * QR < all; ++t) mbar_wait_bounded(qfull + t, 0, kWaitNs);
                 drain_ring(kfull, L::STAGES, k_issued);
                 drain_ring(vfull, L::STAGES, v_issued);
             }
@@ -197,6 +208,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         };
         // Each wait costs some 85 cycles even when there is nothing to wait for: those for the copies
         // are made while MMAs already issued run.
+        if (boxes && nt > 0) wait(qfull + t, 0, guard);
         for (int j = 0; j < 2 && j < nt; ++j) {
             wait(kfull + j, 0, guard);
             scores(j);
@@ -305,7 +317,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             if (!warp_up(guard)) {
                 // every product that read Q has ended: its tile takes the output
                 const int64_t off = real ? row_at(i) : -1;
-                store_rows<D>(to, 1.f / sum, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)a.o, off, tid & 127);
+                if (boxes && first + t * QR + QR <= all)
+                    store_box<D>(to, 1.f / sum, sm + L::Q_ + t * L::QTILE, &tm_o, hk * r, (int)t0 + (first + t * QR) / r, tid & 127, 1 + t);
+                else
+                    store_rows<D>(to, 1.f / sum, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)a.o, off, tid & 127);
                 if (real && a.lse) a.lse[off / D] = (ref * sl + log2f(sum)) * kLn2;
             }
         }
@@ -320,16 +335,19 @@ template <int D>
 cudaError_t forward(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t st)
 {
     using L = Fwd<D>;
-    CUtensorMap k, v;
-    if (!make_map(&k, a.k, s.tokens(), a.Hkv, D, 64, 1, KB) || !make_map(&v, a.v, s.tokens(), a.Hkv, D, 64, 1, KB))
+    CUtensorMap k, v, q{}, o{};
+    const int r = a.H / a.Hkv;
+    const bool boxes = box_rows(r);
+    if (!make_map(&k, a.k, s.tokens(), a.Hkv, D, 64, 1, KB) || !make_map(&v, a.v, s.tokens(), a.Hkv, D, 64, 1, KB) ||
+        (boxes && (!make_map(&q, a.q, s.tokens(), a.H, D, 64, r, QR / r) || !make_map(&o, a.o, s.tokens(), a.H, D, 64, r, QR / r))))
         return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<attn_fwd_kernel<D>>(L::SMEM);
     if (e != cudaSuccess) return e;
     Tiles tiles;
-    const int64_t ctas = make_tiles(tiles, s, a.Hkv, a.H / a.Hkv, 2 * QR);
+    const int64_t ctas = make_tiles(tiles, s, a.Hkv, r, 2 * QR);
     ProfileScope prof("attn_fwd", st);
     count_launch();
-    attn_fwd_kernel<D><<<(unsigned)ctas, L::THREADS, L::SMEM, st>>>(k, v, a, s, tiles, status);
+    attn_fwd_kernel<D><<<(unsigned)ctas, L::THREADS, L::SMEM, st>>>(k, v, q, o, boxes, a, s, tiles, status);
     return cudaGetLastError();
 }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
