@@ -343,7 +343,8 @@ struct Dq {
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
-attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnBwdArgs b,
+attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_g, const __grid_constant__ CUtensorMap tm_dq, bool boxes, AttnBwdArgs b,
                      const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, float* ndelta, int* status)
 {
     using L = Dq<D>;
@@ -354,7 +355,8 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     uint64_t* bars = (uint64_t*)(sm + L::BAR);
     uint64_t *full = bars, *empty = full + L::STAGES, *sfull = empty + L::STAGES, *gfull = sfull + 2, *dready = gfull + 2;
     uint64_t *done = dready + 2, *fix = done + 2, *drain = fix + 1;
-    uint32_t* tm_ptr = (uint32_t*)(drain + 2);
+    uint64_t* qfull = drain + 2;   // by tile, where Q and dO come in boxes
+    uint32_t* tm_ptr = (uint32_t*)(qfull + 2);
     const Guard guard{(volatile int*)(tm_ptr + 1), status};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform_warp();
@@ -392,17 +394,27 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 mbar_init(dready + i, 128);
                 mbar_init(done + i, 1);
                 mbar_init(drain + i, 1);
+                mbar_init(qfull + i, 1);
             }
             mbar_init(fix, 32);
             *guard.flag = 0;
             fence_mbar_init();
             fence_async_smem();
+            // (rows past the sequence's end are another one's, or zeros: no other row sees them)
+            for (int t = 0; boxes && t < 2 && first + t * L::QR < all; ++t) {
+                mbar_arrive_expect_tx(qfull + t, 2 * L::QTILE);
+                for (int p = 0; p < D / 64; ++p) {
+                    const int at = t * L::QTILE + p * L::QPANEL, y = (int)t0 + (first + t * L::QR) / r;
+                    tma_load_3d(sm + L::Q_ + at, &tm_q, qfull + t, p * 64, hk * r, y);
+                    tma_load_3d(sm + L::G_ + at, &tm_g, qfull + t, p * 64, hk * r, y);
+                }
+            }
             for (int j = 0; j < total && j < L::STAGES; ++j) load(j);
         }
     } else if (warp == 8) {
         tmem_alloc(tm_ptr, 512);
         tmem_relinquish();
-    } else if (warp < 8) {
+    } else if (warp < 8 && !boxes) {
         for (int e = tid; e < 2 * L::QR * (D / 8); e += 256) {
             const int piece = e % (D / 8), row = e / (D / 8);
             const bool in = first + row < all;
@@ -428,7 +440,10 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (guard.up()) break;
                 load(issued);
             }
-            if (guard.up()) drain_ring(full, L::STAGES, issued);
+            if (guard.up()) {
+                for (int t = 0; boxes && t < 2 && first + t * L::QR < all; ++t) mbar_wait_bounded(qfull + t, 0, kWaitNs);
+                drain_ring(full, L::STAGES, issued);
+            }
         }
         __syncwarp();
         if (warp == 10 && tail < L::KB && !guard.up()) {   // keys past the end (dS is 0 there): K must be finite
@@ -449,6 +464,7 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         const uint32_t ts = tmem + L::S_ + t * L::BUF, tp = tmem + L::P_ + t * L::BUF, to = tmem + L::DQ_ + t * D;
         const uint64_t dq = desc_rows(base + L::Q_ + t * L::QTILE), dg = desc_rows(base + L::G_ + t * L::QTILE);
         const uint64_t dk = desc_rows(base + L::K_), dv = desc_rows(base + L::V_), dkc = desc_cols(base + L::K_, L::KPANEL);
+        if (boxes && nt > 0) wait(qfull + t, 0, guard);
         for (int g = 0, it = 0, j = 0; g < total; ++g, j = j + 1 == n ? 0 : j + 1) {   // g: block of the ring, it: of this tile
             const int s = g % L::STAGES;
             if (j >= nt) {   // a block that only the other tile sees (as in the forward)
@@ -552,8 +568,12 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             wait(done + t, (passes * nt - 1) & 1, guard);
             tc_fence_after();
             if (!warp_up(guard)) {
-                store_rows<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)b.dq,
-                              real ? row_at(i) : -1, tid & 127);
+                if (boxes && first + t * L::QR + L::QR <= all)
+                    store_box<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, &tm_dq, hk * r,
+                                 (int)t0 + (first + t * L::QR) / r, tid & 127, 1 + t);
+                else
+                    store_rows<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)b.dq,
+                                  real ? row_at(i) : -1, tid & 127);
             }
         }
     }
@@ -570,10 +590,13 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float* nlse, int* stat
     const int64_t T = s.tokens();
     const int r = a.H / a.Hkv;
     float* ndelta = nlse + T * a.H;
-    CUtensorMap k128, v128, k64, v64, q, g;
+    CUtensorMap k128, v128, k64, v64, q, g, q128{}, g128{}, dq{};
+    const bool boxes = box_rows(r);
     if (!make_map(&k128, a.k, T, a.Hkv, D, 64, 1, 128) || !make_map(&v128, a.v, T, a.Hkv, D, 64, 1, 128) ||
         !make_map(&k64, a.k, T, a.Hkv, D, 64, 1, 64) || !make_map(&v64, a.v, T, a.Hkv, D, 64, 1, 64) ||
-        !make_map(&q, a.q, T, a.H, D, 64, r, 64 / r) || !make_map(&g, b.dout, T, a.H, D, 64, r, 64 / r))
+        !make_map(&q, a.q, T, a.H, D, 64, r, 64 / r) || !make_map(&g, b.dout, T, a.H, D, 64, r, 64 / r) ||
+        (boxes && (!make_map(&q128, a.q, T, a.H, D, 64, r, 128 / r) || !make_map(&g128, b.dout, T, a.H, D, 64, r, 128 / r) ||
+                   !make_map(&dq, b.dq, T, a.H, D, 64, r, 128 / r))))
         return cudaErrorInvalidValue;
     cudaError_t e = allow_smem<attn_bwd_keys_kernel<D>>(Keys<D>::SMEM);
     if (e == cudaSuccess) e = allow_smem<attn_bwd_rows_kernel<D>>(Dq<D>::SMEM);
@@ -589,7 +612,7 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float* nlse, int* stat
         ProfileScope prof("attn_bwd_rows", st);
         count_launch();
         const int64_t ctas = make_tiles(tiles, s, a.Hkv, r, 256);
-        attn_bwd_rows_kernel<D><<<(unsigned)ctas, 384, Dq<D>::SMEM, st>>>(k64, v64, b, s, tiles, nlse, ndelta, status);
+        attn_bwd_rows_kernel<D><<<(unsigned)ctas, 384, Dq<D>::SMEM, st>>>(k64, v64, q128, g128, dq, boxes, b, s, tiles, nlse, ndelta, status);
     }
     {
         ProfileScope prof("attn_bwd_keys", st);
