@@ -10,14 +10,14 @@ from __future__ import annotations
 
 import torch
 
-from .gdn import _packed, check_tensors, launch, ptr, scratch
+from .gdn import _packed, check_tensors, empty, launch, ptr, scratch
 from .kda import _check, _code, _dtype_code, load_library
 
 
 def _sizes(q, k, dims):
-    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != dims or k.dim() != dims:
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.ndim != dims or k.ndim != dims:
         raise ValueError(f"q and k must have {dims} dimensions")
-    (H, D), Hkv = q.shape[-2:], k.shape[-2]
+    (*_, H, D), Hkv = q.shape, k.shape[-2]
     if Hkv == 0 or H % Hkv:
         raise ValueError(f"{H} query heads cannot share {Hkv} key/value heads")
     return H, Hkv, D
@@ -26,14 +26,15 @@ def _sizes(q, k, dims):
 def _forward(q, k, v, seqs, scale, o, lse, want_lse, stream, fn, dims):
     H, Hkv, D = _sizes(q, k, dims)
     dt = _dtype_code(q)
-    kv = (*q.shape[:-2], Hkv, D)
-    index = check_tensors(q, [("q", q, q.shape, q.dtype), ("k", k, kv, q.dtype), ("v", v, kv, q.dtype),
-                              ("o", o, q.shape, q.dtype), ("lse", lse, q.shape[:-1], torch.float32)])
+    shape, dtype = q.shape, q.dtype
+    kv, rows = (*shape[:-2], Hkv, D), shape[:-1]
+    index = check_tensors(q, [("q", q, shape, dtype), ("k", k, kv, dtype), ("v", v, kv, dtype), ("o", o, shape, dtype),
+                              ("lse", lse, rows, torch.float32)])
     lib = load_library()
 
     def body(s):
         out = torch.empty_like(q) if o is None else o
-        sums = q.new_empty(q.shape[:-1], dtype=torch.float32) if lse is None and want_lse else lse
+        sums = empty(q, rows) if lse is None and want_lse else lse
         _check(fn, getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(out), ptr(sums), *seqs, H, Hkv, D,
                                     D ** -0.5 if scale is None else float(scale), dt, s))
         return out, sums

@@ -51,6 +51,16 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def empty(like, shape, dtype=torch.float32):
+    """A contiguous tensor of another type on like's device (given its strides it takes the host half as long as
+    from new_empty with a type)."""
+    strides, step = [], 1
+    for n in shape[::-1]:
+        strides.append(step)
+        step *= n or 1
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=like.device)
+
+
 def launch(index, stream, body):
     """body(stream handle) with the tensors' device and the launching stream current, so that what a
     call allocates belongs to the stream it runs on."""
@@ -73,7 +83,7 @@ def scratch(workspace, need, like):
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
         return None, None, 0
-    t = like.new_empty(need, dtype=torch.uint8)
+    t = empty(like, (need,), torch.uint8)
     return t, t.data_ptr(), need
 
 
@@ -127,7 +137,7 @@ def _forward(q, k, v, g, beta, S0, lead, rows, seqs, need, o, S_T, want_state, w
 
     def body(s):
         out = torch.empty_like(v) if o is None else o
-        final = q.new_empty(state, dtype=torch.float32) if S_T is None and want_state else S_T
+        final = empty(q, state) if S_T is None and want_state else S_T
         keep, ws, ws_bytes = scratch(workspace, need(lib, Hk, Hv, Dk, Dv, dt), q)
         _check(fn, getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), ptr(S0), ptr(out), ptr(final), *seqs,
                                     Hk, Hv, Dk, Dv, dt, ws, ws_bytes, s))
@@ -178,7 +188,7 @@ def _backward(q, k, v, g, beta, do, S0, dS_T, lead, rows, seqs, need, want_dS0, 
         d = given
         if out is None:
             d = (*(torch.empty_like(t) for t in (q, k, v, g, beta)),
-                 q.new_empty(state, dtype=torch.float32) if want_dS0 else None)
+                 empty(q, state) if want_dS0 else None)
         keep, ws, ws_bytes = scratch(workspace, need(lib, Hk, Hv, Dk, Dv, dt), q)
         _check(fn, getattr(lib, fn)(ptr(q), ptr(k), ptr(v), ptr(g), ptr(beta), ptr(S0), ptr(do), ptr(dS_T),
                                     *map(ptr, d), *seqs, Hk, Hv, Dk, Dv, dt, ws, ws_bytes, s))
