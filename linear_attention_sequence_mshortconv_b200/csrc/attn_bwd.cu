@@ -567,12 +567,11 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         if (nt > 0) {
             wait(done + t, (passes * nt - 1) & 1, guard);
             tc_fence_after();
-            if (!warp_up(guard)) {
-                if (boxes && first + t * L::QR + L::QR <= all)
-                    store_box<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, &tm_dq, hk * r,
-                                 (int)t0 + (first + t * L::QR) / r, tid & 127, 1 + t);
-                else
-                    store_rows<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)b.dq,
+            if (boxes && first + t * L::QR + L::QR <= all) {   // (after a timeout too, as in the forward)
+                store_box<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, &tm_dq, hk * r,
+                             (int)t0 + (first + t * L::QR) / r, tid & 127, 1 + t);
+            } else if (!warp_up(guard)) {
+                store_rows<D>(tmem + L::DQ_ + t * D + lanes, a.scale, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)b.dq,
                                   real ? row_at(i) : -1, tid & 127);
             }
         }

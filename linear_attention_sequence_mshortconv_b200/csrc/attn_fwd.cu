@@ -314,13 +314,13 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (nt > 0) {
             wait(pvdone + 2 * t + ((nt - 1) & 1), ((nt - 1) >> 1) & 1, guard);
             tc_fence_after();
+            // every product that read Q has ended: its tile takes the output
+            const bool whole = boxes && first + t * QR + QR <= all;
+            if (whole)   // (after a timeout too: the four warps meet in it, and may see the flag at different times)
+                store_box<D>(to, 1.f / sum, sm + L::Q_ + t * L::QTILE, &tm_o, hk * r, (int)t0 + (first + t * QR) / r, tid & 127, 1 + t);
             if (!warp_up(guard)) {
-                // every product that read Q has ended: its tile takes the output
                 const int64_t off = real ? row_at(i) : -1;
-                if (boxes && first + t * QR + QR <= all)
-                    store_box<D>(to, 1.f / sum, sm + L::Q_ + t * L::QTILE, &tm_o, hk * r, (int)t0 + (first + t * QR) / r, tid & 127, 1 + t);
-                else
-                    store_rows<D>(to, 1.f / sum, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)a.o, off, tid & 127);
+                if (!whole) store_rows<D>(to, 1.f / sum, sm + L::Q_ + t * L::QTILE, (__nv_bfloat16*)a.o, off, tid & 127);
                 if (real && a.lse) a.lse[off / D] = (ref * sl + log2f(sum)) * kLn2;
             }
         }
