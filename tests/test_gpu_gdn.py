@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import mixers_ref as R
-from linear_attention_sequence_mshortconv_b200 import gdn, kda
+from linear_attention_sequence_mshortconv_b200 import attention, gdn, kda
 
 pytestmark = pytest.mark.gpu
 BF16_TOL, BF16_GRAD_TOL, FP32_TOL = 2 * 2.0 ** -8, 3 * 2.0 ** -8, 128 * 2.0 ** -24
@@ -422,6 +422,30 @@ def test_many_heads_captured_and_on_two_streams():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(u, w) for u, w in zip(out, want[1]))
+    assert kda.last_device_error() == 0
+
+
+def test_beside_attention_on_another_stream():
+    """Kernels of both mixers, each with all of its tensor memory, at once."""
+    lens = [1000, 65, 300]
+    cu = R.offsets(lens)
+    x, S0, do, dS = make(lens, 16, 32, 128, 128, torch.bfloat16, seed=70)
+    x, S0, do, dS = cuda(x), S0.cuda(), do.cuda(), dS.cuda()
+    gen = torch.Generator().manual_seed(71)
+    q, k, v, dO = (torch.randn(sum(lens), H, 128, generator=gen).to(torch.bfloat16).cuda() for H in (16, 4, 4, 16))
+    lse_o = attention.forward_varlen(q, k, v, cu)
+
+    def both(a, b):
+        return ((*gdn.forward_varlen(*x, cu, S0, stream=a), *gdn.backward_varlen(*x, do, cu, S0, dS, stream=a)),
+                (*attention.forward_varlen(q, k, v, cu, stream=b), *attention.backward_varlen(q, k, v, *lse_o, dO, cu, stream=b)))
+
+    want = both(None, None)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(6):
+        got = both(a, b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, w) for g, n in zip(got, want) for u, w in zip(g, n))
     assert kda.last_device_error() == 0
 
 
