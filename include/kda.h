@@ -457,6 +457,8 @@ kda_status gdn_forward_varlen(const void* q, const void* k, const void* v, const
  *          of a query/key head in a fixed order: results do not change from run to run.
  *   dS0  : [B, Hv, Dk, Dv] fp32, written, or NULL.
  * The gradient of g is that of the logarithm (alpha = e^g).  The call reruns the forward.
+ * A value that is not finite at one token, a gate among them, may reach the gradients of every
+ * token of its row, but never another row's.
  * workspace : gdn_backward_workspace_size(...) bytes.  Errors: as gdn_forward.
  * gdn_backward_varlen -- the same over packed samples.
  */

@@ -95,8 +95,7 @@ __global__ void __launch_bounds__(128, 5) gdn_prologue_kernel(GdnArgs a, const _
         for (int i = 0; i < 2; ++i) {
             const int t = 2 * lane + i;
             const int64_t off = (t0 + t) * a.Hv + h;
-            // e^g is 0 in fp32 below -104: the clamp keeps sums finite for g = -inf
-            s[i] = t < valid ? (double)fmaxf(to_f32(((const __nv_bfloat16*)a.g)[off]), -1000.f) : 0.0;
+            s[i] = t < valid ? (double)finite_gate(to_f32(((const __nv_bfloat16*)a.g)[off])) : 0.0;
             b[i] = t < valid ? to_f32(((const __nv_bfloat16*)a.beta)[off]) : 0.f;
         }
         double sum = s[0] + s[1];

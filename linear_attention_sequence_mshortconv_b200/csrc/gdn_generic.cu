@@ -10,8 +10,7 @@
 namespace kda {
 namespace {
 
-// e^g is 0 in fp32 below about -104; the clamp keeps sums of gates finite for g = -inf.
-__device__ __forceinline__ double gate_of(float g) { return (double)fmaxf(g, -1000.f); }
+__device__ __forceinline__ double gate_of(float g) { return (double)finite_gate(g); }
 
 // ---- forward: one warp per 4 value columns, 8 lanes to a column ------------------------
 // A lane holds Dk / 8 entries of its column of S in registers.  Four tokens at a time: their products with the

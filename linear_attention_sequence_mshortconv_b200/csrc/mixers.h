@@ -68,6 +68,10 @@ cudaError_t allow_smem(int bytes)
 }
 
 // ---- gated delta rule ---------------------------------------------------------------
+// e^g is 0 in fp32 below about -104: the clamp keeps sums of gates finite for g = -inf.  (Not by fmaxf, which
+// would take a gate that is not a number for the bound: its state and all that follows are not numbers either.)
+__device__ __forceinline__ float finite_gate(float g) { return g < -1000.f ? -1000.f : g; }
+
 struct GdnArgs {
     const void *q, *k, *v, *g, *beta;   // [tokens, Hk, Dk] x 2, [tokens, Hv, Dv], [tokens, Hv] x 2
     const float* S0;                    // [sequences, Hv, Dk, Dv] or null

@@ -1,0 +1,64 @@
+"""The gated delta rule and causal attention on the GPU where they can go wrong.  Tolerances as in test_gpu_gdn.py and
+test_gpu_attention.py, or derived beside the test."""
+import numpy as np
+import pytest
+import torch
+
+import mixers_ref as R
+from linear_attention_sequence_mshortconv_b200 import gdn, kda
+from test_gpu_gdn import PIECES, cuda, kernels, make, make_step
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- a gate that is not a number ---------------------------------------------------------------------------------------
+def same_where_finite(got, clean, nan, free):
+    """`got` is NaN where `nan` says so and bit-equal to `clean` elsewhere; entries marked `free` may be either."""
+    got, clean = R.f64(got), R.f64(clean)
+    assert np.isnan(got[nan & ~free]).all() and (got == clean)[~nan & ~free].all() and not np.isnan(clean).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H,Dk,Dv", [(2, 32, 32), (2, 64, 128), (2, 128, 32), (40, 64, 64), (40, 128, 128)])
+def test_a_gate_that_is_not_a_number(H, Dk, Dv, dtype):
+    """One NaN gate: by the recurrence the state and the outputs of its head are NaN from its token on, and every
+    gradient that passes through one of the states.  The rest of its 64-token chunk may be as well; nothing else."""
+    lens, at, chunk = [150, 70], 75, slice(64, 128)
+    x, S0, do, dS = make(lens, H, H, Dk, Dv, dtype, seed=17)
+    args = lambda t: (*cuda(t), do.cuda(), R.offsets(lens), S0.cuda(), dS.cuda())   # noqa: E731
+    clean = gdn.backward_varlen(*args(x))
+    clean_o, clean_S = gdn.forward_varlen(*cuda(x), R.offsets(lens), S0.cuda())
+    x[3][at, 1] = float("nan")
+    ref_o, ref_S = R.gdn(*map(R.f64, x), lens, R.f64(S0))
+    ref = R.gdn_backward(*map(R.f64, x), R.f64(do), lens, R.f64(S0), R.f64(dS))
+    assert np.isnan(ref_S[0, 1]).all() and np.isnan(ref_o[at:150, 1]).all() and np.isnan(ref[3][:150, 1]).all()
+    o, S = gdn.forward_varlen(*cuda(x), R.offsets(lens), S0.cuda())
+    for a, b, want in ((o, clean_o, ref_o), *zip(gdn.backward_varlen(*args(x))[:5], clean, ref)):
+        free = np.zeros(want.shape, bool)
+        free[chunk, 1] = True
+        same_where_finite(a, b, np.isnan(want), free)
+    assert np.isnan(R.f64(o)[at:150, 1]).all()
+    same_where_finite(S, clean_S, np.isnan(ref_S), np.zeros(ref_S.shape, bool))
+    assert kda.last_device_error() == 0
+
+
+def test_a_gate_that_is_not_a_number_in_a_long_sample():
+    lens, at = [6000], 3000
+    x, S0, _, _ = make(lens, 2, 2, 64, 64, torch.bfloat16, seed=18, g_scale=0.02)
+    (clean, clean_S), ran = kernels(PIECES, lambda: gdn.forward_varlen(*cuda(x), R.offsets(lens), S0.cuda()))
+    assert ran == PIECES
+    x[3][at, 1] = float("nan")
+    o, S = gdn.forward_varlen(*cuda(x), R.offsets(lens), S0.cuda())
+    first = at // 64 * 64
+    assert torch.equal(o[:, 0], clean[:, 0]) and torch.equal(o[:first, 1], clean[:first, 1]) and torch.equal(S[0, 0], clean_S[0, 0])
+    assert bool(o[at:, 1].isnan().all()) and bool(S[0, 1].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_gate_that_is_not_a_number_in_a_step(dtype):
+    x, state, at = make_step(3, 5, 2, 2, 64, 64, dtype)
+    x[3][1, 0] = float("nan")
+    S = state.cuda()
+    o = gdn.step(*cuda(x), S, at.cuda())
+    assert bool(o[1, 0].isnan().all()) and bool(S[int(at[1]), 0].isnan().all())
+    assert int(o.isnan().sum()) == 64 and int(S.isnan().sum()) == 64 * 64
