@@ -507,6 +507,8 @@ kda_status gdn_step(const void* q, const void* k, const void* v, const void* g, 
  * weights e^{s - max} are rounded to bf16 for the product with v.  A value that is not finite
  * at one token may reach the earlier tokens of the same row that share its 128-token tile,
  * and every later one, but never another row.
+ * Scores of -inf, or near fp32's lowest value, have weight 0 beside others; a row whose every
+ * score is -inf has o NaN and lse -inf.
  * attn_forward_varlen -- packed samples, cu_seqlens as for gdn_forward_varlen.
  * Errors: KDA_ERR_INVALID_ARG (null tensor with work to do, bad sizes or dtype, H not a
  * multiple of Hkv, scale not finite), KDA_ERR_UNSUPPORTED (D; B or H > 65535; more than
@@ -523,6 +525,8 @@ kda_status attn_forward_varlen(const void* q, const void* k, const void* v, void
  *   d_o : [B, T, H, D] dtype;  dq, dk, dv : written, with the shapes and dtype of q, k, v
  *   (accumulated in fp32, rounded once; dk and dv are summed over the query heads of a
  *   group in a fixed order: results do not change from run to run).
+ * The weights are taken as e^{s - lse}: a relative error of |lse| 2^-23 or so, which leaves no
+ * gradient to a row whose every score is beyond 2^23 or so in magnitude.
  *   workspace : attn_backward_workspace_size(tokens = B * T, ...) bytes, as for kda_forward.
  * attn_backward_varlen -- packed samples (workspace for tokens = cu_seqlens[n_seqs]).
  * Errors: as attn_forward, and KDA_ERR_WORKSPACE.

@@ -273,25 +273,36 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     if (x > seen) s[x] = -INFINITY;
             }
             const float top = max_of(s);
-            if (j == 0) {
-                ref = top;
-            } else if (__any_sync(~0u, (top - ref) * sl > 8.f)) {
+            if (j == 0) ref = top;
+            float off = -ref * sl;
+            if (__any_sync(~0u, (top - ref) * sl > 8.f || fabsf(off) > 1048576.f)) {
                 const bool grown = (top - ref) * sl > 8.f;
-                const float f = grown ? ex2_approx((ref - top) * sl) : 1.f;
-                if (grown) ref = top;
-                sum *= f;
-                wait(pvdone + (w ^ 1), ((j - 1) >> 1) & 1, guard);
-                tc_fence_after();
+                if (__any_sync(~0u, grown)) {
+                    const float f = grown ? ex2_approx((ref - top) * sl) : 1.f;
+                    if (grown) ref = top;
+                    off = -ref * sl;
+                    sum *= f;
+                    wait(pvdone + (w ^ 1), ((j - 1) >> 1) & 1, guard);
+                    tc_fence_after();
 #pragma unroll
-                for (int x = 0; x < D; x += 32) {
-                    float o[32];
-                    tmem_ld32(to + x, o);
+                    for (int x = 0; x < D; x += 32) {
+                        float o[32];
+                        tmem_ld32(to + x, o);
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] *= f;
-                    tmem_st32(to + x, o);
+                        for (int y = 0; y < 32; ++y) o[y] *= f;
+                        tmem_st32(to + x, o);
+                    }
+                }
+                // Far from 0 the product's rounding would be more than the exponent itself (and -inf less -inf is no
+                // number): such a reference is taken off the scores, and a row that has seen only -inf has none.
+                if (__any_sync(~0u, fabsf(off) > 1048576.f)) {
+                    const float from = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) s[x] -= from;
+                    off = 0.f;
                 }
             }
-            const uint64_t sl2 = pair(sl, sl), off2 = pair(-ref * sl, -ref * sl);
+            const uint64_t sl2 = pair(sl, sl), off2 = pair(off, off);
             uint64_t z = 0, y = 0;
             uint32_t p[32];
 #pragma unroll

@@ -5,7 +5,9 @@ import pytest
 import torch
 
 import mixers_ref as R
-from linear_attention_sequence_mshortconv_b200 import gdn, kda
+from linear_attention_sequence_mshortconv_b200 import attention, gdn, kda
+from test_gpu_attention import FP32, FWD
+from test_gpu_attention import make as make_attention
 from test_gpu_gdn import PIECES, cuda, kernels, make, make_step
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +64,27 @@ def test_a_gate_that_is_not_a_number_in_a_step(dtype):
     o = gdn.step(*cuda(x), S, at.cuda())
     assert bool(o[1, 0].isnan().all()) and bool(S[int(at[1]), 0].isnan().all())
     assert int(o.isnan().sum()) == 64 and int(S.isnan().sum()) == 64 * 64
+
+
+# ---- scores of minus infinity ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D,H,masked,value,scale", [
+    (64, 2, 130, -np.inf, None), (128, 4, 64, -np.inf, None), (64, 3, 200, -np.inf, -0.1), (128, 2, 1, -np.inf, 0.2),
+    (64, 2, 130, torch.finfo(torch.bfloat16).min, None), (64, 2, 130, torch.finfo(torch.bfloat16).min, 1.0)], ids=str)
+def test_keys_scored_minus_infinity(D, H, masked, value, scale, dtype):
+    """The first keys score minus infinity (or the type's lowest value) with every query, over whole blocks: the rows that
+    see other keys take those alone, and the rows that see none have no sum."""
+    lens = [300]
+    q, k, v, _ = make_attention(lens, H, 1, D, dtype, seed=21)
+    q[..., 0] = 1.0 if (scale or 1) > 0 else -1.0
+    k[:masked, :, 0] = value
+    far = k.clone()
+    far[:masked, :, 0] = -1e5   # e^-10000 is 0 in 64 bits too
+    ref_o, ref_lse = R.attention(*map(R.f64, (q, far, v)), lens, scale)
+    o, lse = attention.forward_varlen(*cuda((q, k, v)), R.offsets(lens), scale=scale)
+    assert R.norm_error(o[masked:], ref_o[masked:]) <= (FP32 if dtype == torch.float32 else FWD)
+    top = float(max(1.0, np.abs(ref_lse[masked:]).max(), abs(scale or D ** -0.5) * q.double().norm(dim=-1).max() * k[masked:].double().norm(dim=-1).max()))
+    assert np.abs(R.f64(lse)[masked:] - ref_lse[masked:]).max() <= 16 * 2.0 ** -24 * top
+    if value == -np.inf:
+        assert bool((lse[:masked] == -np.inf).all()) and bool(o[:masked].isnan().all())
+    assert kda.last_device_error() == 0
