@@ -566,6 +566,8 @@ uint64_t kda_kernel_launches(void);
  * how the timeout handling is exercised without a fault or a hang).  While `on` is
  * non-zero, every later launch of the tensor-core scan withholds, in each CTA, the
  * first "every tile of the chunk ready" signal to the warps that run the state chain.
+ * The kernels of the gated delta rule and of attention that wait in this way have one barrier
+ * each that expects an arrival which never comes.
  * Their bounded wait (2 s) then runs out: the CTA records the timeout in the device
  * status word, stops waiting, drains its own tensor-core and TMA work, frees its tensor
  * memory and exits.  The call still returns KDA_OK (errors on the device are reported

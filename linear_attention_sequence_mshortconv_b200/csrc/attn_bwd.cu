@@ -59,14 +59,6 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(AttnArgs a, const __nv_
     }
 }
 
-// What an issuing warp does on the way out after a timeout: leave nothing in flight.
-__device__ __forceinline__ void drain_mma(uint64_t* bar, const Guard& guard)
-{
-    if (!warp_up(guard)) return;
-    if (elect()) umma_commit(bar);
-    mbar_wait_bounded(bar, 0, kWaitNs);
-}
-
 // ---- dk and dv ------------------------------------------------------------------------------
 // Keys are rows of every product: S^T = K Q^T and dP^T = V dO^T for 64 rows at a time, then
 // dV += P^T dO and dK += dS^T Q with P^T and dS^T read from tensor memory.  Two buffers of
@@ -91,7 +83,7 @@ template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g, AttnBwdArgs b,
-                     const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, const float* ndelta, int* status)
+                     const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, const float* ndelta, int* status, int drop)
 {
     using L = Keys<D>;
     const AttnArgs& a = b.f;
@@ -132,7 +124,7 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             for (int i = 0; i < 2; ++i) {
                 mbar_init(sfull + i, 1);
                 mbar_init(gfull + i, 1);
-                mbar_init(pready + i, 128);
+                mbar_init(pready + i, 128 + 32 * drop);
                 mbar_init(dready + i, 128);
                 mbar_init(done + i, 1);
                 mbar_init(drain + i, 1);
@@ -172,10 +164,8 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (guard.up()) break;
                 load(issued);
             }
-            if (guard.up()) {
-                mbar_wait_bounded(kvfull, 0, kWaitNs);
-                drain_ring(full, L::STAGES, issued);
-            }
+            mbar_wait_bounded(kvfull, 0, kWaitNs);
+            drain_ring(full, L::STAGES, issued);
         }
         __syncwarp();
         // rows of the last tile past the end: their weights are 0, but 0 times a value that is not
@@ -212,7 +202,7 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 umma_commit(gfull + w);
             }
         }
-        drain_mma(drain + 1, guard);
+        drain_mma(drain + 1);
     } else if (warp == 8) {   // dV and dK
         const uint32_t id_o = idesc_f16(L::KEYS, D, false, true, false, true);
         const uint64_t dq = desc_cols(base + L::Q_, L::RPANEL), dg = desc_cols(base + L::G_, L::RPANEL);
@@ -236,7 +226,7 @@ attn_bwd_keys_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (j == n - 1) umma_commit(all_done);
             }
         }
-        drain_mma(drain, guard);
+        drain_mma(drain);
     } else {
         const int w = warp >> 2, key = key0 + (tid & 127);
         const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
@@ -345,7 +335,7 @@ template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_g, const __grid_constant__ CUtensorMap tm_dq, bool boxes, AttnBwdArgs b,
-                     const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, float* ndelta, int* status)
+                     const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, const float* nlse, float* ndelta, int* status, int drop)
 {
     using L = Dq<D>;
     const AttnArgs& a = b.f;
@@ -391,7 +381,7 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             for (int i = 0; i < 2; ++i) {
                 mbar_init(sfull + i, 1);
                 mbar_init(gfull + i, 1);
-                mbar_init(dready + i, 128);
+                mbar_init(dready + i, 128 + 32 * drop);
                 mbar_init(done + i, 1);
                 mbar_init(drain + i, 1);
                 mbar_init(qfull + i, 1);
@@ -440,10 +430,8 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 if (guard.up()) break;
                 load(issued);
             }
-            if (guard.up()) {
-                for (int t = 0; boxes && t < 2 && first + t * L::QR < all; ++t) mbar_wait_bounded(qfull + t, 0, kWaitNs);
-                drain_ring(full, L::STAGES, issued);
-            }
+            for (int t = 0; boxes && t < 2 && first + t * L::QR < all; ++t) mbar_wait_bounded(qfull + t, 0, kWaitNs);
+            drain_ring(full, L::STAGES, issued);
         }
         __syncwarp();
         if (warp == 10 && tail < L::KB && !guard.up()) {   // keys past the end (dS is 0 there): K must be finite
@@ -502,7 +490,7 @@ attn_bwd_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             ++it;
         }
         __syncwarp();
-        drain_mma(drain + t, guard);
+        drain_mma(drain + t);
     } else {
         const int t = warp >> 2, nt = t ? n1 : n0;
         const uint32_t i = first + t * L::QR + (tid & 127);
@@ -611,13 +599,13 @@ cudaError_t backward(const AttnBwdArgs& b, const Seqs& s, float* nlse, int* stat
         ProfileScope prof("attn_bwd_rows", st);
         count_launch();
         const int64_t ctas = make_tiles(tiles, s, a.Hkv, r, 256);
-        attn_bwd_rows_kernel<D><<<(unsigned)ctas, 384, Dq<D>::SMEM, st>>>(k64, v64, q128, g128, dq, boxes, b, s, tiles, nlse, ndelta, status);
+        attn_bwd_rows_kernel<D><<<(unsigned)ctas, 384, Dq<D>::SMEM, st>>>(k64, v64, q128, g128, dq, boxes, b, s, tiles, nlse, ndelta, status, debug_drop_handoff());
     }
     {
         ProfileScope prof("attn_bwd_keys", st);
         count_launch();
         const int64_t ctas = make_tiles(tiles, s, a.Hkv, 1, 128);
-        attn_bwd_keys_kernel<D><<<(unsigned)ctas, 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, tiles, nlse, ndelta, status);
+        attn_bwd_keys_kernel<D><<<(unsigned)ctas, 384, Keys<D>::SMEM, st>>>(k128, v128, q, g, b, s, tiles, nlse, ndelta, status, debug_drop_handoff());
     }
     return cudaGetLastError();
 }

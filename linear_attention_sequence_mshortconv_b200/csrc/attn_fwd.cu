@@ -63,7 +63,7 @@ template <int D>
 __global__ void __launch_bounds__(384, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ CUtensorMap tm_o, bool boxes, AttnArgs a,
-                const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, int* status)
+                const __grid_constant__ Seqs seqs, const __grid_constant__ Tiles tiles, int* status, int drop)
 {
     using L = Fwd<D>;
     extern __shared__ char raw[];
@@ -113,7 +113,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
             for (int i = 0; i < 4; ++i) {   // 2 x tile + buffer
                 mbar_init(sfull + i, 1);
-                mbar_init(pready + i, QR);
+                mbar_init(pready + i, QR + 32 * drop);
                 mbar_init(pvdone + i, 1);
             }
             mbar_init(vfix, 32);
@@ -169,11 +169,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 load_v(j);
                 ++v_issued;
             }
-            if (guard.up()) {
-                for (int t = 0; boxes && t < 2 && first + t * QR < all; ++t) mbar_wait_bounded(qfull + t, 0, kWaitNs);
-                drain_ring(kfull, L::STAGES, k_issued);
-                drain_ring(vfull, L::STAGES, v_issued);
-            }
+            for (int t = 0; boxes && t < 2 && first + t * QR < all; ++t) mbar_wait_bounded(qfull + t, 0, kWaitNs);
+            drain_ring(kfull, L::STAGES, k_issued);
+            drain_ring(vfull, L::STAGES, v_issued);
         }
         __syncwarp();
         // The last block's rows past the end hold the next sequence, or nothing: their weights are
@@ -244,10 +242,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             }
         }
         __syncwarp();
-        if (warp_up(guard)) {   // leave nothing in flight
-            if (elect()) umma_commit(drain + t);
-            mbar_wait_bounded(drain + t, 0, kWaitNs);
-        }
+        drain_mma(drain + t);
     } else {
         const int t = warp >> 2, nt = t ? n1 : n0;
         const uint32_t i = first + t * QR + (tid & 127);
@@ -358,7 +353,7 @@ cudaError_t forward(const AttnArgs& a, const Seqs& s, int* status, cudaStream_t 
     const int64_t ctas = make_tiles(tiles, s, a.Hkv, r, 2 * QR);
     ProfileScope prof("attn_fwd", st);
     count_launch();
-    attn_fwd_kernel<D><<<(unsigned)ctas, L::THREADS, L::SMEM, st>>>(k, v, q, o, boxes, a, s, tiles, status);
+    attn_fwd_kernel<D><<<(unsigned)ctas, L::THREADS, L::SMEM, st>>>(k, v, q, o, boxes, a, s, tiles, status, debug_drop_handoff());
     return cudaGetLastError();
 }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }

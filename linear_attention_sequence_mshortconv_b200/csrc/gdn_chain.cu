@@ -60,7 +60,7 @@ __host__ __device__ constexpr int y_at(int p, int x) { return (p < 2 ? p * 16 : 
 template <int DK, int DV, int MODE>
 __global__ void __launch_bounds__(448, 1)
 gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv,
-                 GdnArgs a, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status)
+                 GdnArgs a, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status, int drop)
 {
     using L = Chain<DK, DV, MODE>;
     constexpr bool KEEP = L::KEEP, READ = L::READ, HAS_V = L::HAS_V;
@@ -89,7 +89,8 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 mbar_init(full + i, 1);
                 mbar_init(empty + i, READ ? 13 : 9);   // the MMAs, and each warp that reads the stage
                 for (uint64_t* b : {ks_done, ty_done, s_done}) mbar_init(b + i, 1);
-                for (uint64_t* b : {y_ready, u_ready, s_ready}) mbar_init(b + i, 4);
+                mbar_init(y_ready + i, 4 + drop);
+                for (uint64_t* b : {u_ready, s_ready}) mbar_init(b + i, 4);
             }
             for (uint64_t* b : {landed, qs_done, o_done, s_free, u_free, drain}) mbar_init(b, 1);
             for (uint64_t* b : {o_scaled, o_read}) mbar_init(b, 4);
@@ -157,9 +158,8 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 warp_arrive(full + (c & 1));
             }
         }
-        if (warp_up(guard))   // whole chunks still on their way
-            for (int c = max(0, issued - 2); c < issued; ++c)
-                if (len - c * C >= C) mbar_wait_bounded(full + (c & 1), (c >> 1) & 1, kWaitNs);
+        drain_ring(full, 2, issued);
+        if (issued == nch && len % C != 0) mbar_wait_bounded(landed, 0, kWaitNs);
     } else if (warp == 12) {
         const uint64_t dk = desc_rows(base + L::K_), dq = desc_rows(base + L::Q_), dkc = desc_cols(base + L::K_, PANEL);
         const uint64_t dv = desc_cols(base + L::V_, PANEL), de = desc_rows(base + L::EYE);
@@ -265,10 +265,7 @@ gdn_chain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
             if (elect()) umma_commit(empty + (c & 1));
         }
-        if (warp_up(guard)) {
-            if (elect()) umma_commit(drain);
-            mbar_wait_bounded(drain, 0, kWaitNs);
-        }
+        drain_mma(drain);
     } else if (warp < 8) {
         constexpr int HK = DK / 2;   // key channels of a warpgroup's half of the state
         const int hf = warp >> 2, row = tid & 127;   // row: value column
@@ -471,7 +468,7 @@ cudaError_t chain(const GdnArgs& a, const Seqs& s, const void* records, void* ke
     if (e != cudaSuccess) return e;
     ProfileScope prof(MODE == CHAIN_OUT ? "gdn_chain" : MODE == CHAIN_KEEP ? "gdn_chain_keep" : MODE == CHAIN_STATE ? "gdn_chain_state" : "gdn_chain_transition", st);
     count_launch();
-    gdn_chain_kernel<DK, DV, MODE><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, v, a, s, (const char*)records, (char*)kept, status);
+    gdn_chain_kernel<DK, DV, MODE><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, v, a, s, (const char*)records, (char*)kept, status, debug_drop_handoff());
     return cudaGetLastError();
 }
 template <int MODE>

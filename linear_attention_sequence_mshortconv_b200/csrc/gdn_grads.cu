@@ -79,7 +79,7 @@ __device__ __forceinline__ float at_least(float beta) { return fabsf(beta) < 5.9
 template <int DK, int DV>
 __global__ void __launch_bounds__(704, 1)
 gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
-                  GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status)
+                  GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status, int drop)
 {
     using L = TGrads<DK, DV>;
     const GdnArgs& a = b.f;
@@ -102,7 +102,8 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             for (uint64_t* x : {kq_full, y_full, u_full, u_empty, s_full, s_done, d_full, landed, e_done, drain}) mbar_init(x, 1);
             for (uint64_t* x : {y_empty, out_done}) mbar_init(x, 5);            // the MMAs and warps 0-3
             for (uint64_t* x : {d_empty, kq_empty}) mbar_init(x, 17);           // the MMAs and warps 4-19
-            for (uint64_t* x : {nm_ready, ry_ready}) mbar_init(x, 4);
+            mbar_init(nm_ready, 4 + drop);
+            mbar_init(ry_ready, 4);
             for (uint64_t* x : {acc_free, sum_free}) mbar_init(x, 16);
             *guard.flag = 0;
             fence_mbar_init();
@@ -201,14 +202,12 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             ++n;
         }
-        if (warp_up(guard)) {   // copies still on their way (those of ragged chunks land on `landed`)
-            if (ragged > 0) mbar_wait_bounded(landed, (ragged - 1) & 1, kWaitNs);
-            if (kq_in > 0) mbar_wait_bounded(kq_full, (kq_in - 1) & 1, kWaitNs);
-            if (y_in > 0) mbar_wait_bounded(y_full, (y_in - 1) & 1, kWaitNs);
-            if (u_in > 0) mbar_wait_bounded(u_full, (u_in - 1) & 1, kWaitNs);
-            if (s_in > 0) mbar_wait_bounded(s_full, (s_in - 1) & 1, kWaitNs);
-            if (d_in > 0) mbar_wait_bounded(d_full, (d_in - 1) & 1, kWaitNs);
-        }
+        drain_ring(landed, 1, ragged);   // (those of ragged chunks land there)
+        drain_ring(kq_full, 1, kq_in);
+        drain_ring(y_full, 1, y_in);
+        drain_ring(u_full, 1, u_in);
+        drain_ring(s_full, 1, s_in);
+        drain_ring(d_full, 1, d_in);
     } else if (warp == 20) {
         constexpr uint32_t id_rows = idesc_f16(128, C, true, false, false, true);    // right operand: its values are K
         constexpr uint32_t id_cols = idesc_f16(128, C, true, true, false, true);     // its rows are K
@@ -284,10 +283,7 @@ gdn_tgrads_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             ++n;
         }
-        if (warp_up(guard)) {
-            if (elect()) umma_commit(drain);
-            mbar_wait_bounded(drain, 0, kWaitNs);
-        }
+        drain_mma(drain);
     } else if (warp < 4) {
         const int j = tid & 63, own = 32 * (warp >> 1);   // token of U, and 32 of the others
         const uint32_t at = tmem + ((uint32_t)warp * 32u << 16);
@@ -556,7 +552,7 @@ cudaError_t tgrads(const GdnBwdArgs& b, const Seqs& s, const void* records, void
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_grads", st);
     count_launch();
-    gdn_tgrads_kernel<DK, DV><<<(unsigned)min(items, (int64_t)sms), L::THREADS, L::SMEM, st>>>(k, q, g, b, s, (const char*)records, (char*)kept, status);
+    gdn_tgrads_kernel<DK, DV><<<(unsigned)min(items, (int64_t)sms), L::THREADS, L::SMEM, st>>>(k, q, g, b, s, (const char*)records, (char*)kept, status, debug_drop_handoff());
     return cudaGetLastError();
 }
 }  // namespace

@@ -52,7 +52,7 @@ __host__ __device__ constexpr int half_at(int p, int x) { return (x >> 1) * 32 +
 template <int DK, int DV>
 __global__ void __launch_bounds__(480, 1)
 gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
-                  const __grid_constant__ CUtensorMap mv, GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status)
+                  const __grid_constant__ CUtensorMap mv, GdnBwdArgs b, const __grid_constant__ Seqs seqs, const char* records, char* kept, int* status, int drop)
 {
     using L = RChain<DK, DV>;
     const GdnArgs& a = b.f;
@@ -82,7 +82,8 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 mbar_init(full + i, 1);
                 mbar_init(empty + i, 13);   // the MMAs, and each warp that reads the gates
                 for (uint64_t* x : {kd_done, ty_done, d_done}) mbar_init(x + i, 1);
-                for (uint64_t* x : {u_ready, v_ready, d_ready}) mbar_init(x + i, 4);
+                mbar_init(u_ready + i, 4 + drop);
+                for (uint64_t* x : {v_ready, d_ready}) mbar_init(x + i, 4);
             }
             for (uint64_t* x : {g_full, landed, w_done, d_free, y_free, drain}) mbar_init(x, 1);
             mbar_init(g_ready, 4);
@@ -120,8 +121,10 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             ++in;
             __syncwarp();
-            if (it >= 1) wait(g_empty, (it - 1) & 1, guard);
-            if (warp_up(guard)) break;
+            if (it >= 1) {   // (the first step's copies go out whole: a ragged chunk's land on one barrier)
+                wait(g_empty, (it - 1) & 1, guard);
+                if (warp_up(guard)) break;
+            }
             if (lane == 0) {
                 uint64_t* bar = valid < C ? landed : g_full;
                 if (valid == C) mbar_arrive_expect_tx(bar, C * DK * 2 + C * DV * 2 + REC_SCAL - REC_P);
@@ -161,12 +164,9 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
                 __syncwarp();
             }
         }
-        if (warp_up(guard)) {   // copies of whole chunks still on their way
-            const bool ragged = len % C != 0;   // the first step's were awaited
-            for (int it = max(ragged ? 1 : 0, in - 2); it < in; ++it) mbar_wait_bounded(full + (it & 1), (it >> 1) & 1, kWaitNs);
-            if (g_in > (ragged ? 1 : 0)) mbar_wait_bounded(g_full, (g_in - 1) & 1, kWaitNs);
-            if (ragged && in > 0) mbar_wait_bounded(landed, 0, kWaitNs);
-        }
+        drain_ring(full, 2, in);
+        drain_ring(g_full, 1, g_in);
+        if (in > 0 && len % C != 0) mbar_wait_bounded(landed, 0, kWaitNs);
     } else if (warp == 12) {
         const uint64_t dk = desc_rows(base + L::K_), dkc = desc_cols(base + L::K_, PANEL), dqc = desc_cols(base + L::Q_, PANEL);
         // T and P as they stand have the rows as K: core matrices 256 bytes apart along it, 128 along the columns
@@ -265,10 +265,7 @@ gdn_rchain_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant_
             }
             if (elect()) umma_commit(empty + (it & 1));
         }
-        if (warp_up(guard)) {
-            if (elect()) umma_commit(drain);
-            mbar_wait_bounded(drain, 0, kWaitNs);
-        }
+        drain_mma(drain);
     } else if (warp < 8) {
         constexpr int HK = DK / 2, NI = HK / 32;   // key channels of a warpgroup's half of the state
         const int hf = warp >> 2, row = tid & 127;   // row: value column
@@ -468,7 +465,7 @@ cudaError_t rchain(const GdnBwdArgs& b, const Seqs& s, const void* records, void
     if (e != cudaSuccess) return e;
     ProfileScope prof("gdn_rchain", st);
     count_launch();
-    gdn_rchain_kernel<DK, DV><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, g, v, b, s, (const char*)records, (char*)kept, status);
+    gdn_rchain_kernel<DK, DV><<<dim3(a.Hv, s.n), L::THREADS, L::SMEM, st>>>(k, q, g, v, b, s, (const char*)records, (char*)kept, status, debug_drop_handoff());
     return cudaGetLastError();
 }
 }  // namespace

@@ -17,7 +17,13 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The first wait that runs out raises the CTA's flag and records DEV_TIMEOUT; from then on no
 // wait waits, no copy is issued, and every role runs to its end (MMAs still issued work on whatever
 // is there).  Warps that use warp-wide instructions or barriers keep their loops whole: the flag
-// is seen by lanes at different times.
+// is seen by lanes at different times.  Nothing may be in flight when the CTA leaves, and a wait may run out
+// after a role has ended: so whoever issues copies or MMAs waits for its last ones at its end, whether
+// the flag is up or not (they need nothing from anyone, so the wait is short).
+//
+// Test hook (the kernels' `drop`): one barrier of a kernel expects the arrivals of a warp more than there are, so the
+// wait for it runs out.  A whole warp's where all lanes of a warp arrive at once: a phase must not turn within such an
+// arrival (128 + 1 ended in a launch failure; without the hook every count is a multiple of what arrives together).
 struct Guard {
     volatile int* flag;
     int* status;
@@ -41,8 +47,7 @@ __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, const Guard
 
 // Whole-warp form for code with warp-wide instructions: the same answer in every lane.
 __device__ __forceinline__ bool warp_up(const Guard& g) { return __any_sync(~0u, g.up()); }
-// After a timeout: the copies issued into a ring (the last STAGES of `issued`) land before the
-// CTA leaves.
+// The copies issued into a ring (the last STAGES of `issued`) have landed.
 __device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int issued)
 {
     for (int j = issued > stages ? issued - stages : 0; j < issued; ++j)
@@ -77,6 +82,13 @@ __device__ __forceinline__ bool elect()
     return r != 0;
 }
 __device__ __forceinline__ int uniform_warp() { return __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0); }
+// The MMAs that the warp has issued have ended; bar: used for nothing else.
+__device__ __forceinline__ void drain_mma(uint64_t* bar)
+{
+    __syncwarp();
+    if (elect()) umma_commit(bar);
+    mbar_wait_bounded(bar, 0, kWaitNs);
+}
 // K-step x (16 values) of an operand whose values are K, and of one whose rows are K
 __device__ __forceinline__ uint64_t step_rows(uint64_t desc, int x, uint32_t panel)
 {
