@@ -229,6 +229,9 @@ def step(q, k, v, g, beta, state, slots=None, *, o=None, stream=None):
     Hk, Hv, Dk, Dv = _sizes(q, v, 1)
     dt = _dtype_code(q)
     n = q.shape[0]
+    for name, t in (("k", k), ("g", g), ("beta", beta)):
+        if t is None:
+            raise TypeError(f"{name} must be a CUDA tensor")
     if not isinstance(state, _Tensor) or state.ndim != 4:
         raise ValueError("state must be [n_slots,Hv,Dk,Dv]")
     n_slots = state.shape[0]

@@ -88,3 +88,13 @@ def test_keys_scored_minus_infinity(D, H, masked, value, scale, dtype):
     if value == -np.inf:
         assert bool((lse[:masked] == -np.inf).all()) and bool(o[:masked].isnan().all())
     assert kda.last_device_error() == 0
+
+
+# ---- calls without a tensor that they need -------------------------------------------------------------------------------
+@pytest.mark.parametrize("which", range(5))
+def test_a_step_without_an_input_is_refused(which):
+    x, state, at = make_step(3, 5, 2, 2, 64, 64, torch.bfloat16)
+    x = cuda(x)
+    x[which] = None
+    with pytest.raises((TypeError, ValueError)):
+        gdn.step(*x, state.cuda(), at.cuda())
