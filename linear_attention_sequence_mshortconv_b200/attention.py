@@ -45,12 +45,16 @@ def _forward(q, k, v, seqs, scale, o, lse, want_lse, stream, fn, dims):
 def forward(q, k, v, *, scale=None, o=None, lse=None, want_lse: bool = True, stream=None):
     """attn_forward: q [B,T,H,D]; k, v [B,T,Hkv,D]; scale: 1/sqrt(D) unless given.  Returns
     (o [B,T,H,D], lse [B,T,H] fp32 or None)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [B,T,H,D]")
     return _forward(q, k, v, tuple(q.shape[:2]), scale, o, lse, want_lse, stream, "attn_forward", 4)
 
 
 def forward_varlen(q, k, v, cu_seqlens, *, scale=None, o=None, lse=None, want_lse: bool = True, stream=None):
     """attn_forward_varlen: packed samples on one token axis ([T_total, ...] tensors); cu_seqlens: host
     sequence of n + 1 offsets.  Tokens behind the last offset are left as they are in given outputs."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [T_total,H,D]")
     arr, n = _packed(cu_seqlens, q.shape[0])
     return _forward(q, k, v, (arr, n), scale, o, lse, want_lse, stream, "attn_forward_varlen", 3)
 
@@ -86,11 +90,15 @@ def _backward(q, k, v, o, lse, do, seqs, tokens, scale, workspace, stream, out, 
 def backward(q, k, v, o, lse, do, *, scale=None, workspace=None, stream=None, out=None):
     """attn_backward: (dq, dk, dv) for dL/do = do through forward(q, k, v), from the o and lse it
     returned; the gradients have the inputs' shapes and type.  `out` may hold preallocated tensors."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [B,T,H,D]")
     return _backward(q, k, v, o, lse, do, tuple(q.shape[:2]), q.shape[0] * q.shape[1], scale, workspace, stream, out,
                      "attn_backward", 4)
 
 
 def backward_varlen(q, k, v, o, lse, do, cu_seqlens, *, scale=None, workspace=None, stream=None, out=None):
     """attn_backward_varlen: backward() over packed samples, as in forward_varlen()."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [T_total,H,D]")
     arr, n = _packed(cu_seqlens, q.shape[0])
     return _backward(q, k, v, o, lse, do, (arr, n), int(arr[n]), scale, workspace, stream, out, "attn_backward_varlen", 3)
