@@ -8,7 +8,7 @@ import mixers_ref as R
 from linear_attention_sequence_mshortconv_b200 import attention, gdn, kda
 from test_gpu_attention import FP32, FWD
 from test_gpu_attention import make as make_attention
-from test_gpu_gdn import PIECES, cuda, kernels, make, make_step
+from test_gpu_gdn import PIECES, check_grads, cuda, kernels, make, make_step, tol
 
 pytestmark = pytest.mark.gpu
 
@@ -87,6 +87,43 @@ def test_keys_scored_minus_infinity(D, H, masked, value, scale, dtype):
     assert np.abs(R.f64(lse)[masked:] - ref_lse[masked:]).max() <= 16 * 2.0 ** -24 * top
     if value == -np.inf:
         assert bool((lse[:masked] == -np.inf).all()) and bool(o[:masked].isnan().all())
+    assert kda.last_device_error() == 0
+
+
+# ---- the gradients over equal rows -------------------------------------------------------------------------------------
+ROWS = [  # B, T, Hk, Hv, Dk, Dv
+    (2, 130, 2, 2, 128, 128), (3, 64, 1, 4, 64, 64), (1, 1, 2, 2, 128, 128), (2, 77, 1, 1, 32, 32), (4, 65, 1, 3, 64, 32),
+    (5, 63, 16, 32, 128, 64), (3, 193, 16, 32, 64, 128), (7, 129, 8, 24, 128, 32), (100, 1, 1, 2, 64, 64), (90, 65, 1, 2, 128, 64), (255, 64, 1, 1, 64, 32)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("case", ROWS, ids=str)
+def test_gradients_of_rows_equal_packed_samples(case, dtype):
+    B, T, Hk, Hv, Dk, Dv = case
+    x, S0, do, dS = make([T] * B, Hk, Hv, Dk, Dv, dtype, seed=B + T)
+    x, S0, do, dS = cuda(x), S0.cuda(), do.cuda(), dS.cuda()
+    rows = lambda t: t.view(B, T, *t.shape[1:])   # noqa: E731
+    got = gdn.backward(*map(rows, x), rows(do), S0, dS)
+    for a, b in zip(got, gdn.backward_varlen(*x, do, R.offsets([T] * B), S0, dS)):
+        assert torch.equal(a.view_as(b), b)
+    o, S = gdn.forward(*map(rows, x), S0)
+    o2, S2 = gdn.forward_varlen(*x, R.offsets([T] * B), S0)
+    assert torch.equal(o.view_as(o2), o2) and torch.equal(S, S2)
+    assert kda.last_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,T,Dk,Dv", [(300, 1, 64, 64), (300, 63, 64, 128), (300, 64, 128, 64), (300, 65, 64, 32), (700, 17, 128, 128), (1111, 3, 64, 64)])
+def test_many_rows(B, T, Dk, Dv, dtype):
+    """More rows than a launch takes packed samples."""
+    x, S0, do, dS = make([T] * B, 1, 1, Dk, Dv, dtype, seed=B + T)
+    rows = lambda t: t.view(B, T, *t.shape[1:]).cuda()   # noqa: E731
+    ref_o, ref_S = R.gdn(*map(R.f64, x), [T] * B, R.f64(S0))
+    o, S = gdn.forward(*map(rows, x), S0.cuda())
+    assert R.norm_error(o.flatten(0, 1), ref_o) <= tol(dtype) and R.norm_error(S, ref_S) <= tol(torch.float32)
+    ref = R.gdn_backward(*map(R.f64, x), R.f64(do), [T] * B, R.f64(S0), R.f64(dS))
+    got = gdn.backward(*map(rows, x), rows(do), S0.cuda(), dS.cuda())
+    check_grads([t.flatten(0, 1) for t in got[:5]] + [got[5]], ref, x, tol(dtype, grad=True))
     assert kda.last_device_error() == 0
 
 
