@@ -6,7 +6,7 @@ import torch
 
 import mixers_ref as R
 from linear_attention_sequence_mshortconv_b200 import attention, gdn, kda
-from test_gpu_attention import FP32, FWD
+from test_gpu_attention import FP32, FWD, GRAD
 from test_gpu_attention import make as make_attention
 from test_gpu_gdn import PIECES, check_grads, cuda, kernels, make, make_step, tol
 
@@ -125,6 +125,62 @@ def test_many_rows(B, T, Dk, Dv, dtype):
     got = gdn.backward(*map(rows, x), rows(do), S0.cuda(), dS.cuda())
     check_grads([t.flatten(0, 1) for t in got[:5]] + [got[5]], ref, x, tol(dtype, grad=True))
     assert kda.last_device_error() == 0
+
+
+# ---- gradients of flat and of peaked softmaxes ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_gradients_without_a_scale(D, dtype):
+    """scale = 0: q and k have no part in the output, and their gradients are exactly zero."""
+    lens = [200, 65, 400]
+    x = make_attention(lens, 2, 1, D, dtype, seed=6)
+    q, k, v, do = cuda(x)
+    o, lse = attention.forward_varlen(q, k, v, R.offsets(lens), scale=0.0)
+    dq, dk, dv = attention.backward_varlen(q, k, v, o, lse, do, R.offsets(lens), scale=0.0)
+    assert bool((dq == 0).all()) and bool((dk == 0).all())
+    assert R.norm_error(dv, R.attention_backward(*map(R.f64, x), lens, 0.0)[2]) <= (FP32 if dtype == torch.float32 else GRAD)
+
+
+def magnitudes(q, k, v, do, lens, scale):
+    """Per entry of dq, dk, dv the sum of the magnitudes of its terms, the score gradient p (do.v - delta) counted as
+    p (|do.v| + |delta|)."""
+    T, H, D = q.shape
+    r = H // k.shape[1]
+    out = [np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)]
+    at = 0
+    for n in lens:
+        sl = slice(at, at + n)
+        for h in range(H):
+            s = np.where(np.tril(np.ones((n, n), bool)), scale * q[sl, h] @ k[sl, h // r].T, -np.inf)
+            p = np.exp(s - s.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            dp = do[sl, h] @ v[sl, h // r].T
+            ds = abs(scale) * p * (np.abs(dp) + np.abs((p * dp).sum(1, keepdims=True)))
+            out[0][sl, h] = ds @ np.abs(k[sl, h // r])
+            out[1][sl, h // r] += ds.T @ np.abs(q[sl, h])
+            out[2][sl, h // r] += p.T @ np.abs(do[sl, h])
+        at += n
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens", [[200, 65], [600]], ids=str)
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradients_of_scores_in_the_hundreds(D, lens, dtype):
+    """One key takes most of each row.  A weight e^{s - lse} is off by the errors of s and of lse, 16 * 2^-24 times the
+    largest |q||k| each (as the forward's test has them); a term of dq or dk is that, and in bf16 a rounding of the weight or
+    of the score gradient and delta's from the rounded o, 2^-8 each; and each sum is rounded once.  The terms of a
+    peaked row cancel, so the bound is of the sum of their magnitudes: 3 * 2^-8 + 32 * 2^-24 |q||k| in bf16,
+    128 * 2^-24 + 32 * 2^-24 |q||k| in fp32."""
+    x = make_attention(lens, 2, 1, D, dtype, seed=6, size=3.0)
+    q, k, v, do = cuda(x)
+    o, lse = attention.forward_varlen(q, k, v, R.offsets(lens), scale=1.0)
+    got = attention.backward_varlen(q, k, v, o, lse, do, R.offsets(lens), scale=1.0)
+    f = list(map(R.f64, x))
+    top = np.linalg.norm(f[0], axis=-1).max() * np.linalg.norm(f[1], axis=-1).max()
+    bound = 32 * 2.0 ** -24 * top + (FP32 if dtype == torch.float32 else GRAD)
+    for name, a, b, size in zip(("dq", "dk", "dv"), got, R.attention_backward(*f, lens, 1.0), magnitudes(*f, lens, 1.0)):
+        assert np.linalg.norm(R.f64(a) - b) <= bound * np.linalg.norm(size), name
 
 
 # ---- calls without a tensor that they need -------------------------------------------------------------------------------
