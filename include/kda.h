@@ -459,7 +459,9 @@ kda_status gdn_forward_varlen(const void* q, const void* k, const void* v, const
  * The gradient of g is that of the logarithm (alpha = e^g).  The call reruns the forward.
  * A value that is not finite at one token, a gate among them, may reach the gradients of every
  * token of its row, but never another row's.
- * workspace : gdn_backward_workspace_size(...) bytes.  Errors: as gdn_forward.
+ * workspace : gdn_backward_workspace_size(...) bytes.  (With KDA_BF16 and Dk >= 64 that is for
+ * tensors aligned to 16 bytes; with others the call takes the fp32 kernel's way, which may need
+ * more, and then allocates it stream-ordered, as for a NULL workspace.)  Errors: as gdn_forward.
  * gdn_backward_varlen -- the same over packed samples.
  */
 size_t gdn_backward_workspace_size(int B, int T, int Hk, int Hv, int Dk, int Dv, kda_dtype dtype);

@@ -153,28 +153,35 @@ kda_status run_gdn_forward(const GdnArgs& a, const Batch& b, void* workspace, si
     });
 }
 
-size_t gdn_bwd_need(const GdnArgs& a, const Batch& b)
+size_t gdn_bwd_need(const GdnArgs& a, const Batch& b, bool tc)
 {
-    GdnArgs x = a;
-    x.q = x.k = x.v = x.o = nullptr;
-    const bool tc = gdn_tc_supported(x);
     size_t need = 0;
     each_group(b, [&](const Seqs& s, int, int64_t) {
-        need = max_of(need, gdn_generic_bwd_workspace(s.slots(16), s.tokens(), a.Hv, a.Dk, a.Dv));
-        if (tc) need = max_of(need, gdn_tc_bwd_workspace(s, a.Hv, a.Dk, a.Dv));
+        need = max_of(need, tc ? gdn_tc_bwd_workspace(s, a.Hv, a.Dk, a.Dv)
+                               : gdn_generic_bwd_workspace(s.slots(16), s.tokens(), a.Hv, a.Dk, a.Dv));
         return KDA_OK;
     });
     return need;
+}
+// What is stated goes by the sizes alone; a call whose tensors are not aligned, and whose kernel then needs more,
+// allocates for itself.
+size_t gdn_bwd_stated(const GdnArgs& a, const Batch& b)
+{
+    GdnArgs x = a;
+    x.q = x.k = x.v = x.o = nullptr;
+    return gdn_bwd_need(a, b, gdn_tc_supported(x));
 }
 
 kda_status run_gdn_backward(const GdnBwdArgs& a, const Batch& b, void* workspace, size_t workspace_bytes,
                             kda_stream_t stream)
 {
     if (b.n == 0) return KDA_OK;
-    Scratch ws;
-    kda_status st = ws.acquire(workspace, workspace_bytes, gdn_bwd_need(a.f, b), (cudaStream_t)stream);
-    if (st != KDA_OK) return st;
     const bool tc = gdn_tc_bwd_supported(a);
+    const size_t need = gdn_bwd_need(a.f, b, tc), stated = gdn_bwd_stated(a.f, b);
+    Scratch ws;
+    kda_status st = ws.acquire(workspace, workspace_bytes, workspace ? stated : need, (cudaStream_t)stream);
+    if (st == KDA_OK && workspace && need > stated) st = ws.acquire(nullptr, 0, need, (cudaStream_t)stream);
+    if (st != KDA_OK) return st;
     const int sms = num_sms();
     int* status = tc ? device_status_ptr() : nullptr;
     if (tc && !status) return KDA_ERR_CUDA;
@@ -329,7 +336,7 @@ size_t gdn_backward_workspace_size(int B, int T, int Hk, int Hv, int Dk, int Dv,
 {
     const Batch b{nullptr, B, T};
     if (check_batch(b, false) != KDA_OK || check_gdn(Hk, Hv, Dk, Dv, dtype) != KDA_OK) return 0;
-    return gdn_bwd_need(gdn_sizes(Hk, Hv, Dk, Dv, dtype), b);
+    return gdn_bwd_stated(gdn_sizes(Hk, Hv, Dk, Dv, dtype), b);
 }
 
 size_t gdn_backward_varlen_workspace_size(const int32_t* cu_seqlens, int n_seqs, int Hk, int Hv, int Dk, int Dv,
@@ -337,7 +344,7 @@ size_t gdn_backward_varlen_workspace_size(const int32_t* cu_seqlens, int n_seqs,
 {
     const Batch b{cu_seqlens, n_seqs, 0};
     if (check_batch(b, true) != KDA_OK || check_gdn(Hk, Hv, Dk, Dv, dtype) != KDA_OK) return 0;
-    return gdn_bwd_need(gdn_sizes(Hk, Hv, Dk, Dv, dtype), b);
+    return gdn_bwd_stated(gdn_sizes(Hk, Hv, Dk, Dv, dtype), b);
 }
 
 kda_status gdn_backward(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* S0,

@@ -127,6 +127,31 @@ def test_many_rows(B, T, Dk, Dv, dtype):
     assert kda.last_device_error() == 0
 
 
+# ---- workspaces ----------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (128, 32)])
+@pytest.mark.parametrize("lens", [[70, 20], [130, 0, 1, 640]], ids=str)
+def test_unaligned_gradients_with_a_workspace_of_the_stated_size(lens, Dk, Dv):
+    """What is stated is for aligned tensors: views one element into their storage take another kernel, which may need more,
+    and write nothing behind the workspace."""
+    x, S0, do, dS = make(lens, 1, 2, Dk, Dv, torch.bfloat16, seed=44)
+
+    def shift(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        buf[1:] = t.flatten().cuda()
+        return buf[1:].view(t.shape)
+
+    cu = R.offsets(lens)
+    need = gdn.backward_varlen_workspace_size(cu, 1, 2, Dk, Dv)
+    ref = R.gdn_backward(*map(R.f64, x), R.f64(do), lens, R.f64(S0), R.f64(dS))
+    for move in (shift, lambda t: t.cuda()):
+        ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        got = gdn.backward_varlen(*map(move, x), move(do), cu, S0.cuda(), dS.cuda(), workspace=ws[:need])
+        check_grads(got, ref, x, tol(torch.bfloat16, grad=True))
+        assert bool((ws[need:] == 0xA5).all())
+        with pytest.raises(kda.KdaError):
+            gdn.backward_varlen(*map(move, x), move(do), cu, S0.cuda(), dS.cuda(), workspace=ws[:need - 256])
+
+
 # ---- gradients of flat and of peaked softmaxes ---------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("D", [32, 64, 128])
