@@ -425,6 +425,8 @@ kda_status kda_mshortconv_backward(const void* xq, const void* xk, const void* x
  *   Dk, Dv in {32, 64, 128}; dtype KDA_BF16 or KDA_F32 (every tensor but S0 and S_T).
  *   T may be 0 (o untouched, S_T = S0).
  *   workspace : as for kda_forward, of gdn_forward_workspace_size(...) bytes.
+ *   Rows shorter than 64 tokens run in groups of launches, whose workspace is 4 GiB at most or
+ *   that of 255 rows.
  * Sums, states and gates are fp32 or wider.  A value that is not finite at one token may
  * reach every later token of its row and the earlier tokens of its 64-token chunk, but never
  * another row.

@@ -127,6 +127,26 @@ def test_many_rows(B, T, Dk, Dv, dtype):
     assert kda.last_device_error() == 0
 
 
+@pytest.mark.parametrize("B,T,Hk,Hv,Dk,Dv,dtype", [(2800, 2, 4, 16, 64, 64, torch.bfloat16), (2300, 33, 2, 8, 128, 128, torch.bfloat16),
+                                                    (2300, 1, 8, 32, 64, 32, torch.bfloat16), (4200, 1, 4, 16, 128, 128, torch.float32)])
+def test_many_short_rows_of_many_heads(B, T, Hk, Hv, Dk, Dv, dtype):
+    """Rows that go in several groups, for their workspace: the bits of packed samples (255 to a launch)."""
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")   # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)   # noqa: E731
+    x = [t.to(dtype) for t in (unit(n(B * T, Hk, Dk)), unit(n(B * T, Hk, Dk)), n(B * T, Hv, Dv), -0.1 * n(B * T, Hv).abs(), torch.sigmoid(n(B * T, Hv)))]
+    S0, do, dS = n(B, Hv, Dk, Dv), n(B * T, Hv, Dv).to(dtype), n(B, Hv, Dk, Dv)
+    rows = lambda t: t.view(B, T, *t.shape[1:])   # noqa: E731
+    ws = torch.full((gdn.backward_workspace_size(B, T, Hk, Hv, Dk, Dv, dtype) + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    for a, b in zip(gdn.backward(*map(rows, x), rows(do), S0, dS, workspace=ws[:-4096]), gdn.backward_varlen(*x, do, R.offsets([T] * B), S0, dS)):
+        assert torch.equal(a.view_as(b), b)
+    assert bool((ws[-4096:] == 0xA5).all())
+    o, S = gdn.forward(*map(rows, x), S0)
+    o2, S2 = gdn.forward_varlen(*x, R.offsets([T] * B), S0)
+    assert torch.equal(o.view_as(o2), o2) and torch.equal(S, S2)
+    assert kda.last_device_error() == 0
+
+
 # ---- workspaces ----------------------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 128), (128, 32)])
 @pytest.mark.parametrize("lens", [[70, 20], [130, 0, 1, 640]], ids=str)

@@ -26,3 +26,13 @@ def test_gradients_take_what_the_tensor_core_kernels_need(B, T, Hk, Hv, Dk, Dv):
     # fp32: the entry states of chunks of 16 tokens, and dq and dk of every value head
     need = 4 * ((B * T // 16 + B) * Hv * Dk * Dv + 2 * B * T * Hv * Dk)
     assert gdn.backward_workspace_size(B, T, Hk, Hv, Dk, Dv, torch.float32) == need
+
+
+@pytest.mark.parametrize("T", [1, 17, 63])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_short_rows_take_no_chunk_each(T, dtype):
+    """65535 rows, each of less than a chunk: 4 GiB at most, or what 255 rows need."""
+    for Hk, Hv, Dk, Dv in ((16, 16, 128, 128), (1, 1, 64, 64), (4, 8, 128, 32)):
+        for size in (gdn.backward_workspace_size, gdn.workspace_size):
+            most = max(2 ** 32, size(255, T, Hk, Hv, Dk, Dv, dtype))
+            assert size(65535, T, Hk, Hv, Dk, Dv, dtype) <= most + 2 ** 20
