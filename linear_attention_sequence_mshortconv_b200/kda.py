@@ -257,8 +257,10 @@ def forward_gated(q, k, v, g, beta, gate, gamma=None, eps: float = 1e-6, S0=None
 
 
 def _cu_array(cu_seqlens):
-    arr = (ctypes.c_int32 * len(cu_seqlens))(*[int(x) for x in cu_seqlens])
-    return arr, len(cu_seqlens) - 1
+    offs = [int(x) for x in cu_seqlens]
+    if offs and not (-2 ** 31 <= min(offs) and max(offs) < 2 ** 31):   # ctypes would keep the low 32 bits
+        raise ValueError("cu_seqlens must fit 32 bits")
+    return (ctypes.c_int32 * len(offs))(*offs), len(offs) - 1
 
 
 def varlen_workspace_size(cu_seqlens, H, Dk, Dv, dtype=torch.bfloat16, chunk: int = 0, o_dtype=None) -> int:

@@ -3,7 +3,7 @@ other calls are (no GPU needed)."""
 import pytest
 import torch
 
-from linear_attention_sequence_mshortconv_b200 import attention, build, gdn
+from linear_attention_sequence_mshortconv_b200 import attention, build, gdn, kda
 
 z = torch.zeros
 CALLS = {
@@ -35,3 +35,15 @@ def test_a_step_without_an_input(which):
     x[which] = None
     with pytest.raises(TypeError, match=("q", "k", "v", "g", "beta")[which] + " must be"):
         gdn.step(*x, z(4, 2, 64, 64))
+
+
+@pytest.mark.parametrize("cu", [[0, 2 ** 32 + 4], [0, 2 ** 32 + 2, 4], [2 ** 32, 4], [0, -2 ** 32 + 4], [0, 2 ** 31]], ids=str)
+def test_offsets_beyond_32_bits(cu):
+    """Their low 32 bits would be offsets of 4 tokens (or negative ones)."""
+    build.build()
+    q, gate = z(4, 2, 64), z(4, 2)
+    for call in (lambda: gdn.forward_varlen(q, q, q, gate, gate, cu), lambda: gdn.backward_varlen(q, q, q, gate, gate, q, cu),
+                 lambda: attention.forward_varlen(q, q, q, cu), lambda: attention.backward_varlen(q, q, q, q, gate, q, cu),
+                 lambda: gdn.varlen_workspace_size(cu, 2, 2, 64, 64), lambda: kda.varlen_workspace_size(cu, 2, 64, 64)):
+        with pytest.raises(ValueError):
+            call()
