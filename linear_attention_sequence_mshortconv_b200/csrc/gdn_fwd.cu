@@ -31,7 +31,7 @@ namespace gdn {
 // forward substitution, a warp each, a column to a lane; then twice T21 = -T22 (A21 T11), on
 // the two 32x32 and on the one 64x64 block.  Nothing here waits for another chunk, so what bounds
 // it is the latency of these steps against the warps an SM holds: A and T take the place of K and
-// Q, and 102 registers a thread let five CTAs share an SM.  (4352 chunks and heads, Dk = 128: 84 us, 0.25 GB of
+// Q, and 96 registers a thread (12 to 20 bytes spilled) let five CTAs share an SM.  (4352 chunks and heads, Dk = 128: 84 us, 0.25 GB of
 // factors and inputs; the shared-memory pipe is busy 72% of it.)
 constexpr int ALD = 68;   // row of A and T in floats: rows of a warp's reads fall in different banks
 template <int DK>
@@ -584,7 +584,7 @@ namespace gdn {
 // for calls whose time is set by the longest sample's steps in a row, and whole heads for those where
 // the columns' steps, shared out over the SMs, are more than that.
 // Measured (Dk = Dv = 128): 4 x 68 chunks, 16 heads (117 steps of work an SM against 68 in a row): columns
-// 333 us, whole heads 179; 107 chunks in 12 ragged samples, 8 heads (23 against 33): 86 and 94.
+// 333 us, whole heads 179; 108 chunks in 12 ragged samples, 8 heads (23 against 33): 86 and 94.
 bool whole_heads(const GdnArgs& a, const Seqs& s, int sms)
 {
     int64_t longest = 0, all = 0;
