@@ -594,8 +594,9 @@ int piece_chunks(const Seqs& s, int Hv, int Dk, int Dv, int sms)
     const int64_t per = max(lo, (int64_t)8);
     if (pieces(per) * Hv > sms || pieces(per) > kMaxSeqs) return 0;
     // Steps in a row, in units of 0.1 us: 15 a chunk with columns of heads; 26 a chunk and launch, 40 a piece
-    // carried, 150 for the launches.  Measured (Dk = Dv = 128; columns, then pieces): one head pair of 6016 tokens 155
-    // and 128 us, of 12288 303 and 170; 16 heads of 8192 241 and 218, of 32768 920 and 620.
+    // carried, 150 for the launches.  Measured (columns, then pieces): one head pair of 6016 tokens 154 and 128 us, of
+    // 12288 301 and 168; 16 heads of 8192 239 and 217, of 32768 913 and 614 (Dk = Dv = 128; 64 x 128 and 128 x 64 go by Dk);
+    // Dk = Dv = 64: 138 and 91, 269 and 110, 213 and 163, 812 and 502.  (4096 tokens are not cut at any width.)
     const int64_t steps = (longest + per - 1) / per;
     return 3 * 26 * per + 40 * steps + 150 < 15 * longest ? (int)per : 0;
 }

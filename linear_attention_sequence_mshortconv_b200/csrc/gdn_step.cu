@@ -6,8 +6,8 @@
 // A CTA owns 32 value columns of one (request, value head): 128-byte rows of the state,
 // loaded as float4 by 8 lanes, Dk / 32 of them held in registers by each of 256 threads
 // between the sums and the update.  16 KB a CTA and 8 CTAs an SM keep 128 KB in flight per
-// SM; one request alone still spreads over Dv / 32 CTAs per head.  (256 requests, 32 heads, 128 x 128: 204 us,
-// 5.3 TB/s or 81% of a copy's rate; one request of 16 heads: 4.6 us, a launch's latency.)
+// SM; one request alone still spreads over Dv / 32 CTAs per head.  (256 requests, 32 heads, 128 x 128: 194 to 204 us,
+// 5.3 to 5.5 TB/s or 81 to 85% of a copy's rate; one request of 16 heads: 4.6 us, a launch's latency.)
 
 #include "mixers.h"
 
@@ -39,7 +39,9 @@ __global__ void __launch_bounds__(256) gdn_step_kernel(GdnStepArgs a)
     float4 s[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) s[r] = __ldcs(S + r * step);
-    // A slot named twice would be updated by two CTAs at once: the first request has it.
+    // A slot named twice would be updated by two CTAs at once: the first request has it.  (Every CTA reads the slots
+    // before its own, quadratic in the requests: with states of 32 x 32, one head, it costs 14.1 us against 12.8 without
+    // slots at 256 requests, 17.4 against 14.6 at 4096, 68 against 45 at 16384; with 16 heads 202 against 172 at 4096.)
     bool taken = false;
     if (a.slots)
         for (int i = tid; i < req; i += 256) taken |= a.slots[i] == slot;
